@@ -357,6 +357,144 @@ int zg_grad_norm_noalloc(const uint16_t *const *grad_ptrs, int p, int64_t n, flo
 /* Free the context and its workspace (after the stream work using it is done). */
 void zg_destroy(zg_ctx *ctx);
 
+/* ------------------------------------------------------------------------
+ * Training operators. What stands before the step: the calls below produce
+ * a model's gradients the way the step takes them, in bf16 and times the loss
+ * scale. Each takes bf16 or binary32 data and computes in binary32, rounding
+ * once where it stores; each is stream-ordered, allocates nothing and gives
+ * the same bits for the same inputs every time.
+ * ------------------------------------------------------------------------ */
+
+#define ZG_DTYPE_BF16 0
+#define ZG_DTYPE_F32 1
+
+/* The gated linear recurrence over time, channel by channel:
+ *   a_t = sigmoid(f_t),  h_t = a_t * h_{t-1} + (1 - a_t) * x_t,  y_t = h_t,
+ * where 1 - a_t is computed as sigmoid(-f_t), not as a difference. The state h
+ * is binary32. f_t = -inf forgets everything before t. A NaN or infinity in
+ * one sequence or channel stays in that sequence and channel. */
+
+/* Element (b, t, c) is ptr[b * batch_stride + t * token_stride + c], strides
+ * in elements: channels are contiguous, so a tensor can be a part of a wider
+ * projection's output. ptr is aligned to its element; from 2 elements of
+ * alignment on (pointer and strides) loads take two channels at a time. */
+typedef struct {
+    void *ptr;
+    int64_t batch_stride, token_stride; /* >= 0; an output's must not make elements overlap */
+} zg_view;
+
+/* batch x tokens x channels elements of one dtype (ZG_DTYPE_*). seq_start
+ * NULL: each of the batch rows is one sequence. Otherwise batch is 1 and the
+ * tokens hold n_seq sequences end to end: sequence s is the tokens
+ * [seq_start[s], seq_start[s+1]), where seq_start is a device array of
+ * n_seq + 1 non-decreasing int64 from 0 up to at most `tokens`; a sequence
+ * may be empty. Tokens at or past seq_start[n_seq] belong to no sequence:
+ * nothing of them is read or written. (Values that break this give
+ * unspecified results, but no access outside the buffers.) */
+typedef struct {
+    int64_t batch, tokens, channels;
+    const int64_t *seq_start;
+    int64_t n_seq;
+    int dtype;
+} zg_scan_shape;
+
+/* Tokens per saved state: forward saves, and backward starts from, the state
+ * before each token whose index in its row is a multiple of this. */
+#define ZG_SCAN_CHUNK 128
+
+typedef struct zg_scan zg_scan; /* opaque; the workspace of one stream's scans */
+
+/* Create the workspace for scans of up to batch rows of up to `tokens` tokens
+ * by `channels` channels on the current device (each at least 1). One handle
+ * serves any smaller shape too, and one stream at a time. About 0.16 bytes
+ * per element; none for tokens <= ZG_SCAN_CHUNK. *out is NULL on failure. */
+int zg_scan_init(int64_t batch, int64_t tokens, int64_t channels, zg_scan **out);
+void zg_scan_destroy(zg_scan *scan);
+
+/* Forward. x, f and y as the shape says. h0: the state before each sequence's
+ * first token, contiguous (sequences, channels) binary32, or NULL for zeros.
+ * h_last (or NULL): the state after each sequence's last token, laid out
+ * alike (h0 itself for an empty sequence); it may be the same memory as h0.
+ * states (or NULL): receives batch x ceil(tokens / ZG_SCAN_CHUNK) x channels
+ * binary32 for zg_gated_scan_bwd. y must not overlap x or f. One token per
+ * sequence (a decoding step) is the same call with tokens = 1. A shape larger
+ * than the handle's, or memory that is not on the current device, is refused
+ * with ZG_ERR_INVALID_ARG; memory not aligned to its element with
+ * ZG_ERR_MISALIGNED. */
+int zg_gated_scan(zg_scan *scan, const zg_scan_shape *shape, const zg_view *x, const zg_view *f, const float *h0,
+                  const zg_view *y, float *h_last, float *states, zg_stream stream);
+
+/* Backward. dy is the gradient of y, dh_last that of h_last (NULL: zero),
+ * states what forward saved for the same x, f, h0 and shape. Writes the
+ * gradients dx and df (in the shape's dtype) and dh0 (or NULL):
+ *   g_t = dy_t + a_{t+1} g_{t+1} (+ dh_last at a sequence's last token),
+ *   dx_t = (1 - a_t) g_t,  df_t = g_t (h_{t-1} - x_t) a_t (1 - a_t),
+ *   dh0 = a_1 g_1 (dh_last itself for an empty sequence).
+ * The states h are formed again from x and f in binary32. dx and df must not
+ * overlap an input or each other; dh0 may be the same memory as dh_last.
+ * Gradients are linear in dy and dh_last, so a loss scale passes through. */
+int zg_gated_scan_bwd(zg_scan *scan, const zg_scan_shape *shape, const zg_view *x, const zg_view *f,
+                      const zg_view *dy, const float *states, const float *h0, const float *dh_last,
+                      const zg_view *dx, const zg_view *df, float *dh0, zg_stream stream);
+
+/* Wait for `stream`, then report and clear the handle's status: ZG_OK, or
+ * ZG_ERR_DEVICE_TIMEOUT when a part of a scan waited for its predecessor's
+ * state longer than the wait limit (its outputs are then unspecified). */
+int zg_scan_status(zg_scan *scan, zg_stream stream, int *status);
+
+/* Bound, in polls, on that wait (default a few million, far above any healthy
+ * wait). 0 makes every wait run out at once (used to test that path). */
+int zg_scan_set_wait_limit(zg_scan *scan, int64_t polls);
+
+/* The k largest of each row of logits: values (rows x k, the logits' dtype)
+ * and their indices (rows x k), contiguous, largest first. Equal values go to
+ * the lowest index first; -0 equals +0; a NaN of either sign counts as larger than
+ * every number, and NaNs as equal to one another. Row r starts at
+ * logits + r * row_stride elements. 1 <= k <= ZG_TOPK_MAX, k <= vocab < 2^31,
+ * row_stride >= vocab. The teacher's half of the distillation below. */
+#define ZG_TOPK_MAX 256
+int zg_topk(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride, int k, void *values,
+            int32_t *index, zg_stream stream);
+
+/* Distillation of a student from a teacher's top logits. For each row, with z
+ * the student's logits over the vocabulary, T the temperature, and the
+ * teacher's k entries (t_j, i_j) of which those with 0 <= i_j < vocab are
+ * present:
+ *   p_j = softmax over the present entries of t / T,
+ *   q = softmax over the vocabulary of z / T,  lse = log sum exp(z / T),
+ *   loss = T^2 * sum_j p_j (log p_j - log q_{i_j}),
+ *   dlogits_v = scale * dloss * T * (q_v - sum of the p_j with i_j = v).
+ * A term with p_j = 0 counts as zero. A row without a present entry, or whose
+ * present entries are all -inf, is empty: its logits are not looked at, its
+ * loss, lse and gradient are zero (a padding row). A logit of -inf has
+ * q = 0. Entries may come in any order; a repeated index adds up. */
+typedef struct {
+    const void *logits; /* row r starts at logits + r * row_stride elements; aligned to its element */
+    int64_t rows, vocab, row_stride; /* vocab < 2^31, row_stride >= vocab */
+    int dtype;                       /* of logits and dlogits */
+    const void *t_logits;            /* rows x k, contiguous */
+    const int32_t *t_index;          /* rows x k, contiguous */
+    int t_dtype;                     /* of t_logits */
+    int k;                           /* 1 <= k <= ZG_TOPK_MAX */
+    float temperature;               /* finite, > 0 */
+} zg_distill_args;
+
+/* The loss of each row and its lse (rows binary32 each; lse may be NULL). */
+int zg_distill_loss(const zg_distill_args *args, float *loss, float *lse, zg_stream stream);
+
+/* The gradient, from the lse that zg_distill_loss gave for the same logits.
+ * scale (finite) is common to all rows: the loss scale over the number of
+ * rows, say. dloss: one binary32 factor per row, or NULL for ones. dlogits has
+ * the logits' dtype and row_stride drow_stride; it may be the logits
+ * themselves (same pointer and stride), else it must not overlap them. */
+int zg_distill_grad(const zg_distill_args *args, const float *lse, float scale, const float *dloss, void *dlogits,
+                    int64_t drow_stride, zg_stream stream);
+
+/* Both in one pass that reads the logits once from memory. lse may be NULL.
+ * The values are those of the two calls up to the order of the sums. */
+int zg_distill_loss_grad(const zg_distill_args *args, float scale, const float *dloss, float *loss, float *lse,
+                         void *dlogits, int64_t drow_stride, zg_stream stream);
+
 const char *zg_strerror(int code);
 const char *zg_last_error(void); /* this thread's last detailed message */
 int zg_version(void);

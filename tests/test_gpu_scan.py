@@ -1,0 +1,296 @@
+"""The gated linear recurrence against its formulas in 64 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import operators_ref as ref
+from gpu_helpers import Guarded
+from zero_sharded_mixed_flat_gb300 import binding as zb
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def rand(shape, seed, scale=1.0, shift=0.0):
+    rng = np.random.default_rng(seed)
+    return torch.from_numpy(rng.standard_normal(shape) * scale + shift)
+
+
+def views(b, t, c, dtype, layout, seed):
+    """x and f on the GPU in one of the layouts a program has them in."""
+    x, f = rand((b, t, c), seed).to(dtype), rand((b, t, c), seed + 1, 1.5, 2.0).to(dtype)
+    if layout == "plain":
+        return x.cuda(), f.cuda()
+    if layout == "fused":  # halves of one projection's output
+        both = torch.cat([x, f], -1).cuda()
+        return both[..., :c], both[..., c:]
+    if layout == "odd":  # one element off every alignment, odd strides
+        wide = torch.zeros(2, b, t, c + 3, dtype=dtype)
+        wide[0, ..., 1:c + 1], wide[1, ..., 1:c + 1] = x, f
+        wide = wide.cuda()
+        return wide[0, ..., 1:c + 1], wide[1, ..., 1:c + 1]
+    assert layout == "time_major"
+    return x.transpose(0, 1).contiguous().cuda().transpose(0, 1), f.transpose(0, 1).contiguous().cuda().transpose(0, 1)
+
+
+def run_case(b, t, c, dtype, layout="plain", starts=None, seed=0, with_h0=True, f_override=None):
+    dtype = DT[dtype]
+    x, f = views(b, t, c, dtype, layout, seed)
+    if f_override is not None:
+        f.copy_(f_override(f))
+    seqs = b if starts is None else len(starts) - 1
+    bounds = [(r, 0, t) for r in range(b)] if starts is None else [(0, lo, hi) for lo, hi in zip(starts, starts[1:])]
+    h0 = rand((seqs, c), seed + 2).float() if with_h0 else None
+    dh = rand((seqs, c), seed + 3).float() if with_h0 else None
+    dy = rand((b, t, c), seed + 4).to(dtype)
+    seq_start = None if starts is None else torch.tensor(starts, dtype=torch.int64).cuda()
+    scan = zb.GatedScan(b, t, c)
+    gx, gf, gdy = (x, f, dy.cuda()) if starts is None else (x[0], f[0], dy[0].cuda())
+    g0, gdh = (h0.cuda(), dh.cuda()) if with_h0 else (None, None)
+    y, last, kept = scan.forward(gx, gf, g0, seq_start, keep=True)
+    dx, df, dh0 = scan.backward(gx, gf, gdy, kept, g0, gdh, seq_start)
+    assert scan.status() == zb.ZG_OK
+    X, F = x.double().cpu(), f.double().cpu()
+    H0 = h0.double() if with_h0 else torch.zeros(seqs, c, dtype=torch.float64)
+    DH = dh.double() if with_h0 else torch.zeros(seqs, c, dtype=torch.float64)
+    h, wl, _, he, le, _ = ref.scan(X, F, H0, bounds)
+    wx, wf, w0, xe, fe, e0 = ref.scan_grad(X, F, H0, dy.double(), DH, bounds)
+    end = t if starts is None else starts[-1]
+    for got, want, err, what in ((y, h, he, "y"), (dx, wx, xe, "dx"), (df, wf, fe, "df")):
+        got = got[None] if starts is not None else got
+        ref.check(got[:, :end], want[:, :end], ref.stored(want, err, dtype)[:, :end], what)
+    ref.check(last, wl, ref.stored(wl, le, torch.float32), "h_last")
+    ref.check(dh0, w0, ref.stored(w0, e0, torch.float32), "dh0")
+    # the same bits again
+    y2, last2, kept2 = scan.forward(gx, gf, g0, seq_start, keep=True)
+    again = scan.backward(gx, gf, gdy, kept2, g0, gdh, seq_start)
+    y, y2 = (y[:end], y2[:end]) if starts is not None else (y, y2)
+    assert torch.equal(y, y2) and torch.equal(last, last2) and torch.equal(dh0, again[2])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("b,t,c", [(1, 1, 1), (3, 1, 5), (5, 1, 768), (2, 2, 64), (1, 7, 63), (2, 16, 129), (2, 31, 66),
+                                   (1, 127, 65), (2, 128, 64), (1, 129, 130), (2, 255, 32), (3, 257, 96), (1, 1000, 771),
+                                   (1, 4099, 40), (2, 2305, 67)])
+def test_sizes(b, t, c, dtype):
+    run_case(b, t, c, dtype, seed=b * 1000 + t + c)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", ["fused", "odd", "time_major"])
+@pytest.mark.parametrize("b,t,c", [(2, 1, 70), (2, 33, 66), (3, 300, 130)])
+def test_layouts(b, t, c, dtype, layout):
+    run_case(b, t, c, dtype, layout, seed=7)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("starts", [[0, 300], [0, 0, 0, 300], [0, 300, 300, 300], [0, 1, 2, 3, 300], [0, 128, 256, 300],
+                                    [0, 127, 129, 129, 256, 299, 300], [0, 100, 100, 150], [0, 0, 0], [0, 250, 260],
+                                    list(range(301))])
+def test_packed_sequences(starts, dtype):
+    run_case(1, 300, 71, dtype, starts=starts, seed=11)
+
+
+def test_packed_many_sequences_over_many_chunks():
+    rng = np.random.default_rng(5)
+    cuts = sorted(int(v) for v in rng.integers(0, 3001, 40))
+    run_case(1, 3000, 66, "bf16", starts=[0, *cuts, 3000], seed=13)
+    run_case(1, 3000, 65, "f32", "odd", starts=[0, *cuts, 2900 if cuts[-1] <= 2900 else cuts[-1]], seed=14)
+
+
+def test_more_empty_sequences_than_tokens_in_a_chunk():
+    run_case(1, 200, 33, "f32", starts=[0] * 200 + [70] * 300 + [200] * 150, seed=15)
+
+
+@pytest.mark.parametrize("t", [1, 64, 700])
+def test_no_initial_state(t):
+    run_case(2, t, 66, "f32", seed=17, with_h0=False)
+
+
+@pytest.mark.parametrize("shift", [-200.0, -20.0, 9.0, 30.0, 200.0])
+def test_gates_near_and_at_their_ends(shift):
+    """From forgetting everything to holding for ever."""
+    run_case(2, 400, 66, "f32", seed=19, f_override=lambda f: f * 0.5 + shift)
+
+
+def test_infinite_gates():
+    def some(f):
+        g = f.clone()
+        g[:, ::5] = math.inf
+        g[:, ::7] = -math.inf
+        return g
+    run_case(2, 300, 66, "f32", seed=23, f_override=some)
+    run_case(2, 300, 66, "bf16", seed=23, f_override=some)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_non_finite_values_stay_in_their_sequence_and_channel(dtype):
+    t, c = 700, 70
+    starts = torch.tensor([0, 200, 450, 600], dtype=torch.int64).cuda()
+    x, f = (v[0] for v in views(1, t, c, DT[dtype], "plain", 29))
+    x[599:], f[600:] = math.nan, math.nan  # the last token of the third sequence, and all past the end
+    x[250, 3], f[300, 4] = math.nan, math.nan
+    scan = zb.GatedScan(1, t, c)
+    h0 = torch.zeros(3, c, device="cuda")
+    dy = torch.ones_like(x)
+    dy[600:] = math.nan
+    y, last, kept = scan.forward(x, f, h0, starts, keep=True)
+    dx, df, dh0 = scan.backward(x, f, dy, kept, h0, None, starts)
+    bad = torch.zeros(t, c, dtype=torch.bool, device="cuda")
+    bad[250:450, 3] = True
+    bad[300:450, 4] = True
+    bad[599] = True
+    assert torch.equal(torch.isnan(y[:600]), bad[:600])
+    assert torch.equal(torch.isnan(last), torch.stack([bad[199], bad[449], bad[599]]))
+    bad_dx = torch.zeros_like(bad)
+    bad_dx[200:301, 4] = True
+    assert torch.equal(torch.isnan(dx[:600]), bad_dx[:600])
+    bad_df = bad_dx.clone()
+    bad_df[250:450, 3] = True
+    bad_df[300:450, 4] = True
+    bad_df[599] = True
+    assert torch.equal(torch.isnan(df[:600]), bad_df[:600])
+    assert torch.isnan(dh0).nonzero().tolist() == [[1, 4]]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t,end", [(5, 4), (300, 290)])
+def test_only_the_outputs_are_written(t, end, dtype):
+    """Guards around every output, and the rows past the last sequence, keep their bytes."""
+    c, dt = 67, DT[dtype]
+    x, f = (v[0] for v in views(1, t, c, dt, "plain", 31))
+    starts = torch.tensor([0, 2, end], dtype=torch.int64).cuda()
+    big = {k: Guarded(t * c, dt) for k in ("y", "dx", "df")}
+    last = Guarded(2 * c, torch.float32)
+    scan = zb.GatedScan(1, t, c)
+    out = {k: g.view.view(t, c) for k, g in big.items()}
+    _, _, kept = scan.forward(x, f, None, starts, keep=True, out=out["y"], h_last=last.view.view(2, c))
+    scan.backward(x, f, torch.ones_like(x), kept, None, None, starts, out=(out["dx"], out["df"]))
+    torch.cuda.synchronize()
+    assert last.intact()
+    for k, g in big.items():
+        assert g.intact(), k
+        tail = out[k][end:].contiguous().view(torch.uint8)
+        assert bool((tail == 0xA5).all()), k
+        assert bool(torch.isfinite(out[k][:end]).all()), k
+
+
+def test_state_updated_in_place_token_by_token():
+    """Decoding one token at a time gives what one call over all tokens gives."""
+    b, t, c = 3, 9, 768
+    x, f = views(b, t, c, torch.bfloat16, "plain", 37)
+    h0 = rand((b, c), 38).float().cuda()
+    scan = zb.GatedScan(b, t, c)
+    y, last, _ = scan.forward(x, f, h0)
+    state = h0.clone()
+    for i in range(t):
+        yi, s = scan.step(x[:, i], f[:, i], state, out_state=state)
+        assert s is state
+        ref.check(yi, y[:, i].double().cpu(), ref.BF16 * y[:, i].double().abs().cpu() + 1e-6, i)
+    ref.check(state, last.double().cpu(), 1e-6 + ref.EPS * last.double().abs().cpu())
+    # in place over many chunks
+    x, f = views(b, 700, c, torch.bfloat16, "plain", 39)
+    scan = zb.GatedScan(b, 700, c)
+    _, want, _ = scan.forward(x, f, h0)
+    state = h0.clone()
+    scan.forward(x, f, state, h_last=state)
+    assert torch.equal(state, want)
+
+
+def test_gradient_against_differences():
+    b, t, c = 1, 150, 9
+    x, f = (v.double().cpu() for v in views(b, t, c, torch.float32, "plain", 41))
+    h0, w = rand((1, c), 42).float().double(), rand((b, t, c), 43).float().double()
+    bounds = [(0, 0, t)]
+    scan = zb.GatedScan(b, t, c)
+    gx, gf, g0 = x.float().cuda(), f.float().cuda(), h0.float().cuda()
+    _, _, kept = scan.forward(gx, gf, g0, keep=True)
+    dx, df, dh0 = scan.backward(gx, gf, w.float().cuda(), kept, g0)
+    for which, grad in (("x", dx), ("f", df), ("h", dh0)):
+        d = rand(grad.shape, 44)
+        step = 1e-5
+
+        def value(sign):
+            at = {"x": x, "f": f, "h": h0}
+            at[which] = at[which] + sign * step * d
+            return float((ref.scan(at["x"], at["f"], at["h"], bounds)[0] * w).sum())
+
+        slope = (value(1) - value(-1)) / (2 * step)
+        mine = float((grad.double().cpu() * d).sum())
+        # the difference's own error is of the order step^2; the gradient's is its rounding
+        assert abs(slope - mine) <= 1e-5 * float((grad.double().cpu() * d).abs().sum()), which
+
+
+def test_another_stream_and_graph_replay():
+    b, t, c = 2, 600, 130
+    x, f = views(b, t, c, torch.bfloat16, "plain", 47)
+    scan = zb.GatedScan(b, t, c)
+    want = [v.clone() for v in scan.forward(x, f)[:2]]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = scan.forward(x, f)[:2]
+    side.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    sx, sf = torch.zeros_like(x), torch.zeros_like(f)
+    out, last = torch.empty_like(x), torch.empty(b, c, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        scan.forward(sx, sf, out=out, h_last=last)
+    for _ in range(3):
+        sx.copy_(x)
+        sf.copy_(f)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(last, want[1])
+
+
+def test_one_handle_serves_smaller_shapes():
+    scan = zb.GatedScan(3, 900, 200)
+    for b, t, c in ((3, 900, 200), (1, 1, 1), (2, 300, 64), (3, 129, 200), (1, 900, 33)):
+        x, f = views(b, t, c, torch.float32, "plain", 53)
+        y, _, _ = scan.forward(x, f)
+        h, _, _, e, _, _ = ref.scan(x.double().cpu(), f.double().cpu(), torch.zeros(b, c, dtype=torch.float64),
+                                    [(r, 0, t) for r in range(b)])
+        ref.check(y, h, ref.stored(h, e, torch.float32))
+
+
+def test_offsets_past_32_bits():
+    """Rows so far apart that element offsets pass 2^31 (the same memory read with a wide stride)."""
+    b, t, c = 2, 200, 64
+    gap = (1 << 31) + 64
+    x = torch.zeros(gap + t * c, dtype=torch.bfloat16, device="cuda")
+    dense, f = views(b, t, c, torch.bfloat16, "plain", 59)
+    far = x.as_strided((b, t, c), (gap, c, 1))
+    far.copy_(dense)
+    scan = zb.GatedScan(b, t, c)
+    assert torch.equal(scan.forward(far, f)[0], scan.forward(dense, f)[0])
+
+
+def test_refusals():
+    scan = zb.GatedScan(2, 64, 32)
+    x = torch.zeros(2, 64, 32, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(zb.ZgError, match="larger than the handle"):
+        scan.forward(torch.zeros(2, 65, 32, device="cuda"), torch.zeros(2, 65, 32, device="cuda"))
+    with pytest.raises(TypeError, match="f must have dtype"):
+        scan.forward(x, x.float())
+    with pytest.raises(ValueError, match="f must have shape"):
+        scan.forward(x, x[:, :3])
+    with pytest.raises(TypeError, match="bfloat16 or float32"):
+        scan.forward(x.half(), x.half())
+    with pytest.raises(ValueError, match="contiguous"):
+        scan.forward(x.transpose(1, 2)[:, :, :32], x.transpose(1, 2)[:, :, :32])
+    with pytest.raises(ValueError, match="h0 must have shape"):
+        scan.forward(x, x, torch.zeros(3, 32, device="cuda"))
+    with pytest.raises(TypeError, match="h0 must have dtype"):
+        scan.forward(x, x, torch.zeros(2, 32, device="cuda", dtype=torch.float64))
+    with pytest.raises(zb.ZgError, match="batch = 1"):
+        scan.forward(x, x, seq_start=torch.tensor([0, 64], device="cuda"))
+    with pytest.raises(zb.ZgError, match="overlap"):
+        scan.forward(x, x, out=x[:, :1].expand(2, 64, 32))
+    with pytest.raises(ValueError, match="kept is None"):
+        scan.backward(x, x, x, None)

@@ -36,6 +36,10 @@ ZG_VARIANT_SINGLE = 3
 ZG_MAX_RANKS = 16
 ZG_BUCKET_FIRST = 1
 ZG_BUCKET_LAST = 2
+ZG_DTYPE_BF16 = 0
+ZG_DTYPE_F32 = 1
+ZG_SCAN_CHUNK = 128
+ZG_TOPK_MAX = 256
 
 
 class ZgError(RuntimeError):
@@ -57,6 +61,24 @@ class _Info(ctypes.Structure):
         ("sumsq", ctypes.c_double), ("norm", ctypes.c_double), ("clip_coef", ctypes.c_float),
         ("found_inf", ctypes.c_int), ("step_t", ctypes.c_int64), ("status", ctypes.c_int),
     ]
+
+
+_P, _I64 = ctypes.c_void_p, ctypes.c_int64
+
+
+class _View(ctypes.Structure):
+    _fields_ = [("ptr", _P), ("batch_stride", _I64), ("token_stride", _I64)]
+
+
+class _ScanShape(ctypes.Structure):
+    _fields_ = [("batch", _I64), ("tokens", _I64), ("channels", _I64), ("seq_start", _P), ("n_seq", _I64),
+                ("dtype", ctypes.c_int)]
+
+
+class _Distill(ctypes.Structure):
+    _fields_ = [("logits", _P), ("rows", _I64), ("vocab", _I64), ("row_stride", _I64), ("dtype", ctypes.c_int),
+                ("t_logits", _P), ("t_index", _P), ("t_dtype", ctypes.c_int), ("k", ctypes.c_int),
+                ("temperature", ctypes.c_float)]
 
 
 @dataclass(frozen=True)
@@ -82,7 +104,6 @@ class StepInfo:
 
 
 _lib = None
-_P, _I64 = ctypes.c_void_p, ctypes.c_int64
 
 
 def lib() -> ctypes.CDLL:
@@ -117,6 +138,16 @@ def lib() -> ctypes.CDLL:
             "zg_gather_params_dma": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P]),
             "zg_grad_norm_noalloc": (ctypes.c_int, [_P, ctypes.c_int, _I64, ctypes.c_float, ctypes.c_int, _P, _P]),
             "zg_destroy": (None, [_P]),
+            "zg_scan_init": (ctypes.c_int, [_I64, _I64, _I64, ctypes.POINTER(_P)]),
+            "zg_scan_destroy": (None, [_P]),
+            "zg_gated_scan": (ctypes.c_int, [_P] * 9),
+            "zg_gated_scan_bwd": (ctypes.c_int, [_P] * 12),
+            "zg_scan_status": (ctypes.c_int, [_P, _P, ctypes.POINTER(ctypes.c_int)]),
+            "zg_scan_set_wait_limit": (ctypes.c_int, [_P, _I64]),
+            "zg_topk": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, ctypes.c_int, _P, _P, _P]),
+            "zg_distill_loss": (ctypes.c_int, [_P, _P, _P, _P]),
+            "zg_distill_grad": (ctypes.c_int, [_P, _P, ctypes.c_float, _P, _P, _I64, _P]),
+            "zg_distill_loss_grad": (ctypes.c_int, [_P, ctypes.c_float, _P, _P, _P, _P, _I64, _P]),
             "zg_strerror": (ctypes.c_char_p, [ctypes.c_int]),
             "zg_last_error": (ctypes.c_char_p, []),
             "zg_version": (ctypes.c_int, []),
@@ -424,3 +455,215 @@ class ShardedAdamW:
         else:
             zg_gather_params(self.ctx, self.params, lo, hi, out, stream)
         return out
+
+
+# ----------------------------------------------------------------- training operators
+
+_DTYPES = {torch.bfloat16: ZG_DTYPE_BF16, torch.float32: ZG_DTYPE_F32}
+
+
+def _dtype(t: torch.Tensor, what: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a tensor")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{what} must be bfloat16 or float32 (got {t.dtype})")
+    return _DTYPES[t.dtype]
+
+
+def _like(t: torch.Tensor, ref: torch.Tensor, what: str) -> torch.Tensor:
+    """A CUDA tensor of ref's device, dtype and shape whose last dimension is contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a tensor")
+    if not t.is_cuda:
+        raise TypeError(f"{what} must be a CUDA tensor")
+    if t.device != ref.device:
+        raise ValueError(f"{what} is on {t.device}, not on {ref.device}")
+    if t.dtype != ref.dtype:
+        raise TypeError(f"{what} must have dtype {ref.dtype} (got {t.dtype})")
+    if t.shape != ref.shape:
+        raise ValueError(f"{what} must have shape {tuple(ref.shape)} (got {tuple(t.shape)})")
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"the last dimension of {what} must be contiguous")
+    return t
+
+
+def _side(t: torch.Tensor | None, dtype: torch.dtype, shape, ref: torch.Tensor, what: str) -> int | None:
+    """The address of an optional contiguous CUDA tensor of exactly ``shape``."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if t.is_cuda and t.device != ref.device:
+        raise ValueError(f"{what} is on {t.device}, not on {ref.device}")
+    return _dev_ptr(t, dtype, 0, what)
+
+
+class GatedScan:
+    """The gated linear recurrence h_t = sigmoid(f_t) h_{t-1} + sigmoid(-f_t) x_t
+    over time, channel by channel, with its backward pass, on a handle for up
+    to ``batch`` rows of up to ``tokens`` tokens by ``channels`` channels.
+
+    x and f are (batch, tokens, channels), or (tokens, channels) for one row,
+    bfloat16 or float32, the channels contiguous (parts of a wider projection
+    are fine). ``seq_start``: for one row that holds several sequences end to
+    end, the int64 CUDA tensor of their starts and the last one's end. States
+    are float32 (sequences, channels). One handle serves one stream at a time.
+    """
+
+    def __init__(self, batch: int, tokens: int, channels: int):
+        out = ctypes.c_void_p()
+        self.handle = None
+        _check(lib().zg_scan_init(batch, tokens, channels, ctypes.byref(out)), "zg_scan_init")
+        self.handle = out.value
+
+    def __del__(self):
+        if getattr(self, "handle", None) and _lib is not None:
+            _lib.zg_scan_destroy(self.handle)
+            self.handle = None
+
+    def _shape(self, x, seq_start) -> tuple[_ScanShape, int]:
+        dt = _dtype(x, "x")
+        if x.dim() not in (2, 3):
+            raise ValueError(f"x must be (batch, tokens, channels) or (tokens, channels) (got {tuple(x.shape)})")
+        b, t, c = x.shape if x.dim() == 3 else (1, *x.shape)
+        _like(x, x, "x")
+        if seq_start is None:
+            return _ScanShape(b, t, c, None, 0, dt), b
+        if seq_start.dim() != 1 or seq_start.numel() < 2:
+            raise ValueError("seq_start must hold the starts of the sequences and the end of the last")
+        n = seq_start.numel() - 1
+        return _ScanShape(b, t, c, _side(seq_start, torch.int64, (n + 1,), x, "seq_start"), n, dt), n
+
+    @staticmethod
+    def _view(t) -> _View:
+        return _View(t.data_ptr(), t.stride(0) if t.dim() == 3 else 0, t.stride(-2))
+
+    def forward(self, x, f, h0=None, seq_start=None, keep: bool = False, out=None, h_last=None, stream=None):
+        """y, the state after each sequence, and with ``keep`` the states that
+        ``backward`` starts from (else None). ``out`` and ``h_last`` are
+        allocated when None; h_last may be h0 itself."""
+        shape, n = self._shape(x, seq_start)
+        _like(f, x, "f")
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else _like(out, x, "out")
+        last = torch.empty(n, shape.channels, dtype=torch.float32, device=x.device) if h_last is None else h_last
+        side = (n, shape.channels)
+        p0, p1 = _side(h0, torch.float32, side, x, "h0"), _side(last, torch.float32, side, x, "h_last")
+        kept = None
+        if keep:
+            chunks = -(-shape.tokens // ZG_SCAN_CHUNK)
+            kept = torch.empty(shape.batch, chunks, shape.channels, dtype=torch.float32, device=x.device)
+        _check(lib().zg_gated_scan(self.handle, ctypes.byref(shape), ctypes.byref(self._view(x)),
+                                   ctypes.byref(self._view(f)), p0, ctypes.byref(self._view(y)), p1,
+                                   kept.data_ptr() if keep else None, _stream(stream)), "zg_gated_scan")
+        return y, last, kept
+
+    def backward(self, x, f, dy, kept, h0=None, dh_last=None, seq_start=None, out=None, stream=None):
+        """The gradients (dx, df, dh0) from dy and dh_last (None: zero), for the
+        x, f and h0 of the forward call that gave ``kept``. ``out``: (dx, df)
+        to write into, for instance the parts of one projection's gradient."""
+        shape, n = self._shape(x, seq_start)
+        _like(f, x, "f")
+        _like(dy, x, "dy")
+        if out is None:
+            out = (torch.empty(x.shape, dtype=x.dtype, device=x.device), torch.empty(x.shape, dtype=x.dtype, device=x.device))
+        dx, df = _like(out[0], x, "dx"), _like(out[1], x, "df")
+        dh0 = torch.empty(n, shape.channels, dtype=torch.float32, device=x.device)
+        side = (n, shape.channels)
+        chunks = -(-shape.tokens // ZG_SCAN_CHUNK)
+        if kept is None:
+            raise ValueError("kept is None: call forward with keep=True")
+        _check(lib().zg_gated_scan_bwd(
+            self.handle, ctypes.byref(shape), ctypes.byref(self._view(x)), ctypes.byref(self._view(f)),
+            ctypes.byref(self._view(dy)), _side(kept, torch.float32, (shape.batch, chunks, shape.channels), x, "kept"),
+            _side(h0, torch.float32, side, x, "h0"), _side(dh_last, torch.float32, side, x, "dh_last"),
+            ctypes.byref(self._view(dx)), ctypes.byref(self._view(df)), dh0.data_ptr(), _stream(stream)),
+            "zg_gated_scan_bwd")
+        return dx, df, dh0
+
+    def step(self, x, f, state, out_state=None, out=None, stream=None):
+        """One token for each of x's rows (batch, channels): y and the new
+        state, written to ``out_state`` (``state`` itself to update it in place)."""
+        if not isinstance(x, torch.Tensor) or x.dim() != 2:
+            raise ValueError("x must be (batch, channels)")
+        y, last, _ = self.forward(x[:, None], f[:, None], state, out=None if out is None else out[:, None],
+                                  h_last=out_state, stream=stream)
+        return y[:, 0], last
+
+    def status(self, stream=None) -> int:
+        """ZG_OK, or ZG_ERR_DEVICE_TIMEOUT when a scan's bounded wait ran out (waits for the stream)."""
+        st = ctypes.c_int()
+        _check(lib().zg_scan_status(self.handle, _stream(stream), ctypes.byref(st)), "zg_scan_status")
+        return st.value
+
+
+def _rows(t, what: str) -> torch.Tensor:
+    _dtype(t, what)
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be (rows, vocab) (got {tuple(t.shape)})")
+    return _like(t, t, what)
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def topk_logits(logits, k: int, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The k largest of each row of ``logits`` (rows, vocab), largest first,
+    ties to the lowest index: values (rows, k) and int32 indices."""
+    _rows(logits, "logits")
+    n, v = logits.shape
+    values = torch.empty(n, k, dtype=logits.dtype, device=logits.device)
+    index = torch.empty(n, k, dtype=torch.int32, device=logits.device)
+    _check(lib().zg_topk(logits.data_ptr(), _DTYPES[logits.dtype], n, v, _row_stride(logits), k, values.data_ptr(),
+                         index.data_ptr(), _stream(stream)), "zg_topk")
+    return values, index
+
+
+def _distill(logits, t_logits, t_index, temperature: float) -> _Distill:
+    _rows(logits, "logits")
+    tdt = _dtype(t_logits, "t_logits")
+    n, v = logits.shape
+    if t_logits.dim() != 2:
+        raise ValueError(f"t_logits must be (rows, k) (got {tuple(t_logits.shape)})")
+    k = t_logits.shape[1]
+    return _Distill(logits.data_ptr(), n, v, _row_stride(logits), _DTYPES[logits.dtype],
+                    _side(t_logits, t_logits.dtype, (n, k), logits, "t_logits"),
+                    _side(t_index, torch.int32, (n, k), logits, "t_index"), tdt, k, temperature)
+
+
+def distill_loss(logits, t_logits, t_index, temperature: float, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The distillation loss of each row of student ``logits`` (rows, vocab)
+    against the teacher's entries ``t_logits`` and ``t_index`` (rows, k; index
+    -1 for none), and each row's log-sum-exp of logits / temperature."""
+    a = _distill(logits, t_logits, t_index, temperature)
+    loss = torch.empty(2, a.rows, dtype=torch.float32, device=logits.device)
+    _check(lib().zg_distill_loss(ctypes.byref(a), loss.data_ptr(), loss.data_ptr() + 4 * a.rows, _stream(stream)),
+           "zg_distill_loss")
+    return loss[0], loss[1]
+
+
+def distill_grad(logits, lse, t_logits, t_index, temperature: float, scale: float = 1.0, dloss=None, out=None,
+                 stream=None) -> torch.Tensor:
+    """The gradient of sum(scale * dloss * loss) by the logits, from the lse of
+    ``distill_loss`` (dloss None: ones). ``out`` may be the logits themselves."""
+    a = _distill(logits, t_logits, t_index, temperature)
+    out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device) if out is None else _like(out, logits, "out")
+    _check(lib().zg_distill_grad(ctypes.byref(a), _side(lse, torch.float32, (a.rows,), logits, "lse"), scale,
+                                 _side(dloss, torch.float32, (a.rows,), logits, "dloss"), out.data_ptr(),
+                                 _row_stride(out), _stream(stream)), "zg_distill_grad")
+    return out
+
+
+def distill_loss_grad(logits, t_logits, t_index, temperature: float, scale: float = 1.0, dloss=None, out=None,
+                      stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The loss of each row and the gradient of sum(scale * dloss * loss) by the
+    logits, in one pass over them. ``out`` may be the logits themselves."""
+    a = _distill(logits, t_logits, t_index, temperature)
+    out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device) if out is None else _like(out, logits, "out")
+    loss = torch.empty(a.rows, dtype=torch.float32, device=logits.device)
+    _check(lib().zg_distill_loss_grad(ctypes.byref(a), scale, _side(dloss, torch.float32, (a.rows,), logits, "dloss"),
+                                      loss.data_ptr(), None, out.data_ptr(), _row_stride(out), _stream(stream)),
+           "zg_distill_loss_grad")
+    return loss, out
