@@ -28,8 +28,20 @@ struct ScanArgs {
     float *dh0;                // or null
 };
 
-cudaError_t launch_scan(const ScanArgs &a, cudaStream_t st);
-cudaError_t launch_scan_bwd(const ScanArgs &a, cudaStream_t st);
+// Device memory of a scan handle: the words that blocks take their places from
+// and hand states on through.
+struct ScanWork {
+    unsigned long long *ctl;
+    int *status;
+    void *records;
+    long long wait_limit;
+};
+
+// Bytes of `records` that a shape needs (none when one chunk holds every row).
+int64_t scan_record_bytes(int64_t batch, int64_t tokens, int64_t channels);
+
+cudaError_t launch_scan(const ScanArgs &a, const ScanWork &w, cudaStream_t st);
+cudaError_t launch_scan_bwd(const ScanArgs &a, const ScanWork &w, cudaStream_t st);
 
 cudaError_t launch_topk(const void *logits, int dtype, int64_t rows, int vocab, int64_t stride, int k, void *values,
                         int32_t *index, cudaStream_t st);

@@ -15,6 +15,10 @@
 struct zg_scan {
     int device;
     int64_t batch, tokens, channels;
+    int64_t record_bytes;
+    char *d_mem;  // ctl (8 bytes), status (4 bytes), and from kHead on the records
+    int *h_status;
+    long long wait_limit;
 };
 
 namespace {
@@ -54,6 +58,14 @@ int check_ptr(const void *p, int align, bool optional, const char *what)
 // ------------------------------------------------------------------ scan
 
 constexpr int64_t kFar = int64_t(1) << 60;  // strides and extents stay below this
+constexpr int64_t kHead = 256;
+constexpr long long kScanWaitLimit = 4000000;
+
+zg::ScanWork work_of(const zg_scan *s)
+{
+    return zg::ScanWork{reinterpret_cast<unsigned long long *>(s->d_mem), reinterpret_cast<int *>(s->d_mem + 8),
+                        s->d_mem + kHead, s->wait_limit};
+}
 
 // `out`: no two elements may share memory.
 int check_view(const zg_view *v, const zg_scan_shape *s, bool out, const char *what)
@@ -92,6 +104,8 @@ int check_shape(const zg_scan *scan, const zg_scan_shape *s)
             return fail(ZG_ERR_INVALID_ARG, "n_seq must be in [1, 2^31) (got %lld)", (long long)s->n_seq);
         if (int rc = check_ptr(s->seq_start, 8, false, "seq_start")) return rc;
     }
+    if (zg::scan_record_bytes(s->batch, s->tokens, s->channels) > scan->record_bytes)
+        return fail(ZG_ERR_INVALID_ARG, "the shape needs more workspace than the handle has");
     int dev = 0;
     if (int rc = finish(cudaGetDevice(&dev), "zg_gated_scan")) return rc;
     if (dev != scan->device)
@@ -191,7 +205,21 @@ int zg_scan_init(int64_t batch, int64_t tokens, int64_t channels, zg_scan **out)
     s->batch = batch;
     s->tokens = tokens;
     s->channels = channels;
-    if (int rc = finish(cudaGetDevice(&s->device), "zg_scan_init")) {
+    s->wait_limit = kScanWaitLimit;
+    s->record_bytes = zg::scan_record_bytes(batch, tokens, channels);
+    cudaError_t e = cudaGetDevice(&s->device);
+    if (e == cudaSuccess) e = cudaMallocHost(&s->h_status, sizeof(int));
+    if (e == cudaSuccess) e = cudaMalloc(&s->d_mem, size_t(kHead + s->record_bytes));
+    if (e == cudaSuccess) e = cudaMemset(s->d_mem, 0, size_t(kHead + s->record_bytes));
+    // epoch 1: the cleared records belong to no launch
+    const unsigned long long ctl = 1ull << 32;
+    if (e == cudaSuccess) e = cudaMemcpy(s->d_mem, &ctl, sizeof ctl, cudaMemcpyHostToDevice);
+    if (e != cudaSuccess) {
+        const int rc = e == cudaErrorMemoryAllocation
+                           ? fail(ZG_ERR_NO_MEMORY, "zg_scan_init: %lld bytes of workspace: %s",
+                                  (long long)(kHead + s->record_bytes), cudaGetErrorString(e))
+                           : finish(e, "zg_scan_init workspace");
+        cudaGetLastError();
         zg_scan_destroy(s);
         return rc;
     }
@@ -199,12 +227,19 @@ int zg_scan_init(int64_t batch, int64_t tokens, int64_t channels, zg_scan **out)
     return ZG_OK;
 }
 
-void zg_scan_destroy(zg_scan *s) { delete s; }
+void zg_scan_destroy(zg_scan *s)
+{
+    if (!s) return;
+    if (s->d_mem) cudaFree(s->d_mem);
+    if (s->h_status) cudaFreeHost(s->h_status);
+    delete s;
+}
 
 int zg_scan_set_wait_limit(zg_scan *s, int64_t polls)
 {
     if (!s) return fail(ZG_ERR_INVALID_ARG, "scan handle is NULL");
     if (polls < 0) return fail(ZG_ERR_INVALID_ARG, "polls must be >= 0");
+    s->wait_limit = polls;
     return ZG_OK;
 }
 
@@ -212,8 +247,13 @@ int zg_scan_status(zg_scan *s, zg_stream stream, int *status)
 {
     if (!s) return fail(ZG_ERR_INVALID_ARG, "scan handle is NULL");
     if (!status) return fail(ZG_ERR_INVALID_ARG, "status is NULL");
-    *status = ZG_OK;
-    return finish(cudaStreamSynchronize(stream), "zg_scan_status");
+    int *d_status = work_of(s).status;
+    cudaError_t e = cudaMemcpyAsync(s->h_status, d_status, sizeof(int), cudaMemcpyDeviceToHost, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    if (e != cudaSuccess) return finish(e, "zg_scan_status");
+    *status = *s->h_status;
+    if (*status == ZG_OK) return ZG_OK;
+    return finish(cudaMemsetAsync(d_status, 0, sizeof(int), stream), "zg_scan_status reset");
 }
 
 int zg_gated_scan(zg_scan *scan, const zg_scan_shape *shape, const zg_view *x, const zg_view *f, const float *h0,
@@ -233,7 +273,7 @@ int zg_gated_scan(zg_scan *scan, const zg_scan_shape *shape, const zg_view *x, c
     a.h0 = h0;
     a.h_last = h_last;
     a.states = states;
-    return finish(zg::launch_scan(a, stream), "scan launch");
+    return finish(zg::launch_scan(a, work_of(scan), stream), "scan launch");
 }
 
 int zg_gated_scan_bwd(zg_scan *scan, const zg_scan_shape *shape, const zg_view *x, const zg_view *f,
@@ -260,7 +300,7 @@ int zg_gated_scan_bwd(zg_scan *scan, const zg_scan_shape *shape, const zg_view *
     a.df = view(df);
     a.dh_last = dh_last;
     a.dh0 = dh0;
-    return finish(zg::launch_scan_bwd(a, stream), "scan backward launch");
+    return finish(zg::launch_scan_bwd(a, work_of(scan), stream), "scan backward launch");
 }
 
 int zg_topk(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride, int k, void *values,
