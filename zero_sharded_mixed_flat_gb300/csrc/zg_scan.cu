@@ -4,23 +4,26 @@
 // The recurrence is a scan over affine maps: a run of tokens takes the state
 // h to A h + B, with A the product of its gates, and two runs compose to
 // (A2 A1, A2 B1 + B2). Backward is the same scan from the end, of
-// r -> a_t (dy_t + r). A block takes a tile of kTile channels by kChunk
-// tokens: each warp holds its few tokens of the tile in registers, reduces
-// them to one map, the warps' maps are composed through shared memory, and
-// the blocks' maps through a workspace in global memory, where a block waits
-// for those before it. With the state at its first token known, each warp runs
-// the recurrence through its tokens again from the registers and stores.
+// r -> a_t (dy_t + r). A tile is kChunk tokens by kTile channels: each half
+// warp holds a run of kRun tokens in registers, four channels to a lane, and
+// reduces it to one map; the runs' maps are composed through shared memory, and
+// the chunks' maps through a workspace in global memory, where a block waits
+// for the chunks before its own. With the state at its first token known, each
+// run goes through its tokens again from the registers and stores.
 //
 // So x and f are read once and y is written once: 6 bytes per element in
 // bf16 (10 in backward, with dy, dx and df) and about 0.3 in the workspace.
+// Blocks stay on their SM and take tile after tile; the next tile's copies
+// into shared memory are in flight while a tile is worked on, so memory stays
+// busy through the waits.
 //
-// The maps of earlier blocks are composed in a fixed order, by a tree of
+// The maps of earlier chunks are composed in a fixed order, by a tree of
 // kGroup chunks to a group and kGroup groups to a span, whatever the order
 // in which blocks run: the same inputs give the same bits. Only the state at
 // the end of a span hangs on the span before it, so the chain of waits is one
 // step per kGroup^2 chunks.
 //
-// Sequences that begin inside a chunk cut the scan: a run that holds a
+// Packed sequences that begin inside a chunk cut the scan: a run that holds a
 // beginning has a constant map, marked by A = kConst (every real A is >= 0),
 // so nothing before it, a NaN included, is multiplied into what follows.
 #include <cuda_bf16.h>
@@ -31,123 +34,138 @@
 namespace zg {
 namespace {
 
-constexpr int kTile = 64;  // channels of a block: two to a lane
+constexpr int kTile = 64;  // channels of a tile: four to a lane of a half warp
 constexpr int kChunk = ZG_SCAN_CHUNK;
+constexpr int kWarps = 8;
+constexpr int kRun = kChunk / (2 * kWarps);  // tokens of a half warp
+constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 16;
 constexpr float kConst = -1.0f;
-#ifndef ZG_SCAN_FT
-#define ZG_SCAN_FT 16
-#endif
-#ifndef ZG_SCAN_BT
-#define ZG_SCAN_BT 8
-#endif
-#ifndef ZG_SCAN_FB
-#define ZG_SCAN_FB 2
-#endif
-#ifndef ZG_SCAN_BB
-#define ZG_SCAN_BB 1
-#endif
 
-// ------------------------------------------------------------------ elements
+// ------------------------------------------------------------------ arithmetic
 
-// Two elements as they lie in memory, so that bf16 pairs take one register.
-template <class T, bool PAIR>
-struct Raw;
-template <bool PAIR>
-struct Raw<uint16_t, PAIR> {
-    uint32_t w;
-    __device__ __forceinline__ void load(const uint16_t *p, int64_t c0, int64_t c1, bool ok0, bool ok1)
-    {
-        if (PAIR)
-            w = ok0 ? __ldcs(reinterpret_cast<const uint32_t *>(p + c0)) : 0u;
-        else
-            w = (ok0 ? uint32_t(__ldcs(p + c0)) : 0u) | ((ok1 ? uint32_t(__ldcs(p + c1)) : 0u) << 16);
-    }
-    __device__ __forceinline__ void zero() { w = 0u; }
-    __device__ __forceinline__ float2 get() const { return make_float2(bf16_lo(w), bf16_hi(w)); }
+// Four channels of a lane, two to a packed operation.
+struct F4 {
+    float2 lo, hi;
 };
-template <bool PAIR>
-struct Raw<float, PAIR> {
-    float2 w;
-    __device__ __forceinline__ void load(const float *p, int64_t c0, int64_t c1, bool ok0, bool ok1)
-    {
-        if (PAIR)
-            w = ok0 ? __ldcs(reinterpret_cast<const float2 *>(p + c0)) : make_float2(0.0f, 0.0f);
-        else
-            w = make_float2(ok0 ? __ldcs(p + c0) : 0.0f, ok1 ? __ldcs(p + c1) : 0.0f);
-    }
-    __device__ __forceinline__ void zero() { w = make_float2(0.0f, 0.0f); }
-    __device__ __forceinline__ float2 get() const { return w; }
-};
-
-template <bool PAIR>
-__device__ __forceinline__ void store2(uint16_t *p, int64_t c0, int64_t c1, bool ok0, bool ok1, float2 v)
+__device__ __forceinline__ F4 all(float v) { return F4{make_float2(v, v), make_float2(v, v)}; }
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b)
 {
-    const uint32_t w = pack_bf16x2(v.x, v.y);
-    if (PAIR) {
-        if (ok0) __stcs(reinterpret_cast<uint32_t *>(p + c0), w);
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<const uint64_t *>(&a)), "l"(*reinterpret_cast<const uint64_t *>(&b)));
+    return *reinterpret_cast<const float2 *>(&d);
+}
+__device__ __forceinline__ float2 neg(float2 v) { return make_float2(-v.x, -v.y); }
+__device__ __forceinline__ F4 mul(F4 a, F4 b) { return F4{mul_f32x2(a.lo, b.lo), mul_f32x2(a.hi, b.hi)}; }
+__device__ __forceinline__ F4 add(F4 a, F4 b) { return F4{add_f32x2(a.lo, b.lo), add_f32x2(a.hi, b.hi)}; }
+__device__ __forceinline__ F4 fma(F4 a, F4 b, F4 c)
+{
+    return F4{fma_f32x2(a.lo, b.lo, c.lo), fma_f32x2(a.hi, b.hi, c.hi)};
+}
+__device__ __forceinline__ F4 sub(F4 a, F4 b) { return fma(b, all(-1.0f), a); }
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float exp2_approx(float v)
+{
+    float d;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
+    return d;
+}
+__device__ __forceinline__ float rcp_approx(float v)
+{
+    float d;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
+    return d;
+}
+
+// keep = sigmoid(f) = 1 / (1 + e) and take = sigmoid(-f) = e / (1 + e) with
+// e = exp(-f): neither is a difference, so both hold to a few units in the
+// last place however near to one the other is. f is held above kLowest, where
+// e and its sum are still finite, and keep is taken down by just less than its
+// value there (far below any other keep's last place), so that it ends at zero,
+// never below; a NaN stays. For binary32 data the exponent's argument is reduced first, which
+// keeps its rounding out of e; for bf16 data that rounding (|f| 2^-24 of e)
+// is far below the data's own.
+constexpr float kLowest = -86.5f;
+constexpr float kKeepAtLowest = 2.71337577e-38f;  // exp(kLowest), less 4e-5 of itself for the roundings on the way
+constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f;
+
+template <class T>
+__device__ __forceinline__ float2 decay(float2 f)
+{
+    f = make_float2(max_nan(f.x, kLowest), max_nan(f.y, kLowest));
+    float2 e;
+    if (sizeof(T) == 2) {
+        const float2 t = mul_f32x2(f, make_float2(-kLog2e, -kLog2e));
+        e = make_float2(exp2_approx(t.x), exp2_approx(t.y));
     } else {
-        if (ok0) __stcs(p + c0, uint16_t(w));
-        if (ok1) __stcs(p + c1, uint16_t(w >> 16));
+        const float2 t = mul_f32x2(f, make_float2(-kLog2e, -kLog2e));
+        // whole part of the exponent; a multiplication by 2^n at or above 2^-126
+        const float2 n = make_float2(rintf(max_nan(t.x, -126.0f)), rintf(max_nan(t.y, -126.0f)));
+        float2 r = fma_f32x2(f, make_float2(-kLog2e, -kLog2e), neg(n));
+        r = fma_f32x2(make_float2(fminf(f.x, 1e30f), fminf(f.y, 1e30f)), make_float2(-kLog2eRest, -kLog2eRest), r);
+        e = mul_f32x2(make_float2(exp2_approx(r.x), exp2_approx(r.y)),
+                      make_float2(__int_as_float((__float2int_rn(n.x) + 127) << 23),
+                                  __int_as_float((__float2int_rn(n.y) + 127) << 23)));
     }
+    return e;
 }
-template <bool PAIR>
-__device__ __forceinline__ void store2(float *p, int64_t c0, int64_t c1, bool ok0, bool ok1, float2 v)
+template <class T>
+__device__ __forceinline__ F4 decay(F4 f)
 {
-    if (PAIR) {
-        if (ok0) __stcs(reinterpret_cast<float2 *>(p + c0), v);
-    } else {
-        if (ok0) __stcs(p + c0, v.x);
-        if (ok1) __stcs(p + c1, v.y);
-    }
+    return F4{decay<T>(f.lo), decay<T>(f.hi)};
 }
-
-// ------------------------------------------------------------------ gates
-
-// The smaller of sigmoid(f) and sigmoid(-f), at most a half, with its sign
-// set when it is sigmoid(-f): the larger one is one minus it, exactly rounded,
-// so one register keeps both gates to a few units in the last place.
-__device__ __forceinline__ float gate(float f)
+__device__ __forceinline__ void gates(float2 e, float2 &keep, float2 &take)
 {
-    const float e = __expf(-fabsf(f));
-    const float small = __fdividef(e, 1.0f + e);
-    return copysignf(small, -f);
+    const float2 d = add_f32x2(e, make_float2(1.0f, 1.0f));
+    const float2 r = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+    keep = add_f32x2(r, make_float2(-kKeepAtLowest, -kKeepAtLowest));
+    take = mul_f32x2(e, r);
 }
-__device__ __forceinline__ float keep_of(float v) { return signbit(v) ? 1.0f + v : v; }  // sigmoid(f)
-__device__ __forceinline__ float take_of(float v) { return signbit(v) ? -v : 1.0f - v; }  // sigmoid(-f)
-__device__ __forceinline__ float2 keep_of(float2 v) { return make_float2(keep_of(v.x), keep_of(v.y)); }
-__device__ __forceinline__ float2 take_of(float2 v) { return make_float2(take_of(v.x), take_of(v.y)); }
-
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+__device__ __forceinline__ void gates(F4 e, F4 &keep, F4 &take)
 {
-    return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
+    gates(e.lo, keep.lo, take.lo);
+    gates(e.hi, keep.hi, take.hi);
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
-__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return make_float2(a.x - b.x, a.y - b.y); }
 
-// A map of the state, for a lane's two channels.
+// A map of the state, h -> a h + b, for a lane's four channels of a half warp
+// and for its two of a whole warp. A constant one is marked in all channels;
+// there are none unless sequences are packed (CUT).
 struct Map {
+    F4 a, b;
+};
+struct Map2 {
     float2 a, b;
 };
-__device__ __forceinline__ Map identity() { return Map{make_float2(1.0f, 1.0f), make_float2(0.0f, 0.0f)}; }
-// `first`, then `second`. Both channels of a constant map are marked.
-__device__ __forceinline__ Map then(const Map &first, const Map &second)
+__device__ __forceinline__ Map2 identity2() { return Map2{make_float2(1.0f, 1.0f), make_float2(0.0f, 0.0f)}; }
+// `first`, then `second`.
+template <bool CUT>
+__device__ __forceinline__ Map2 then(const Map2 &first, const Map2 &second)
 {
-    if (second.a.x < 0.0f) return second;
-    const float2 b = fma2(second.a, first.b, second.b);
-    if (first.a.x < 0.0f) return Map{first.a, b};
-    return Map{mul2(second.a, first.a), b};
+    if (CUT && second.a.x < 0.0f) return second;
+    return Map2{CUT && first.a.x < 0.0f ? first.a : mul_f32x2(second.a, first.a),
+                fma_f32x2(second.a, first.b, second.b)};
 }
-__device__ __forceinline__ float2 apply(const Map &m, float2 h) { return m.a.x < 0.0f ? m.b : fma2(m.a, h, m.b); }
+template <bool CUT>
+__device__ __forceinline__ float2 apply(const Map2 &m, float2 h)
+{
+    return CUT && m.a.x < 0.0f ? m.b : fma_f32x2(m.a, h, m.b);
+}
 
 // ------------------------------------------------------------------ the workspace
 //
 // Every binary32 goes with a 32-bit tag in one 64-bit word, which is written
 // and read whole: a word whose tag is the launch's epoch holds that launch's
 // value, so nothing has to be cleared between launches and no fence orders
-// data and flag. ctl holds the epoch (high half) and how many blocks have
-// taken a place (low half).
+// data and flag. ctl holds the epoch (high half) and how many places have been
+// taken (low half).
 
 struct Work {
     unsigned long long *ctl;
@@ -179,24 +197,269 @@ __device__ __forceinline__ bool got(const ulonglong2 *p, uint32_t tag, float &x,
 __device__ __noinline__ bool try_on(const Work &w, long long &polls)
 {
     if (++polls > w.wait_limit) {
-        atomicExch(w.status, ZG_ERR_DEVICE_TIMEOUT);
+        atomicExch(w.status, kStatusTimeout);
         return false;
     }
     return (polls & 63) || *reinterpret_cast<volatile int *>(w.status) == 0;
 }
 
-__device__ __forceinline__ Map wait_map(const ulonglong2 *p, uint32_t tag, const Work &w)
+__device__ __forceinline__ Map2 wait_map(const ulonglong2 *p, uint32_t tag, const Work &w)
 {
-    Map m;
+    Map2 m;
     long long polls = 0;
     while (!(got(p, tag, m.a.x, m.b.x) & got(p + 1, tag, m.a.y, m.b.y)))
-        if (!try_on(w, polls)) return identity();
+        if (!try_on(w, polls)) return identity2();
     return m;
 }
-__device__ __forceinline__ void put_map(ulonglong2 *p, const Map &m, uint32_t tag)
+__device__ __forceinline__ void put_map(ulonglong2 *p, const Map2 &m, uint32_t tag)
 {
     put(p, m.a.x, m.b.x, tag);
     put(p + 1, m.a.y, m.b.y, tag);
+}
+
+// ------------------------------------------------------------------ a tile's place
+
+struct Grid {
+    int64_t tiles;   // of channels
+    int64_t width;   // batch rows x tiles: the tiles of one chunk
+    int64_t chunks;
+    int64_t places;  // width x chunks
+    int load_mode;   // bytes of a copy into shared memory: 16, 4 or 2
+};
+
+// Places are taken in scan order, chunk by chunk, as blocks become free, and
+// each block works through the ones it took in that order. So whoever waits
+// for a chunk waits for one whose place was taken earlier, and the lowest place
+// not yet done never waits: the waits end. Without anything to wait for (one
+// chunk) the places are dealt out by block number.
+struct Places {
+    unsigned long long *ctl;
+    int64_t next;  // used where nothing waits
+    __device__ __forceinline__ unsigned long long take(const Grid &g)
+    {
+        if (g.chunks == 1) {
+            const int64_t n = next;
+            next += gridDim.x;
+            return (unsigned long long)(n < g.places ? n : 0xffffffffll);
+        }
+        const unsigned long long got = atomicAdd(ctl, 1ull);
+        // every block stops at its first place past the end, so that many are
+        // taken in all; the last one leaves ctl ready for the next launch,
+        // under another epoch
+        if (uint32_t(got) == uint32_t(g.places) + gridDim.x - 1) atomicExch(ctl, ((got >> 32) + 1ull) << 32);
+        return got;
+    }
+};
+
+struct Tile {
+    bool valid;
+    uint32_t k;     // chunk in scan order
+    uint32_t rest;  // batch row x tiles + tile
+    uint32_t row;
+    uint32_t chunk;
+    int64_t ch;     // first channel
+};
+
+template <bool BWD>
+__device__ __forceinline__ Tile tile_at(unsigned long long taken, const Grid &g)
+{
+    const uint32_t place = uint32_t(taken), width = uint32_t(g.width), tiles = uint32_t(g.tiles);
+    Tile t;
+    t.valid = place < uint32_t(g.places);
+    t.k = place / width;
+    t.rest = place % width;
+    t.row = t.rest / tiles;
+    t.ch = int64_t(t.rest % tiles) * kTile;
+    t.chunk = BWD ? uint32_t(g.chunks) - 1 - t.k : t.k;
+    return t;
+}
+
+// ------------------------------------------------------------------ shared memory
+
+struct Cuts {  // where sequences begin and end in a chunk: their number by token, or -1
+    int first[kChunk];
+    int last[kChunk];
+    int64_t range[2];
+};
+
+constexpr int kRuns = 2 * kWarps;
+
+// The runs' maps, in scan order; slot 4 l + j of a run is channel j of lane l
+// of its half warp. b gives way to the state before each run.
+struct Runs {
+    float a[kRuns][kTile], b[kRuns][kTile];
+};
+
+struct Shared {
+    Runs runs;
+    Runs fwd;  // backward's runs of h
+    float4 part[8][32];
+    float2 start[32];
+    Tile tile;
+    uint32_t tag;
+    Cuts cuts;
+};
+
+__device__ __forceinline__ F4 lds4(const float *p)
+{
+    const float4 v = *reinterpret_cast<const float4 *>(p);
+    return F4{make_float2(v.x, v.y), make_float2(v.z, v.w)};
+}
+__device__ __forceinline__ void sts4(float *p, F4 v)
+{
+    *reinterpret_cast<float4 *>(p) = make_float4(v.lo.x, v.lo.y, v.hi.x, v.hi.y);
+}
+
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, int bytes)
+{
+    if (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// Copies of N bytes of a tile of v into dst[token][channel]; what lies past the
+// tensor becomes zero.
+template <class T, int N>
+__device__ __forceinline__ void copy_tile(T *dst, const ScanView &v, const Tile &t, const ScanArgs &a)
+{
+    constexpr int kEach = N / int(sizeof(T)), kPerRow = kTile / kEach, kRows = kThreads / kPerRow;
+    const int r0 = threadIdx.x / kPerRow, e = threadIdx.x % kPerRow * kEach;
+    const int64_t c0 = int64_t(t.chunk) * kChunk;
+    const T *src = static_cast<const T *>(v.ptr) + t.row * v.sb + (c0 + r0) * v.st + t.ch + e;
+    const uint32_t to = uint32_t(__cvta_generic_to_shared(dst + r0 * kTile + e));
+    const int64_t far = kRows * v.st;
+    if (c0 + kChunk <= a.tokens && t.ch + kTile <= a.channels) {
+#pragma unroll
+        for (int r = 0; r < kChunk; r += kRows) {
+            copy_async<N>(to + r * kTile * int(sizeof(T)), src, N);
+            src += far;
+        }
+        return;
+    }
+    const int64_t left = (a.channels - t.ch - e) * int64_t(sizeof(T));
+    const int bytes = left <= 0 ? 0 : left < N ? int(left) : N;
+    const int rows = int(a.tokens - c0 < kChunk ? a.tokens - c0 : kChunk);
+#pragma unroll 1
+    for (int r = 0; r < kChunk; r += kRows) {
+        const int n = r0 + r < rows ? bytes : 0;
+        copy_async<N>(to + r * kTile * int(sizeof(T)), n ? src : static_cast<const T *>(v.ptr), n);
+        src += far;
+    }
+}
+// The same by plain loads, for bf16 rows that begin between words.
+__device__ __forceinline__ void copy_tile_2(uint16_t *dst, const ScanView &v, const Tile &t, const ScanArgs &a)
+{
+    const int r0 = threadIdx.x / kTile, e = threadIdx.x % kTile;
+    const int64_t c0 = int64_t(t.chunk) * kChunk;
+    const uint16_t *src = static_cast<const uint16_t *>(v.ptr) + t.row * v.sb + (c0 + r0) * v.st + t.ch + e;
+    const bool in = t.ch + e < a.channels;
+    const int rows = int(a.tokens - c0 < kChunk ? a.tokens - c0 : kChunk);
+    constexpr int kRows = kThreads / kTile;
+#pragma unroll 8
+    for (int r = 0; r < kChunk; r += kRows) {
+        dst[(r0 + r) * kTile + e] = in && r0 + r < rows ? *src : uint16_t(0);
+        src += kRows * v.st;
+    }
+}
+template <class T>
+__device__ __forceinline__ void start_copy(T *dst, const ScanView &v, const Tile &t, const ScanArgs &a, int mode)
+{
+    if (mode == 16)
+        copy_tile<T, 16>(dst, v, t, a);
+    else if (sizeof(T) == 4 || mode == 4)
+        copy_tile<T, 4>(dst, v, t, a);
+    else
+        copy_tile_2(reinterpret_cast<uint16_t *>(dst), v, t, a);
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// A lane's channels: four neighbours (VEC) or every sixteenth, so that rows
+// whose alignment forbids wide stores are written in whole sectors all the same.
+template <bool VEC>
+__device__ __forceinline__ int channel_of(int l, int j) { return VEC ? 4 * l + j : l + 16 * j; }
+
+// Four elements as they lie in memory.
+template <class T>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+    uint2 w;
+    template <bool VEC>
+    __device__ __forceinline__ void load(const uint16_t *row, int l)
+    {
+        if (VEC)
+            w = *reinterpret_cast<const uint2 *>(row + 4 * l);
+        else
+            w = make_uint2(row[l] | uint32_t(row[l + 16]) << 16, row[l + 32] | uint32_t(row[l + 48]) << 16);
+    }
+    __device__ __forceinline__ F4 get() const
+    {
+        return F4{make_float2(bf16_lo(w.x), bf16_hi(w.x)), make_float2(bf16_lo(w.y), bf16_hi(w.y))};
+    }
+};
+template <>
+struct Raw<float> {
+    F4 w;
+    template <bool VEC>
+    __device__ __forceinline__ void load(const float *row, int l)
+    {
+        if (VEC)
+            w = lds4(row + 4 * l);
+        else
+            w = F4{make_float2(row[l], row[l + 16]), make_float2(row[l + 32], row[l + 48])};
+    }
+    __device__ __forceinline__ F4 get() const { return w; }
+};
+
+// Lane l's four channels of a row of a tile, `n` of whose channels exist.
+template <bool VEC>
+__device__ __forceinline__ void store4(uint16_t *row, int l, int n, F4 v)
+{
+    const uint32_t w0 = pack_bf16x2(v.lo.x, v.lo.y), w1 = pack_bf16x2(v.hi.x, v.hi.y);
+    if (VEC) {
+        if (4 * l < n) __stcs(reinterpret_cast<uint2 *>(row + 4 * l), make_uint2(w0, w1));
+    } else {
+        if (l < n) __stcs(row + l, uint16_t(w0));
+        if (l + 16 < n) __stcs(row + l + 16, uint16_t(w0 >> 16));
+        if (l + 32 < n) __stcs(row + l + 32, uint16_t(w1));
+        if (l + 48 < n) __stcs(row + l + 48, uint16_t(w1 >> 16));
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void store4(float *row, int l, int n, F4 v)
+{
+    if (VEC) {
+        if (4 * l < n) __stcs(reinterpret_cast<float4 *>(row + 4 * l), make_float4(v.lo.x, v.lo.y, v.hi.x, v.hi.y));
+    } else {
+        if (l < n) __stcs(row + l, v.lo.x);
+        if (l + 16 < n) __stcs(row + l + 16, v.lo.y);
+        if (l + 32 < n) __stcs(row + l + 32, v.hi.x);
+        if (l + 48 < n) __stcs(row + l + 48, v.hi.y);
+    }
+}
+
+// Rows of binary32 states (contiguous, of any alignment), from a tile's first channel.
+template <bool VEC>
+__device__ __forceinline__ F4 state4(const float *row, int l, int n)
+{
+    F4 v = all(0.0f);
+    if (!row) return v;
+    if (channel_of<VEC>(l, 0) < n) v.lo.x = row[channel_of<VEC>(l, 0)];
+    if (channel_of<VEC>(l, 1) < n) v.lo.y = row[channel_of<VEC>(l, 1)];
+    if (channel_of<VEC>(l, 2) < n) v.hi.x = row[channel_of<VEC>(l, 2)];
+    if (channel_of<VEC>(l, 3) < n) v.hi.y = row[channel_of<VEC>(l, 3)];
+    return v;
+}
+template <bool VEC>
+__device__ __forceinline__ void put_state4(float *row, int l, int n, F4 v)
+{
+    if (channel_of<VEC>(l, 0) < n) row[channel_of<VEC>(l, 0)] = v.lo.x;
+    if (channel_of<VEC>(l, 1) < n) row[channel_of<VEC>(l, 1)] = v.lo.y;
+    if (channel_of<VEC>(l, 2) < n) row[channel_of<VEC>(l, 2)] = v.hi.x;
+    if (channel_of<VEC>(l, 3) < n) row[channel_of<VEC>(l, 3)] = v.hi.y;
 }
 
 // ------------------------------------------------------------------ packed sequences
@@ -212,395 +475,566 @@ __device__ __forceinline__ int64_t lower_bound(const int64_t *v, int64_t n, int6
         const int m = __popc(__ballot_sync(0xffffffffu, at < hi && v[at] < key));
         const int64_t end = lo + m * step;
         hi = end < hi ? end : hi;
-        lo = m ? lo + (m - 1) * step + 1 : lo;
-        if (!m) hi = lo;
+        if (m)
+            lo = lo + (m - 1) * step + 1;
+        else
+            hi = lo;
     }
     return lo;
 }
 
-// Where sequences begin and end in a chunk: their number by token, or -1.
-struct Cuts {
-    int first[kChunk];
-    int last[kChunk];
-    int64_t range[2];
-};
-
-// Fills `cuts` for the tokens [c0, c0 + kChunk) and copies the state of the
-// empty sequences that lie there. All threads of the block; ends with a
-// barrier.
-template <int W>
-__device__ __forceinline__ void find_cuts(Cuts &cuts, const ScanArgs &a, int64_t c0, int64_t ch0, int64_t ch1, bool ok0,
-                                          bool ok1, const float *from, float *to)
+// Fills `cuts` for the chunk at c0 and copies the state of the empty sequences
+// that lie there, for the tile's n channels. All threads; ends with a barrier.
+__device__ __forceinline__ void find_cuts(Cuts &cuts, const ScanArgs &a, const Tile &t, int n, const float *from, float *to)
 {
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int64_t c1 = c0 + kChunk < a.tokens ? c0 + kChunk : a.tokens;
-    for (int i = threadIdx.x; i < kChunk; i += 32 * W) cuts.first[i] = cuts.last[i] = -1;
+    const int64_t c0 = int64_t(t.chunk) * kChunk, c1 = c0 + kChunk < a.tokens ? c0 + kChunk : a.tokens;
+    if (threadIdx.x < kChunk) cuts.first[threadIdx.x] = cuts.last[threadIdx.x] = -1;
     if (warp == 0) {
         const int64_t lo = lower_bound(a.seq_start, a.n_seq, c0);
         if (lane == 0) cuts.range[0] = lo > 0 ? lo - 1 : 0;
     }
-    if (warp == W - 1) {
+    if (warp == 1) {
         const int64_t hi = c1 == a.tokens ? a.n_seq : lower_bound(a.seq_start, a.n_seq, c1);
         if (lane == 0) cuts.range[1] = hi;
     }
     __syncthreads();
-    for (int64_t s = cuts.range[0] + warp; s < cuts.range[1]; s += W) {
+    for (int64_t s = cuts.range[0] + warp; s < cuts.range[1]; s += kWarps) {
         const int64_t lo = a.seq_start[s], hi = a.seq_start[s + 1];
         if (hi > lo) {
             if (lane == 0 && lo >= c0 && lo < c1) cuts.first[lo - c0] = int(s);
             if (lane == 0 && hi > c0 && hi <= c1) cuts.last[hi - 1 - c0] = int(s);
         } else if (to && lo >= c0 && (lo < c1 || c1 == a.tokens)) {
-            if (ok0) to[s * a.channels + ch0] = from ? from[s * a.channels + ch0] : 0.0f;
-            if (ok1) to[s * a.channels + ch1] = from ? from[s * a.channels + ch1] : 0.0f;
+            for (int c = lane; c < n; c += 32)
+                to[s * a.channels + t.ch + c] = from ? from[s * a.channels + t.ch + c] : 0.0f;
         }
     }
     __syncthreads();
 }
 
-__device__ __forceinline__ float2 state2(const float *p, int64_t s, int64_t channels, int64_t c0, int64_t c1, bool ok0,
-                                         bool ok1)
+// ------------------------------------------------------------------ the chunks before
+
+__device__ __forceinline__ float4 pack(const Map2 &m) { return make_float4(m.a.x, m.a.y, m.b.x, m.b.y); }
+__device__ __forceinline__ Map2 unpack(float4 v) { return Map2{make_float2(v.x, v.y), make_float2(v.z, v.w)}; }
+__device__ __forceinline__ Map2 run_map(const Runs &runs, int r, int lane)
 {
-    if (!p) return make_float2(0.0f, 0.0f);
-    return make_float2(ok0 ? p[s * channels + c0] : 0.0f, ok1 ? p[s * channels + c1] : 0.0f);
+    return Map2{*reinterpret_cast<const float2 *>(&runs.a[r][2 * lane]),
+                *reinterpret_cast<const float2 *>(&runs.b[r][2 * lane])};
 }
-__device__ __forceinline__ void put_state2(float *p, int64_t s, int64_t channels, int64_t c0, int64_t c1, bool ok0,
-                                           bool ok1, float2 v)
+// From the state before the first run, the state before each, in place of the
+// runs' b; returns the state after the last. One warp.
+template <bool CUT>
+__device__ __forceinline__ float2 run_states(Runs &runs, int lane, float2 h)
 {
-    if (ok0) p[s * channels + c0] = v.x;
-    if (ok1) p[s * channels + c1] = v.y;
-}
-
-// ------------------------------------------------------------------ a block's place and its predecessors
-
-struct Place {
-    int64_t k, rest;  // chunk in scan order, and batch row x tile
-    uint32_t epoch;
-};
-
-// Blocks take their places in scan order as they start, so the ones that a
-// block waits for have all started before it.
-__device__ __forceinline__ Place take_place(const Work &w, int64_t width, bool alone, unsigned long long *shared)
-{
-    if (alone) return Place{0, int64_t(blockIdx.x), 0u};
-    if (threadIdx.x == 0) {
-        const unsigned long long got = atomicAdd(w.ctl, 1ull);
-        if (uint32_t(got) == gridDim.x - 1)  // the last place: the next launch has another epoch
-            atomicExch(w.ctl, ((got >> 32) + 1ull) << 32);
-        *shared = got;
-    }
-    __syncthreads();
-    const unsigned long long got = *shared;
-    const uint32_t n = uint32_t(got);
-    return Place{int64_t(n) / width, int64_t(n) % width, uint32_t(got >> 32)};
-}
-
-template <int W>
-struct Shared {
-    float4 warp_map[W][32];  // a.x, a.y, b.x, b.y
-    float4 part[8][32];
-    unsigned long long place;
-};
-
-__device__ __forceinline__ float4 pack(const Map &m) { return make_float4(m.a.x, m.a.y, m.b.x, m.b.y); }
-__device__ __forceinline__ Map unpack(float4 v) { return Map{make_float2(v.x, v.y), make_float2(v.z, v.w)}; }
-
-// Publishes this block's map and returns the state before its first token (in
-// scan order) from the blocks before it. sh.warp_map holds the warps' maps in
-// scan order and has been fenced by a barrier. `slot`: index of the record of
-// chunk k at this tile; chunks, groups and spans of a tile are `width` records
-// of 32 lanes apart.
-template <int W>
-__device__ __forceinline__ float2 state_before(Shared<W> &sh, const Work &w, const Place &at, int64_t chunks, int64_t width)
-{
-    static_assert(W >= 8, "four warps compose the groups and four the chunks");
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int in_group = int(at.k % kGroup), group = int(at.k / kGroup % kGroup);
-    const int64_t first_chunk = at.k - in_group, this_group = at.k / kGroup, first_group = this_group - group;
-    auto chunk_at = [&](int64_t k) { return w.chunk + 2 * ((k * width + at.rest) * 32 + lane); };
-    auto group_at = [&](int64_t g) { return w.group + 2 * ((g * width + at.rest) * 32 + lane); };
-    auto span_at = [&](int64_t s) { return w.span + (s * width + at.rest) * 32 + lane; };
-    const bool ends_group = in_group == kGroup - 1 && at.k + 1 < chunks;
-    Map mine = identity();
-    if (warp == 4) {
 #pragma unroll
-        for (int v = 0; v < W; ++v) mine = then(mine, unpack(sh.warp_map[v][lane]));
-        if (!ends_group && at.k + 1 < chunks) put_map(chunk_at(at.k), mine, at.epoch);
-    }
-    if (warp < 8) {
-        Map m = identity();
-        if (warp >= 4) {  // chunks of this group, four to a warp
-            const int lo = 4 * (warp - 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (lo + i < in_group) m = then(m, wait_map(chunk_at(first_chunk + lo + i), at.epoch, w));
-        } else {  // the span before, then groups of this span
-            const int lo = 4 * warp - 1;
-            if (warp == 0 && first_group > 0) {
-                long long polls = 0;
-                float2 s;
-                while (!got(span_at(first_group / kGroup - 1), at.epoch, s.x, s.y))
-                    if (!try_on(w, polls)) {
-                        s = make_float2(0.0f, 0.0f);
-                        break;
-                    }
-                m = Map{make_float2(kConst, kConst), s};
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (lo + i >= 0 && lo + i < group) m = then(m, wait_map(group_at(first_group + lo + i), at.epoch, w));
-        }
-        sh.part[warp][lane] = pack(m);
-        if (warp >= 4 && ends_group) {
-            // the group's map must not wait for the groups before it
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (warp == 4) {
-                Map g = unpack(sh.part[4][lane]);
-#pragma unroll
-                for (int v = 5; v < 8; ++v) g = then(g, unpack(sh.part[v][lane]));
-                if (group < kGroup - 1) put_map(group_at(this_group), then(g, mine), at.epoch);
-            }
-        }
-    }
-    __syncthreads();
-    float2 h = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int v = 0; v < 8; ++v) h = apply(unpack(sh.part[v][lane]), h);
-    if (warp == 4 && ends_group && group == kGroup - 1) {
-        const float2 s = apply(mine, h);
-        put(span_at(this_group / kGroup), s.x, s.y, at.epoch);
+    for (int r = 0; r < kRuns; ++r) {
+        const Map2 m = run_map(runs, r, lane);
+        *reinterpret_cast<float2 *>(&runs.b[r][2 * lane]) = h;
+        h = apply<CUT>(m, h);
     }
     return h;
 }
 
-// ------------------------------------------------------------------ forward
+constexpr int kSolver = 4;  // the warp that composes the runs
 
-template <class T, bool PAIR, bool PACKED, int TPT, int W>
-__global__ void __launch_bounds__(32 * W, W == 1 ? 8 : W == 8 ? ZG_SCAN_FB : 1) scan_kernel(ScanArgs a, Work w, int64_t chunks, int64_t tiles)
+// Publishes this chunk's map, waits for the chunks before it, and leaves the
+// state before each run in sh.runs.b. `start` is the state before the row's
+// first token, in slots 2 lane and 2 lane + 1 of the solver. The runs' maps
+// are behind a barrier; ends with a barrier. Records of 32 lanes lie by chunk
+// (group, span) and then by tile.
+template <bool CUT>
+__device__ __forceinline__ void solve(Shared &sh, const Work &w, const Tile &t, const Grid &g, uint32_t tag, float2 start)
 {
-    __shared__ Shared<W> sh;
-    __shared__ Cuts cuts;  // unused, and not allocated, unless PACKED
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const Place at = take_place(w, a.batch * tiles, chunks == 1, &sh.place);
-    const int64_t row = at.rest / tiles, tile = at.rest % tiles;
-    const int64_t ch0 = tile * kTile + (PAIR ? 2 * lane : lane), ch1 = ch0 + (PAIR ? 1 : 32);
-    const bool ok0 = ch0 < a.channels, ok1 = ch1 < a.channels;
-    const int64_t c0 = at.k * (TPT * W), t0 = c0 + warp * TPT;
-
-    Raw<T, PAIR> x[TPT], f[TPT];
-    {
-        const T *px = static_cast<const T *>(a.x.ptr) + row * a.x.sb + t0 * a.x.st;
-        const T *pf = static_cast<const T *>(a.f.ptr) + row * a.f.sb + t0 * a.f.st;
+    if (g.chunks == 1) {
+        if (warp == kSolver) run_states<CUT>(sh.runs, lane, start);
+        __syncthreads();
+        return;
+    }
+    const uint32_t in_group = t.k % kGroup, group = t.k / kGroup % kGroup;
+    const uint32_t first_chunk = t.k - in_group, this_group = t.k / kGroup, first_group = this_group - group;
+    const int64_t width = g.width, at = int64_t(t.rest) * 32 + lane;
+    auto chunk_at = [&](uint32_t k) { return w.chunk + 2 * (k * width * 32 + at); };
+    auto group_at = [&](uint32_t k) { return w.group + 2 * (k * width * 32 + at); };
+    auto span_at = [&](uint32_t k) { return w.span + (k * width * 32 + at); };
+    const bool followed = t.k + 1 < uint32_t(g.chunks), ends_group = in_group == kGroup - 1 && followed;
+    Map2 mine = identity2();
+    if (warp == kSolver) {
+        if (followed) {
 #pragma unroll
-        for (int i = 0; i < TPT; ++i) {
-            const bool in = t0 + i < a.tokens;
-            f[i].load(pf + i * a.f.st, ch0, ch1, in && ok0, in && ok1);
-            x[i].load(px + i * a.x.st, ch0, ch1, in && ok0, in && ok1);
+            for (int r = 0; r < kRuns; ++r) mine = then<CUT>(mine, run_map(sh.runs, r, lane));
+            if (!ends_group) put_map(chunk_at(t.k), mine, tag);
+        }
+    } else {
+        Map2 m = identity2();
+        if (warp > kSolver) {  // chunks of this group, five to a warp
+            const uint32_t lo = 5 * (warp - kSolver - 1);
+#pragma unroll
+            for (uint32_t i = 0; i < 5; ++i)
+                if (lo + i < in_group) m = then<CUT>(m, wait_map(chunk_at(first_chunk + lo + i), tag, w));
+        } else {  // groups of this span, four to a warp, and the span before
+            const uint32_t lo = 4 * warp;
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i)
+                if (lo + i < group) m = then<CUT>(m, wait_map(group_at(first_group + lo + i), tag, w));
+            if (warp == 3 && first_group > 0) {
+                float2 s;
+                long long polls = 0;
+                while (!got(span_at(first_group / kGroup - 1), tag, s.x, s.y))
+                    if (!try_on(w, polls)) {
+                        s = make_float2(0.0f, 0.0f);
+                        break;
+                    }
+                sh.start[lane] = s;
+            }
+        }
+        sh.part[warp][lane] = pack(m);
+    }
+    if (warp >= kSolver && ends_group) {
+        // the group's map must not wait for the groups before it
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (warp == kSolver && group < kGroup - 1) {
+            Map2 m = unpack(sh.part[kSolver + 1][lane]);
+            m = then<CUT>(m, unpack(sh.part[kSolver + 2][lane]));
+            m = then<CUT>(m, unpack(sh.part[kSolver + 3][lane]));
+            put_map(group_at(this_group), then<CUT>(m, mine), tag);
         }
     }
+    __syncthreads();
+    if (warp == kSolver) {
+        float2 h = first_group > 0 ? sh.start[lane] : start;
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+            if (v != kSolver) h = apply<CUT>(unpack(sh.part[v][lane]), h);
+        h = run_states<CUT>(sh.runs, lane, h);
+        if (ends_group && group == kGroup - 1) put(span_at(this_group / kGroup), h.x, h.y, tag);
+    }
+    __syncthreads();
+}
+
+// The masks of a run's tokens (bit i: token i) at which packed sequences begin and end.
+struct Marks {
+    uint32_t first, last;
+};
+__device__ __forceinline__ Marks marks_of(const Shared &sh)
+{
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, half = lane >> 4;
+    const int at = warp * 2 * kRun + (lane & 15);
+    const uint32_t f = __ballot_sync(0xffffffffu, sh.cuts.first[at] >= 0);
+    const uint32_t l = __ballot_sync(0xffffffffu, sh.cuts.last[at] >= 0);
+    return Marks{(f >> (kRun * half)) & 0xffu, (l >> (kRun * half)) & 0xffu};
+}
+
+// State row `row` of p (null: zeros) at the slots of a lane of a whole warp.
+template <bool VEC>
+__device__ __forceinline__ float2 state2(const float *p, int64_t row, const ScanArgs &a, const Tile &t, int lane)
+{
+    float2 v = make_float2(0.0f, 0.0f);
+    if (!p) return v;
+    p += row * a.channels;
+    const int64_t c0 = t.ch + channel_of<VEC>(lane >> 1, 2 * (lane & 1)), c1 = t.ch + channel_of<VEC>(lane >> 1, 2 * (lane & 1) + 1);
+    if (c0 < a.channels) v.x = p[c0];
+    if (c1 < a.channels) v.y = p[c1];
+    return v;
+}
+
+// ------------------------------------------------------------------ forward
+
+template <class T, bool VEC, bool PACKED>
+__global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, Grid g)
+{
+    extern __shared__ __align__(16) unsigned char raw[];
+    T *const bx = reinterpret_cast<T *>(raw), *const bf = bx + kChunk * kTile;
+    __shared__ Shared sh;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, l = lane & 15, run = threadIdx.x / 16;
+    Places places{w.ctl, int64_t(blockIdx.x)};
+    unsigned long long next = 0;
+    bool begun = false;
+    if (threadIdx.x == 0) {
+        next = places.take(g);
+        sh.tile = tile_at<false>(next, g);
+        sh.tag = uint32_t(next >> 32);
+    }
+    __syncthreads();
+    Tile t = sh.tile;
+    const uint32_t tag = sh.tag;
+    if (t.valid) {
+        start_copy(bx, a.x, t, a, g.load_mode);
+        start_copy(bf, a.f, t, a, g.load_mode);
+    }
+    commit_copies();
     int64_t end = a.tokens;
-    uint32_t first = !PACKED && t0 == 0, last = 0;
     if (PACKED) {
         end = a.seq_start[a.n_seq];
         end = end < a.tokens ? end : a.tokens;
-        find_cuts<W>(cuts, a, c0, ch0, ch1, ok0, ok1, a.h0, a.h_last);
-        first = __ballot_sync(0xffffffffu, lane < TPT && cuts.first[warp * TPT + (lane < TPT ? lane : 0)] >= 0);
-        last = __ballot_sync(0xffffffffu, lane < TPT && cuts.last[warp * TPT + (lane < TPT ? lane : 0)] >= 0);
-    } else if (t0 < end && t0 + TPT >= end) {
-        last = 1u << (end - 1 - t0);
     }
-    auto first_seq = [&](int i) { return PACKED ? int64_t(cuts.first[warp * TPT + i]) : row; };
-    auto last_seq = [&](int i) { return PACKED ? int64_t(cuts.last[warp * TPT + i]) : row; };
-
-    float2 keep[TPT], add[TPT];
-    Map m = identity();
-#pragma unroll
-    for (int i = 0; i < TPT; ++i) {
-        const float2 ff = f[i].get();
-        const float2 v = make_float2(gate(ff.x), gate(ff.y));
-        keep[i] = keep_of(v);
-        add[i] = mul2(take_of(v), x[i].get());
-        if (first >> i & 1) {
-            m.b = fma2(keep[i], state2(a.h0, first_seq(i), a.channels, ch0, ch1, ok0, ok1), add[i]);
-            m.a = make_float2(kConst, kConst);
-        } else if (t0 + i < a.tokens) {
-            m.b = fma2(keep[i], m.b, add[i]);
-            if (m.a.x >= 0.0f) m.a = mul2(m.a, keep[i]);
-        }
-    }
-    float2 h = make_float2(0.0f, 0.0f);
-    if (W > 1) {
-        sh.warp_map[warp][lane] = pack(m);
+    __syncthreads();
+    while (t.valid) {
+        const int n = int(a.channels - t.ch < kTile ? a.channels - t.ch : kTile);
+        const int64_t t0 = int64_t(t.chunk) * kChunk + run * kRun;
+        float2 start = make_float2(0.0f, 0.0f);
+        if (!PACKED && warp == kSolver && t.k < kGroup * kGroup) start = state2<VEC>(a.h0, t.row, a, t, lane);
+        wait_copies();
+        // a block's second place is taken only now, when all blocks have begun
+        // and taken their first; from then on it is taken a tile ahead
+        if (threadIdx.x == 0 && !begun) sh.tile = tile_at<false>(places.take(g), g);
+        begun = true;
         __syncthreads();
-        if constexpr (W >= 8) {
-            if (chunks > 1) h = state_before<W>(sh, w, at, chunks, a.batch * tiles);
-        }
-    }
-    if (a.states && warp == 0)
-        put_state2(a.states + (row * chunks + at.k) * a.channels, 0, 0, ch0, ch1, ok0, ok1, h);
-    for (int v = 0; v < warp; ++v) h = apply(unpack(sh.warp_map[v][lane]), h);
-    T *py = static_cast<T *>(a.y.ptr) + row * a.y.sb + t0 * a.y.st;
+        Raw<T> x[kRun], f[kRun];
 #pragma unroll
-    for (int i = 0; i < TPT; ++i) {
-        if (first >> i & 1) h = state2(a.h0, first_seq(i), a.channels, ch0, ch1, ok0, ok1);
-        h = fma2(keep[i], h, add[i]);
-        const bool in = t0 + i < end;
-        store2<PAIR>(py + i * a.y.st, ch0, ch1, in && ok0, in && ok1, h);
-        if (a.h_last && (last >> i & 1)) put_state2(a.h_last, last_seq(i), a.channels, ch0, ch1, ok0, ok1, h);
+        for (int i = 0; i < kRun; ++i) {
+            f[i].template load<VEC>(bf + (run * kRun + i) * kTile, l);
+            x[i].template load<VEC>(bx + (run * kRun + i) * kTile, l);
+        }
+        const Tile u = sh.tile;
+        __syncthreads();
+        if (u.valid) {
+            if (threadIdx.x == 0) next = places.take(g);
+            start_copy(bx, a.x, u, a, g.load_mode);
+            start_copy(bf, a.f, u, a, g.load_mode);
+        }
+        commit_copies();
+        Marks mk{0u, 0u};
+        if (PACKED) {
+            find_cuts(sh.cuts, a, t, n, a.h0, a.h_last);
+            mk = marks_of(sh);
+        }
+        auto initial = [&](int i) {
+            return state4<VEC>(a.h0 ? a.h0 + sh.cuts.first[run * kRun + i] * a.channels + t.ch : nullptr, l, n);
+        };
+
+        F4 keep[kRun], in[kRun];
+        Map m;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            F4 take;
+            gates(decay<T>(f[i].get()), keep[i], take);
+            in[i] = mul(take, x[i].get());
+            if (PACKED && (mk.first >> i & 1)) {
+                m.b = fma(keep[i], initial(i), in[i]);
+                m.a = all(kConst);
+            } else if (i == 0) {
+                m = Map{keep[0], in[0]};
+            } else {
+                m.b = fma(keep[i], m.b, in[i]);
+                if (!PACKED || m.a.lo.x >= 0.0f) m.a = mul(keep[i], m.a);
+            }
+        }
+        sts4(&sh.runs.a[run][4 * l], m.a);
+        sts4(&sh.runs.b[run][4 * l], m.b);
+        __syncthreads();
+        solve<PACKED>(sh, w, t, g, tag, start);
+        F4 h = lds4(&sh.runs.b[run][4 * l]);
+        if (a.states && run == 0)
+            put_state4<VEC>(a.states + (t.row * g.chunks + t.chunk) * a.channels + t.ch, l, n, h);
+        T *py = static_cast<T *>(a.y.ptr) + t.row * a.y.sb + t0 * a.y.st + t.ch;
+        if (t0 + kRun < end && (!PACKED || !(mk.first | mk.last))) {
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) {
+                h = fma(keep[i], h, in[i]);
+                store4<VEC>(py, l, n, h);
+                py += a.y.st;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) {
+                if (PACKED && (mk.first >> i & 1)) h = initial(i);
+                h = fma(keep[i], h, in[i]);
+                if (t0 + i < end) store4<VEC>(py, l, n, h);
+                py += a.y.st;
+                if (a.h_last && (PACKED ? mk.last >> i & 1 : t0 + i == end - 1))
+                    put_state4<VEC>(a.h_last + (PACKED ? int64_t(sh.cuts.last[run * kRun + i]) : int64_t(t.row)) * a.channels + t.ch,
+                                    l, n, h);
+            }
+        }
+        if (threadIdx.x == 0 && u.valid) sh.tile = tile_at<false>(next, g);
+        t = u;
     }
 }
 
 // ------------------------------------------------------------------ backward
 
-template <class T, bool PAIR, bool PACKED, int TPT, int W>
-__global__ void __launch_bounds__(32 * W, W == 1 ? 8 : W == 16 ? ZG_SCAN_BB : 1) scan_bwd_kernel(ScanArgs a, Work w, int64_t chunks, int64_t tiles)
+template <class T, bool VEC, bool PACKED>
+__global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work w, Grid g)
 {
-    __shared__ Shared<W> sh;
-    __shared__ float4 fwd[W][32];
-    __shared__ Cuts cuts;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const Place at = take_place(w, a.batch * tiles, chunks == 1, &sh.place);
-    const int64_t row = at.rest / tiles, tile = at.rest % tiles;
-    const int64_t ch0 = tile * kTile + (PAIR ? 2 * lane : lane), ch1 = ch0 + (PAIR ? 1 : 32);
-    const bool ok0 = ch0 < a.channels, ok1 = ch1 < a.channels;
-    const int64_t k = chunks - 1 - at.k;  // the scan goes from the end
-    const int64_t c0 = k * (TPT * W), t0 = c0 + warp * TPT;
-
-    Raw<T, PAIR> x[TPT], f[TPT], dy[TPT];
-    {
-        const T *px = static_cast<const T *>(a.x.ptr) + row * a.x.sb + t0 * a.x.st;
-        const T *pf = static_cast<const T *>(a.f.ptr) + row * a.f.sb + t0 * a.f.st;
-        const T *pd = static_cast<const T *>(a.y.ptr) + row * a.y.sb + t0 * a.y.st;
-#pragma unroll
-        for (int i = 0; i < TPT; ++i) {
-            const bool in = t0 + i < a.tokens;
-            f[i].load(pf + i * a.f.st, ch0, ch1, in && ok0, in && ok1);
-            dy[i].load(pd + i * a.y.st, ch0, ch1, in && ok0, in && ok1);
-            x[i].load(px + i * a.x.st, ch0, ch1, in && ok0, in && ok1);
-        }
+    extern __shared__ __align__(16) unsigned char raw[];
+    T *const bx = reinterpret_cast<T *>(raw), *const bf = bx + kChunk * kTile, *const bd = bf + kChunk * kTile;
+    __shared__ Shared sh;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, l = lane & 15, run = threadIdx.x / 16;
+    Places places{w.ctl, int64_t(blockIdx.x)};
+    unsigned long long next = 0;
+    bool begun = false;
+    if (threadIdx.x == 0) {
+        next = places.take(g);
+        sh.tile = tile_at<true>(next, g);
+        sh.tag = uint32_t(next >> 32);
     }
-    float2 h = make_float2(0.0f, 0.0f);
-    if (k > 0) h = state2(a.states + (row * chunks + k) * a.channels, 0, 0, ch0, ch1, ok0, ok1);
+    __syncthreads();
+    Tile t = sh.tile;
+    const uint32_t tag = sh.tag;
+    if (t.valid) {
+        start_copy(bx, a.x, t, a, g.load_mode);
+        start_copy(bf, a.f, t, a, g.load_mode);
+        start_copy(bd, a.y, t, a, g.load_mode);
+    }
+    commit_copies();
     int64_t end = a.tokens;
-    uint32_t first = !PACKED && t0 == 0, last = 0;
     if (PACKED) {
         end = a.seq_start[a.n_seq];
         end = end < a.tokens ? end : a.tokens;
-        find_cuts<W>(cuts, a, c0, ch0, ch1, ok0, ok1, a.dh_last, a.dh0);
-        first = __ballot_sync(0xffffffffu, lane < TPT && cuts.first[warp * TPT + (lane < TPT ? lane : 0)] >= 0);
-        last = __ballot_sync(0xffffffffu, lane < TPT && cuts.last[warp * TPT + (lane < TPT ? lane : 0)] >= 0);
-    } else if (t0 < end && t0 + TPT >= end) {
-        last = 1u << (end - 1 - t0);
     }
-    auto first_seq = [&](int i) { return PACKED ? int64_t(cuts.first[warp * TPT + i]) : row; };
-    auto last_seq = [&](int i) { return PACKED ? int64_t(cuts.last[warp * TPT + i]) : row; };
-
-    float2 gates[TPT], slope[TPT];
-    Map m = identity(), r = identity();
-#pragma unroll
-    for (int i = 0; i < TPT; ++i) {
-        const float2 ff = f[i].get();
-        gates[i] = make_float2(gate(ff.x), gate(ff.y));
-        const float2 keep = keep_of(gates[i]), add = mul2(take_of(gates[i]), x[i].get());
-        if (first >> i & 1) {
-            m.b = fma2(keep, state2(a.h0, first_seq(i), a.channels, ch0, ch1, ok0, ok1), add);
-            m.a = make_float2(kConst, kConst);
-        } else {
-            m.b = fma2(keep, m.b, add);
-            if (m.a.x >= 0.0f) m.a = mul2(m.a, keep);
+    __syncthreads();
+    while (t.valid) {
+        const int n = int(a.channels - t.ch < kTile ? a.channels - t.ch : kTile);
+        const int64_t t0 = int64_t(t.chunk) * kChunk + run * kRun;
+        float2 start = make_float2(0.0f, 0.0f), before = start;
+        if (!PACKED && warp == kSolver && t.k < kGroup * kGroup) start = state2<VEC>(a.dh_last, t.row, a, t, lane);
+        if (warp == kSolver - 1) {
+            if (t.chunk > 0)
+                before = state2<VEC>(a.states, t.row * g.chunks + t.chunk, a, t, lane);
+            else if (!PACKED)
+                before = state2<VEC>(a.h0, t.row, a, t, lane);
         }
-    }
-#pragma unroll
-    for (int i = TPT - 1; i >= 0; --i) {
-        if (t0 + i >= end) continue;
-        const float2 keep = keep_of(gates[i]);
-        if (last >> i & 1) {
-            r.b = mul2(keep, add2(dy[i].get(), state2(a.dh_last, last_seq(i), a.channels, ch0, ch1, ok0, ok1)));
-            r.a = make_float2(kConst, kConst);
-        } else {
-            r.b = mul2(keep, add2(dy[i].get(), r.b));
-            if (r.a.x >= 0.0f) r.a = mul2(r.a, keep);
-        }
-    }
-    float2 g = make_float2(0.0f, 0.0f);
-    if (W > 1) {
-        sh.warp_map[W - 1 - warp][lane] = pack(r);
-        fwd[warp][lane] = pack(m);
+        wait_copies();
+        if (threadIdx.x == 0 && !begun) sh.tile = tile_at<true>(places.take(g), g);  // as in the forward kernel
+        begun = true;
         __syncthreads();
-        if constexpr (W >= 8) {
-            if (chunks > 1) g = state_before<W>(sh, w, at, chunks, a.batch * tiles);
+        Raw<T> x[kRun], f[kRun], dy[kRun];
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            f[i].template load<VEC>(bf + (run * kRun + i) * kTile, l);
+            x[i].template load<VEC>(bx + (run * kRun + i) * kTile, l);
+            dy[i].template load<VEC>(bd + (run * kRun + i) * kTile, l);
         }
-        for (int v = 0; v < warp; ++v) h = apply(unpack(fwd[v][lane]), h);
-        for (int v = 0; v < W - 1 - warp; ++v) g = apply(unpack(sh.warp_map[v][lane]), g);
-    }
-    // forward once more: x gives way to (h_{t-1} - x_t) a_t (1 - a_t)
+        const Tile u = sh.tile;
+        __syncthreads();
+        if (u.valid) {
+            if (threadIdx.x == 0) next = places.take(g);
+            start_copy(bx, a.x, u, a, g.load_mode);
+            start_copy(bf, a.f, u, a, g.load_mode);
+            start_copy(bd, a.y, u, a, g.load_mode);
+        }
+        commit_copies();
+        Marks mk{0u, 0u};
+        if (PACKED) {
+            find_cuts(sh.cuts, a, t, n, a.dh_last, a.dh0);
+            mk = marks_of(sh);
+        }
+        auto side = [&](const float *p, const int *table, int i) {
+            return state4<VEC>(p ? p + table[run * kRun + i] * a.channels + t.ch : nullptr, l, n);
+        };
+
+        // Both maps in one pass over the tokens: the later tokens' gradient
+        // comes in through the product of the gates so far. exp(-f) alone is
+        // kept of the gates, which are formed again from it where they are
+        // needed (a reciprocal each), to hold the tile in 128 registers.
+        F4 e[kRun];
+        Map m, r;
+        F4 weight = all(1.0f);  // of a token's dy in the run's gradient
+        bool cut = false;       // a packed sequence ended: the later tokens do not count
+        r.b = all(0.0f);
 #pragma unroll
-    for (int i = 0; i < TPT; ++i) {
-        if (first >> i & 1) h = state2(a.h0, first_seq(i), a.channels, ch0, ch1, ok0, ok1);
-        const float2 keep = keep_of(gates[i]), take = take_of(gates[i]), xx = x[i].get();
-        slope[i] = mul2(sub2(h, xx), mul2(keep, take));
-        h = fma2(keep, h, mul2(take, xx));
-    }
-    T *px = static_cast<T *>(a.dx.ptr) + row * a.dx.sb + t0 * a.dx.st;
-    T *pf = static_cast<T *>(a.df.ptr) + row * a.df.sb + t0 * a.df.st;
+        for (int i = 0; i < kRun; ++i) {
+            F4 keep, take;
+            e[i] = decay<T>(f[i].get());
+            gates(e[i], keep, take);
+            const F4 in = mul(take, x[i].get());
+            if (PACKED && (mk.first >> i & 1)) {
+                m.b = fma(keep, side(a.h0, sh.cuts.first, i), in);
+                m.a = all(kConst);
+            } else if (i == 0) {
+                m = Map{keep, in};
+            } else {
+                m.b = fma(keep, m.b, in);
+                if (!PACKED || m.a.lo.x >= 0.0f) m.a = mul(keep, m.a);
+            }
+            // tokens past the end have no gradient: what comes in there is zero or dh_last, unchanged
+            if (PACKED ? !cut && t0 + i < end : t0 + i < a.tokens) {
+                weight = mul(weight, keep);
+                r.b = fma(weight, dy[i].get(), r.b);
+                if (PACKED && (mk.last >> i & 1)) {
+                    r.b = fma(weight, side(a.dh_last, sh.cuts.last, i), r.b);
+                    cut = true;
+                }
+            }
+        }
+        r.a = cut ? all(kConst) : weight;
+        sts4(&sh.fwd.a[run][4 * l], m.a);
+        sts4(&sh.fwd.b[run][4 * l], m.b);
+        sts4(&sh.runs.a[kRuns - 1 - run][4 * l], r.a);
+        sts4(&sh.runs.b[kRuns - 1 - run][4 * l], r.b);
+        __syncthreads();
+        if (warp == kSolver - 1) run_states<PACKED>(sh.fwd, lane, before);
+        solve<PACKED>(sh, w, t, g, tag, start);
+        F4 h = lds4(&sh.fwd.b[run][4 * l]), gr = lds4(&sh.runs.b[kRuns - 1 - run][4 * l]);
+        // forward once more, for h_{t-1} - x_t
+        F4 over[kRun];
 #pragma unroll
-    for (int i = TPT - 1; i >= 0; --i) {
-        if (t0 + i >= end) continue;
-        if (last >> i & 1) g = state2(a.dh_last, last_seq(i), a.channels, ch0, ch1, ok0, ok1);
-        g = add2(dy[i].get(), g);
-        store2<PAIR>(px + i * a.dx.st, ch0, ch1, ok0, ok1, mul2(take_of(gates[i]), g));
-        store2<PAIR>(pf + i * a.df.st, ch0, ch1, ok0, ok1, mul2(slope[i], g));
-        g = mul2(keep_of(gates[i]), g);
-        if (a.dh0 && (first >> i & 1)) put_state2(a.dh0, first_seq(i), a.channels, ch0, ch1, ok0, ok1, g);
+        for (int i = 0; i < kRun; ++i) {
+            if (PACKED && (mk.first >> i & 1)) h = side(a.h0, sh.cuts.first, i);
+            F4 keep, take;
+            gates(e[i], keep, take);
+            const F4 xx = x[i].get();
+            over[i] = sub(h, xx);
+            h = fma(keep, h, mul(take, xx));
+        }
+        T *px = static_cast<T *>(a.dx.ptr) + t.row * a.dx.sb + (t0 + kRun - 1) * a.dx.st + t.ch;
+        T *pf = static_cast<T *>(a.df.ptr) + t.row * a.df.sb + (t0 + kRun - 1) * a.df.st + t.ch;
+        const bool plain = t0 + kRun <= end && (!PACKED || !(mk.first | mk.last));
+#pragma unroll
+        for (int i = kRun - 1; i >= 0; --i) {
+            if (plain || t0 + i < end) {
+                if (PACKED && (mk.last >> i & 1)) gr = side(a.dh_last, sh.cuts.last, i);
+                F4 keep, take;
+                gates(e[i], keep, take);
+                gr = add(dy[i].get(), gr);
+                const F4 dx = mul(take, gr);
+                store4<VEC>(px, l, n, dx);
+                gr = mul(keep, gr);
+                store4<VEC>(pf, l, n, mul(mul(over[i], keep), dx));
+                if (PACKED && a.dh0 && (mk.first >> i & 1))
+                    put_state4<VEC>(a.dh0 + sh.cuts.first[run * kRun + i] * a.channels + t.ch, l, n, gr);
+            }
+            px -= a.dx.st;
+            pf -= a.df.st;
+        }
+        if (!PACKED && a.dh0 && t0 == 0) put_state4<VEC>(a.dh0 + t.row * a.channels + t.ch, l, n, gr);
+        if (threadIdx.x == 0 && u.valid) sh.tile = tile_at<true>(next, g);
+        t = u;
     }
+}
+
+// ------------------------------------------------------------------ a few tokens
+
+__device__ __forceinline__ float load1(const float *p) { return *p; }
+__device__ __forceinline__ float load1(const uint16_t *p) { return __uint_as_float(uint32_t(*p) << 16); }
+__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store1(uint16_t *p, float v) { *p = uint16_t(pack_bf16x2(v, 0.0f)); }
+
+constexpr int kFew = 16;
+
+// Rows of at most kFew tokens: a thread to a channel, all its loads at once.
+template <class T, int N, bool BWD>
+__global__ void __launch_bounds__(128) few_kernel(ScanArgs a)
+{
+    const int64_t i0 = int64_t(blockIdx.x) * 128 + threadIdx.x;
+    if (i0 >= a.batch * a.channels) return;
+    const int64_t row = i0 / a.channels, c = i0 % a.channels;
+    const T *px = static_cast<const T *>(a.x.ptr) + row * a.x.sb + c;
+    const T *pf = static_cast<const T *>(a.f.ptr) + row * a.f.sb + c;
+    const T *pd = static_cast<const T *>(a.y.ptr) + row * a.y.sb + c;
+    float x[N], f[N], dy[N], before[N], take[N];
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        const bool in = t < a.tokens;
+        f[t] = in ? load1(pf + t * a.f.st) : 0.0f;
+        x[t] = in ? load1(px + t * a.x.st) : 0.0f;
+        if (BWD) dy[t] = in ? load1(pd + t * a.y.st) : 0.0f;
+    }
+    float h = a.h0 ? a.h0[i0] : 0.0f;
+    float r = BWD && a.dh_last ? a.dh_last[i0] : 0.0f;
+    if (!BWD && a.states) a.states[i0] = h;
+    T *py = static_cast<T *>(a.y.ptr) + row * a.y.sb + c;
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        float2 k, u;
+        gates(decay<T>(make_float2(f[t], f[t])), k, u);
+        before[t] = h;
+        f[t] = k.x;
+        take[t] = u.x;
+        if (t < a.tokens) {
+            h = fmaf(k.x, h, u.x * x[t]);
+            if (!BWD) store1(py + t * a.y.st, h);
+        }
+    }
+    if (!BWD) {
+        if (a.h_last) a.h_last[i0] = h;
+        return;
+    }
+    T *dx = static_cast<T *>(a.dx.ptr) + row * a.dx.sb + c, *df = static_cast<T *>(a.df.ptr) + row * a.df.sb + c;
+#pragma unroll
+    for (int t = N - 1; t >= 0; --t) {
+        if (t >= a.tokens) continue;
+        const float g = dy[t] + r;
+        store1(dx + t * a.dx.st, take[t] * g);
+        store1(df + t * a.df.st, g * (before[t] - x[t]) * (f[t] * take[t]));
+        r = f[t] * g;
+    }
+    if (a.dh0) a.dh0[i0] = r;
 }
 
 // ------------------------------------------------------------------ launches
 
-bool pairs(const ScanView &v, int size, int64_t channels)
+// The widest unit (16, 4 or 2 bytes) at whose multiples all rows of v begin.
+int unit_of(const ScanView &v, int size)
 {
-    return channels % 2 == 0 && v.sb % 2 == 0 && v.st % 2 == 0 && reinterpret_cast<uintptr_t>(v.ptr) % (2 * size) == 0;
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(v.ptr) | uintptr_t(v.sb * size) | uintptr_t(v.st * size);
+    return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+}
+bool fours(const ScanView &v, int size, int64_t channels)
+{
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(v.ptr) | uintptr_t(v.sb * size) | uintptr_t(v.st * size);
+    return channels % 4 == 0 && bits % (4 * size) == 0;
 }
 
-template <class T, bool PAIR, bool PACKED, int TPT, int W, bool BWD>
-cudaError_t launch(const ScanArgs &a, const ScanWork &sw, cudaStream_t st)
+template <class T, bool VEC, bool PACKED, bool BWD>
+cudaError_t launch(const ScanArgs &a, const ScanWork &sw, int load_mode, cudaStream_t st)
 {
-    const int64_t tiles = (a.channels + kTile - 1) / kTile, chunks = (a.tokens + TPT * W - 1) / (TPT * W);
-    const int64_t blocks = a.batch * tiles * chunks;
-    if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
+    auto *kernel = BWD ? &scan_bwd_kernel<T, VEC, PACKED> : &scan_kernel<T, VEC, PACKED>;
+    constexpr size_t smem = (BWD ? 3 : 2) * kChunk * kTile * sizeof(T);
+    Grid g{};
+    g.tiles = (a.channels + kTile - 1) / kTile;
+    g.width = a.batch * g.tiles;
+    g.chunks = (a.tokens + kChunk - 1) / kChunk;
+    g.places = g.width * g.chunks;
+    g.load_mode = load_mode;
+    if (g.places >= int64_t(0xf0000000)) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
     Work w{};
     w.ctl = sw.ctl;
     w.status = sw.status;
     w.wait_limit = sw.wait_limit;
     w.chunk = reinterpret_cast<ulonglong2 *>(sw.records);
-    w.group = w.chunk + 2 * 32 * (a.batch * tiles * chunks);
-    w.span = w.group + 2 * 32 * (a.batch * tiles * (chunks / kGroup));
-    if (BWD)
-        scan_bwd_kernel<T, PAIR, PACKED, TPT, W><<<unsigned(blocks), 32 * W, 0, st>>>(a, w, chunks, tiles);
-    else
-        scan_kernel<T, PAIR, PACKED, TPT, W><<<unsigned(blocks), 32 * W, 0, st>>>(a, w, chunks, tiles);
+    w.group = w.chunk + 2 * 32 * (g.width * g.chunks);
+    w.span = w.group + 2 * 32 * (g.width * (g.chunks / kGroup));
+    const int64_t wave = wave_blocks(reinterpret_cast<const void *>(kernel), kThreads, smem);
+    kernel<<<unsigned(g.places < wave ? g.places : wave), kThreads, smem, st>>>(a, w, g);
     return cudaGetLastError();
 }
 
-template <class T, bool PAIR, bool BWD>
+template <class T, bool BWD>
+cudaError_t launch_few(const ScanArgs &a, cudaStream_t st)
+{
+    const int64_t blocks = (a.batch * a.channels + 127) / 128;
+    if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
+    if (a.tokens == 1)
+        few_kernel<T, 1, BWD><<<unsigned(blocks), 128, 0, st>>>(a);
+    else
+        few_kernel<T, kFew, BWD><<<unsigned(blocks), 128, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <class T, bool BWD>
 cudaError_t pick(const ScanArgs &a, const ScanWork &w, cudaStream_t st)
 {
-    // One warp walks a short row alone, its tokens all in registers; packed
-    // rows always take whole chunks, in whose tables their sequences are found.
-    constexpr int TPT = BWD ? ZG_SCAN_BT : ZG_SCAN_FT;
-    if (a.seq_start) return launch<T, PAIR, true, TPT, kChunk / TPT, BWD>(a, w, st);
-    if (a.tokens == 1) return launch<T, PAIR, false, 1, 1, BWD>(a, w, st);
-    if (a.tokens <= 8) return launch<T, PAIR, false, 8, 1, BWD>(a, w, st);
-    return launch<T, PAIR, false, TPT, kChunk / TPT, BWD>(a, w, st);
+    if (!a.seq_start && a.tokens <= kFew) return launch_few<T, BWD>(a, st);
+    constexpr int size = int(sizeof(T));
+    int mode = unit_of(a.x, size);
+    mode = mode < unit_of(a.f, size) ? mode : unit_of(a.f, size);
+    bool vec = fours(a.x, size, a.channels) && fours(a.f, size, a.channels) && fours(a.y, size, a.channels);
+    if (BWD) {
+        mode = mode < unit_of(a.y, size) ? mode : unit_of(a.y, size);
+        vec = vec && fours(a.dx, size, a.channels) && fours(a.df, size, a.channels);
+    }
+    if (a.seq_start) return vec ? launch<T, true, true, BWD>(a, w, mode, st) : launch<T, false, true, BWD>(a, w, mode, st);
+    return vec ? launch<T, true, false, BWD>(a, w, mode, st) : launch<T, false, false, BWD>(a, w, mode, st);
 }
 
 template <bool BWD>
 cudaError_t by_type(const ScanArgs &a, const ScanWork &w, cudaStream_t st)
 {
-    const int size = a.dtype == ZG_DTYPE_BF16 ? 2 : 4;
-    bool pair = pairs(a.x, size, a.channels) && pairs(a.f, size, a.channels) && pairs(a.y, size, a.channels);
-    if (BWD) pair = pair && pairs(a.dx, size, a.channels) && pairs(a.df, size, a.channels);
-    if (size == 2) return pair ? pick<uint16_t, true, BWD>(a, w, st) : pick<uint16_t, false, BWD>(a, w, st);
-    return pair ? pick<float, true, BWD>(a, w, st) : pick<float, false, BWD>(a, w, st);
+    return a.dtype == ZG_DTYPE_BF16 ? pick<uint16_t, BWD>(a, w, st) : pick<float, BWD>(a, w, st);
 }
 
 }  // namespace
