@@ -41,7 +41,6 @@ constexpr int kRun = kChunk / (2 * kWarps);  // tokens of a half warp
 constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 16;
 constexpr float kConst = -1.0f;
-
 // ------------------------------------------------------------------ arithmetic
 
 // Four channels of a lane, two to a packed operation.
@@ -135,28 +134,23 @@ __device__ __forceinline__ void gates(F4 e, F4 &keep, F4 &take)
     gates(e.hi, keep.hi, take.hi);
 }
 
-// A map of the state, h -> a h + b, for a lane's four channels of a half warp
-// and for its two of a whole warp. A constant one is marked in all channels;
-// there are none unless sequences are packed (CUT).
+// A map of the state, h -> a h + b: for a lane's four channels of a run, and for
+// one slot (x = a, y = b). A constant one is marked in all channels; there are
+// none unless sequences are packed (CUT).
 struct Map {
     F4 a, b;
 };
-struct Map2 {
-    float2 a, b;
-};
-__device__ __forceinline__ Map2 identity2() { return Map2{make_float2(1.0f, 1.0f), make_float2(0.0f, 0.0f)}; }
 // `first`, then `second`.
 template <bool CUT>
-__device__ __forceinline__ Map2 then(const Map2 &first, const Map2 &second)
+__device__ __forceinline__ float2 then(float2 first, float2 second)
 {
-    if (CUT && second.a.x < 0.0f) return second;
-    return Map2{CUT && first.a.x < 0.0f ? first.a : mul_f32x2(second.a, first.a),
-                fma_f32x2(second.a, first.b, second.b)};
+    if (CUT && second.x < 0.0f) return second;
+    return make_float2(CUT && first.x < 0.0f ? first.x : second.x * first.x, fmaf(second.x, first.y, second.y));
 }
 template <bool CUT>
-__device__ __forceinline__ float2 apply(const Map2 &m, float2 h)
+__device__ __forceinline__ float apply(float2 m, float h)
 {
-    return CUT && m.a.x < 0.0f ? m.b : fma_f32x2(m.a, h, m.b);
+    return CUT && m.x < 0.0f ? m.y : fmaf(m.x, h, m.y);
 }
 
 // ------------------------------------------------------------------ the workspace
@@ -169,9 +163,9 @@ __device__ __forceinline__ float2 apply(const Map2 &m, float2 h)
 
 struct Work {
     unsigned long long *ctl;
-    ulonglong2 *chunk;  // per chunk, tile and lane: a.x, b.x and a.y, b.y
+    ulonglong2 *chunk;  // per chunk, tile and slot: a, b
     ulonglong2 *group;  // the same per group
-    ulonglong2 *span;   // per span, tile and lane: the state after it
+    ulonglong2 *span;   // per span, tile and slot: the state after it (twice)
     int *status;
     long long wait_limit;
 };
@@ -183,39 +177,63 @@ __device__ __forceinline__ void put(ulonglong2 *p, float x, float y, uint32_t ta
                  "l"(t | __float_as_uint(y))
                  : "memory");
 }
-__device__ __forceinline__ bool got(const ulonglong2 *p, uint32_t tag, float &x, float &y)
+__device__ __forceinline__ ulonglong2 look(const ulonglong2 *p)
 {
-    unsigned long long u, v;
-    asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(u), "=l"(v) : "l"(p) : "memory");
-    x = __uint_as_float(uint32_t(u));
-    y = __uint_as_float(uint32_t(v));
-    return uint32_t(u >> 32) == tag && uint32_t(v >> 32) == tag;
+    ulonglong2 v;
+    asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ bool there(ulonglong2 v, uint32_t tag)
+{
+    return uint32_t(v.x >> 32) == tag && uint32_t(v.y >> 32) == tag;
+}
+__device__ __forceinline__ float2 values(ulonglong2 v)
+{
+    return make_float2(__uint_as_float(uint32_t(v.x)), __uint_as_float(uint32_t(v.y)));
 }
 
-// Another try at a word that is not there yet; false when the wait ran out,
-// here or in another block (which then must not be waited for).
-__device__ __noinline__ bool try_on(const Work &w, long long &polls)
+// Whether to ask again for words that are not there yet; false when the wait ran
+// out, here or in another block (which then must not be waited for).
+__device__ __forceinline__ bool go_on(const Work &w, long long polls)
 {
-    if (++polls > w.wait_limit) {
+    if (polls >= w.wait_limit) {
         atomicExch(w.status, kStatusTimeout);
         return false;
     }
-    return (polls & 63) || *reinterpret_cast<volatile int *>(w.status) == 0;
+    return (polls & 63) != 63 || *reinterpret_cast<volatile int *>(w.status) == 0;
 }
 
-__device__ __forceinline__ Map2 wait_map(const ulonglong2 *p, uint32_t tag, const Work &w)
-{
-    Map2 m;
-    long long polls = 0;
-    while (!(got(p, tag, m.a.x, m.b.x) & got(p + 1, tag, m.a.y, m.b.y)))
-        if (!try_on(w, polls)) return identity2();
-    return m;
-}
-__device__ __forceinline__ void put_map(ulonglong2 *p, const Map2 &m, uint32_t tag)
-{
-    put(p, m.a.x, m.b.x, tag);
-    put(p + 1, m.a.y, m.b.y, tag);
-}
+// Up to four maps of one slot, asked for together and composed in order.
+struct Four {
+    const ulonglong2 *p;
+    int64_t step;
+    int count;
+    ulonglong2 v[4];
+    __device__ __forceinline__ void ask()
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < count) v[i] = look(p + i * step);
+    }
+    // Where the wait runs out, what is not there is undefined.
+    template <bool CUT>
+    __device__ __forceinline__ float2 get(uint32_t tag, const Work &w)
+    {
+        for (long long polls = 0;; ++polls) {
+            bool ready = true;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < count) ready = ready && there(v[i], tag);
+            if (ready || !go_on(w, polls)) break;
+            ask();
+        }
+        float2 m = make_float2(1.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < count) m = then<CUT>(m, values(v[i]));
+        return m;
+    }
+};
 
 // ------------------------------------------------------------------ a tile's place
 
@@ -290,11 +308,23 @@ struct Runs {
     float a[kRuns][kTile], b[kRuns][kTile];
 };
 
+template <bool BWD>
 struct Shared {
     Runs runs;
-    Runs fwd;  // backward's runs of h
-    float4 part[8][32];
-    float2 start[32];
+    Runs fwd;  // of h
+    float2 fwd_quarters[4][kTile];
+    // maps of four runs, and of the chunks and groups before, by fours: a, b
+    float2 quarters[4][kTile], chunks[4][kTile], groups[4][kTile];
+    float span[kTile];
+    Tile tile;
+    uint32_t tag;
+    Cuts cuts;
+};
+template <>
+struct Shared<false> {
+    Runs runs;
+    float2 quarters[4][kTile], chunks[4][kTile], groups[4][kTile];
+    float span[kTile];
     Tile tile;
     uint32_t tag;
     Cuts cuts;
@@ -381,38 +411,22 @@ __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_grou
 template <bool VEC>
 __device__ __forceinline__ int channel_of(int l, int j) { return VEC ? 4 * l + j : l + 16 * j; }
 
-// Four elements as they lie in memory.
-template <class T>
-struct Raw;
-template <>
-struct Raw<uint16_t> {
-    uint2 w;
-    template <bool VEC>
-    __device__ __forceinline__ void load(const uint16_t *row, int l)
-    {
-        if (VEC)
-            w = *reinterpret_cast<const uint2 *>(row + 4 * l);
-        else
-            w = make_uint2(row[l] | uint32_t(row[l + 16]) << 16, row[l + 32] | uint32_t(row[l + 48]) << 16);
-    }
-    __device__ __forceinline__ F4 get() const
-    {
+// Lane l's four channels of a row in shared memory.
+template <bool VEC>
+__device__ __forceinline__ F4 read4(const uint16_t *row, int l)
+{
+    if (VEC) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(row + 4 * l);
         return F4{make_float2(bf16_lo(w.x), bf16_hi(w.x)), make_float2(bf16_lo(w.y), bf16_hi(w.y))};
     }
-};
-template <>
-struct Raw<float> {
-    F4 w;
-    template <bool VEC>
-    __device__ __forceinline__ void load(const float *row, int l)
-    {
-        if (VEC)
-            w = lds4(row + 4 * l);
-        else
-            w = F4{make_float2(row[l], row[l + 16]), make_float2(row[l + 32], row[l + 48])};
-    }
-    __device__ __forceinline__ F4 get() const { return w; }
-};
+    return F4{make_float2(bf16_lo(row[l]), bf16_lo(row[l + 16])), make_float2(bf16_lo(row[l + 32]), bf16_lo(row[l + 48]))};
+}
+template <bool VEC>
+__device__ __forceinline__ F4 read4(const float *row, int l)
+{
+    if (VEC) return lds4(row + 4 * l);
+    return F4{make_float2(row[l], row[l + 16]), make_float2(row[l + 32], row[l + 48])};
+}
 
 // Lane l's four channels of a row of a tile, `n` of whose channels exist.
 template <bool VEC>
@@ -514,101 +528,112 @@ __device__ __forceinline__ void find_cuts(Cuts &cuts, const ScanArgs &a, const T
 
 // ------------------------------------------------------------------ the chunks before
 
-__device__ __forceinline__ float4 pack(const Map2 &m) { return make_float4(m.a.x, m.a.y, m.b.x, m.b.y); }
-__device__ __forceinline__ Map2 unpack(float4 v) { return Map2{make_float2(v.x, v.y), make_float2(v.z, v.w)}; }
-__device__ __forceinline__ Map2 run_map(const Runs &runs, int r, int lane)
-{
-    return Map2{*reinterpret_cast<const float2 *>(&runs.a[r][2 * lane]),
-                *reinterpret_cast<const float2 *>(&runs.b[r][2 * lane])};
-}
-// From the state before the first run, the state before each, in place of the
-// runs' b; returns the state after the last. One warp.
-template <bool CUT>
-__device__ __forceinline__ float2 run_states(Runs &runs, int lane, float2 h)
-{
+// Four runs of one slot: their maps, and the state before each in place of
+// the runs' b.
+struct Quarter {
+    float2 m[4];
+    __device__ __forceinline__ void load(const Runs &runs, int part, int slot)
+    {
 #pragma unroll
-    for (int r = 0; r < kRuns; ++r) {
-        const Map2 m = run_map(runs, r, lane);
-        *reinterpret_cast<float2 *>(&runs.b[r][2 * lane]) = h;
-        h = apply<CUT>(m, h);
+        for (int i = 0; i < 4; ++i) m[i] = make_float2(runs.a[4 * part + i][slot], runs.b[4 * part + i][slot]);
     }
-    return h;
-}
+    template <bool CUT>
+    __device__ __forceinline__ float2 whole() const
+    {
+        return then<CUT>(then<CUT>(m[0], m[1]), then<CUT>(m[2], m[3]));
+    }
+    template <bool CUT>
+    __device__ __forceinline__ float run(Runs &runs, int part, int slot, float h) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            runs.b[4 * part + i][slot] = h;
+            h = apply<CUT>(m[i], h);
+        }
+        return h;
+    }
+};
 
-constexpr int kSolver = 4;  // the warp that composes the runs
+// The chunks before a tile: what a thread waits for, which is four chunks and
+// four groups at one slot (and, for the last four, the span). All are asked
+// for when the tile is begun; where the blocks before are a round ahead, they
+// are there when the tile's own maps are.
+struct Before {
+    Four chunks, groups;
+    uint32_t in_group, group, first_group;
+    __device__ __forceinline__ Before(const Work &w, const Tile &t, const Grid &g)
+    {
+        const int slot = threadIdx.x % kTile, part = threadIdx.x / kTile;
+        in_group = t.k % kGroup;
+        group = t.k / kGroup % kGroup;
+        first_group = t.k / kGroup - group;
+        const int64_t step = g.width * kTile, at = int64_t(t.rest) * kTile + slot;
+        chunks = Four{w.chunk + (t.k - in_group + 4 * part) * step + at, step, int(in_group) - 4 * part};
+        groups = Four{w.group + (first_group + 4 * part) * step + at, step, int(group) - 4 * part};
+        chunks.ask();
+        groups.ask();
+    }
+};
 
 // Publishes this chunk's map, waits for the chunks before it, and leaves the
-// state before each run in sh.runs.b. `start` is the state before the row's
-// first token, in slots 2 lane and 2 lane + 1 of the solver. The runs' maps
-// are behind a barrier; ends with a barrier. Records of 32 lanes lie by chunk
-// (group, span) and then by tile.
-template <bool CUT>
-__device__ __forceinline__ void solve(Shared &sh, const Work &w, const Tile &t, const Grid &g, uint32_t tag, float2 start)
+// state before each run in sh.runs.b. The chunk's own map never waits for
+// others, nor does the group's for earlier groups. `start` is the state before
+// the row's first token, at the thread's slot. The runs' maps are behind a
+// barrier; ends with one. Records of kTile slots lie by chunk (group, span) and
+// then by tile.
+template <bool CUT, class Sh>
+__device__ __forceinline__ void solve(Sh &sh, Before &before, const Work &w, const Tile &t, const Grid &g, uint32_t tag,
+                                      float start)
 {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int slot = threadIdx.x % kTile, part = threadIdx.x / kTile;
+    Quarter mine;
+    mine.load(sh.runs, part, slot);
+    sh.quarters[part][slot] = mine.whole<CUT>();
     if (g.chunks == 1) {
-        if (warp == kSolver) run_states<CUT>(sh.runs, lane, start);
+        __syncthreads();
+        float h = start;
+        for (int i = 0; i < part; ++i) h = apply<CUT>(sh.quarters[i][slot], h);
+        mine.run<CUT>(sh.runs, part, slot, h);
         __syncthreads();
         return;
     }
-    const uint32_t in_group = t.k % kGroup, group = t.k / kGroup % kGroup;
-    const uint32_t first_chunk = t.k - in_group, this_group = t.k / kGroup, first_group = this_group - group;
-    const int64_t width = g.width, at = int64_t(t.rest) * 32 + lane;
-    auto chunk_at = [&](uint32_t k) { return w.chunk + 2 * (k * width * 32 + at); };
-    auto group_at = [&](uint32_t k) { return w.group + 2 * (k * width * 32 + at); };
-    auto span_at = [&](uint32_t k) { return w.span + (k * width * 32 + at); };
-    const bool followed = t.k + 1 < uint32_t(g.chunks), ends_group = in_group == kGroup - 1 && followed;
-    Map2 mine = identity2();
-    if (warp == kSolver) {
-        if (followed) {
+    const bool followed = t.k + 1 < uint32_t(g.chunks), ends_group = before.in_group == kGroup - 1 && followed;
+    const int64_t step = g.width * kTile, at = int64_t(t.rest) * kTile + slot;
+    const uint32_t this_group = t.k / kGroup;
+    __syncthreads();
+    float2 all_runs = make_float2(1.0f, 0.0f);
+    if (part == 0 && followed) {
 #pragma unroll
-            for (int r = 0; r < kRuns; ++r) mine = then<CUT>(mine, run_map(sh.runs, r, lane));
-            if (!ends_group) put_map(chunk_at(t.k), mine, tag);
-        }
-    } else {
-        Map2 m = identity2();
-        if (warp > kSolver) {  // chunks of this group, five to a warp
-            const uint32_t lo = 5 * (warp - kSolver - 1);
-#pragma unroll
-            for (uint32_t i = 0; i < 5; ++i)
-                if (lo + i < in_group) m = then<CUT>(m, wait_map(chunk_at(first_chunk + lo + i), tag, w));
-        } else {  // groups of this span, four to a warp, and the span before
-            const uint32_t lo = 4 * warp;
-#pragma unroll
-            for (uint32_t i = 0; i < 4; ++i)
-                if (lo + i < group) m = then<CUT>(m, wait_map(group_at(first_group + lo + i), tag, w));
-            if (warp == 3 && first_group > 0) {
-                float2 s;
-                long long polls = 0;
-                while (!got(span_at(first_group / kGroup - 1), tag, s.x, s.y))
-                    if (!try_on(w, polls)) {
-                        s = make_float2(0.0f, 0.0f);
-                        break;
-                    }
-                sh.start[lane] = s;
-            }
-        }
-        sh.part[warp][lane] = pack(m);
+        for (int i = 0; i < 4; ++i) all_runs = then<CUT>(all_runs, sh.quarters[i][slot]);
+        if (!ends_group) put(w.chunk + t.k * step + at, all_runs.x, all_runs.y, tag);
     }
-    if (warp >= kSolver && ends_group) {
-        // the group's map must not wait for the groups before it
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (warp == kSolver && group < kGroup - 1) {
-            Map2 m = unpack(sh.part[kSolver + 1][lane]);
-            m = then<CUT>(m, unpack(sh.part[kSolver + 2][lane]));
-            m = then<CUT>(m, unpack(sh.part[kSolver + 3][lane]));
-            put_map(group_at(this_group), then<CUT>(m, mine), tag);
+    sh.chunks[part][slot] = before.chunks.get<CUT>(tag, w);
+    if (ends_group && before.group < kGroup - 1) {
+        __syncthreads();
+        if (part == 0) {
+            float2 m = make_float2(1.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = then<CUT>(m, sh.chunks[i][slot]);
+            m = then<CUT>(m, all_runs);
+            put(w.group + this_group * step + at, m.x, m.y, tag);
         }
+    }
+    sh.groups[part][slot] = before.groups.get<CUT>(tag, w);
+    if (part == 3 && before.first_group > 0) {
+        const ulonglong2 *p = w.span + (before.first_group / kGroup - 1) * step + at;
+        ulonglong2 v = look(p);
+        for (long long polls = 0; !there(v, tag) && go_on(w, polls); ++polls) v = look(p);
+        sh.span[slot] = values(v).x;
     }
     __syncthreads();
-    if (warp == kSolver) {
-        float2 h = first_group > 0 ? sh.start[lane] : start;
+    float h = before.first_group > 0 ? sh.span[slot] : start;
 #pragma unroll
-        for (int v = 0; v < 8; ++v)
-            if (v != kSolver) h = apply<CUT>(unpack(sh.part[v][lane]), h);
-        h = run_states<CUT>(sh.runs, lane, h);
-        if (ends_group && group == kGroup - 1) put(span_at(this_group / kGroup), h.x, h.y, tag);
-    }
+    for (int i = 0; i < 4; ++i) h = apply<CUT>(sh.groups[i][slot], h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h = apply<CUT>(sh.chunks[i][slot], h);
+    for (int i = 0; i < part; ++i) h = apply<CUT>(sh.quarters[i][slot], h);
+    h = mine.run<CUT>(sh.runs, part, slot, h);
+    if (part == 3 && ends_group && before.group == kGroup - 1) put(w.span + this_group / kGroup * step + at, h, h, tag);
     __syncthreads();
 }
 
@@ -616,51 +641,82 @@ __device__ __forceinline__ void solve(Shared &sh, const Work &w, const Tile &t, 
 struct Marks {
     uint32_t first, last;
 };
-__device__ __forceinline__ Marks marks_of(const Shared &sh)
+__device__ __forceinline__ Marks marks_of(const Cuts &cuts)
 {
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, half = lane >> 4;
     const int at = warp * 2 * kRun + (lane & 15);
-    const uint32_t f = __ballot_sync(0xffffffffu, sh.cuts.first[at] >= 0);
-    const uint32_t l = __ballot_sync(0xffffffffu, sh.cuts.last[at] >= 0);
+    const uint32_t f = __ballot_sync(0xffffffffu, cuts.first[at] >= 0);
+    const uint32_t l = __ballot_sync(0xffffffffu, cuts.last[at] >= 0);
     return Marks{(f >> (kRun * half)) & 0xffu, (l >> (kRun * half)) & 0xffu};
 }
 
-// State row `row` of p (null: zeros) at the slots of a lane of a whole warp.
+// State row `row` of p (null: zeros) at the thread's slot.
 template <bool VEC>
-__device__ __forceinline__ float2 state2(const float *p, int64_t row, const ScanArgs &a, const Tile &t, int lane)
+__device__ __forceinline__ float state1(const float *p, int64_t row, const ScanArgs &a, const Tile &t)
 {
-    float2 v = make_float2(0.0f, 0.0f);
-    if (!p) return v;
-    p += row * a.channels;
-    const int64_t c0 = t.ch + channel_of<VEC>(lane >> 1, 2 * (lane & 1)), c1 = t.ch + channel_of<VEC>(lane >> 1, 2 * (lane & 1) + 1);
-    if (c0 < a.channels) v.x = p[c0];
-    if (c1 < a.channels) v.y = p[c1];
-    return v;
+    const int slot = threadIdx.x % kTile;
+    const int64_t c = t.ch + channel_of<VEC>(slot >> 2, slot & 3);
+    return p && c < a.channels ? p[row * a.channels + c] : 0.0f;
 }
 
 // ------------------------------------------------------------------ forward
+
+// Buffers of x and dy per block in backward: with two, the next tile's copies
+// start as soon as a tile's maps are formed; with one (binary32, where two
+// would leave one block to an SM) when it is done.
+template <class T>
+constexpr int kBuffers = sizeof(T) == 4 ? 1 : 2;
+template <class T, bool BWD>
+constexpr size_t kTileBytes = (BWD ? 2 * kBuffers<T> + 1 : 2) * kChunk * kTile * sizeof(T);
+
+// A block's places. The second is taken when the first tile's copies are
+// there, when all blocks have begun and taken their first; from then on a place
+// is taken a tile ahead, in the shadow of a tile's work.
+template <bool BWD, class Sh>
+struct Ahead {
+    Sh &sh;
+    Places places;
+    unsigned long long next;
+    bool begun;
+    __device__ __forceinline__ Ahead(Sh &s, const Work &w, const Grid &g) : sh(s), places{w.ctl, int64_t(blockIdx.x)}, next(0), begun(false)
+    {
+        if (threadIdx.x == 0) {
+            const unsigned long long taken = places.take(g);
+            sh.tile = tile_at<BWD>(taken, g);
+            sh.tag = uint32_t(taken >> 32);
+        }
+    }
+    // Before the barrier that opens a tile; sh.tile is then the one after it.
+    __device__ __forceinline__ void open(const Grid &g)
+    {
+        if (threadIdx.x == 0 && !begun) sh.tile = tile_at<BWD>(places.take(g), g);
+        begun = true;
+    }
+    __device__ __forceinline__ void ask(const Tile &u, const Grid &g)
+    {
+        if (threadIdx.x == 0 && u.valid) next = places.take(g);
+    }
+    // After the last use of sh.tile.
+    __device__ __forceinline__ void close(const Tile &u, const Grid &g)
+    {
+        if (threadIdx.x == 0 && u.valid) sh.tile = tile_at<BWD>(next, g);
+    }
+};
 
 template <class T, bool VEC, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, Grid g)
 {
     extern __shared__ __align__(16) unsigned char raw[];
-    T *const bx = reinterpret_cast<T *>(raw), *const bf = bx + kChunk * kTile;
-    __shared__ Shared sh;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, l = lane & 15, run = threadIdx.x / 16;
-    Places places{w.ctl, int64_t(blockIdx.x)};
-    unsigned long long next = 0;
-    bool begun = false;
-    if (threadIdx.x == 0) {
-        next = places.take(g);
-        sh.tile = tile_at<false>(next, g);
-        sh.tag = uint32_t(next >> 32);
-    }
+    T *const bf = reinterpret_cast<T *>(raw), *const bx = bf + kChunk * kTile;
+    __shared__ Shared<false> sh;
+    const int l = threadIdx.x & 15, run = threadIdx.x / 16;
+    Ahead<false, Shared<false>> ahead(sh, w, g);
     __syncthreads();
     Tile t = sh.tile;
     const uint32_t tag = sh.tag;
     if (t.valid) {
-        start_copy(bx, a.x, t, a, g.load_mode);
         start_copy(bf, a.f, t, a, g.load_mode);
+        start_copy(bx, a.x, t, a, g.load_mode);
     }
     commit_copies();
     int64_t end = a.tokens;
@@ -672,32 +728,17 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
     while (t.valid) {
         const int n = int(a.channels - t.ch < kTile ? a.channels - t.ch : kTile);
         const int64_t t0 = int64_t(t.chunk) * kChunk + run * kRun;
-        float2 start = make_float2(0.0f, 0.0f);
-        if (!PACKED && warp == kSolver && t.k < kGroup * kGroup) start = state2<VEC>(a.h0, t.row, a, t, lane);
+        const float start = PACKED ? 0.0f : state1<VEC>(a.h0, t.row, a, t);
         wait_copies();
-        // a block's second place is taken only now, when all blocks have begun
-        // and taken their first; from then on it is taken a tile ahead
-        if (threadIdx.x == 0 && !begun) sh.tile = tile_at<false>(places.take(g), g);
-        begun = true;
+        ahead.open(g);
         __syncthreads();
-        Raw<T> x[kRun], f[kRun];
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            f[i].template load<VEC>(bf + (run * kRun + i) * kTile, l);
-            x[i].template load<VEC>(bx + (run * kRun + i) * kTile, l);
-        }
         const Tile u = sh.tile;
-        __syncthreads();
-        if (u.valid) {
-            if (threadIdx.x == 0) next = places.take(g);
-            start_copy(bx, a.x, u, a, g.load_mode);
-            start_copy(bf, a.f, u, a, g.load_mode);
-        }
-        commit_copies();
+        ahead.ask(u, g);
+        Before before(w, t, g);
         Marks mk{0u, 0u};
         if (PACKED) {
             find_cuts(sh.cuts, a, t, n, a.h0, a.h_last);
-            mk = marks_of(sh);
+            mk = marks_of(sh.cuts);
         }
         auto initial = [&](int i) {
             return state4<VEC>(a.h0 ? a.h0 + sh.cuts.first[run * kRun + i] * a.channels + t.ch : nullptr, l, n);
@@ -708,8 +749,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
             F4 take;
-            gates(decay<T>(f[i].get()), keep[i], take);
-            in[i] = mul(take, x[i].get());
+            gates(decay<T>(read4<VEC>(bf + (run * kRun + i) * kTile, l)), keep[i], take);
+            in[i] = mul(take, read4<VEC>(bx + (run * kRun + i) * kTile, l));
             if (PACKED && (mk.first >> i & 1)) {
                 m.b = fma(keep[i], initial(i), in[i]);
                 m.a = all(kConst);
@@ -723,31 +764,28 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
         sts4(&sh.runs.a[run][4 * l], m.a);
         sts4(&sh.runs.b[run][4 * l], m.b);
         __syncthreads();
-        solve<PACKED>(sh, w, t, g, tag, start);
+        if (u.valid) {
+            start_copy(bf, a.f, u, a, g.load_mode);
+            start_copy(bx, a.x, u, a, g.load_mode);
+        }
+        commit_copies();
+        solve<PACKED>(sh, before, w, t, g, tag, start);
         F4 h = lds4(&sh.runs.b[run][4 * l]);
         if (a.states && run == 0)
             put_state4<VEC>(a.states + (t.row * g.chunks + t.chunk) * a.channels + t.ch, l, n, h);
         T *py = static_cast<T *>(a.y.ptr) + t.row * a.y.sb + t0 * a.y.st + t.ch;
-        if (t0 + kRun < end && (!PACKED || !(mk.first | mk.last))) {
+        const bool plain = t0 + kRun < end && (!PACKED || !(mk.first | mk.last));
 #pragma unroll
-            for (int i = 0; i < kRun; ++i) {
-                h = fma(keep[i], h, in[i]);
-                store4<VEC>(py, l, n, h);
-                py += a.y.st;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kRun; ++i) {
-                if (PACKED && (mk.first >> i & 1)) h = initial(i);
-                h = fma(keep[i], h, in[i]);
-                if (t0 + i < end) store4<VEC>(py, l, n, h);
-                py += a.y.st;
-                if (a.h_last && (PACKED ? mk.last >> i & 1 : t0 + i == end - 1))
-                    put_state4<VEC>(a.h_last + (PACKED ? int64_t(sh.cuts.last[run * kRun + i]) : int64_t(t.row)) * a.channels + t.ch,
-                                    l, n, h);
-            }
+        for (int i = 0; i < kRun; ++i) {
+            if (PACKED && (mk.first >> i & 1)) h = initial(i);
+            h = fma(keep[i], h, in[i]);
+            if (plain || t0 + i < end) store4<VEC>(py, l, n, h);
+            py += a.y.st;
+            if (!plain && a.h_last && (PACKED ? mk.last >> i & 1 : t0 + i == end - 1))
+                put_state4<VEC>(a.h_last + (PACKED ? int64_t(sh.cuts.last[run * kRun + i]) : int64_t(t.row)) * a.channels + t.ch,
+                                l, n, h);
         }
-        if (threadIdx.x == 0 && u.valid) sh.tile = tile_at<false>(next, g);
+        ahead.close(u, g);
         t = u;
     }
 }
@@ -758,24 +796,19 @@ template <class T, bool VEC, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work w, Grid g)
 {
     extern __shared__ __align__(16) unsigned char raw[];
-    T *const bx = reinterpret_cast<T *>(raw), *const bf = bx + kChunk * kTile, *const bd = bf + kChunk * kTile;
-    __shared__ Shared sh;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, l = lane & 15, run = threadIdx.x / 16;
-    Places places{w.ctl, int64_t(blockIdx.x)};
-    unsigned long long next = 0;
-    bool begun = false;
-    if (threadIdx.x == 0) {
-        next = places.take(g);
-        sh.tile = tile_at<true>(next, g);
-        sh.tag = uint32_t(next >> 32);
-    }
+    constexpr int kSize = kChunk * kTile;
+    constexpr bool kTwo = kBuffers<T> == 2;
+    T *const bf = reinterpret_cast<T *>(raw), *bx = bf + kSize, *other = kTwo ? bx + 2 * kSize : bx;  // dy behind x
+    __shared__ Shared<true> sh;
+    const int l = threadIdx.x & 15, run = threadIdx.x / 16;
+    Ahead<true, Shared<true>> ahead(sh, w, g);
     __syncthreads();
     Tile t = sh.tile;
     const uint32_t tag = sh.tag;
     if (t.valid) {
-        start_copy(bx, a.x, t, a, g.load_mode);
         start_copy(bf, a.f, t, a, g.load_mode);
-        start_copy(bd, a.y, t, a, g.load_mode);
+        start_copy(bx, a.x, t, a, g.load_mode);
+        start_copy(bx + kSize, a.y, t, a, g.load_mode);
     }
     commit_copies();
     int64_t end = a.tokens;
@@ -787,38 +820,24 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
     while (t.valid) {
         const int n = int(a.channels - t.ch < kTile ? a.channels - t.ch : kTile);
         const int64_t t0 = int64_t(t.chunk) * kChunk + run * kRun;
-        float2 start = make_float2(0.0f, 0.0f), before = start;
-        if (!PACKED && warp == kSolver && t.k < kGroup * kGroup) start = state2<VEC>(a.dh_last, t.row, a, t, lane);
-        if (warp == kSolver - 1) {
-            if (t.chunk > 0)
-                before = state2<VEC>(a.states, t.row * g.chunks + t.chunk, a, t, lane);
-            else if (!PACKED)
-                before = state2<VEC>(a.h0, t.row, a, t, lane);
-        }
+        const float start = PACKED ? 0.0f : state1<VEC>(a.dh_last, t.row, a, t);
+        const float h_start = t.chunk > 0 ? state1<VEC>(a.states, t.row * g.chunks + t.chunk, a, t)
+                              : PACKED    ? 0.0f
+                                          : state1<VEC>(a.h0, t.row, a, t);
         wait_copies();
-        if (threadIdx.x == 0 && !begun) sh.tile = tile_at<true>(places.take(g), g);  // as in the forward kernel
-        begun = true;
+        ahead.open(g);
         __syncthreads();
-        Raw<T> x[kRun], f[kRun], dy[kRun];
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            f[i].template load<VEC>(bf + (run * kRun + i) * kTile, l);
-            x[i].template load<VEC>(bx + (run * kRun + i) * kTile, l);
-            dy[i].template load<VEC>(bd + (run * kRun + i) * kTile, l);
-        }
         const Tile u = sh.tile;
-        __syncthreads();
-        if (u.valid) {
-            if (threadIdx.x == 0) next = places.take(g);
-            start_copy(bx, a.x, u, a, g.load_mode);
-            start_copy(bf, a.f, u, a, g.load_mode);
-            start_copy(bd, a.y, u, a, g.load_mode);
+        ahead.ask(u, g);
+        Before before(w, t, g);
+        if (kTwo && u.valid) {
+            start_copy(other, a.x, u, a, g.load_mode);
+            start_copy(other + kSize, a.y, u, a, g.load_mode);
         }
-        commit_copies();
         Marks mk{0u, 0u};
         if (PACKED) {
             find_cuts(sh.cuts, a, t, n, a.dh_last, a.dh0);
-            mk = marks_of(sh);
+            mk = marks_of(sh.cuts);
         }
         auto side = [&](const float *p, const int *table, int i) {
             return state4<VEC>(p ? p + table[run * kRun + i] * a.channels + t.ch : nullptr, l, n);
@@ -836,9 +855,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
             F4 keep, take;
-            e[i] = decay<T>(f[i].get());
+            e[i] = decay<T>(read4<VEC>(bf + (run * kRun + i) * kTile, l));
             gates(e[i], keep, take);
-            const F4 in = mul(take, x[i].get());
+            const F4 in = mul(take, read4<VEC>(bx + (run * kRun + i) * kTile, l));
             if (PACKED && (mk.first >> i & 1)) {
                 m.b = fma(keep, side(a.h0, sh.cuts.first, i), in);
                 m.a = all(kConst);
@@ -851,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
             // tokens past the end have no gradient: what comes in there is zero or dh_last, unchanged
             if (PACKED ? !cut && t0 + i < end : t0 + i < a.tokens) {
                 weight = mul(weight, keep);
-                r.b = fma(weight, dy[i].get(), r.b);
+                r.b = fma(weight, read4<VEC>(bx + kSize + (run * kRun + i) * kTile, l), r.b);
                 if (PACKED && (mk.last >> i & 1)) {
                     r.b = fma(weight, side(a.dh_last, sh.cuts.last, i), r.b);
                     cut = true;
@@ -864,8 +883,19 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
         sts4(&sh.runs.a[kRuns - 1 - run][4 * l], r.a);
         sts4(&sh.runs.b[kRuns - 1 - run][4 * l], r.b);
         __syncthreads();
-        if (warp == kSolver - 1) run_states<PACKED>(sh.fwd, lane, before);
-        solve<PACKED>(sh, w, t, g, tag, start);
+        if (u.valid) start_copy(bf, a.f, u, a, g.load_mode);
+        if (kTwo) commit_copies();
+        {
+            const int slot = threadIdx.x % kTile, part = threadIdx.x / kTile;
+            Quarter q;
+            q.load(sh.fwd, part, slot);
+            sh.fwd_quarters[part][slot] = q.whole<PACKED>();
+            __syncthreads();
+            float h = h_start;
+            for (int i = 0; i < part; ++i) h = apply<PACKED>(sh.fwd_quarters[i][slot], h);
+            q.run<PACKED>(sh.fwd, part, slot, h);
+        }
+        solve<PACKED>(sh, before, w, t, g, tag, start);
         F4 h = lds4(&sh.fwd.b[run][4 * l]), gr = lds4(&sh.runs.b[kRuns - 1 - run][4 * l]);
         // forward once more, for h_{t-1} - x_t
         F4 over[kRun];
@@ -874,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
             if (PACKED && (mk.first >> i & 1)) h = side(a.h0, sh.cuts.first, i);
             F4 keep, take;
             gates(e[i], keep, take);
-            const F4 xx = x[i].get();
+            const F4 xx = read4<VEC>(bx + (run * kRun + i) * kTile, l);
             over[i] = sub(h, xx);
             h = fma(keep, h, mul(take, xx));
         }
@@ -887,7 +917,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
                 if (PACKED && (mk.last >> i & 1)) gr = side(a.dh_last, sh.cuts.last, i);
                 F4 keep, take;
                 gates(e[i], keep, take);
-                gr = add(dy[i].get(), gr);
+                gr = add(read4<VEC>(bx + kSize + (run * kRun + i) * kTile, l), gr);
                 const F4 dx = mul(take, gr);
                 store4<VEC>(px, l, n, dx);
                 gr = mul(keep, gr);
@@ -899,8 +929,20 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
             pf -= a.df.st;
         }
         if (!PACKED && a.dh0 && t0 == 0) put_state4<VEC>(a.dh0 + t.row * a.channels + t.ch, l, n, gr);
-        if (threadIdx.x == 0 && u.valid) sh.tile = tile_at<true>(next, g);
+        ahead.close(u, g);
         t = u;
+        if (kTwo) {
+            T *const swap = bx;
+            bx = other;
+            other = swap;
+        } else {
+            __syncthreads();
+            if (u.valid) {
+                start_copy(bx, a.x, u, a, g.load_mode);
+                start_copy(bx + kSize, a.y, u, a, g.load_mode);
+            }
+            commit_copies();
+        }
     }
 }
 
@@ -981,7 +1023,7 @@ template <class T, bool VEC, bool PACKED, bool BWD>
 cudaError_t launch(const ScanArgs &a, const ScanWork &sw, int load_mode, cudaStream_t st)
 {
     auto *kernel = BWD ? &scan_bwd_kernel<T, VEC, PACKED> : &scan_kernel<T, VEC, PACKED>;
-    constexpr size_t smem = (BWD ? 3 : 2) * kChunk * kTile * sizeof(T);
+    constexpr size_t smem = kTileBytes<T, BWD>;
     Grid g{};
     g.tiles = (a.channels + kTile - 1) / kTile;
     g.width = a.batch * g.tiles;
@@ -996,8 +1038,8 @@ cudaError_t launch(const ScanArgs &a, const ScanWork &sw, int load_mode, cudaStr
     w.status = sw.status;
     w.wait_limit = sw.wait_limit;
     w.chunk = reinterpret_cast<ulonglong2 *>(sw.records);
-    w.group = w.chunk + 2 * 32 * (g.width * g.chunks);
-    w.span = w.group + 2 * 32 * (g.width * (g.chunks / kGroup));
+    w.group = w.chunk + kTile * g.width * g.chunks;
+    w.span = w.group + kTile * g.width * (g.chunks / kGroup);
     const int64_t wave = wave_blocks(reinterpret_cast<const void *>(kernel), kThreads, smem);
     kernel<<<unsigned(g.places < wave ? g.places : wave), kThreads, smem, st>>>(a, w, g);
     return cudaGetLastError();
@@ -1043,7 +1085,7 @@ int64_t scan_record_bytes(int64_t batch, int64_t tokens, int64_t channels)
 {
     const int64_t width = batch * ((channels + kTile - 1) / kTile), chunks = (tokens + kChunk - 1) / kChunk;
     if (chunks == 1) return 0;
-    return width * 32 * 16 * (2 * chunks + 2 * (chunks / kGroup) + chunks / (kGroup * kGroup));
+    return width * kTile * int64_t(sizeof(ulonglong2)) * (chunks + chunks / kGroup + chunks / (kGroup * kGroup));
 }
 
 cudaError_t launch_scan(const ScanArgs &a, const ScanWork &w, cudaStream_t st) { return by_type<false>(a, w, st); }
