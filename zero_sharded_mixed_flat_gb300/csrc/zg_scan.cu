@@ -41,6 +41,7 @@ constexpr int kRun = kChunk / (2 * kWarps);  // tokens of a half warp
 constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 16;
 constexpr float kConst = -1.0f;
+
 // ------------------------------------------------------------------ arithmetic
 
 // Four channels of a lane, two to a packed operation.
@@ -555,13 +556,12 @@ struct Quarter {
 };
 
 // The chunks before a tile: what a thread waits for, which is four chunks and
-// four groups at one slot (and, for the last four, the span). All are asked
-// for when the tile is begun; where the blocks before are a round ahead, they
-// are there when the tile's own maps are.
+// four groups at one slot (and, for the last four, the span), all asked for
+// before the first is looked at.
 struct Before {
     Four chunks, groups;
     uint32_t in_group, group, first_group;
-    __device__ __forceinline__ Before(const Work &w, const Tile &t, const Grid &g)
+    __device__ __forceinline__ void ask(const Work &w, const Tile &t, const Grid &g)
     {
         const int slot = threadIdx.x % kTile, part = threadIdx.x / kTile;
         in_group = t.k % kGroup;
@@ -661,18 +661,21 @@ __device__ __forceinline__ float state1(const float *p, int64_t row, const ScanA
 
 // ------------------------------------------------------------------ forward
 
-// Buffers of x and dy per block in backward: with two, the next tile's copies
-// start as soon as a tile's maps are formed; with one (binary32, where two
-// would leave one block to an SM) when it is done.
-template <class T>
-constexpr int kBuffers = sizeof(T) == 4 ? 1 : 2;
+// Backward's buffers of x and dy per block: with two, the next tile's copies
+// start when a tile is begun; with one (binary32, where two would leave one block
+// to an SM) when it is done.
 template <class T, bool BWD>
-constexpr size_t kTileBytes = (BWD ? 2 * kBuffers<T> + 1 : 2) * kChunk * kTile * sizeof(T);
+constexpr int kBuffers = BWD && sizeof(T) == 2 ? 2 : 1;
+template <class T, bool BWD>
+constexpr size_t kTileBytes = (BWD ? 2 * kBuffers<T, BWD> + 1 : 2) * kChunk * kTile * sizeof(T);
 
-// A block's places. The second is taken when the first tile's copies are
-// there, when all blocks have begun and taken their first; from then on a place
-// is taken a tile ahead, in the shadow of a tile's work.
-template <bool BWD, class Sh>
+// A block's places. Where rows and tiles of channels alone fill the GPU
+// (EARLY) the next place is taken when a tile is begun, so that its copies can
+// start at once; a block's second place then waits for its first tile's copies,
+// when all blocks have begun and taken their first. Where blocks work side by
+// side on few rows, a place that is taken but not begun holds up every block
+// after it, so the next one is taken only when a tile waits for nothing more.
+template <bool BWD, bool EARLY, class Sh>
 struct Ahead {
     Sh &sh;
     Places places;
@@ -686,31 +689,45 @@ struct Ahead {
             sh.tag = uint32_t(taken >> 32);
         }
     }
-    // Before the barrier that opens a tile; sh.tile is then the one after it.
+    // Before the barrier that opens a tile.
     __device__ __forceinline__ void open(const Grid &g)
     {
-        if (threadIdx.x == 0 && !begun) sh.tile = tile_at<BWD>(places.take(g), g);
+        if (EARLY && threadIdx.x == 0 && !begun) sh.tile = tile_at<BWD>(places.take(g), g);
         begun = true;
     }
-    __device__ __forceinline__ void ask(const Tile &u, const Grid &g)
+    // Early: the tile after the one just opened, whose successor is asked for.
+    __device__ __forceinline__ Tile after_open(const Grid &g)
     {
+        const Tile u = sh.tile;
         if (threadIdx.x == 0 && u.valid) next = places.take(g);
+        return u;
     }
-    // After the last use of sh.tile.
-    __device__ __forceinline__ void close(const Tile &u, const Grid &g)
+    __device__ __forceinline__ void done(const Tile &u, const Grid &g)
     {
         if (threadIdx.x == 0 && u.valid) sh.tile = tile_at<BWD>(next, g);
     }
+    // Late: around the second pass.
+    __device__ __forceinline__ void ask(const Grid &g)
+    {
+        if (!EARLY && threadIdx.x == 0) next = places.take(g);
+    }
+    __device__ __forceinline__ Tile close(const Grid &g)
+    {
+        if (threadIdx.x == 0) sh.tile = tile_at<BWD>(next, g);
+        __syncthreads();
+        return sh.tile;
+    }
 };
 
-template <class T, bool VEC, bool PACKED>
+template <class T, bool VEC, bool PACKED, bool EARLY>
 __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, Grid g)
 {
     extern __shared__ __align__(16) unsigned char raw[];
-    T *const bf = reinterpret_cast<T *>(raw), *const bx = bf + kChunk * kTile;
+    constexpr int kSize = kChunk * kTile;
+    T *const bf = reinterpret_cast<T *>(raw), *const bx = bf + kSize;
     __shared__ Shared<false> sh;
     const int l = threadIdx.x & 15, run = threadIdx.x / 16;
-    Ahead<false, Shared<false>> ahead(sh, w, g);
+    Ahead<false, EARLY, Shared<false>> ahead(sh, w, g);
     __syncthreads();
     Tile t = sh.tile;
     const uint32_t tag = sh.tag;
@@ -732,9 +749,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
         wait_copies();
         ahead.open(g);
         __syncthreads();
-        const Tile u = sh.tile;
-        ahead.ask(u, g);
-        Before before(w, t, g);
+        Tile u;
+        if (EARLY) u = ahead.after_open(g);
+        Before before;
+        if (EARLY) before.ask(w, t, g);
         Marks mk{0u, 0u};
         if (PACKED) {
             find_cuts(sh.cuts, a, t, n, a.h0, a.h_last);
@@ -761,15 +779,19 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
                 if (!PACKED || m.a.lo.x >= 0.0f) m.a = mul(keep[i], m.a);
             }
         }
+        if (!EARLY) before.ask(w, t, g);
         sts4(&sh.runs.a[run][4 * l], m.a);
         sts4(&sh.runs.b[run][4 * l], m.b);
         __syncthreads();
-        if (u.valid) {
-            start_copy(bf, a.f, u, a, g.load_mode);
-            start_copy(bx, a.x, u, a, g.load_mode);
+        if (EARLY) {
+            if (u.valid) {
+                start_copy(bf, a.f, u, a, g.load_mode);
+                start_copy(bx, a.x, u, a, g.load_mode);
+            }
+            commit_copies();
         }
-        commit_copies();
         solve<PACKED>(sh, before, w, t, g, tag, start);
+        ahead.ask(g);
         F4 h = lds4(&sh.runs.b[run][4 * l]);
         if (a.states && run == 0)
             put_state4<VEC>(a.states + (t.row * g.chunks + t.chunk) * a.channels + t.ch, l, n, h);
@@ -785,23 +807,32 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
                 put_state4<VEC>(a.h_last + (PACKED ? int64_t(sh.cuts.last[run * kRun + i]) : int64_t(t.row)) * a.channels + t.ch,
                                 l, n, h);
         }
-        ahead.close(u, g);
-        t = u;
+        if (EARLY) {
+            ahead.done(u, g);
+            t = u;
+        } else {
+            t = ahead.close(g);
+            if (t.valid) {
+                start_copy(bf, a.f, t, a, g.load_mode);
+                start_copy(bx, a.x, t, a, g.load_mode);
+            }
+            commit_copies();
+        }
     }
 }
 
 // ------------------------------------------------------------------ backward
 
-template <class T, bool VEC, bool PACKED>
+template <class T, bool VEC, bool PACKED, bool EARLY>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work w, Grid g)
 {
     extern __shared__ __align__(16) unsigned char raw[];
     constexpr int kSize = kChunk * kTile;
-    constexpr bool kTwo = kBuffers<T> == 2;
+    constexpr bool kTwo = kBuffers<T, true> == 2;
     T *const bf = reinterpret_cast<T *>(raw), *bx = bf + kSize, *other = kTwo ? bx + 2 * kSize : bx;  // dy behind x
     __shared__ Shared<true> sh;
     const int l = threadIdx.x & 15, run = threadIdx.x / 16;
-    Ahead<true, Shared<true>> ahead(sh, w, g);
+    Ahead<true, EARLY, Shared<true>> ahead(sh, w, g);
     __syncthreads();
     Tile t = sh.tile;
     const uint32_t tag = sh.tag;
@@ -827,12 +858,15 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
         wait_copies();
         ahead.open(g);
         __syncthreads();
-        const Tile u = sh.tile;
-        ahead.ask(u, g);
-        Before before(w, t, g);
-        if (kTwo && u.valid) {
-            start_copy(other, a.x, u, a, g.load_mode);
-            start_copy(other + kSize, a.y, u, a, g.load_mode);
+        Tile u;
+        Before before;
+        if (EARLY) before.ask(w, t, g);
+        if (EARLY) {
+            u = ahead.after_open(g);
+            if (u.valid) {
+                start_copy(other, a.x, u, a, g.load_mode);
+                start_copy(other + kSize, a.y, u, a, g.load_mode);
+            }
         }
         Marks mk{0u, 0u};
         if (PACKED) {
@@ -878,13 +912,16 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
             }
         }
         r.a = cut ? all(kConst) : weight;
+        if (!EARLY) before.ask(w, t, g);
         sts4(&sh.fwd.a[run][4 * l], m.a);
         sts4(&sh.fwd.b[run][4 * l], m.b);
         sts4(&sh.runs.a[kRuns - 1 - run][4 * l], r.a);
         sts4(&sh.runs.b[kRuns - 1 - run][4 * l], r.b);
         __syncthreads();
-        if (u.valid) start_copy(bf, a.f, u, a, g.load_mode);
-        if (kTwo) commit_copies();
+        if (EARLY) {
+            if (u.valid) start_copy(bf, a.f, u, a, g.load_mode);
+            commit_copies();
+        }
         {
             const int slot = threadIdx.x % kTile, part = threadIdx.x / kTile;
             Quarter q;
@@ -896,6 +933,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
             q.run<PACKED>(sh.fwd, part, slot, h);
         }
         solve<PACKED>(sh, before, w, t, g, tag, start);
+        ahead.ask(g);
         F4 h = lds4(&sh.fwd.b[run][4 * l]), gr = lds4(&sh.runs.b[kRuns - 1 - run][4 * l]);
         // forward once more, for h_{t-1} - x_t
         F4 over[kRun];
@@ -929,17 +967,18 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
             pf -= a.df.st;
         }
         if (!PACKED && a.dh0 && t0 == 0) put_state4<VEC>(a.dh0 + t.row * a.channels + t.ch, l, n, gr);
-        ahead.close(u, g);
-        t = u;
-        if (kTwo) {
+        if (EARLY) {
+            ahead.done(u, g);
+            t = u;
             T *const swap = bx;
             bx = other;
             other = swap;
         } else {
-            __syncthreads();
-            if (u.valid) {
-                start_copy(bx, a.x, u, a, g.load_mode);
-                start_copy(bx + kSize, a.y, u, a, g.load_mode);
+            t = ahead.close(g);
+            if (t.valid) {
+                start_copy(bf, a.f, t, a, g.load_mode);
+                start_copy(bx, a.x, t, a, g.load_mode);
+                start_copy(bx + kSize, a.y, t, a, g.load_mode);
             }
             commit_copies();
         }
@@ -1019,17 +1058,21 @@ bool fours(const ScanView &v, int size, int64_t channels)
     return channels % 4 == 0 && bits % (4 * size) == 0;
 }
 
-template <class T, bool VEC, bool PACKED, bool BWD>
-cudaError_t launch(const ScanArgs &a, const ScanWork &sw, int load_mode, cudaStream_t st)
+Grid grid_of(const ScanArgs &a, int load_mode)
 {
-    auto *kernel = BWD ? &scan_bwd_kernel<T, VEC, PACKED> : &scan_kernel<T, VEC, PACKED>;
-    constexpr size_t smem = kTileBytes<T, BWD>;
     Grid g{};
     g.tiles = (a.channels + kTile - 1) / kTile;
     g.width = a.batch * g.tiles;
     g.chunks = (a.tokens + kChunk - 1) / kChunk;
     g.places = g.width * g.chunks;
     g.load_mode = load_mode;
+    return g;
+}
+
+template <class T, bool BWD, class Kernel>
+cudaError_t launch(Kernel *kernel, const ScanArgs &a, const ScanWork &sw, const Grid &g, cudaStream_t st)
+{
+    constexpr size_t smem = kTileBytes<T, BWD>;
     if (g.places >= int64_t(0xf0000000)) return cudaErrorInvalidConfiguration;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
@@ -1043,6 +1086,24 @@ cudaError_t launch(const ScanArgs &a, const ScanWork &sw, int load_mode, cudaStr
     const int64_t wave = wave_blocks(reinterpret_cast<const void *>(kernel), kThreads, smem);
     kernel<<<unsigned(g.places < wave ? g.places : wave), kThreads, smem, st>>>(a, w, g);
     return cudaGetLastError();
+}
+
+template <class T, bool VEC, bool PACKED, bool BWD>
+cudaError_t choose(const ScanArgs &a, const ScanWork &sw, int load_mode, cudaStream_t st)
+{
+    const Grid g = grid_of(a, load_mode);
+    // Measured in bf16, places a tile ahead against at the end of a tile: 192
+    // tiles to a chunk (8 x 4096 x 1536) 78 against 95 us, 96 tiles
+    // (8 x 1024 x 768) the same, 12 tiles (1 x 65536 x 768) 138 against 115.
+    const bool early = g.width >= 128;
+    if constexpr (BWD) {
+        if constexpr (kBuffers<T, true> == 2)
+            if (early) return launch<T, BWD>(&scan_bwd_kernel<T, VEC, PACKED, true>, a, sw, g, st);
+        return launch<T, BWD>(&scan_bwd_kernel<T, VEC, PACKED, false>, a, sw, g, st);
+    } else {
+        if (early) return launch<T, BWD>(&scan_kernel<T, VEC, PACKED, true>, a, sw, g, st);
+        return launch<T, BWD>(&scan_kernel<T, VEC, PACKED, false>, a, sw, g, st);
+    }
 }
 
 template <class T, bool BWD>
@@ -1069,8 +1130,8 @@ cudaError_t pick(const ScanArgs &a, const ScanWork &w, cudaStream_t st)
         mode = mode < unit_of(a.y, size) ? mode : unit_of(a.y, size);
         vec = vec && fours(a.dx, size, a.channels) && fours(a.df, size, a.channels);
     }
-    if (a.seq_start) return vec ? launch<T, true, true, BWD>(a, w, mode, st) : launch<T, false, true, BWD>(a, w, mode, st);
-    return vec ? launch<T, true, false, BWD>(a, w, mode, st) : launch<T, false, false, BWD>(a, w, mode, st);
+    if (a.seq_start) return vec ? choose<T, true, true, BWD>(a, w, mode, st) : choose<T, false, true, BWD>(a, w, mode, st);
+    return vec ? choose<T, true, false, BWD>(a, w, mode, st) : choose<T, false, false, BWD>(a, w, mode, st);
 }
 
 template <bool BWD>
