@@ -450,7 +450,7 @@ int zg_scan_set_wait_limit(zg_scan *scan, int64_t polls);
  * and their indices (rows x k), contiguous, largest first. Equal values go to
  * the lowest index first; -0 equals +0; a NaN of either sign counts as larger than
  * every number, and NaNs as equal to one another. Row r starts at
- * logits + r * row_stride elements. 1 <= k <= ZG_TOPK_MAX, k <= vocab < 2^31,
+ * logits + r * row_stride elements. 1 <= k <= ZG_TOPK_MAX, k <= vocab <= 2^30,
  * row_stride >= vocab. The teacher's half of the distillation below. */
 #define ZG_TOPK_MAX 256
 int zg_topk(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride, int k, void *values,
@@ -470,7 +470,7 @@ int zg_topk(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t 
  * q = 0. Entries may come in any order; a repeated index adds up. */
 typedef struct {
     const void *logits; /* row r starts at logits + r * row_stride elements; aligned to its element */
-    int64_t rows, vocab, row_stride; /* vocab < 2^31, row_stride >= vocab */
+    int64_t rows, vocab, row_stride; /* vocab <= 2^30, row_stride >= vocab */
     int dtype;                       /* of logits and dlogits */
     const void *t_logits;            /* rows x k, contiguous */
     const int32_t *t_index;          /* rows x k, contiguous */

@@ -53,20 +53,34 @@ __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b)
     return *reinterpret_cast<const float2 *>(&d);
 }
 
-// A sum of exponentials as sum 2^((z - top) c), c = log2(e) / T, with top the
-// largest z seen: differences first, so that rows of a type's lowest value
-// neither overflow nor count as masked.
+// A sum of exponentials as sum 2^((v - top) c), with top the largest v seen:
+// differences first, so that rows of a type's lowest value neither overflow nor
+// count as masked. Nothing but -inf gives top = -inf and sum = 0; a NaN or +inf
+// makes the sum NaN.
 struct Sum {
     float top, sum;
 };
 __device__ __forceinline__ Sum none() { return Sum{-INFINITY, 0.0f}; }
-// An empty part (top = -inf) adds nothing; a NaN or +inf makes the sum NaN.
+__device__ __forceinline__ float rescaled(Sum s, float top, float c)
+{
+    return s.top == -INFINITY ? 0.0f : s.sum * exp2_approx((s.top - top) * c);
+}
 __device__ __forceinline__ Sum join(Sum a, Sum b, float c)
 {
     const float top = max_nan(a.top, b.top);
-    const float sa = a.top == -INFINITY ? 0.0f : a.sum * exp2_approx((a.top - top) * c);
-    const float sb = b.top == -INFINITY ? 0.0f : b.sum * exp2_approx((b.top - top) * c);
-    return Sum{top, sa + sb};
+    return Sum{top, rescaled(a, top, c) + rescaled(b, top, c)};
+}
+// Over WIDTH neighbouring lanes, the same in all of them.
+template <int WIDTH>
+__device__ __forceinline__ Sum across(Sum s, float c)
+{
+    float top = s.top;
+#pragma unroll
+    for (int o = WIDTH / 2; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float sum = rescaled(s, top, c);
+#pragma unroll
+    for (int o = WIDTH / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return Sum{top, sum};
 }
 
 // Sixteen bytes of logits: eight bf16 or four binary32.
@@ -76,6 +90,18 @@ template <>
 struct Unit<uint16_t> {
     static constexpr int kN = 8;
     uint4 w;
+    // Running maxima of the low and the high halves.
+    struct Top {
+        uint32_t m = 0xff80ff80u;  // -inf
+        __device__ __forceinline__ void add(const Unit &x) { m = max2(max2(m, max2(x.w.x, x.w.y)), max2(x.w.z, x.w.w)); }
+        __device__ __forceinline__ float get() const { return max_nan(bf16_lo(m), bf16_hi(m)); }
+        __device__ static __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+        {
+            uint32_t d;
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+            return d;
+        }
+    };
     __device__ __forceinline__ void get(float2 (&v)[4]) const
     {
         v[0] = make_float2(bf16_lo(w.x), bf16_hi(w.x));
@@ -93,6 +119,15 @@ template <>
 struct Unit<float> {
     static constexpr int kN = 4;
     uint4 w;
+    struct Top {
+        float m = -INFINITY;
+        __device__ __forceinline__ void add(const Unit &x)
+        {
+            m = max_nan(max_nan(m, max_nan(__uint_as_float(x.w.x), __uint_as_float(x.w.y))),
+                        max_nan(__uint_as_float(x.w.z), __uint_as_float(x.w.w)));
+        }
+        __device__ __forceinline__ float get() const { return m; }
+    };
     __device__ __forceinline__ void get(float2 (&v)[2]) const
     {
         v[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
@@ -104,69 +139,57 @@ struct Unit<float> {
     }
 };
 
-// A unit's logits joined to a thread's running sum.
-template <int N>
-__device__ __forceinline__ void take_in(const float2 (&v)[N], float c, Sum &s)
+// Raises a running sum's top, and adds a unit's logits under it.
+__device__ __forceinline__ void raise(Sum &s, float top, float c)
 {
-    float top = s.top;
-#pragma unroll
-    for (int i = 0; i < N; ++i) top = max_nan(top, max_nan(v[i].x, v[i].y));
-    if (top == -INFINITY) return;  // nothing but masked logits so far
+    top = max_nan(s.top, top);
     if (top != s.top) {
-        s.sum = s.top == -INFINITY ? 0.0f : s.sum * exp2_approx((s.top - top) * c);
+        s.sum = rescaled(s, top, c);
         s.top = top;
     }
-    float2 part = make_float2(0.0f, 0.0f);
+}
+template <class T>
+__device__ __forceinline__ float2 add_under(float2 part, const Unit<T> &x, float top, float c)
+{
+    float2 v[Unit<T>::kN / 2];
+    x.get(v);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < Unit<T>::kN / 2; ++i) {
         const float2 t = mul_f32x2(add_f32x2(v[i], make_float2(-top, -top)), make_float2(c, c));
         part = add_f32x2(part, make_float2(exp2_approx(t.x), exp2_approx(t.y)));
     }
-    s.sum += part.x + part.y;
+    return part;
 }
 
 template <int THREADS>
 struct Shared {
-    Sum warps[THREADS / 32];
+    Sum student[THREADS / 32], teacher[THREADS / 32];
     float red[THREADS / 32];
     Sum block;  // this block's part, read by the others of its row
-    // the teacher's entries: weight, index (-1: absent), the student's logit
-    float p[ZG_TOPK_MAX], z[ZG_TOPK_MAX];
+    // the teacher's entries: exponential, and index (-1: absent)
+    float e[ZG_TOPK_MAX];
     __align__(16) int at[ZG_TOPK_MAX];
 };
 
-template <int WARPS, class Op>
-__device__ __forceinline__ float block_fold(float v, float *red, Op op)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
-    __syncthreads();
-    v = red[threadIdx.x % WARPS];
-#pragma unroll
-    for (int o = WARPS / 2; o; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-    __syncthreads();
-    return v;
-}
-
-// The parts of a row. Elements are counted from the 16-byte boundary at or
-// below the row's first: the row is [head, head + vocab), units [lo, hi) are a
-// block's, and its elements [first, last).
+// A block's part of a row. Elements are counted from the 16-byte boundary at
+// or below the row's first, so the row is [head, head + vocab); the part is the
+// elements [first, last), and units [u0, u1) are whole in it.
 struct Part {
-    int head;
-    int64_t lo, hi, first, last;
+    int head, lo, first, last, u0, u1;
 };
 template <class T>
-__device__ __forceinline__ Part part_of(const T *row, int vocab, int blocks, int rank)
+__device__ __forceinline__ Part part_of(const T *row, int vocab, int each, int rank)
 {
     constexpr int N = Unit<T>::kN;
     Part p;
     p.head = int((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
-    const int64_t units = (int64_t(p.head) + vocab + N - 1) / N, each = (units + blocks - 1) / blocks;
-    p.lo = rank * each < units ? rank * each : units;
-    p.hi = p.lo + each < units ? p.lo + each : units;
-    p.first = p.lo * N > p.head ? p.lo * N : p.head;
-    p.last = p.hi * N < p.head + int64_t(vocab) ? p.hi * N : p.head + int64_t(vocab);
+    const int end = p.head + vocab;  // vocab is at most 2^30
+    p.lo = rank * each;
+    p.first = max(min(p.lo * N, end), p.head);
+    p.last = p.lo + each < (end + N - 1) / N ? (p.lo + each) * N : end;
+    p.last = max(p.last, p.first);
+    p.u0 = (p.first + N - 1) / N;
+    p.u1 = max(p.last / N, p.u0);
     return p;
 }
 
@@ -184,7 +207,7 @@ __device__ __forceinline__ void wait_copies()
 
 // Sixteen bytes from element i of `base`, which is aligned to its units only,
 // by whole words: up to one element before and after them is read too.
-__device__ __forceinline__ void read_shifted(const uint16_t *base, int64_t i, Unit<uint16_t> &x)
+__device__ __forceinline__ void read_shifted(const uint16_t *base, int i, Unit<uint16_t> &x)
 {
     const uint32_t *w = reinterpret_cast<const uint32_t *>(base) + (i >> 1);
     x.w = make_uint4(w[0], w[1], w[2], w[3]);
@@ -194,7 +217,7 @@ __device__ __forceinline__ void read_shifted(const uint16_t *base, int64_t i, Un
                          __funnelshift_r(x.w.z, x.w.w, 16), __funnelshift_r(x.w.w, last, 16));
     }
 }
-__device__ __forceinline__ void read_shifted(const float *base, int64_t i, Unit<float> &x)
+__device__ __forceinline__ void read_shifted(const float *base, int i, Unit<float> &x)
 {
     const uint32_t *w = reinterpret_cast<const uint32_t *>(base) + i;
     x.w = make_uint4(w[0], w[1], w[2], w[3]);
@@ -203,141 +226,127 @@ __device__ __forceinline__ void read_shifted(const float *base, int64_t i, Unit<
 constexpr int kStages = 4;
 
 // KEEP: the part is copied into shared memory, in kStages groups, and both
-// passes read it there; else each reads it from memory (L2). Without LOSS, lse
-// is given. A row takes `blocks` blocks: a cluster where they exchange sums.
+// passes read it there; else the one pass reads it from memory. Without LOSS,
+// lse is given. A row takes `blocks` blocks of `each` units: with LOSS a cluster,
+// in which they exchange sums.
 template <class T, class E, bool LOSS, bool GRAD, bool KEEP, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(DistillArgs a, int blocks)
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(DistillArgs a, int blocks, int each)
 {
     extern __shared__ __align__(16) unsigned char raw[];
     __shared__ Shared<THREADS> sh;
-    constexpr int N = Unit<T>::kN, kWarps = THREADS / 32;
+    constexpr int N = Unit<T>::kN, kWarps = THREADS / 32, kEntries = (ZG_TOPK_MAX + THREADS - 1) / THREADS;
     const int tid = threadIdx.x;
     const int64_t r = blockIdx.x / unsigned(blocks);
     const int rank = int(blockIdx.x % unsigned(blocks));
     const T *const z = static_cast<const T *>(a.logits) + r * a.row_stride;
     const float rt = 1.0f / a.temperature, c = rt * kLog2e;
-    const Part part = part_of(z, a.vocab, blocks, rank);
+    const Part part = part_of(z, a.vocab, each, rank);
     const T *const base = z - part.head;  // only elements [head, head + vocab) are touched
-    const int64_t u0 = (part.first + N - 1) / N, u1 = part.last / N;  // whole units; the ends are ragged
-    const uint4 *const from = reinterpret_cast<const uint4 *>(base);
-    Unit<T> *const kept = reinterpret_cast<Unit<T> *>(raw) - part.lo;
-    const int per_stage = int((u1 - u0 + THREADS * kStages - 1) / (THREADS * kStages)) * THREADS;
+    const uint4 *const from = reinterpret_cast<const uint4 *>(base) + part.u0;
+    Unit<T> *const kept = reinterpret_cast<Unit<T> *>(raw);  // unit u0 + i at kept[i]
+    const int units = part.u1 - part.u0;
+    const int stage = (units + THREADS * kStages - 1) / (THREADS * kStages) * THREADS;
 
     if (KEEP) {
 #pragma unroll
         for (int g = 0; g < kStages; ++g) {
-            for (int64_t u = u0 + g * per_stage + tid; u < u1 && u < u0 + (g + 1) * per_stage; u += THREADS)
-                copy_async(&kept[u], from + u);
+            const int end = min((g + 1) * stage, units);
+            for (int u = g * stage + tid; u < end; u += THREADS) copy_async(&kept[u], from + u);
             commit_copies();
         }
     }
-
-    // The teacher's entries, and the logits at them before anything is written
-    // over those: a block needs those of its part for their gradients, the first
-    // block all for the loss.
-    float tm = -INFINITY;
-    for (int j = tid; j < ZG_TOPK_MAX; j += THREADS) {
-        int at = -1;
-        float t = -INFINITY, zt = 0.0f;
+    // The teacher's entries, one or two to a thread, and the logits at them
+    // before anything is written over those.
+    int at[kEntries];
+    float te[kEntries], zt[kEntries];
+#pragma unroll
+    for (int n = 0; n < kEntries; ++n) {
+        const int j = tid + n * THREADS;
+        at[n] = -1;
+        te[n] = -INFINITY;
+        zt[n] = 0.0f;
         if (j < a.k) {
-            at = a.t_index[r * a.k + j];
-            if (at < 0 || at >= a.vocab) at = -1;
-            if (at >= 0) {
-                t = load1(static_cast<const E *>(a.t_logits) + r * a.k + j) * rt;
-                zt = load1(z + at);
+            at[n] = a.t_index[r * a.k + j];
+            if (at[n] < 0 || at[n] >= a.vocab) at[n] = -1;
+            if (at[n] >= 0) {
+                te[n] = load1(static_cast<const E *>(a.t_logits) + r * a.k + j);
+                zt[n] = load1(z + at[n]);
             }
         }
-        sh.at[j] = at;
-        sh.p[j] = t;
-        sh.z[j] = zt;
-        tm = max_nan(tm, t);
     }
-    tm = block_fold<kWarps>(tm, sh.red, [](float x, float y) { return max_nan(x, y); });
-    if (tm == -INFINITY) {  // a row without entries: the same in every block of it
-        if (KEEP) wait_copies<0>();
-        if (LOSS && rank == 0 && tid == 0) {
-            a.loss[r] = 0.0f;
-            if (a.lse) a.lse[r] = 0.0f;
-        }
-        if (GRAD) {
-            T *const dz = static_cast<T *>(a.dlogits) + r * a.drow_stride - part.head;
-            if ((reinterpret_cast<uintptr_t>(dz) & 15u) == 0) {
-                for (int64_t u = u0 + tid; u < u1; u += THREADS)
-                    __stcs(reinterpret_cast<uint4 *>(dz) + u, make_uint4(0u, 0u, 0u, 0u));
-                for (int64_t i = part.first + tid; i < part.last && i < u0 * N; i += THREADS) store1(dz + i, 0.0f);
-                for (int64_t i = (u1 > u0 ? u1 : u0) * N + tid; i < part.last; i += THREADS) store1(dz + i, 0.0f);
-            } else {
-                for (int64_t i = part.first + tid; i < part.last; i += THREADS) store1(dz + i, 0.0f);
-            }
-        }
-        return;
-    }
-    float mine = 0.0f;
-    for (int j = tid; j < a.k; j += THREADS) {
-        const float e = sh.at[j] >= 0 ? exp2_approx((sh.p[j] - tm) * kLog2e) : 0.0f;
-        mine += e;
-        if (!LOSS) sh.p[j] = e;
-    }
-    const float total = block_fold<kWarps>(mine, sh.red, [](float x, float y) { return x + y; });
 
-    float lse;
+    Sum s = none();
+    if (LOSS && KEEP) {
+#pragma unroll
+        for (int g = 0; g < kStages; ++g) {
+            if (g == 0) wait_copies<3>();
+            if (g == 1) wait_copies<2>();
+            if (g == 2) wait_copies<1>();
+            if (g == 3) wait_copies<0>();
+            // a thread reads what it copied itself: first for its largest, then for the sum
+            const int begin = g * stage + tid, end = min((g + 1) * stage, units);
+            typename Unit<T>::Top top;
+#pragma unroll 2
+            for (int u = begin; u < end; u += THREADS) top.add(kept[u]);
+            raise(s, top.get(), c);
+            if (s.top == -INFINITY) continue;  // nothing but masked logits so far
+            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll 2
+            for (int u = begin; u < end; u += THREADS) sum = add_under(sum, kept[u], s.top, c);
+            s.sum += sum.x + sum.y;
+        }
+    }
+    if (LOSS && !KEEP) {
+        for (int u = tid; u < units; u += kAhead * THREADS) {
+            Unit<T> x[kAhead];
+            typename Unit<T>::Top top;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (u + i * THREADS < units) x[i].w = from[u + i * THREADS];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (u + i * THREADS < units) top.add(x[i]);
+            raise(s, top.get(), c);
+            if (s.top == -INFINITY) continue;
+            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (u + i * THREADS < units) sum = add_under(sum, x[i], s.top, c);
+            s.sum += sum.x + sum.y;
+        }
+    }
+    if (LOSS) {  // the ragged ends: fewer elements than a unit each
+        const int head_end = min(part.u0 * N, part.last), tail = max(part.u1 * N, head_end);
+        int i = -1;
+        if (part.first + tid < head_end) i = part.first + tid;
+        if (tid >= 32 && tail + tid - 32 < part.last) i = tail + tid - 32;
+        if (i >= 0) {
+            const float v = load1(base + i);
+            s = join(s, Sum{v, v == -INFINITY ? 0.0f : v - v + 1.0f}, c);
+        }
+    }
+    // one barrier for both sums, the student's and the teacher's
+    {
+        Sum t = none();
+#pragma unroll
+        for (int n = 0; n < kEntries; ++n) {
+            const int j = tid + n * THREADS;
+            if (j < ZG_TOPK_MAX) sh.at[j] = at[n];
+            t = join(t, Sum{te[n], te[n] == -INFINITY ? 0.0f : te[n] - te[n] + 1.0f}, c);
+        }
+        t = across<32>(t, c);
+        if (LOSS) s = across<32>(s, c);
+        if (tid % 32 == 0) {
+            sh.teacher[tid / 32] = t;
+            if (LOSS) sh.student[tid / 32] = s;
+        }
+    }
+    __syncthreads();
+    const Sum t = across<kWarps>(sh.teacher[tid % kWarps], c);
+    const bool empty = t.top == -INFINITY;
+    float lse = 0.0f;
     if (LOSS) {
-        Sum s = none();
-        if (KEEP) {
-#pragma unroll
-            for (int g = 0; g < kStages; ++g) {
-                if (g == 0) wait_copies<3>();
-                if (g == 1) wait_copies<2>();
-                if (g == 2) wait_copies<1>();
-                if (g == 3) wait_copies<0>();
-                // a thread reads what it copied itself
-                for (int64_t u = u0 + g * per_stage + tid; u < u1 && u < u0 + (g + 1) * per_stage; u += THREADS) {
-                    float2 v[N / 2];
-                    kept[u].get(v);
-                    take_in(v, c, s);
-                }
-            }
-        } else {
-            int64_t u = u0 + tid;
-            for (; u + (kAhead - 1) * THREADS < u1; u += kAhead * THREADS) {
-                Unit<T> x[kAhead];
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) x[i].w = from[u + i * THREADS];
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    float2 v[N / 2];
-                    x[i].get(v);
-                    take_in(v, c, s);
-                }
-            }
-            for (; u < u1; u += THREADS) {
-                Unit<T> x;
-                x.w = from[u];
-                float2 v[N / 2];
-                x.get(v);
-                take_in(v, c, s);
-            }
-        }
-        {  // the ragged ends
-            const int64_t head_end = u0 * N < part.last ? u0 * N : part.last;
-            const int64_t tail = u1 * N > head_end ? u1 * N : head_end;
-            int64_t i = -1;
-            if (part.first + tid < head_end) i = part.first + tid;
-            if (tid >= 32 && tail + tid - 32 < part.last) i = tail + tid - 32;
-            if (i >= 0) {
-                const float v = load1(base + i);
-                s = join(s, Sum{v, v == -INFINITY ? 0.0f : v - v + 1.0f}, c);
-            }
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-            s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.top, o), __shfl_xor_sync(0xffffffffu, s.sum, o)}, c);
-        if (tid % 32 == 0) sh.warps[tid / 32] = s;
-        __syncthreads();
-        s = sh.warps[tid % kWarps];
-#pragma unroll
-        for (int o = kWarps / 2; o; o >>= 1)
-            s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.top, o), __shfl_xor_sync(0xffffffffu, s.sum, o)}, c);
+        s = across<kWarps>(sh.student[tid % kWarps], c);
         if (blocks > 1) {
             cg::cluster_group cluster = cg::this_cluster();
             if (tid == 0) sh.block = s;
@@ -349,109 +358,129 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
         const float log_sum = logf(s.sum);
         lse = fmaf(s.top, rt, log_sum);
         if (rank == 0) {
-            // p_j = 0 leaves its term out; a NaN stays
+            // p = 0 leaves its term out; a NaN stays
             float term = 0.0f;
-            const float log_total = logf(total);
-            for (int j = tid; j < a.k; j += THREADS) {
-                const float t = sh.p[j] - tm, p = sh.at[j] >= 0 ? exp2_approx(t * kLog2e) / total : 0.0f;
-                if (p != 0.0f) term += p * ((t - log_total) - ((sh.z[j] - s.top) * rt - log_sum));
+            const float log_total = logf(t.sum);
+#pragma unroll
+            for (int n = 0; n < kEntries; ++n) {
+                const float d = te[n] - t.top, p = at[n] >= 0 ? exp2_approx(d * c) / t.sum : 0.0f;
+                if (p != 0.0f) term += p * ((d * rt - log_total) - ((zt[n] - s.top) * rt - log_sum));
             }
-            const float loss = block_fold<kWarps>(term, sh.red, [](float x, float y) { return x + y; });
-            if (tid == 0) {
-                a.loss[r] = a.temperature * a.temperature * loss;
-                if (a.lse) a.lse[r] = lse;
-            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
+            if (tid % 32 == 0) sh.red[tid / 32] = term;
         }
-        if (GRAD) {
-            for (int j = tid; j < a.k; j += THREADS) sh.p[j] = sh.at[j] >= 0 ? exp2_approx((sh.p[j] - tm) * kLog2e) : 0.0f;
-            __syncthreads();
-        }
-    } else {
+        if (rank == 0 && tid == 0 && a.lse) a.lse[r] = empty ? 0.0f : lse;
+    } else if (!empty) {
         lse = a.lse_in[r];
     }
-    if (!GRAD) return;
-
-    const float g = a.scale * a.temperature * (a.dloss ? a.dloss[r] : 1.0f);
-    T *const dz = static_cast<T *>(a.dlogits) + r * a.drow_stride - part.head;
-    auto gradient = [&](Unit<T> &x) {
-        float2 v[N / 2];
-        x.get(v);
+    if (GRAD) {
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            const float2 q = mul_f32x2(fma_f32x2(v[i], make_float2(rt, rt), make_float2(-lse, -lse)), make_float2(kLog2e, kLog2e));
-            v[i] = mul_f32x2(make_float2(exp2_approx(q.x), exp2_approx(q.y)), make_float2(g, g));
+        for (int n = 0; n < kEntries; ++n) {
+            const int j = tid + n * THREADS;
+            if (j < ZG_TOPK_MAX) sh.e[j] = at[n] >= 0 ? exp2_approx((te[n] - t.top) * c) : 0.0f;
         }
-        x.set(v);
-    };
-    const int phase = int((reinterpret_cast<uintptr_t>(dz) & 15u) / sizeof(T));
-    int64_t i0, i1;  // what is written in whole units
-    if (phase == 0) {
-        uint4 *const to = reinterpret_cast<uint4 *>(dz);
-        i0 = u0 * N;
-        i1 = (u1 > u0 ? u1 : u0) * N;
-        int64_t u = u0 + tid;
-        if (!KEEP)
-            for (; u + (kAhead - 1) * THREADS < u1; u += kAhead * THREADS) {
-                Unit<T> x[kAhead];
+        const float g = a.scale * a.temperature * (a.dloss ? a.dloss[r] : 1.0f);
+        T *const dz = static_cast<T *>(a.dlogits) + r * a.drow_stride - part.head;
+        auto gradient1 = [&](float v) { return empty ? 0.0f : exp2_approx(fmaf(v, rt, -lse) * kLog2e) * g; };
+        auto gradient = [&](Unit<T> &x) {
+            if (empty) {
+                x.w = make_uint4(0u, 0u, 0u, 0u);
+                return;
+            }
+            float2 v[N / 2];
+            x.get(v);
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) x[i].w = from[u + i * THREADS];
+            for (int i = 0; i < N / 2; ++i) {
+                const float2 q = mul_f32x2(fma_f32x2(v[i], make_float2(rt, rt), make_float2(-lse, -lse)), make_float2(kLog2e, kLog2e));
+                v[i] = mul_f32x2(make_float2(exp2_approx(q.x), exp2_approx(q.y)), make_float2(g, g));
+            }
+            x.set(v);
+        };
+        const int phase = int((reinterpret_cast<uintptr_t>(dz) & 15u) / sizeof(T));
+        int i0, i1;  // what is written in whole units
+        if (phase == 0) {
+            uint4 *const to = reinterpret_cast<uint4 *>(dz) + part.u0;
+            i0 = part.u0 * N;
+            i1 = part.u1 * N;
+            if (KEEP) {
+#pragma unroll 2
+                for (int u = tid; u < units; u += THREADS) {
+                    Unit<T> x = kept[u];
+                    gradient(x);
+                    __stcs(to + u, x.w);
+                }
+            } else {
+                int u = tid;
+                for (; u + (kAhead - 1) * THREADS < units; u += kAhead * THREADS) {
+                    Unit<T> x[kAhead];
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    gradient(x[i]);
-                    __stcs(to + u + i * THREADS, x[i].w);
+                    for (int i = 0; i < kAhead; ++i) x[i].w = from[u + i * THREADS];
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) {
+                        gradient(x[i]);
+                        __stcs(to + u + i * THREADS, x[i].w);
+                    }
+                }
+                for (; u < units; u += THREADS) {
+                    Unit<T> x;
+                    x.w = from[u];
+                    gradient(x);
+                    __stcs(to + u, x.w);
                 }
             }
-        for (; u < u1; u += THREADS) {
-            Unit<T> x;
-            if (KEEP)
-                x = kept[u];
-            else
-                x.w = from[u];
-            gradient(x);
-            __stcs(to + u, x.w);
+        } else {
+            // the output's units lie across the input's: whole ones of the output,
+            // read a word at a time, with an element to spare at both ends
+            i0 = (part.u0 * N + 1 + phase + N - 1) / N * N - phase;
+            i1 = max((part.u1 * N - 1 + phase) / N * N - phase, i0);
+            const T *const src = KEEP ? reinterpret_cast<const T *>(kept) - part.u0 * N : base;
+            for (int i = i0 + tid * N; i < i1; i += THREADS * N) {
+                Unit<T> x;
+                read_shifted(src, i, x);
+                gradient(x);
+                __stcs(reinterpret_cast<uint4 *>(dz + i), x.w);
+            }
+        }
+        // the rest, less than two units at either end
+        i0 = min(i0, part.last);
+        i1 = min(i1, part.last);
+        if (part.first + tid < i0) store1(dz + part.first + tid, gradient1(load1(base + part.first + tid)));
+        if (i1 + tid < part.last) store1(dz + i1 + tid, gradient1(load1(base + i1 + tid)));
+        __syncthreads();
+        // The entries of this part; the first of a repeated index answers for all.
+#pragma unroll
+        for (int n = 0; n < kEntries; ++n) {
+            const int j = tid + n * THREADS, i = part.head + at[n];
+            if (empty || at[n] < 0 || i < part.first || i >= part.last) continue;
+            float sum = 0.0f;
+            bool write = true;
+            for (int m = 0; m < a.k; m += 4) {
+                const int4 other = *reinterpret_cast<const int4 *>(&sh.at[m]);
+                if (other.x == at[n]) sum += sh.e[m], write = write && m >= j;
+                if (other.y == at[n]) sum += sh.e[m + 1], write = write && m + 1 >= j;
+                if (other.z == at[n]) sum += sh.e[m + 2], write = write && m + 2 >= j;
+                if (other.w == at[n]) sum += sh.e[m + 3], write = write && m + 3 >= j;
+            }
+            if (write) store1(dz + i, (exp2_approx(fmaf(zt[n], rt, -lse) * kLog2e) - sum / t.sum) * g);
         }
     } else {
-        // the output's units lie across the input's: whole ones of the output,
-        // read a word at a time, with an element to spare at both ends
-        i0 = (u0 * N + 1 + phase + N - 1) / N * N - phase;
-        i1 = (u1 * N - 1 + phase) / N * N - phase;
-        if (i1 < i0) i1 = i0;
-        const T *const src = KEEP ? reinterpret_cast<const T *>(kept) : base;
-        for (int64_t i = i0 + int64_t(tid) * N; i < i1; i += THREADS * N) {
-            Unit<T> x;
-            read_shifted(src, i, x);
-            gradient(x);
-            __stcs(reinterpret_cast<uint4 *>(dz + i), x.w);
-        }
+        __syncthreads();
     }
-    // the rest, at most two units' elements at either end
-    if (i0 > part.last) i0 = i1 = part.last;
-    for (int64_t i = part.first + tid; i < i0; i += THREADS) store1(dz + i, exp2_approx(fmaf(load1(base + i), rt, -lse) * kLog2e) * g);
-    for (int64_t i = i1 + tid; i < part.last; i += THREADS) store1(dz + i, exp2_approx(fmaf(load1(base + i), rt, -lse) * kLog2e) * g);
-    __syncthreads();
-    // The entries of this part; the first of a repeated index answers for all.
-    const float weight = 1.0f / total;
-    for (int j = tid; j < a.k; j += THREADS) {
-        const int at = sh.at[j];
-        const int64_t i = part.head + int64_t(at);
-        if (at < 0 || i < part.first || i >= part.last) continue;
-        float sum = 0.0f;
-        bool write = true;
-        for (int n = 0; n < a.k; n += 4) {
-            const int4 other = *reinterpret_cast<const int4 *>(&sh.at[n]);
-            if (other.x == at) sum += sh.p[n], write = write && n >= j;
-            if (other.y == at) sum += sh.p[n + 1], write = write && n + 1 >= j;
-            if (other.z == at) sum += sh.p[n + 2], write = write && n + 2 >= j;
-            if (other.w == at) sum += sh.p[n + 3], write = write && n + 3 >= j;
-        }
-        if (write) store1(dz + i, (exp2_approx(fmaf(sh.z[j], rt, -lse) * kLog2e) - sum * weight) * g);
+    if (LOSS && rank == 0 && tid == 0) {
+        float loss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) loss += sh.red[i];
+        a.loss[r] = empty ? 0.0f : a.temperature * a.temperature * loss;
     }
 }
 
 template <class T, class E, bool LOSS, bool GRAD, bool KEEP, int THREADS>
-cudaError_t launch(const DistillArgs &a, int blocks, size_t smem, cudaStream_t st)
+cudaError_t launch(const DistillArgs &a, int blocks, int each, cudaStream_t st)
 {
     auto *kernel = &distill_kernel<T, E, LOSS, GRAD, KEEP, THREADS>;
+    // a spare unit, which a read across units may touch
+    const size_t smem = KEEP ? size_t(each + 1) * 16 : 0;
     if (smem) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return e;
@@ -468,7 +497,7 @@ cudaError_t launch(const DistillArgs &a, int blocks, size_t smem, cudaStream_t s
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = LOSS && blocks > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, a, blocks);
+    return cudaLaunchKernelEx(&cfg, kernel, a, blocks, each);
 }
 
 #ifndef ZG_DT
@@ -481,22 +510,22 @@ cudaError_t launch(const DistillArgs &a, int blocks, size_t smem, cudaStream_t s
 template <class T, class E, bool LOSS, bool GRAD>
 cudaError_t by_size(const DistillArgs &a, cudaStream_t st)
 {
-    const int64_t bytes = int64_t(a.vocab) * int64_t(sizeof(T)) + 32;
     constexpr int64_t kEach = 27 * 1024;  // shared memory of 128 threads: eight such blocks to an SM
+    const int64_t units = (int64_t(a.vocab) * int64_t(sizeof(T)) + 30) / 16, bytes = units * 16;
     int threads = bytes <= kEach ? 128 : bytes <= 2 * kEach ? 256 : 512;
     int blocks = 1;
     while (blocks < 8 && ((bytes + blocks - 1) / blocks > kEach * threads / 128 || (a.rows * blocks < 152 && bytes / blocks > 16384)))
         blocks *= 2;
     if (ZG_DT && threads == 512) threads = ZG_DT;
     if (ZG_DB && blocks == 1 && bytes > 2 * kEach) blocks = ZG_DB;
-    const int64_t part = ((bytes + 15) / 16 + blocks - 1) / blocks * 16 + 32;
-    if (LOSS && part <= 200 * 1024) {
-        if (threads == 128) return launch<T, E, LOSS, GRAD, LOSS, 128>(a, blocks, size_t(part), st);
-        if (threads == 256) return launch<T, E, LOSS, GRAD, LOSS, 256>(a, blocks, size_t(part), st);
-        return launch<T, E, LOSS, GRAD, LOSS, 512>(a, blocks, size_t(part), st);
+    const int each = int((units + blocks - 1) / blocks);
+    if (LOSS && int64_t(each) * 16 <= 200 * 1024) {
+        if (threads == 128) return launch<T, E, LOSS, GRAD, LOSS, 128>(a, blocks, each, st);
+        if (threads == 256) return launch<T, E, LOSS, GRAD, LOSS, 256>(a, blocks, each, st);
+        return launch<T, E, LOSS, GRAD, LOSS, 512>(a, blocks, each, st);
     }
-    if (threads == 128) return launch<T, E, LOSS, GRAD, false, 128>(a, blocks, 0, st);
-    return launch<T, E, LOSS, GRAD, false, 512>(a, blocks, 0, st);
+    if (threads == 128) return launch<T, E, LOSS, GRAD, false, 128>(a, blocks, each, st);
+    return launch<T, E, LOSS, GRAD, false, 512>(a, blocks, each, st);
 }
 
 template <class T, class E>

@@ -133,8 +133,8 @@ int check_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, int64
 {
     if (int rc = check_dtype(dtype, "dtype")) return rc;
     if (rows < 0) return fail(ZG_ERR_INVALID_ARG, "rows must not be negative (got %lld)", (long long)rows);
-    if (vocab < 1 || vocab >= (int64_t(1) << 31))
-        return fail(ZG_ERR_INVALID_ARG, "vocab must be in [1, 2^31) (got %lld)", (long long)vocab);
+    if (vocab < 1 || vocab > (int64_t(1) << 30))
+        return fail(ZG_ERR_INVALID_ARG, "vocab must be in [1, 2^30] (got %lld)", (long long)vocab);
     if (stride < vocab || stride >= kFar)
         return fail(ZG_ERR_INVALID_ARG, "row_stride %lld is not at least vocab %lld", (long long)stride, (long long)vocab);
     if (double(rows) * double(stride) >= double(kFar)) return fail(ZG_ERR_INVALID_ARG, "rows x row_stride is out of range");
