@@ -23,7 +23,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr float kLog2e = 1.44269504f;
+constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f;
 constexpr int kAhead = 4;  // units that a thread asks for before it uses the first
 
 __device__ __forceinline__ float load1(const float *p) { return *p; }
@@ -148,18 +148,36 @@ __device__ __forceinline__ void raise(Sum &s, float top, float c)
         s.top = top;
     }
 }
+// sum 2^((v - top) c) over units, each element one packed multiply-add and an
+// exponential: top c is rounded once, and what that takes off every exponent
+// is given back to the sum. Where top c could overflow (rows of a type's lowest
+// value) differences come first.
 template <class T>
-__device__ __forceinline__ float2 add_under(float2 part, const Unit<T> &x, float top, float c)
-{
-    float2 v[Unit<T>::kN / 2];
-    x.get(v);
-#pragma unroll
-    for (int i = 0; i < Unit<T>::kN / 2; ++i) {
-        const float2 t = mul_f32x2(add_f32x2(v[i], make_float2(-top, -top)), make_float2(c, c));
-        part = add_f32x2(part, make_float2(exp2_approx(t.x), exp2_approx(t.y)));
+struct Under {
+    float top, c, off;
+    bool far;
+    float2 sum;
+    __device__ __forceinline__ Under(float t, float cc) : top(t), c(cc), off(t * cc), sum(make_float2(0.0f, 0.0f))
+    {
+        far = !(fabsf(off) < 1e30f);
     }
-    return part;
-}
+    __device__ __forceinline__ void add(const Unit<T> &x)
+    {
+        float2 v[Unit<T>::kN / 2];
+        x.get(v);
+#pragma unroll
+        for (int i = 0; i < Unit<T>::kN / 2; ++i) {
+            const float2 t = far ? mul_f32x2(add_f32x2(v[i], make_float2(-top, -top)), make_float2(c, c))
+                                 : fma_f32x2(v[i], make_float2(c, c), make_float2(-off, -off));
+            sum = add_f32x2(sum, make_float2(exp2_approx(t.x), exp2_approx(t.y)));
+        }
+    }
+    __device__ __forceinline__ float get() const
+    {
+        const float s = sum.x + sum.y;
+        return far ? s : s * exp2_approx(-fmaf(top, c, -off));
+    }
+};
 
 template <int THREADS>
 struct Shared {
@@ -167,7 +185,7 @@ struct Shared {
     float red[THREADS / 32];
     Sum block;  // this block's part, read by the others of its row
     // the teacher's entries: exponential, and index (-1: absent)
-    float e[ZG_TOPK_MAX];
+    __align__(16) float e[ZG_TOPK_MAX];
     __align__(16) int at[ZG_TOPK_MAX];
 };
 
@@ -225,6 +243,31 @@ __device__ __forceinline__ void read_shifted(const float *base, int i, Unit<floa
 
 constexpr int kStages = 4;
 
+// A block's part of row r, and how it lies in memory.
+template <class T>
+struct Row {
+    const T *z;     // the row
+    const T *base;  // element 0 of the part's count: only [head, head + vocab) is touched
+    Part part;
+    int units, stage;  // whole units, and of them in each group of copies
+    __device__ __forceinline__ Row(const DistillArgs &a, int64_t r, int each, int rank, int threads)
+    {
+        z = static_cast<const T *>(a.logits) + r * a.row_stride;
+        part = part_of(z, a.vocab, each, rank);
+        base = z - part.head;
+        units = part.u1 - part.u0;
+        stage = (units + threads * kStages - 1) / (threads * kStages) * threads;
+    }
+    __device__ __forceinline__ const uint4 *from() const { return reinterpret_cast<const uint4 *>(base) + part.u0; }
+    __device__ __forceinline__ int stage_end(int g) const { return min((g + 1) * stage, units); }
+    template <int THREADS>
+    __device__ __forceinline__ void start_copies(Unit<T> *kept, int g) const
+    {
+        const int end = stage_end(g);
+        for (int u = g * stage + int(threadIdx.x); u < end; u += THREADS) copy_async(&kept[u], from() + u);
+    }
+};
+
 // KEEP: the part is copied into shared memory, in kStages groups, and both
 // passes read it there; else the one pass reads it from memory. Without LOSS,
 // lse is given. A row takes `blocks` blocks of `each` units: with LOSS a cluster,
@@ -238,41 +281,40 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
     const int tid = threadIdx.x;
     const int64_t r = blockIdx.x / unsigned(blocks);
     const int rank = int(blockIdx.x % unsigned(blocks));
-    const T *const z = static_cast<const T *>(a.logits) + r * a.row_stride;
     const float rt = 1.0f / a.temperature, c = rt * kLog2e;
-    const Part part = part_of(z, a.vocab, each, rank);
-    const T *const base = z - part.head;  // only elements [head, head + vocab) are touched
-    const uint4 *const from = reinterpret_cast<const uint4 *>(base) + part.u0;
     Unit<T> *const kept = reinterpret_cast<Unit<T> *>(raw);  // unit u0 + i at kept[i]
-    const int units = part.u1 - part.u0;
-    const int stage = (units + THREADS * kStages - 1) / (THREADS * kStages) * THREADS;
+    const Row<T> row(a, r, each, rank, THREADS);
+    const Part &part = row.part;
+    const T *const z = row.z, *const base = row.base;
+    const uint4 *const from = row.from();
+    const int units = row.units, stage = row.stage;
 
-    if (KEEP) {
-#pragma unroll
-        for (int g = 0; g < kStages; ++g) {
-            const int end = min((g + 1) * stage, units);
-            for (int u = g * stage + tid; u < end; u += THREADS) copy_async(&kept[u], from + u);
-            commit_copies();
-        }
-    }
-    // The teacher's entries, one or two to a thread, and the logits at them
-    // before anything is written over those.
+    // The teacher's entries, one or two to a thread: asked for before the row, so
+    // as not to queue behind it.
     int at[kEntries];
-    float te[kEntries], zt[kEntries];
+    E given[kEntries];
+    const bool entries = (tid & ~31) < a.k;  // of this warp
 #pragma unroll
     for (int n = 0; n < kEntries; ++n) {
         const int j = tid + n * THREADS;
-        at[n] = -1;
-        te[n] = -INFINITY;
-        zt[n] = 0.0f;
-        if (j < a.k) {
-            at[n] = a.t_index[r * a.k + j];
-            if (at[n] < 0 || at[n] >= a.vocab) at[n] = -1;
-            if (at[n] >= 0) {
-                te[n] = load1(static_cast<const E *>(a.t_logits) + r * a.k + j);
-                zt[n] = load1(z + at[n]);
-            }
+        const bool in = entries && j < a.k;
+        at[n] = in ? a.t_index[r * a.k + j] : -1;
+        given[n] = in ? static_cast<const E *>(a.t_logits)[r * a.k + j] : E(0);
+    }
+    if (KEEP) {
+#pragma unroll
+        for (int g = 0; g < kStages; ++g) {
+            row.template start_copies<THREADS>(kept, g);
+            commit_copies();
         }
+    }
+    // and the logits at them, before anything is written over those
+    float te[kEntries], zt[kEntries];
+#pragma unroll
+    for (int n = 0; n < kEntries; ++n) {
+        if (at[n] < 0 || at[n] >= a.vocab) at[n] = -1;
+        te[n] = at[n] >= 0 ? load1(&given[n]) : -INFINITY;
+        zt[n] = at[n] >= 0 ? load1(z + at[n]) : 0.0f;
     }
 
     Sum s = none();
@@ -289,11 +331,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
 #pragma unroll 2
             for (int u = begin; u < end; u += THREADS) top.add(kept[u]);
             raise(s, top.get(), c);
-            if (s.top == -INFINITY) continue;  // nothing but masked logits so far
-            float2 sum = make_float2(0.0f, 0.0f);
+            if (s.top != -INFINITY) {  // else nothing but masked logits so far
+                Under<T> under(s.top, c);
+                if (under.far) {
+                    for (int u = begin; u < end; u += THREADS) under.add(kept[u]);
+                } else {
+                    under.far = false;
 #pragma unroll 2
-            for (int u = begin; u < end; u += THREADS) sum = add_under(sum, kept[u], s.top, c);
-            s.sum += sum.x + sum.y;
+                    for (int u = begin; u < end; u += THREADS) under.add(kept[u]);
+                }
+                s.sum += under.get();
+            }
         }
     }
     if (LOSS && !KEEP) {
@@ -308,11 +356,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
                 if (u + i * THREADS < units) top.add(x[i]);
             raise(s, top.get(), c);
             if (s.top == -INFINITY) continue;
-            float2 sum = make_float2(0.0f, 0.0f);
+            Under<T> under(s.top, c);
 #pragma unroll
             for (int i = 0; i < kAhead; ++i)
-                if (u + i * THREADS < units) sum = add_under(sum, x[i], s.top, c);
-            s.sum += sum.x + sum.y;
+                if (u + i * THREADS < units) under.add(x[i]);
+            s.sum += under.get();
         }
     }
     if (LOSS) {  // the ragged ends: fewer elements than a unit each
@@ -331,22 +379,24 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
 #pragma unroll
         for (int n = 0; n < kEntries; ++n) {
             const int j = tid + n * THREADS;
-            if (j < ZG_TOPK_MAX) sh.at[j] = at[n];
-            t = join(t, Sum{te[n], te[n] == -INFINITY ? 0.0f : te[n] - te[n] + 1.0f}, c);
+            if (entries && j < ZG_TOPK_MAX) sh.at[j] = at[n];
+            if (entries) t = join(t, Sum{te[n], te[n] == -INFINITY ? 0.0f : te[n] - te[n] + 1.0f}, c);
         }
-        t = across<32>(t, c);
+        if (entries) t = across<32>(t, c);
         if (LOSS) s = across<32>(s, c);
         if (tid % 32 == 0) {
             sh.teacher[tid / 32] = t;
-            if (LOSS) sh.student[tid / 32] = s;
+            sh.student[tid / 32] = s;
         }
     }
     __syncthreads();
-    const Sum t = across<kWarps>(sh.teacher[tid % kWarps], c);
+    // the lower half of a warp joins the student's, the upper the teacher's
+    Sum t = across<kWarps>((tid & 16 ? sh.teacher : sh.student)[tid % kWarps], c);
+    s = Sum{__shfl_sync(0xffffffffu, t.top, 0), __shfl_sync(0xffffffffu, t.sum, 0)};
+    t = Sum{__shfl_sync(0xffffffffu, t.top, 16), __shfl_sync(0xffffffffu, t.sum, 16)};
     const bool empty = t.top == -INFINITY;
     float lse = 0.0f;
     if (LOSS) {
-        s = across<kWarps>(sh.student[tid % kWarps], c);
         if (blocks > 1) {
             cg::cluster_group cluster = cg::this_cluster();
             if (tid == 0) sh.block = s;
@@ -357,7 +407,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
         }
         const float log_sum = logf(s.sum);
         lse = fmaf(s.top, rt, log_sum);
-        if (rank == 0) {
+        if (rank == 0 && !entries && tid % 32 == 0) sh.red[tid / 32] = 0.0f;
+        if (rank == 0 && entries) {
             // p = 0 leaves its term out; a NaN stays
             float term = 0.0f;
             const float log_total = logf(t.sum);
@@ -378,11 +429,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
 #pragma unroll
         for (int n = 0; n < kEntries; ++n) {
             const int j = tid + n * THREADS;
-            if (j < ZG_TOPK_MAX) sh.e[j] = at[n] >= 0 ? exp2_approx((te[n] - t.top) * c) : 0.0f;
+            if (entries && j < ZG_TOPK_MAX) sh.e[j] = at[n] >= 0 ? exp2_approx((te[n] - t.top) * c) : 0.0f;
         }
         const float g = a.scale * a.temperature * (a.dloss ? a.dloss[r] : 1.0f);
         T *const dz = static_cast<T *>(a.dlogits) + r * a.drow_stride - part.head;
-        auto gradient1 = [&](float v) { return empty ? 0.0f : exp2_approx(fmaf(v, rt, -lse) * kLog2e) * g; };
+        // 2^(v c - low), low = lse log2(e) rounded once and made good in the factor
+        const float low = lse * kLog2e;
+        const bool far = !(fabsf(low) < 1e30f);
+        const float gg = far ? g : g * exp2_approx(-fmaf(lse, kLog2eRest, fmaf(lse, kLog2e, -low)));
+        auto gradient1 = [&](float v) {
+            return empty ? 0.0f : exp2_approx(far ? fmaf(v, rt, -lse) * kLog2e : fmaf(v, c, -low)) * gg;
+        };
         auto gradient = [&](Unit<T> &x) {
             if (empty) {
                 x.w = make_uint4(0u, 0u, 0u, 0u);
@@ -392,8 +449,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
             x.get(v);
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) {
-                const float2 q = mul_f32x2(fma_f32x2(v[i], make_float2(rt, rt), make_float2(-lse, -lse)), make_float2(kLog2e, kLog2e));
-                v[i] = mul_f32x2(make_float2(exp2_approx(q.x), exp2_approx(q.y)), make_float2(g, g));
+                const float2 q = far ? mul_f32x2(fma_f32x2(v[i], make_float2(rt, rt), make_float2(-lse, -lse)), make_float2(kLog2e, kLog2e))
+                                     : fma_f32x2(v[i], make_float2(c, c), make_float2(-low, -low));
+                v[i] = mul_f32x2(make_float2(exp2_approx(q.x), exp2_approx(q.y)), make_float2(gg, gg));
             }
             x.set(v);
         };
@@ -454,14 +512,19 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
             const int j = tid + n * THREADS, i = part.head + at[n];
             if (empty || at[n] < 0 || i < part.first || i >= part.last) continue;
             float sum = 0.0f;
-            bool write = true;
+            int first = j;
+#pragma unroll 2
             for (int m = 0; m < a.k; m += 4) {
                 const int4 other = *reinterpret_cast<const int4 *>(&sh.at[m]);
-                if (other.x == at[n]) sum += sh.e[m], write = write && m >= j;
-                if (other.y == at[n]) sum += sh.e[m + 1], write = write && m + 1 >= j;
-                if (other.z == at[n]) sum += sh.e[m + 2], write = write && m + 2 >= j;
-                if (other.w == at[n]) sum += sh.e[m + 3], write = write && m + 3 >= j;
+                const float4 e = *reinterpret_cast<const float4 *>(&sh.e[m]);
+                sum += other.x == at[n] ? e.x : 0.0f;
+                sum += other.y == at[n] ? e.y : 0.0f;
+                sum += other.z == at[n] ? e.z : 0.0f;
+                sum += other.w == at[n] ? e.w : 0.0f;
+                first = min(first, min(min(other.x == at[n] ? m : j, other.y == at[n] ? m + 1 : j),
+                                       min(other.z == at[n] ? m + 2 : j, other.w == at[n] ? m + 3 : j)));
             }
+            const bool write = first == j;
             if (write) store1(dz + i, (exp2_approx(fmaf(zt[n], rt, -lse) * kLog2e) - sum / t.sum) * g);
         }
     } else {
@@ -500,11 +563,8 @@ cudaError_t launch(const DistillArgs &a, int blocks, int each, cudaStream_t st)
     return cudaLaunchKernelEx(&cfg, kernel, a, blocks, each);
 }
 
-#ifndef ZG_DT
-#define ZG_DT 0
-#endif
-#ifndef ZG_DB
-#define ZG_DB 0
+#ifndef ZG_FEW
+#define ZG_FEW 152
 #endif
 
 template <class T, class E, bool LOSS, bool GRAD>
@@ -512,20 +572,27 @@ cudaError_t by_size(const DistillArgs &a, cudaStream_t st)
 {
     constexpr int64_t kEach = 27 * 1024;  // shared memory of 128 threads: eight such blocks to an SM
     const int64_t units = (int64_t(a.vocab) * int64_t(sizeof(T)) + 30) / 16, bytes = units * 16;
-    int threads = bytes <= kEach ? 128 : bytes <= 2 * kEach ? 256 : 512;
-    int blocks = 1;
-    while (blocks < 8 && ((bytes + blocks - 1) / blocks > kEach * threads / 128 || (a.rows * blocks < 152 && bytes / blocks > 16384)))
-        blocks *= 2;
-    if (ZG_DT && threads == 512) threads = ZG_DT;
-    if (ZG_DB && blocks == 1 && bytes > 2 * kEach) blocks = ZG_DB;
-    const int each = int((units + blocks - 1) / blocks);
-    if (LOSS && int64_t(each) * 16 <= 200 * 1024) {
-        if (threads == 128) return launch<T, E, LOSS, GRAD, LOSS, 128>(a, blocks, each, st);
-        if (threads == 256) return launch<T, E, LOSS, GRAD, LOSS, 256>(a, blocks, each, st);
-        return launch<T, E, LOSS, GRAD, LOSS, 512>(a, blocks, each, st);
+    auto each = [&](int64_t blocks) { return int((units + blocks - 1) / blocks); };
+    if constexpr (LOSS) {
+        // The smallest block that holds a row, or as few of the largest as do;
+        // more of them while rows are so few that SMs are left over.
+        const int threads = bytes <= kEach ? 128 : bytes <= 2 * kEach ? 256 : 512;
+        const int64_t most = kEach * threads / 128;
+        int64_t blocks = (bytes + most - 1) / most;
+        while (blocks < 8 && a.rows * blocks < ZG_FEW && bytes / blocks > 16384) blocks = blocks * 2 < 8 ? blocks * 2 : 8;
+        if (blocks > 8) blocks = 8;  // parts of up to 200 KB: one block to an SM
+        if (int64_t(each(blocks)) * 16 <= 200 * 1024) {
+            if (threads == 128) return launch<T, E, true, GRAD, true, 128>(a, int(blocks), each(blocks), st);
+            if (threads == 256) return launch<T, E, true, GRAD, true, 256>(a, int(blocks), each(blocks), st);
+            return launch<T, E, true, GRAD, true, 512>(a, int(blocks), each(blocks), st);
+        }
+        return launch<T, E, true, GRAD, false, 512>(a, 8, each(8), st);
+    } else {
+        // nothing to exchange: as many small blocks as a row has parts for
+        int64_t blocks = (bytes + kEach - 1) / kEach;
+        if (a.rows * blocks < ZG_FEW) blocks = (bytes + 16383) / 16384;
+        return launch<T, E, false, true, false, 128>(a, int(blocks), each(blocks), st);
     }
-    if (threads == 128) return launch<T, E, LOSS, GRAD, false, 128>(a, blocks, each, st);
-    return launch<T, E, LOSS, GRAD, false, 512>(a, blocks, each, st);
 }
 
 template <class T, class E>
