@@ -152,22 +152,18 @@ __device__ __forceinline__ void raise(Sum &s, float top, float c)
 // exponential: top c is rounded once, and what that takes off every exponent
 // is given back to the sum. Where top c could overflow (rows of a type's lowest
 // value) differences come first.
-template <class T>
+template <class T, bool FAR>
 struct Under {
     float top, c, off;
-    bool far;
     float2 sum;
-    __device__ __forceinline__ Under(float t, float cc) : top(t), c(cc), off(t * cc), sum(make_float2(0.0f, 0.0f))
-    {
-        far = !(fabsf(off) < 1e30f);
-    }
+    __device__ __forceinline__ Under(float t, float cc) : top(t), c(cc), off(t * cc), sum(make_float2(0.0f, 0.0f)) {}
     __device__ __forceinline__ void add(const Unit<T> &x)
     {
         float2 v[Unit<T>::kN / 2];
         x.get(v);
 #pragma unroll
         for (int i = 0; i < Unit<T>::kN / 2; ++i) {
-            const float2 t = far ? mul_f32x2(add_f32x2(v[i], make_float2(-top, -top)), make_float2(c, c))
+            const float2 t = FAR ? mul_f32x2(add_f32x2(v[i], make_float2(-top, -top)), make_float2(c, c))
                                  : fma_f32x2(v[i], make_float2(c, c), make_float2(-off, -off));
             sum = add_f32x2(sum, make_float2(exp2_approx(t.x), exp2_approx(t.y)));
         }
@@ -175,9 +171,10 @@ struct Under {
     __device__ __forceinline__ float get() const
     {
         const float s = sum.x + sum.y;
-        return far ? s : s * exp2_approx(-fmaf(top, c, -off));
+        return FAR ? s : s * exp2_approx(-fmaf(top, c, -off));
     }
 };
+__device__ __forceinline__ bool is_far(float v) { return !(fabsf(v) < 1e30f); }
 
 template <int THREADS>
 struct Shared {
@@ -241,7 +238,7 @@ __device__ __forceinline__ void read_shifted(const float *base, int i, Unit<floa
     x.w = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-constexpr int kStages = 4;
+constexpr int kStages = 2;
 
 // A block's part of row r, and how it lies in memory.
 template <class T>
@@ -279,8 +276,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
     __shared__ Shared<THREADS> sh;
     constexpr int N = Unit<T>::kN, kWarps = THREADS / 32, kEntries = (ZG_TOPK_MAX + THREADS - 1) / THREADS;
     const int tid = threadIdx.x;
-    const int64_t r = blockIdx.x / unsigned(blocks);
-    const int rank = int(blockIdx.x % unsigned(blocks));
+    const unsigned number = blockIdx.x / unsigned(blocks);
+    const int64_t r = number;
+    const int rank = int(blockIdx.x - number * unsigned(blocks));
     const float rt = 1.0f / a.temperature, c = rt * kLog2e;
     Unit<T> *const kept = reinterpret_cast<Unit<T> *>(raw);  // unit u0 + i at kept[i]
     const Row<T> row(a, r, each, rank, THREADS);
@@ -321,10 +319,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
     if (LOSS && KEEP) {
 #pragma unroll
         for (int g = 0; g < kStages; ++g) {
-            if (g == 0) wait_copies<3>();
-            if (g == 1) wait_copies<2>();
-            if (g == 2) wait_copies<1>();
-            if (g == 3) wait_copies<0>();
+            if (g == 0) wait_copies<1>();
+            if (g == 1) wait_copies<0>();
             // a thread reads what it copied itself: first for its largest, then for the sum
             const int begin = g * stage + tid, end = min((g + 1) * stage, units);
             typename Unit<T>::Top top;
@@ -332,15 +328,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
             for (int u = begin; u < end; u += THREADS) top.add(kept[u]);
             raise(s, top.get(), c);
             if (s.top != -INFINITY) {  // else nothing but masked logits so far
-                Under<T> under(s.top, c);
-                if (under.far) {
+                if (is_far(s.top * c)) {
+                    Under<T, true> under(s.top, c);
                     for (int u = begin; u < end; u += THREADS) under.add(kept[u]);
+                    s.sum += under.get();
                 } else {
-                    under.far = false;
+                    Under<T, false> under(s.top, c);
 #pragma unroll 2
                     for (int u = begin; u < end; u += THREADS) under.add(kept[u]);
+                    s.sum += under.get();
                 }
-                s.sum += under.get();
             }
         }
     }
@@ -356,11 +353,19 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
                 if (u + i * THREADS < units) top.add(x[i]);
             raise(s, top.get(), c);
             if (s.top == -INFINITY) continue;
-            Under<T> under(s.top, c);
+            if (is_far(s.top * c)) {
+                Under<T, true> under(s.top, c);
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (u + i * THREADS < units) under.add(x[i]);
-            s.sum += under.get();
+                for (int i = 0; i < kAhead; ++i)
+                    if (u + i * THREADS < units) under.add(x[i]);
+                s.sum += under.get();
+            } else {
+                Under<T, false> under(s.top, c);
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    if (u + i * THREADS < units) under.add(x[i]);
+                s.sum += under.get();
+            }
         }
     }
     if (LOSS) {  // the ragged ends: fewer elements than a unit each
@@ -435,21 +440,18 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
         T *const dz = static_cast<T *>(a.dlogits) + r * a.drow_stride - part.head;
         // 2^(v c - low), low = lse log2(e) rounded once and made good in the factor
         const float low = lse * kLog2e;
-        const bool far = !(fabsf(low) < 1e30f);
+        const bool far = is_far(low);
         const float gg = far ? g : g * exp2_approx(-fmaf(lse, kLog2eRest, fmaf(lse, kLog2e, -low)));
         auto gradient1 = [&](float v) {
             return empty ? 0.0f : exp2_approx(far ? fmaf(v, rt, -lse) * kLog2e : fmaf(v, c, -low)) * gg;
         };
-        auto gradient = [&](Unit<T> &x) {
-            if (empty) {
-                x.w = make_uint4(0u, 0u, 0u, 0u);
-                return;
-            }
+        auto gradient = [&](Unit<T> &x, auto is_far_too) {
             float2 v[N / 2];
             x.get(v);
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) {
-                const float2 q = far ? mul_f32x2(fma_f32x2(v[i], make_float2(rt, rt), make_float2(-lse, -lse)), make_float2(kLog2e, kLog2e))
+                const float2 q = decltype(is_far_too)::value
+                                     ? mul_f32x2(fma_f32x2(v[i], make_float2(rt, rt), make_float2(-lse, -lse)), make_float2(kLog2e, kLog2e))
                                      : fma_f32x2(v[i], make_float2(c, c), make_float2(-low, -low));
                 v[i] = mul_f32x2(make_float2(exp2_approx(q.x), exp2_approx(q.y)), make_float2(gg, gg));
             }
@@ -458,48 +460,56 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
         const int phase = int((reinterpret_cast<uintptr_t>(dz) & 15u) / sizeof(T));
         int i0, i1;  // what is written in whole units
         if (phase == 0) {
-            uint4 *const to = reinterpret_cast<uint4 *>(dz) + part.u0;
             i0 = part.u0 * N;
             i1 = part.u1 * N;
-            if (KEEP) {
-#pragma unroll 2
-                for (int u = tid; u < units; u += THREADS) {
-                    Unit<T> x = kept[u];
-                    gradient(x);
-                    __stcs(to + u, x.w);
+        } else {
+            // the output's units lie across the input's: whole ones of the output,
+            // read a word at a time, with an element to spare at both ends
+            i0 = (part.u0 * N + 1 + phase + N - 1) / N * N - phase;
+            i1 = max((part.u1 * N - 1 + phase) / N * N - phase, i0);
+        }
+        auto pass = [&](auto is_far_too) {
+            if (phase != 0) {
+                const T *const src = KEEP ? reinterpret_cast<const T *>(kept) - part.u0 * N : base;
+                for (int i = i0 + tid * N; i < i1; i += THREADS * N) {
+                    Unit<T> x;
+                    read_shifted(src, i, x);
+                    gradient(x, is_far_too);
+                    __stcs(reinterpret_cast<uint4 *>(dz + i), x.w);
                 }
-            } else {
-                int u = tid;
+                return;
+            }
+            uint4 *const to = reinterpret_cast<uint4 *>(dz) + part.u0;
+            int u = tid;
+            if (!KEEP)
                 for (; u + (kAhead - 1) * THREADS < units; u += kAhead * THREADS) {
                     Unit<T> x[kAhead];
 #pragma unroll
                     for (int i = 0; i < kAhead; ++i) x[i].w = from[u + i * THREADS];
 #pragma unroll
                     for (int i = 0; i < kAhead; ++i) {
-                        gradient(x[i]);
+                        gradient(x[i], is_far_too);
                         __stcs(to + u + i * THREADS, x[i].w);
                     }
                 }
-                for (; u < units; u += THREADS) {
-                    Unit<T> x;
-                    x.w = from[u];
-                    gradient(x);
-                    __stcs(to + u, x.w);
-                }
-            }
-        } else {
-            // the output's units lie across the input's: whole ones of the output,
-            // read a word at a time, with an element to spare at both ends
-            i0 = (part.u0 * N + 1 + phase + N - 1) / N * N - phase;
-            i1 = max((part.u1 * N - 1 + phase) / N * N - phase, i0);
-            const T *const src = KEEP ? reinterpret_cast<const T *>(kept) - part.u0 * N : base;
-            for (int i = i0 + tid * N; i < i1; i += THREADS * N) {
+#pragma unroll 2
+            for (; u < units; u += THREADS) {
                 Unit<T> x;
-                read_shifted(src, i, x);
-                gradient(x);
-                __stcs(reinterpret_cast<uint4 *>(dz + i), x.w);
+                if (KEEP)
+                    x = kept[u];
+                else
+                    x.w = from[u];
+                gradient(x, is_far_too);
+                __stcs(to + u, x.w);
             }
-        }
+        };
+        if (empty)
+            for (int i = i0 + tid * N; i < i1; i += THREADS * N)
+                __stcs(reinterpret_cast<uint4 *>(dz + i), make_uint4(0u, 0u, 0u, 0u));
+        else if (far)
+            pass(std::true_type{});
+        else
+            pass(std::false_type{});
         // the rest, less than two units at either end
         i0 = min(i0, part.last);
         i1 = min(i1, part.last);
