@@ -17,6 +17,7 @@
 
 #include "zg_launch.h"
 #include "zg_ops.h"
+#include "zg_rows.cuh"
 
 namespace zg {
 namespace {
@@ -26,22 +27,10 @@ namespace cg = cooperative_groups;
 constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f;
 constexpr int kAhead = 4;  // units that a thread asks for before it uses the first
 
-__device__ __forceinline__ float load1(const float *p) { return *p; }
-__device__ __forceinline__ float load1(const uint16_t *p) { return __uint_as_float(uint32_t(*p) << 16); }
-__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store1(uint16_t *p, float v) { *p = uint16_t(pack_bf16x2(v, 0.0f)); }
-
 __device__ __forceinline__ float exp2_approx(float v)
 {
     float d;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
-    return d;
-}
-// max that keeps a NaN.
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
 __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b)
@@ -82,62 +71,6 @@ __device__ __forceinline__ Sum across(Sum s, float c)
     for (int o = WIDTH / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return Sum{top, sum};
 }
-
-// Sixteen bytes of logits: eight bf16 or four binary32.
-template <class T>
-struct Unit;
-template <>
-struct Unit<uint16_t> {
-    static constexpr int kN = 8;
-    uint4 w;
-    // Running maxima of the low and the high halves.
-    struct Top {
-        uint32_t m = 0xff80ff80u;  // -inf
-        __device__ __forceinline__ void add(const Unit &x) { m = max2(max2(m, max2(x.w.x, x.w.y)), max2(x.w.z, x.w.w)); }
-        __device__ __forceinline__ float get() const { return max_nan(bf16_lo(m), bf16_hi(m)); }
-        __device__ static __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
-        {
-            uint32_t d;
-            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-            return d;
-        }
-    };
-    __device__ __forceinline__ void get(float2 (&v)[4]) const
-    {
-        v[0] = make_float2(bf16_lo(w.x), bf16_hi(w.x));
-        v[1] = make_float2(bf16_lo(w.y), bf16_hi(w.y));
-        v[2] = make_float2(bf16_lo(w.z), bf16_hi(w.z));
-        v[3] = make_float2(bf16_lo(w.w), bf16_hi(w.w));
-    }
-    __device__ __forceinline__ void set(const float2 (&v)[4])
-    {
-        w = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
-                       pack_bf16x2(v[3].x, v[3].y));
-    }
-};
-template <>
-struct Unit<float> {
-    static constexpr int kN = 4;
-    uint4 w;
-    struct Top {
-        float m = -INFINITY;
-        __device__ __forceinline__ void add(const Unit &x)
-        {
-            m = max_nan(max_nan(m, max_nan(__uint_as_float(x.w.x), __uint_as_float(x.w.y))),
-                        max_nan(__uint_as_float(x.w.z), __uint_as_float(x.w.w)));
-        }
-        __device__ __forceinline__ float get() const { return m; }
-    };
-    __device__ __forceinline__ void get(float2 (&v)[2]) const
-    {
-        v[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
-        v[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
-    }
-    __device__ __forceinline__ void set(const float2 (&v)[2])
-    {
-        w = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
-    }
-};
 
 // Raises a running sum's top, and adds a unit's logits under it.
 __device__ __forceinline__ void raise(Sum &s, float top, float c)
@@ -186,40 +119,6 @@ struct Shared {
     __align__(16) int at[ZG_TOPK_MAX];
 };
 
-// A block's part of a row. Elements are counted from the 16-byte boundary at
-// or below the row's first, so the row is [head, head + vocab); the part is the
-// elements [first, last), and units [u0, u1) are whole in it.
-struct Part {
-    int head, lo, first, last, u0, u1;
-};
-template <class T>
-__device__ __forceinline__ Part part_of(const T *row, int vocab, int each, int rank)
-{
-    constexpr int N = Unit<T>::kN;
-    Part p;
-    p.head = int((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
-    const int end = p.head + vocab;  // vocab is at most 2^30
-    p.lo = rank * each;
-    p.first = max(min(p.lo * N, end), p.head);
-    p.last = p.lo + each < (end + N - 1) / N ? (p.lo + each) * N : end;
-    p.last = max(p.last, p.first);
-    p.u0 = (p.first + N - 1) / N;
-    p.u1 = max(p.last / N, p.u0);
-    return p;
-}
-
-__device__ __forceinline__ void copy_async(void *dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void wait_copies()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Sixteen bytes from element i of `base`, which is aligned to its units only,
 // by whole words: up to one element before and after them is read too.
 __device__ __forceinline__ void read_shifted(const uint16_t *base, int i, Unit<uint16_t> &x)
@@ -238,33 +137,6 @@ __device__ __forceinline__ void read_shifted(const float *base, int i, Unit<floa
     x.w = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-constexpr int kStages = 2;
-
-// A block's part of row r, and how it lies in memory.
-template <class T>
-struct Row {
-    const T *z;     // the row
-    const T *base;  // element 0 of the part's count: only [head, head + vocab) is touched
-    Part part;
-    int units, stage;  // whole units, and of them in each group of copies
-    __device__ __forceinline__ Row(const DistillArgs &a, int64_t r, int each, int rank, int threads)
-    {
-        z = static_cast<const T *>(a.logits) + r * a.row_stride;
-        part = part_of(z, a.vocab, each, rank);
-        base = z - part.head;
-        units = part.u1 - part.u0;
-        stage = (units + threads * kStages - 1) / (threads * kStages) * threads;
-    }
-    __device__ __forceinline__ const uint4 *from() const { return reinterpret_cast<const uint4 *>(base) + part.u0; }
-    __device__ __forceinline__ int stage_end(int g) const { return min((g + 1) * stage, units); }
-    template <int THREADS>
-    __device__ __forceinline__ void start_copies(Unit<T> *kept, int g) const
-    {
-        const int end = stage_end(g);
-        for (int u = g * stage + int(threadIdx.x); u < end; u += THREADS) copy_async(&kept[u], from() + u);
-    }
-};
-
 // KEEP: the part is copied into shared memory, in kStages groups, and both
 // passes read it there; else the one pass reads it from memory. Without LOSS,
 // lse is given. A row takes `blocks` blocks of `each` units: with LOSS a cluster,
@@ -281,7 +153,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
     const int rank = int(blockIdx.x - number * unsigned(blocks));
     const float rt = 1.0f / a.temperature, c = rt * kLog2e;
     Unit<T> *const kept = reinterpret_cast<Unit<T> *>(raw);  // unit u0 + i at kept[i]
-    const Row<T> row(a, r, each, rank, THREADS);
+    const Row<T> row(static_cast<const T *>(a.logits) + r * a.row_stride, a.vocab, each, rank, THREADS);
     const Part &part = row.part;
     const T *const z = row.z, *const base = row.base;
     const uint4 *const from = row.from();

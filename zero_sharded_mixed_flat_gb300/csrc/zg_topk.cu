@@ -1,55 +1,344 @@
 // The k largest of each row of logits, largest first, ties to the lowest index.
+//
+// Bound by memory: a row is read once. Each thread takes the maximum of its
+// share of the row while it arrives in shared memory. The k-th largest of these
+// maxima is no more than the row's k-th largest logit (k shares each hold one
+// at least as large), so it is a bound below which nothing has to be looked at:
+// only threads whose maximum reaches it go over their share again, and about k
+// logits pass. Those are put in order by counting, for each, how many come
+// before it. Rows in which too many pass (many equal values) have their k-th
+// largest found bit by bit. A row of several parts (few rows, or a vocabulary
+// beyond one block's shared memory) takes a cluster of blocks, whose lists are
+// merged through distributed shared memory.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "zg_launch.h"
 #include "zg_ops.h"
+#include "zg_rows.cuh"
 
 namespace zg {
 namespace {
 
-constexpr int kThreads = 256;
+namespace cg = cooperative_groups;
 
-// An unsigned key in the order of the values: NaN above everything, -0 = +0.
+constexpr int kMost = 1024;  // logits that may pass the bound
+
+// Unsigned keys in the order of the values, NaN above everything, -0 = +0, none
+// zero: 16 bits for bf16, 32 for binary32. `bits` are the value's as binary32.
+template <class T>
 __device__ __forceinline__ uint32_t key_of(uint32_t bits)
 {
-    if ((bits & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
-    if (bits == 0x80000000u) bits = 0u;
-    return (bits & 0x80000000u) ? ~bits : (bits | 0x80000000u);
+    uint32_t key = (bits & 0x80000000u) ? ~bits : (bits | 0x80000000u);
+    if (bits == 0x80000000u) key = 0x80000000u;
+    if ((bits & 0x7fffffffu) > 0x7f800000u) key = 0xffffffffu;
+    return sizeof(T) == 2 ? key >> 16 : key;
 }
 __device__ __forceinline__ uint32_t bits_at(const float *p) { return __float_as_uint(*p); }
 __device__ __forceinline__ uint32_t bits_at(const uint16_t *p) { return uint32_t(*p) << 16; }
-
-// One block per row takes the largest (key, lowest index) below the last one taken, k times.
 template <class T>
-__global__ void __launch_bounds__(kThreads) topk_kernel(const T *logits, int64_t rows, int vocab, int64_t stride, int k, T *values, int32_t *index)
+__device__ __forceinline__ uint32_t bits_in(const Unit<T> &x, int i)
 {
-    __shared__ uint64_t best[kThreads / 32];
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const T *row = logits + r * stride;
-        uint64_t last = ~uint64_t(0);
-        for (int j = 0; j < k; ++j) {
-            uint64_t m = 0;
-            for (int v = threadIdx.x; v < vocab; v += kThreads) {
-                const uint64_t key = (uint64_t(key_of(bits_at(row + v))) << 32) | uint32_t(0x7fffffff - v);
-                if (key < last && key > m) m = key;
-            }
-            for (int o = 16; o; o >>= 1) {
-                const uint64_t n = __shfl_xor_sync(0xffffffffu, m, o);
-                m = n > m ? n : m;
-            }
-            __syncthreads();
-            if (threadIdx.x % 32 == 0) best[threadIdx.x / 32] = m;
-            __syncthreads();
-            m = best[0];
-            for (int w = 1; w < kThreads / 32; ++w) m = best[w] > m ? best[w] : m;
-            last = m;
-            if (threadIdx.x == 0) {
-                const int v = 0x7fffffff - int(uint32_t(m));
-                values[r * k + j] = row[v];
-                index[r * k + j] = v;
+    const uint32_t w[4] = {x.w.x, x.w.y, x.w.z, x.w.w};
+    if (sizeof(T) == 4) return w[i & 3];
+    return (i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16;
+}
+
+// Larger keys first, then lower indices: one number, larger first.
+__device__ __forceinline__ uint64_t entry(uint32_t key, int v) { return (uint64_t(key) << 32) | uint32_t(0x7fffffff - v); }
+__device__ __forceinline__ int index_of(uint64_t e) { return 0x7fffffff - int(uint32_t(e)); }
+
+struct Shared {
+    uint64_t list[kMost];
+    uint64_t top[ZG_TOPK_MAX];  // this part's, in order; read by the others
+    int count, tops;
+    int warps[16];
+};
+
+template <int WARPS>
+__device__ __forceinline__ int block_sum(int v, int *red)
+{
+    v = __reduce_add_sync(0xffffffffu, v);
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) v += red[i];
+    __syncthreads();
+    return v;
+}
+
+template <class T, bool KEEP, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *logits, int vocab, int64_t row_stride, int k,
+                                                                      T *values, int32_t *index, int blocks, int each)
+{
+    extern __shared__ __align__(16) unsigned char raw[];
+    __shared__ Shared sh;
+    constexpr int N = Unit<T>::kN, kWarps = THREADS / 32, kBits = 8 * int(sizeof(T));
+    const int tid = threadIdx.x;
+    const unsigned number = blockIdx.x / unsigned(blocks);
+    const int64_t r = number;
+    const int rank = int(blockIdx.x - number * unsigned(blocks));
+    const T *const z = logits + r * row_stride;
+    const Row<T> row(z, vocab, each, rank, THREADS);
+    const Part &part = row.part;
+    Unit<T> *const kept = reinterpret_cast<Unit<T> *>(raw);
+    const uint4 *const from = row.from();
+    const int units = row.units;
+    auto unit_at = [&](int u) {
+        Unit<T> x;
+        if (KEEP)
+            x = kept[u];
+        else
+            x.w = from[u];
+        return x;
+    };
+    // a thread's one element of the ragged ends, or -1
+    int ragged = -1;
+    {
+        const int head_end = min(part.u0 * N, part.last), tail = max(part.u1 * N, head_end);
+        if (part.first + tid < head_end) ragged = part.first + tid - part.head;
+        if (tid >= 32 && tail + tid - 32 < part.last) ragged = tail + tid - 32 - part.head;
+    }
+    const uint32_t ragged_key = ragged >= 0 ? key_of<T>(bits_at(z + ragged)) : 0u;
+    const int base = part.u0 * N - part.head;  // vocabulary index of unit 0's first element
+
+    if (KEEP) {
+#pragma unroll
+        for (int g = 0; g < kStages; ++g) {
+            row.template start_copies<THREADS>(kept, g);
+            commit_copies();
+        }
+    }
+    if (tid == 0) sh.count = 0;
+    typename Unit<T>::Top most;
+    if (KEEP) {
+#pragma unroll
+        for (int g = 0; g < kStages; ++g) {
+            if (g == 0) wait_copies<1>();
+            if (g == 1) wait_copies<0>();
+            const int end = row.stage_end(g);
+#pragma unroll 2
+            for (int u = g * row.stage + tid; u < end; u += THREADS) most.add(kept[u]);
+        }
+    } else {
+#pragma unroll 4
+        for (int u = tid; u < units; u += THREADS) most.add(unit_at(u));
+    }
+    uint32_t best = ragged_key;
+    if (tid < units) best = max(best, key_of<T>(__float_as_uint(most.get())));
+
+    // the largest bound, to 16 bits, that k of the threads' maxima reach
+    uint32_t bound = 0u;
+#pragma unroll 1
+    for (int b = kBits - 1; b >= kBits - 16; --b) {
+        const uint32_t with = bound | (1u << b);
+        if (__syncthreads_count(best >= with) >= k) bound = with;
+    }
+    // what reaches it
+    auto put = [&](uint32_t key, int v) {
+        const int n = atomicAdd(&sh.count, 1);
+        if (n < kMost) sh.list[n] = entry(key, v);
+    };
+    if (best >= bound && best) {
+        if (ragged >= 0 && ragged_key >= bound) put(ragged_key, ragged);
+        for (int u = tid; u < units; u += THREADS) {
+            const Unit<T> x = unit_at(u);
+            typename Unit<T>::Top top;
+            top.add(x);
+            if (key_of<T>(__float_as_uint(top.get())) < bound) continue;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t key = key_of<T>(bits_in(x, i));
+                if (key >= bound) put(key, base + u * N + i);
             }
         }
     }
+    __syncthreads();
+    if (sh.count > kMost) {
+        // The k-th largest key itself, bit by bit: then all above it, and of its
+        // equals the first ones by index.
+        const int size = part.last - part.first, want = min(k, size);
+        auto reaching = [&](uint32_t key) {
+            int n = ragged >= 0 && ragged_key >= key;
+            for (int u = tid; u < units; u += THREADS) {
+                const Unit<T> x = unit_at(u);
+#pragma unroll
+                for (int i = 0; i < N; ++i) n += key_of<T>(bits_in(x, i)) >= key;
+            }
+            return block_sum<kWarps>(n, sh.warps);
+        };
+        uint32_t kth = 0u;
+        for (int b = kBits - 1; b >= 0; --b) {
+            const uint32_t with = kth | (1u << b);
+            if (reaching(with) >= want) kth = with;
+        }
+        if (tid == 0) sh.count = 0;
+        __syncthreads();
+        if (ragged >= 0 && ragged_key > kth) put(ragged_key, ragged);
+        for (int u = tid; u < units; u += THREADS) {
+            const Unit<T> x = unit_at(u);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t key = key_of<T>(bits_in(x, i));
+                if (key > kth) put(key, base + u * N + i);
+            }
+        }
+        __syncthreads();
+        // the equals, in the order of their indices: the head, the units, the tail
+        int have = sh.count;
+        __syncthreads();
+        auto equals = [&](int n, auto each_one) {  // n of this thread's, after those of the threads before it
+            int before = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, before, o);
+                if (tid % 32 >= o) before += v;
+            }
+            if (tid % 32 == 31) sh.warps[tid / 32] = before;
+            __syncthreads();
+            int all = 0;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w == tid / 32) before += all;
+                all += sh.warps[w];
+            }
+            if (n) each_one(have + before - n);
+            have += all;
+            __syncthreads();
+        };
+        const bool head = ragged >= 0 && ragged < base, tail = ragged >= 0 && !head;
+        equals(head && ragged_key == kth, [&](int at) {
+            if (at < want) sh.list[at] = entry(kth, ragged);
+        });
+        for (int u0 = 0; u0 < units && have < want; u0 += THREADS) {
+            const int u = u0 + tid;
+            Unit<T> x;
+            int n = 0;
+            if (u < units) {
+                x = unit_at(u);
+#pragma unroll
+                for (int i = 0; i < N; ++i) n += key_of<T>(bits_in(x, i)) == kth;
+            }
+            equals(n, [&](int at) {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (key_of<T>(bits_in(x, i)) == kth) {
+                        if (at < want) sh.list[at] = entry(kth, base + u * N + i);
+                        ++at;
+                    }
+            });
+        }
+        if (have < want)
+            equals(tail && ragged_key == kth, [&](int at) {
+                if (at < want) sh.list[at] = entry(kth, ragged);
+            });
+        if (tid == 0) sh.count = min(have, want);
+        __syncthreads();
+    }
+    // In order: an entry's place is the number of those before it, counted by
+    // the threads that share it.
+    const int count = sh.count;
+    int share = 1;
+    while (share < 32 && count * share * 2 <= THREADS) share *= 2;
+    for (int e0 = 0; e0 < count; e0 += THREADS / share) {
+        const int e = e0 + tid / share;
+        const uint64_t mine = e < count ? sh.list[e] : 0u;
+        int place = 0;
+        for (int j = tid % share; j < count; j += share) place += sh.list[j] > mine;
+        for (int o = share / 2; o; o >>= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
+        if (e < count && tid % share == 0 && place < k) {
+            if (blocks == 1) {
+                const int v = index_of(mine);
+                values[r * k + place] = z[v];
+                index[r * k + place] = v;
+            } else {
+                sh.top[place] = mine;
+            }
+        }
+    }
+    if (blocks == 1) return;
+
+    // Several parts: all their lists, each in order, into this block's shared
+    // memory (over the row, which is done with); an entry's place is then the sum
+    // of its places among them.
+    cg::cluster_group cluster = cg::this_cluster();
+    const int mine = min(count, k);
+    if (tid == 0) sh.tops = mine;
+    cluster.sync();
+    uint64_t *const lists = reinterpret_cast<uint64_t *>(raw);
+    __shared__ int counts[8];
+    if (tid < blocks) counts[tid] = cluster.map_shared_rank(&sh, tid)->tops;
+    for (int i = tid; i < blocks * k; i += THREADS) {
+        const int b = i / k, j = i - b * k;
+        lists[i] = cluster.map_shared_rank(&sh, b)->top[j];
+    }
+    cluster.sync();  // nobody leaves while its list may be read
+    for (int e = tid; e < mine; e += THREADS) {
+        const uint64_t m = sh.top[e];
+        int place = e;
+        for (int b = 0; b < blocks; ++b) {
+            if (b == rank) continue;
+            int lo = 0, hi = counts[b];
+            while (lo < hi) {
+                const int mid = (lo + hi) / 2;
+                if (lists[b * k + mid] > m)
+                    lo = mid + 1;
+                else
+                    hi = mid;
+            }
+            place += lo;
+        }
+        if (place < k) {
+            const int v = index_of(m);
+            values[r * k + place] = z[v];
+            index[r * k + place] = v;
+        }
+    }
+}
+
+template <class T, bool KEEP, int THREADS>
+cudaError_t launch(const T *logits, int64_t rows, int vocab, int64_t stride, int k, T *values, int32_t *index, int blocks,
+                   int each, cudaStream_t st)
+{
+    auto *kernel = &topk_kernel<T, KEEP, THREADS>;
+    size_t smem = KEEP ? size_t(each + 1) * 16 : 16;
+    if (blocks > 1 && smem < size_t(blocks) * k * 8) smem = size_t(blocks) * k * 8;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    if (rows * blocks >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(rows * blocks));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(blocks);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = blocks > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, logits, vocab, stride, k, values, index, blocks, each);
+}
+
+template <class T>
+cudaError_t by_size(const T *logits, int64_t rows, int vocab, int64_t stride, int k, T *values, int32_t *index, cudaStream_t st)
+{
+    // The smallest block that holds a row and has threads enough for a close
+    // bound, or as few of the largest as hold it; more of them while rows are so
+    // few that SMs are left over.
+    constexpr int64_t kEach = 25 * 1024 + 512;  // shared memory of 128 threads: eight such blocks to an SM
+    const int64_t units = (int64_t(vocab) * int64_t(sizeof(T)) + 30) / 16, bytes = units * 16;
+    auto each = [&](int64_t blocks) { return int((units + blocks - 1) / blocks); };
+    int threads = bytes <= kEach && k <= 64 ? 128 : bytes <= 2 * kEach && k <= 128 ? 256 : 512;
+    const int64_t most = kEach * threads / 128;
+    int64_t blocks = (bytes + most - 1) / most;
+    while (blocks < 8 && rows * blocks < 152 && bytes / blocks > 16384) blocks = blocks * 2 < 8 ? blocks * 2 : 8;
+    if (blocks > 8) blocks = 8;
+    if (int64_t(each(blocks)) * 16 > 200 * 1024)
+        return launch<T, false, 512>(logits, rows, vocab, stride, k, values, index, int(blocks), each(blocks), st);
+    if (threads == 128) return launch<T, true, 128>(logits, rows, vocab, stride, k, values, index, int(blocks), each(blocks), st);
+    if (threads == 256) return launch<T, true, 256>(logits, rows, vocab, stride, k, values, index, int(blocks), each(blocks), st);
+    return launch<T, true, 512>(logits, rows, vocab, stride, k, values, index, int(blocks), each(blocks), st);
 }
 
 }  // namespace
@@ -57,14 +346,9 @@ __global__ void __launch_bounds__(kThreads) topk_kernel(const T *logits, int64_t
 cudaError_t launch_topk(const void *logits, int dtype, int64_t rows, int vocab, int64_t stride, int k, void *values,
                         int32_t *index, cudaStream_t st)
 {
-    const unsigned blocks = unsigned(rows < 65535 ? rows : 65535);
     if (dtype == ZG_DTYPE_BF16)
-        topk_kernel<<<blocks, kThreads, 0, st>>>(static_cast<const uint16_t *>(logits), rows, vocab, stride, k,
-                                                 static_cast<uint16_t *>(values), index);
-    else
-        topk_kernel<<<blocks, kThreads, 0, st>>>(static_cast<const float *>(logits), rows, vocab, stride, k,
-                                                 static_cast<float *>(values), index);
-    return cudaGetLastError();
+        return by_size(static_cast<const uint16_t *>(logits), rows, vocab, stride, k, static_cast<uint16_t *>(values), index, st);
+    return by_size(static_cast<const float *>(logits), rows, vocab, stride, k, static_cast<float *>(values), index, st);
 }
 
 }  // namespace zg
