@@ -51,7 +51,9 @@ __device__ __forceinline__ int index_of(uint64_t e) { return 0x7fffffff - int(ui
 struct Shared {
     uint64_t list[kMost];
     uint64_t top[ZG_TOPK_MAX];  // this part's, in order; read by the others
-    int count, tops;
+    uint16_t hot[512];  // threads whose maximum reaches the bound
+    uint32_t bound;
+    int hots, count, tops;
     int warps[16];
 };
 
@@ -110,7 +112,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
             commit_copies();
         }
     }
-    if (tid == 0) sh.count = 0;
     typename Unit<T>::Top most;
     if (KEEP) {
 #pragma unroll
@@ -128,29 +129,74 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
     uint32_t best = ragged_key;
     if (tid < units) best = max(best, key_of<T>(__float_as_uint(most.get())));
 
-    // the largest bound, to 16 bits, that k of the threads' maxima reach
-    uint32_t bound = 0u;
-#pragma unroll 1
-    for (int b = kBits - 1; b >= kBits - 16; --b) {
-        const uint32_t with = bound | (1u << b);
-        if (__syncthreads_count(best >= with) >= k) bound = with;
+    // the largest bound, to 16 bits, that k of the threads' maxima reach: one
+    // warp looks for it between the least and the largest of them
+    uint32_t *const bests = reinterpret_cast<uint32_t *>(sh.list);
+    bests[tid] = best >> (kBits - 16);
+    __syncthreads();
+    if (tid < 32) {
+        uint32_t v[kWarps], lo = 0xffffffffu, hi = 0u;
+        int some = 0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            v[i] = bests[tid + 32 * i];
+            some += v[i] != 0u;
+            lo = min(lo, v[i] ? v[i] : 0xffffffffu);
+            hi = max(hi, v[i]);
+        }
+        some = __reduce_add_sync(0xffffffffu, some);
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if (some < k) {
+            lo = 0u;  // everything passes
+        } else {
+            while (lo < hi) {  // lo is reached by k, hi + 1 is not
+                const uint32_t mid = lo + (hi - lo + 1) / 2;
+                int n = 0;
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i) n += v[i] >= mid;
+                if (__reduce_add_sync(0xffffffffu, n) >= k)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+        }
+        if (tid == 0) {
+            sh.bound = lo << (kBits - 16);
+            sh.hots = 0;
+            sh.count = 0;
+        }
     }
-    // what reaches it
+    __syncthreads();
+    const uint32_t bound = sh.bound;
+    // what reaches it: the shares of the threads whose maximum does, spread over all threads
     auto put = [&](uint32_t key, int v) {
         const int n = atomicAdd(&sh.count, 1);
         if (n < kMost) sh.list[n] = entry(key, v);
     };
-    if (best >= bound && best) {
+    if (best && best >= bound) {
         if (ragged >= 0 && ragged_key >= bound) put(ragged_key, ragged);
-        for (int u = tid; u < units; u += THREADS) {
-            const Unit<T> x = unit_at(u);
-            typename Unit<T>::Top top;
-            top.add(x);
-            if (key_of<T>(__float_as_uint(top.get())) < bound) continue;
+        if (tid < units) sh.hot[atomicAdd(&sh.hots, 1)] = uint16_t(tid);
+    }
+    __syncthreads();
+    {
+        const int hots = sh.hots, per = (units + THREADS - 1) / THREADS;
+        int side = 0;  // lanes to a hot thread: a power of two, at most a warp
+        while (side < 5 && (1 << side) < per) ++side;
+        for (int h = tid >> side; h < hots; h += THREADS >> side) {
+            const int first = sh.hot[h];
+            for (int i = tid & ((1 << side) - 1); i < per; i += 1 << side) {
+                const int u = first + i * THREADS;
+                if (u >= units) break;
+                const Unit<T> x = unit_at(u);
+                typename Unit<T>::Top top;
+                top.add(x);
+                if (key_of<T>(__float_as_uint(top.get())) < bound) continue;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint32_t key = key_of<T>(bits_in(x, i));
-                if (key >= bound) put(key, base + u * N + i);
+                for (int j = 0; j < N; ++j) {
+                    const uint32_t key = key_of<T>(bits_in(x, j));
+                    if (key >= bound) put(key, base + u * N + j);
+                }
             }
         }
     }
@@ -248,8 +294,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
         for (int o = share / 2; o; o >>= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
         if (e < count && tid % share == 0 && place < k) {
             if (blocks == 1) {
-                const int v = index_of(mine);
-                values[r * k + place] = z[v];
+                const int v = index_of(mine), i = v - base;
+                values[r * k + place] = KEEP && i >= 0 && i < units * N ? reinterpret_cast<const T *>(kept)[i] : z[v];
                 index[r * k + place] = v;
             } else {
                 sh.top[place] = mine;
