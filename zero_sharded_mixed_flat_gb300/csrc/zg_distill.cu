@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
             cluster.sync();
             s = none();
             for (int i = 0; i < blocks; ++i) s = join(s, cluster.map_shared_rank(&sh, i)->block, c);
-            cluster.sync();  // nobody leaves while its part may be read
+            cluster.barrier_arrive();  // its reads are done; nobody leaves before all are
         }
         const float log_sum = logf(s.sum);
         lse = fmaf(s.top, rt, log_sum);
@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
         for (int i = 0; i < kWarps; ++i) loss += sh.red[i];
         a.loss[r] = empty ? 0.0f : a.temperature * a.temperature * loss;
     }
+    if (LOSS && blocks > 1) cg::this_cluster().barrier_wait();
 }
 
 template <class T, class E, bool LOSS, bool GRAD, bool KEEP, int THREADS>

@@ -34,6 +34,15 @@ __device__ __forceinline__ uint32_t key_of(uint32_t bits)
     if ((bits & 0x7fffffffu) > 0x7f800000u) key = 0xffffffffu;
     return sizeof(T) == 2 ? key >> 16 : key;
 }
+// A binary32 that no value whose key is at least `key` is less than.
+template <class T>
+__device__ __forceinline__ float value_of(uint32_t key)
+{
+    if (sizeof(T) == 2) key <<= 16;
+    if (key == 0u) return -INFINITY;
+    if (key > 0xff800000u) return INFINITY;  // NaNs alone reach it: they are less than nothing
+    return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
+}
 __device__ __forceinline__ uint32_t bits_at(const float *p) { return __float_as_uint(*p); }
 __device__ __forceinline__ uint32_t bits_at(const uint16_t *p) { return uint32_t(*p) << 16; }
 template <class T>
@@ -76,6 +85,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
 {
     extern __shared__ __align__(16) unsigned char raw[];
     __shared__ Shared sh;
+    __shared__ T tops[ZG_TOPK_MAX];  // the logits at sh.top
     constexpr int N = Unit<T>::kN, kWarps = THREADS / 32, kBits = 8 * int(sizeof(T));
     const int tid = threadIdx.x;
     const unsigned number = blockIdx.x / unsigned(blocks);
@@ -169,6 +179,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
     }
     __syncthreads();
     const uint32_t bound = sh.bound;
+    const float least = value_of<T>(bound);
     // what reaches it: the shares of the threads whose maximum does, spread over all threads
     auto put = [&](uint32_t key, int v) {
         const int n = atomicAdd(&sh.count, 1);
@@ -191,11 +202,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
                 const Unit<T> x = unit_at(u);
                 typename Unit<T>::Top top;
                 top.add(x);
-                if (key_of<T>(__float_as_uint(top.get())) < bound) continue;
+                if (top.get() < least) continue;
+                uint32_t hits = 0u;
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const uint32_t key = key_of<T>(bits_in(x, j));
-                    if (key >= bound) put(key, base + u * N + j);
+                for (int j = 0; j < N; ++j) hits |= uint32_t(!(__uint_as_float(bits_in(x, j)) < least)) << j;
+                while (hits) {
+                    const int j = __ffs(int(hits)) - 1;
+                    hits &= hits - 1;
+                    const int v = base + u * N + j;
+                    put(key_of<T>(KEEP ? bits_at(reinterpret_cast<const T *>(&kept[u]) + j) : bits_at(z + v)), v);
                 }
             }
         }
@@ -281,25 +296,64 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
         if (tid == 0) sh.count = min(have, want);
         __syncthreads();
     }
-    // In order: an entry's place is the number of those before it, counted by
-    // the threads that share it.
     const int count = sh.count;
-    int share = 1;
-    while (share < 32 && count * share * 2 <= THREADS) share *= 2;
-    for (int e0 = 0; e0 < count; e0 += THREADS / share) {
-        const int e = e0 + tid / share;
-        const uint64_t mine = e < count ? sh.list[e] : 0u;
-        int place = 0;
-        for (int j = tid % share; j < count; j += share) place += sh.list[j] > mine;
-        for (int o = share / 2; o; o >>= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
-        if (e < count && tid % share == 0 && place < k) {
-            if (blocks == 1) {
-                const int v = index_of(mine), i = v - base;
-                values[r * k + place] = KEEP && i >= 0 && i < units * N ? reinterpret_cast<const T *>(kept)[i] : z[v];
-                index[r * k + place] = v;
-            } else {
-                sh.top[place] = mine;
+    auto value_at = [&](int v) {
+        const int i = v - base;
+        return KEEP && i >= 0 && i < units * N ? reinterpret_cast<const T *>(kept)[i] : z[v];
+    };
+    auto settle = [&](uint64_t e, int place) {
+        const int v = index_of(e);
+        if (blocks == 1) {
+            values[r * k + place] = value_at(v);
+            index[r * k + place] = v;
+        } else {
+            sh.top[place] = e;
+            tops[place] = value_at(v);
+        }
+    };
+    if (count <= 128) {
+        // An entry's place is the number of those before it, counted by the
+        // threads that share it.
+        int share = 1;
+        while (share < 32 && count * share * 2 <= THREADS) share *= 2;
+        for (int e0 = 0; e0 < count; e0 += THREADS / share) {
+            const int e = e0 + tid / share;
+            const uint64_t mine = e < count ? sh.list[e] : 0u;
+            int place = 0;
+            for (int j = tid % share; j < count; j += share) place += sh.list[j] > mine;
+            for (int o = share / 2; o; o >>= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
+            if (e < count && tid % share == 0 && place < k) settle(mine, place);
+        }
+    } else {
+        // More than counting is good for: runs of 32 are sorted by a warp each,
+        // and an entry's place is the sum of its places among the runs.
+        const int runs = (count + 31) / 32;
+        for (int n = tid / 32; n < runs; n += kWarps) {
+            const int e = n * 32 + tid % 32;
+            uint64_t m = e < count ? sh.list[e] : 0u;
+#pragma unroll
+            for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+                for (int o = size / 2; o; o /= 2) {
+                    const uint64_t other = __shfl_xor_sync(0xffffffffu, m, o);
+                    const bool larger = ((tid & o) == 0) == ((tid & 31 & size) == 0);  // this lane takes the larger
+                    if ((other > m) == larger) m = other;
+                }
+            sh.list[e] = m;
+        }
+        __syncthreads();
+        for (int n = tid / 32; n < runs; n += kWarps) {
+            const uint64_t m = sh.list[n * 32 + tid % 32];
+            int place = tid % 32;
+            for (int b = 0; b < runs; ++b) {
+                if (b == n) continue;
+                int at = 0;
+#pragma unroll
+                for (int step = 16; step; step /= 2)
+                    if (sh.list[b * 32 + at + step - 1] > m) at += step;
+                place += at + (at == 31 && sh.list[b * 32 + 31] > m);
             }
+            if (m && place < k) settle(m, place);
         }
     }
     if (blocks == 1) return;
@@ -318,28 +372,28 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
         const int b = i / k, j = i - b * k;
         lists[i] = cluster.map_shared_rank(&sh, b)->top[j];
     }
-    cluster.sync();  // nobody leaves while its list may be read
-    for (int e = tid; e < mine; e += THREADS) {
-        const uint64_t m = sh.top[e];
-        int place = e;
-        for (int b = 0; b < blocks; ++b) {
-            if (b == rank) continue;
-            int lo = 0, hi = counts[b];
-            while (lo < hi) {
-                const int mid = (lo + hi) / 2;
-                if (lists[b * k + mid] > m)
-                    lo = mid + 1;
-                else
-                    hi = mid;
-            }
-            place += lo;
+    cluster.barrier_arrive();  // its reads are done; nobody leaves before all are
+    __syncthreads();
+    // eight lanes to an entry, a list to each
+    for (int e0 = 0; e0 < mine; e0 += THREADS / 8) {
+        const int e = e0 + tid / 8, b = tid % 8;
+        const uint64_t m = e < mine ? sh.top[e] : 0u;
+        int lo = 0, hi = b < blocks && e < mine ? counts[b] : 0;
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (lists[b * k + mid] > m)
+                lo = mid + 1;
+            else
+                hi = mid;
         }
-        if (place < k) {
-            const int v = index_of(m);
-            values[r * k + place] = z[v];
-            index[r * k + place] = v;
+#pragma unroll
+        for (int o = 4; o; o >>= 1) lo += __shfl_xor_sync(0xffffffffu, lo, o);
+        if (e < mine && b == 0 && lo < k) {
+            values[r * k + lo] = tops[e];
+            index[r * k + lo] = index_of(m);
         }
     }
+    cluster.barrier_wait();
 }
 
 template <class T, bool KEEP, int THREADS>
