@@ -476,28 +476,34 @@ def _like(t: torch.Tensor, ref: torch.Tensor, what: str) -> torch.Tensor:
         raise TypeError(f"{what} must be a tensor")
     if not t.is_cuda:
         raise TypeError(f"{what} must be a CUDA tensor")
-    if t.device != ref.device:
-        raise ValueError(f"{what} is on {t.device}, not on {ref.device}")
-    if t.dtype != ref.dtype:
-        raise TypeError(f"{what} must have dtype {ref.dtype} (got {t.dtype})")
-    if t.shape != ref.shape:
-        raise ValueError(f"{what} must have shape {tuple(ref.shape)} (got {tuple(t.shape)})")
+    if t is not ref:
+        if t.get_device() != ref.get_device():
+            raise ValueError(f"{what} is on {t.device}, not on {ref.device}")
+        if t.dtype != ref.dtype:
+            raise TypeError(f"{what} must have dtype {ref.dtype} (got {t.dtype})")
+        if t.shape != ref.shape:
+            raise ValueError(f"{what} must have shape {tuple(ref.shape)} (got {tuple(t.shape)})")
     if t.stride(-1) != 1 and t.shape[-1] != 1:
         raise ValueError(f"the last dimension of {what} must be contiguous")
     return t
 
 
-def _side(t: torch.Tensor | None, dtype: torch.dtype, shape, ref: torch.Tensor, what: str) -> int | None:
+def _side(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, ref: torch.Tensor, what: str) -> int | None:
     """The address of an optional contiguous CUDA tensor of exactly ``shape``."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a tensor")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    if t.is_cuda and t.device != ref.device:
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {shape} (got {tuple(t.shape)})")
+    if t.is_cuda and t.get_device() != ref.get_device():
         raise ValueError(f"{what} is on {t.device}, not on {ref.device}")
     return _dev_ptr(t, dtype, 0, what)
+
+
+def _stream_of(stream, ref: torch.Tensor) -> int:
+    """The given stream's address, or that of ref's device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(ref.get_device()) if stream is None else _stream(stream)
 
 
 class GatedScan:
@@ -517,69 +523,90 @@ class GatedScan:
         self.handle = None
         _check(lib().zg_scan_init(batch, tokens, channels, ctypes.byref(out)), "zg_scan_init")
         self.handle = out.value
+        self._prepare()
+
+    def _prepare(self) -> None:
+        # filled anew by every call, kept only to spare their construction
+        self._shape = _ScanShape()
+        self._views = [_View() for _ in range(5)]
+        self._refs = [ctypes.byref(self._shape), *[ctypes.byref(v) for v in self._views]]
 
     def __del__(self):
         if getattr(self, "handle", None) and _lib is not None:
             _lib.zg_scan_destroy(self.handle)
             self.handle = None
 
-    def _shape(self, x, seq_start) -> tuple[_ScanShape, int]:
-        dt = _dtype(x, "x")
-        if x.dim() not in (2, 3):
-            raise ValueError(f"x must be (batch, tokens, channels) or (tokens, channels) (got {tuple(x.shape)})")
-        b, t, c = x.shape if x.dim() == 3 else (1, *x.shape)
+    def _describe(self, x, f, seq_start) -> int:
+        """Fill the shape and the views of x and f; returns the number of sequences."""
+        dtype = _dtype(x, "x")
         _like(x, x, "x")
+        _like(f, x, "f")
+        s, dims = self._shape, x.dim()
+        s.dtype = dtype
+        if dims == 3:
+            s.batch, s.tokens, s.channels = x.shape
+        elif dims == 2:
+            s.batch = 1
+            s.tokens, s.channels = x.shape
+        else:
+            raise ValueError(f"x must be (batch, tokens, channels) or (tokens, channels) (got {tuple(x.shape)})")
+        self._view(0, x)
+        self._view(1, f)
         if seq_start is None:
-            return _ScanShape(b, t, c, None, 0, dt), b
-        if seq_start.dim() != 1 or seq_start.numel() < 2:
+            s.seq_start, s.n_seq = None, 0
+            return s.batch
+        if not isinstance(seq_start, torch.Tensor) or seq_start.dim() != 1 or seq_start.numel() < 2:
             raise ValueError("seq_start must hold the starts of the sequences and the end of the last")
-        n = seq_start.numel() - 1
-        return _ScanShape(b, t, c, _side(seq_start, torch.int64, (n + 1,), x, "seq_start"), n, dt), n
+        s.n_seq = seq_start.numel() - 1
+        s.seq_start = _side(seq_start, torch.int64, (s.n_seq + 1,), x, "seq_start")
+        return s.n_seq
 
-    @staticmethod
-    def _view(t) -> _View:
-        return _View(t.data_ptr(), t.stride(0) if t.dim() == 3 else 0, t.stride(-2))
+    def _view(self, n: int, t: torch.Tensor) -> None:
+        v = self._views[n]
+        v.ptr = t.data_ptr()
+        if t.dim() == 3:
+            v.batch_stride, v.token_stride, _ = t.stride()
+        else:
+            v.batch_stride, v.token_stride = 0, t.stride(0)
 
     def forward(self, x, f, h0=None, seq_start=None, keep: bool = False, out=None, h_last=None, stream=None):
         """y, the state after each sequence, and with ``keep`` the states that
         ``backward`` starts from (else None). ``out`` and ``h_last`` are
         allocated when None; h_last may be h0 itself."""
-        shape, n = self._shape(x, seq_start)
-        _like(f, x, "f")
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else _like(out, x, "out")
-        last = torch.empty(n, shape.channels, dtype=torch.float32, device=x.device) if h_last is None else h_last
-        side = (n, shape.channels)
-        p0, p1 = _side(h0, torch.float32, side, x, "h0"), _side(last, torch.float32, side, x, "h_last")
-        kept = None
-        if keep:
-            chunks = -(-shape.tokens // ZG_SCAN_CHUNK)
-            kept = torch.empty(shape.batch, chunks, shape.channels, dtype=torch.float32, device=x.device)
-        _check(lib().zg_gated_scan(self.handle, ctypes.byref(shape), ctypes.byref(self._view(x)),
-                                   ctypes.byref(self._view(f)), p0, ctypes.byref(self._view(y)), p1,
-                                   kept.data_ptr() if keep else None, _stream(stream)), "zg_gated_scan")
+        n = self._describe(x, f, seq_start)
+        s, side = self._shape, (n, self._shape.channels)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format) if out is None else _like(out, x, "out")
+        self._view(2, y)
+        p0 = _side(h0, torch.float32, side, x, "h0")
+        last = x.new_empty(side, dtype=torch.float32) if h_last is None else h_last
+        p1 = last.data_ptr() if h_last is None else _side(last, torch.float32, side, x, "h_last")
+        kept = x.new_empty((s.batch, -(-s.tokens // ZG_SCAN_CHUNK), s.channels), dtype=torch.float32) if keep else None
+        r = self._refs
+        _check(_lib.zg_gated_scan(self.handle, r[0], r[1], r[2], p0, r[3], p1, kept.data_ptr() if keep else None,
+                                  _stream_of(stream, x)), "zg_gated_scan")
         return y, last, kept
 
     def backward(self, x, f, dy, kept, h0=None, dh_last=None, seq_start=None, out=None, stream=None):
         """The gradients (dx, df, dh0) from dy and dh_last (None: zero), for the
         x, f and h0 of the forward call that gave ``kept``. ``out``: (dx, df)
         to write into, for instance the parts of one projection's gradient."""
-        shape, n = self._shape(x, seq_start)
-        _like(f, x, "f")
-        _like(dy, x, "dy")
-        if out is None:
-            out = (torch.empty(x.shape, dtype=x.dtype, device=x.device), torch.empty(x.shape, dtype=x.dtype, device=x.device))
-        dx, df = _like(out[0], x, "dx"), _like(out[1], x, "df")
-        dh0 = torch.empty(n, shape.channels, dtype=torch.float32, device=x.device)
-        side = (n, shape.channels)
-        chunks = -(-shape.tokens // ZG_SCAN_CHUNK)
+        n = self._describe(x, f, seq_start)
+        s, side = self._shape, (n, self._shape.channels)
+        self._view(2, _like(dy, x, "dy"))
         if kept is None:
             raise ValueError("kept is None: call forward with keep=True")
-        _check(lib().zg_gated_scan_bwd(
-            self.handle, ctypes.byref(shape), ctypes.byref(self._view(x)), ctypes.byref(self._view(f)),
-            ctypes.byref(self._view(dy)), _side(kept, torch.float32, (shape.batch, chunks, shape.channels), x, "kept"),
-            _side(h0, torch.float32, side, x, "h0"), _side(dh_last, torch.float32, side, x, "dh_last"),
-            ctypes.byref(self._view(dx)), ctypes.byref(self._view(df)), dh0.data_ptr(), _stream(stream)),
-            "zg_gated_scan_bwd")
+        if out is None:
+            dx, df = (torch.empty_like(x, memory_format=torch.contiguous_format) for _ in range(2))
+        else:
+            dx, df = _like(out[0], x, "dx"), _like(out[1], x, "df")
+        self._view(3, dx)
+        self._view(4, df)
+        dh0 = x.new_empty(side, dtype=torch.float32)
+        pk = _side(kept, torch.float32, (s.batch, -(-s.tokens // ZG_SCAN_CHUNK), s.channels), x, "kept")
+        r = self._refs
+        _check(_lib.zg_gated_scan_bwd(self.handle, r[0], r[1], r[2], r[3], pk, _side(h0, torch.float32, side, x, "h0"),
+                                      _side(dh_last, torch.float32, side, x, "dh_last"), r[4], r[5], dh0.data_ptr(),
+                                      _stream_of(stream, x)), "zg_gated_scan_bwd")
         return dx, df, dh0
 
     def step(self, x, f, state, out_state=None, out=None, stream=None):
@@ -587,9 +614,21 @@ class GatedScan:
         state, written to ``out_state`` (``state`` itself to update it in place)."""
         if not isinstance(x, torch.Tensor) or x.dim() != 2:
             raise ValueError("x must be (batch, channels)")
-        y, last, _ = self.forward(x[:, None], f[:, None], state, out=None if out is None else out[:, None],
-                                  h_last=out_state, stream=stream)
-        return y[:, 0], last
+        self._describe(x, f, None)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format) if out is None else _like(out, x, "out")
+        self._view(2, y)
+        # each row is a sequence of one token: what was the token stride leads from row to row
+        s, side = self._shape, tuple(x.shape)
+        s.batch, s.tokens = s.tokens, 1
+        for v in self._views[:3]:
+            v.batch_stride = v.token_stride
+        p0 = _side(state, torch.float32, side, x, "state")
+        last = x.new_empty(side, dtype=torch.float32) if out_state is None else out_state
+        p1 = last.data_ptr() if out_state is None else _side(last, torch.float32, side, x, "out_state")
+        r = self._refs
+        _check(_lib.zg_gated_scan(self.handle, r[0], r[1], r[2], p0, r[3], p1, None, _stream_of(stream, x)),
+               "zg_gated_scan")
+        return y, last
 
     def status(self, stream=None) -> int:
         """ZG_OK, or ZG_ERR_DEVICE_TIMEOUT when a scan's bounded wait ran out (waits for the stream)."""
@@ -614,10 +653,9 @@ def topk_logits(logits, k: int, stream=None) -> tuple[torch.Tensor, torch.Tensor
     ties to the lowest index: values (rows, k) and int32 indices."""
     _rows(logits, "logits")
     n, v = logits.shape
-    values = torch.empty(n, k, dtype=logits.dtype, device=logits.device)
-    index = torch.empty(n, k, dtype=torch.int32, device=logits.device)
+    values, index = logits.new_empty((n, k)), logits.new_empty((n, k), dtype=torch.int32)
     _check(lib().zg_topk(logits.data_ptr(), _DTYPES[logits.dtype], n, v, _row_stride(logits), k, values.data_ptr(),
-                         index.data_ptr(), _stream(stream)), "zg_topk")
+                         index.data_ptr(), _stream_of(stream, logits)), "zg_topk")
     return values, index
 
 
@@ -638,10 +676,14 @@ def distill_loss(logits, t_logits, t_index, temperature: float, stream=None) -> 
     against the teacher's entries ``t_logits`` and ``t_index`` (rows, k; index
     -1 for none), and each row's log-sum-exp of logits / temperature."""
     a = _distill(logits, t_logits, t_index, temperature)
-    loss = torch.empty(2, a.rows, dtype=torch.float32, device=logits.device)
-    _check(lib().zg_distill_loss(ctypes.byref(a), loss.data_ptr(), loss.data_ptr() + 4 * a.rows, _stream(stream)),
+    loss, lse = (logits.new_empty(a.rows, dtype=torch.float32) for _ in range(2))
+    _check(lib().zg_distill_loss(ctypes.byref(a), loss.data_ptr(), lse.data_ptr(), _stream_of(stream, logits)),
            "zg_distill_loss")
-    return loss[0], loss[1]
+    return loss, lse
+
+
+def _gradient_of(logits, out) -> torch.Tensor:
+    return torch.empty_like(logits, memory_format=torch.contiguous_format) if out is None else _like(out, logits, "out")
 
 
 def distill_grad(logits, lse, t_logits, t_index, temperature: float, scale: float = 1.0, dloss=None, out=None,
@@ -649,10 +691,10 @@ def distill_grad(logits, lse, t_logits, t_index, temperature: float, scale: floa
     """The gradient of sum(scale * dloss * loss) by the logits, from the lse of
     ``distill_loss`` (dloss None: ones). ``out`` may be the logits themselves."""
     a = _distill(logits, t_logits, t_index, temperature)
-    out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device) if out is None else _like(out, logits, "out")
+    out = _gradient_of(logits, out)
     _check(lib().zg_distill_grad(ctypes.byref(a), _side(lse, torch.float32, (a.rows,), logits, "lse"), scale,
                                  _side(dloss, torch.float32, (a.rows,), logits, "dloss"), out.data_ptr(),
-                                 _row_stride(out), _stream(stream)), "zg_distill_grad")
+                                 _row_stride(out), _stream_of(stream, logits)), "zg_distill_grad")
     return out
 
 
@@ -661,9 +703,9 @@ def distill_loss_grad(logits, t_logits, t_index, temperature: float, scale: floa
     """The loss of each row and the gradient of sum(scale * dloss * loss) by the
     logits, in one pass over them. ``out`` may be the logits themselves."""
     a = _distill(logits, t_logits, t_index, temperature)
-    out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device) if out is None else _like(out, logits, "out")
-    loss = torch.empty(a.rows, dtype=torch.float32, device=logits.device)
+    out = _gradient_of(logits, out)
+    loss = logits.new_empty(a.rows, dtype=torch.float32)
     _check(lib().zg_distill_loss_grad(ctypes.byref(a), scale, _side(dloss, torch.float32, (a.rows,), logits, "dloss"),
-                                      loss.data_ptr(), None, out.data_ptr(), _row_stride(out), _stream(stream)),
-           "zg_distill_loss_grad")
+                                      loss.data_ptr(), None, out.data_ptr(), _row_stride(out),
+                                      _stream_of(stream, logits)), "zg_distill_loss_grad")
     return loss, out

@@ -428,7 +428,7 @@ cudaError_t launch(const DistillArgs &a, int blocks, int each, cudaStream_t st)
     // a spare unit, which a read across units may touch
     const size_t smem = KEEP ? size_t(each + 1) * 16 : 0;
     if (smem) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
         if (e != cudaSuccess) return e;
     }
     if (a.rows * blocks >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;

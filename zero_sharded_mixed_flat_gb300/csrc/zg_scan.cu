@@ -1074,7 +1074,7 @@ cudaError_t launch(Kernel *kernel, const ScanArgs &a, const ScanWork &sw, const 
 {
     constexpr size_t smem = kTileBytes<T, BWD>;
     if (g.places >= int64_t(0xf0000000)) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
     Work w{};
     w.ctl = sw.ctl;

@@ -403,7 +403,7 @@ cudaError_t launch(const T *logits, int64_t rows, int vocab, int64_t stride, int
     auto *kernel = &topk_kernel<T, KEEP, THREADS>;
     size_t smem = KEEP ? size_t(each + 1) * 16 : 16;
     if (blocks > 1 && smem < size_t(blocks) * k * 8) smem = size_t(blocks) * k * 8;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
     if (rows * blocks >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg{};
