@@ -371,13 +371,14 @@ void zg_destroy(zg_ctx *ctx);
 /* The gated linear recurrence over time, channel by channel:
  *   a_t = sigmoid(f_t),  h_t = a_t * h_{t-1} + (1 - a_t) * x_t,  y_t = h_t,
  * where 1 - a_t is computed as sigmoid(-f_t), not as a difference. The state h
- * is binary32. f_t = -inf forgets everything before t. A NaN or infinity in
+ * is binary32. f_t = -inf leaves less than 2^-120 of what was
+ * before t, f_t = +inf holds it and adds nothing. A NaN or infinity in
  * one sequence or channel stays in that sequence and channel. */
 
 /* Element (b, t, c) is ptr[b * batch_stride + t * token_stride + c], strides
  * in elements: channels are contiguous, so a tensor can be a part of a wider
- * projection's output. ptr is aligned to its element; from 2 elements of
- * alignment on (pointer and strides) loads take two channels at a time. */
+ * projection's output. ptr is aligned to its element; pointers and strides that
+ * are multiples of 16 bytes are read fastest. */
 typedef struct {
     void *ptr;
     int64_t batch_stride, token_stride; /* >= 0; an output's must not make elements overlap */
@@ -389,8 +390,9 @@ typedef struct {
  * [seq_start[s], seq_start[s+1]), where seq_start is a device array of
  * n_seq + 1 non-decreasing int64 from 0 up to at most `tokens`; a sequence
  * may be empty. Tokens at or past seq_start[n_seq] belong to no sequence:
- * nothing of them is read or written. (Values that break this give
- * unspecified results, but no access outside the buffers.) */
+ * what they hold does not matter, and nothing of theirs is written. (Values
+ * that break this give unspecified results, but no access outside the
+ * buffers.) */
 typedef struct {
     int64_t batch, tokens, channels;
     const int64_t *seq_start;
@@ -406,8 +408,9 @@ typedef struct zg_scan zg_scan; /* opaque; the workspace of one stream's scans *
 
 /* Create the workspace for scans of up to batch rows of up to `tokens` tokens
  * by `channels` channels on the current device (each at least 1). One handle
- * serves any smaller shape too, and one stream at a time. About 0.16 bytes
- * per element; none for tokens <= ZG_SCAN_CHUNK. *out is NULL on failure. */
+ * serves any smaller shape too, and one stream at a time. About 0.14 bytes per
+ * element (channels counted in 64s); next to none for tokens <= ZG_SCAN_CHUNK.
+ * *out is NULL on failure. */
 int zg_scan_init(int64_t batch, int64_t tokens, int64_t channels, zg_scan **out);
 void zg_scan_destroy(zg_scan *scan);
 
@@ -465,8 +468,8 @@ int zg_topk(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t 
  *   loss = T^2 * sum_j p_j (log p_j - log q_{i_j}),
  *   dlogits_v = scale * dloss * T * (q_v - sum of the p_j with i_j = v).
  * A term with p_j = 0 counts as zero. A row without a present entry, or whose
- * present entries are all -inf, is empty: its logits are not looked at, its
- * loss, lse and gradient are zero (a padding row). A logit of -inf has
+ * present entries are all -inf, is empty (a padding row): its loss, lse and
+ * gradient are zero, whatever its logits are. A logit of -inf has
  * q = 0. Entries may come in any order; a repeated index adds up. */
 typedef struct {
     const void *logits; /* row r starts at logits + r * row_stride elements; aligned to its element */

@@ -294,3 +294,18 @@ def test_refusals():
         scan.forward(x, x, out=x[:, :1].expand(2, 64, 32))
     with pytest.raises(ValueError, match="kept is None"):
         scan.backward(x, x, x, None)
+
+
+def test_a_wait_that_runs_out_is_reported_and_forgotten():
+    b, t, c = 1, 20000, 130
+    x, f = views(b, t, c, torch.bfloat16, "plain", 61)
+    scan = zb.GatedScan(b, t, c)
+    want = scan.forward(x, f)[0]
+    assert scan.status() == zb.ZG_OK
+    scan.set_wait_limit(0)  # every first look that finds nothing gives up
+    scan.forward(x, f)
+    assert scan.status() == zb.ZG_ERR_DEVICE_TIMEOUT
+    assert scan.status() == zb.ZG_OK
+    scan.set_wait_limit(4000000)
+    assert torch.equal(scan.forward(x, f)[0], want)
+    assert scan.status() == zb.ZG_OK

@@ -630,6 +630,10 @@ class GatedScan:
                "zg_gated_scan")
         return y, last
 
+    def set_wait_limit(self, polls: int) -> None:
+        """Bound, in polls, on a block's wait for the tokens before its own."""
+        _check(lib().zg_scan_set_wait_limit(self.handle, polls), "zg_scan_set_wait_limit")
+
     def status(self, stream=None) -> int:
         """ZG_OK, or ZG_ERR_DEVICE_TIMEOUT when a scan's bounded wait ran out (waits for the stream)."""
         st = ctypes.c_int()

@@ -17,7 +17,6 @@ struct zg_scan {
     int64_t batch, tokens, channels;
     int64_t record_bytes;
     char *d_mem;  // ctl (8 bytes), status (4 bytes), and from kHead on the records
-    int *h_status;
     long long wait_limit;
 };
 
@@ -208,7 +207,6 @@ int zg_scan_init(int64_t batch, int64_t tokens, int64_t channels, zg_scan **out)
     s->wait_limit = kScanWaitLimit;
     s->record_bytes = zg::scan_record_bytes(batch, tokens, channels);
     cudaError_t e = cudaGetDevice(&s->device);
-    if (e == cudaSuccess) e = cudaMallocHost(&s->h_status, sizeof(int));
     if (e == cudaSuccess) e = cudaMalloc(&s->d_mem, size_t(kHead + s->record_bytes));
     if (e == cudaSuccess) e = cudaMemset(s->d_mem, 0, size_t(kHead + s->record_bytes));
     // epoch 1: the cleared records belong to no launch
@@ -231,7 +229,6 @@ void zg_scan_destroy(zg_scan *s)
 {
     if (!s) return;
     if (s->d_mem) cudaFree(s->d_mem);
-    if (s->h_status) cudaFreeHost(s->h_status);
     delete s;
 }
 
@@ -248,10 +245,11 @@ int zg_scan_status(zg_scan *s, zg_stream stream, int *status)
     if (!s) return fail(ZG_ERR_INVALID_ARG, "scan handle is NULL");
     if (!status) return fail(ZG_ERR_INVALID_ARG, "status is NULL");
     int *d_status = work_of(s).status;
-    cudaError_t e = cudaMemcpyAsync(s->h_status, d_status, sizeof(int), cudaMemcpyDeviceToHost, stream);
+    int found = 0;
+    cudaError_t e = cudaMemcpyAsync(&found, d_status, sizeof(int), cudaMemcpyDeviceToHost, stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return finish(e, "zg_scan_status");
-    *status = *s->h_status;
+    *status = found;
     if (*status == ZG_OK) return ZG_OK;
     return finish(cudaMemsetAsync(d_status, 0, sizeof(int), stream), "zg_scan_status reset");
 }
