@@ -122,6 +122,21 @@ __device__ __forceinline__ F4 decay(F4 f)
 {
     return F4{decay<T>(f.lo), decay<T>(f.hi)};
 }
+// The reciprocal once more, in a pass that is not to find the first one's kept
+// in registers.
+__device__ __forceinline__ float rcp_again(float v)
+{
+    float d;
+    asm volatile("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
+    return d;
+}
+__device__ __forceinline__ void gates_again(float2 e, float2 &keep, float2 &take)
+{
+    const float2 d = add_f32x2(e, make_float2(1.0f, 1.0f));
+    const float2 r = make_float2(rcp_again(d.x), rcp_again(d.y));
+    keep = add_f32x2(r, make_float2(-kKeepAtLowest, -kKeepAtLowest));
+    take = mul_f32x2(e, r);
+}
 __device__ __forceinline__ void gates(float2 e, float2 &keep, float2 &take)
 {
     const float2 d = add_f32x2(e, make_float2(1.0f, 1.0f));
@@ -133,6 +148,12 @@ __device__ __forceinline__ void gates(F4 e, F4 &keep, F4 &take)
 {
     gates(e.lo, keep.lo, take.lo);
     gates(e.hi, keep.hi, take.hi);
+}
+
+__device__ __forceinline__ void gates_again(F4 e, F4 &keep, F4 &take)
+{
+    gates_again(e.lo, keep.lo, take.lo);
+    gates_again(e.hi, keep.hi, take.hi);
 }
 
 // A map of the state, h -> a h + b: for a lane's four channels of a run, and for
@@ -941,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
         for (int i = 0; i < kRun; ++i) {
             if (PACKED && (mk.first >> i & 1)) h = side(a.h0, sh.cuts.first, i);
             F4 keep, take;
-            gates(e[i], keep, take);
+            gates_again(e[i], keep, take);
             const F4 xx = read4<VEC>(bx + (run * kRun + i) * kTile, l);
             over[i] = sub(h, xx);
             h = fma(keep, h, mul(take, xx));
@@ -954,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
             if (plain || t0 + i < end) {
                 if (PACKED && (mk.last >> i & 1)) gr = side(a.dh_last, sh.cuts.last, i);
                 F4 keep, take;
-                gates(e[i], keep, take);
+                gates_again(e[i], keep, take);
                 gr = add(read4<VEC>(bx + kSize + (run * kRun + i) * kTile, l), gr);
                 const F4 dx = mul(take, gr);
                 store4<VEC>(px, l, n, dx);
