@@ -578,9 +578,11 @@ class GatedScan:
         y = torch.empty_like(x, memory_format=torch.contiguous_format) if out is None else _like(out, x, "out")
         self._view(2, y)
         p0 = _side(h0, torch.float32, side, x, "h0")
-        last = x.new_empty(side, dtype=torch.float32) if h_last is None else h_last
+        last = torch.empty(side, dtype=torch.float32, device=x.device) if h_last is None else h_last
         p1 = last.data_ptr() if h_last is None else _side(last, torch.float32, side, x, "h_last")
-        kept = x.new_empty((s.batch, -(-s.tokens // ZG_SCAN_CHUNK), s.channels), dtype=torch.float32) if keep else None
+        kept = None
+        if keep:
+            kept = torch.empty((s.batch, -(-s.tokens // ZG_SCAN_CHUNK), s.channels), dtype=torch.float32, device=x.device)
         r = self._refs
         _check(_lib.zg_gated_scan(self.handle, r[0], r[1], r[2], p0, r[3], p1, kept.data_ptr() if keep else None,
                                   _stream_of(stream, x)), "zg_gated_scan")
@@ -601,7 +603,7 @@ class GatedScan:
             dx, df = _like(out[0], x, "dx"), _like(out[1], x, "df")
         self._view(3, dx)
         self._view(4, df)
-        dh0 = x.new_empty(side, dtype=torch.float32)
+        dh0 = torch.empty(side, dtype=torch.float32, device=x.device)
         pk = _side(kept, torch.float32, (s.batch, -(-s.tokens // ZG_SCAN_CHUNK), s.channels), x, "kept")
         r = self._refs
         _check(_lib.zg_gated_scan_bwd(self.handle, r[0], r[1], r[2], r[3], pk, _side(h0, torch.float32, side, x, "h0"),
@@ -623,7 +625,7 @@ class GatedScan:
         for v in self._views[:3]:
             v.batch_stride = v.token_stride
         p0 = _side(state, torch.float32, side, x, "state")
-        last = x.new_empty(side, dtype=torch.float32) if out_state is None else out_state
+        last = torch.empty(side, dtype=torch.float32, device=x.device) if out_state is None else out_state
         p1 = last.data_ptr() if out_state is None else _side(last, torch.float32, side, x, "out_state")
         r = self._refs
         _check(_lib.zg_gated_scan(self.handle, r[0], r[1], r[2], p0, r[3], p1, None, _stream_of(stream, x)),
@@ -657,7 +659,8 @@ def topk_logits(logits, k: int, stream=None) -> tuple[torch.Tensor, torch.Tensor
     ties to the lowest index: values (rows, k) and int32 indices."""
     _rows(logits, "logits")
     n, v = logits.shape
-    values, index = logits.new_empty((n, k)), logits.new_empty((n, k), dtype=torch.int32)
+    values = torch.empty((n, k), dtype=logits.dtype, device=logits.device)
+    index = torch.empty((n, k), dtype=torch.int32, device=logits.device)
     _check(lib().zg_topk(logits.data_ptr(), _DTYPES[logits.dtype], n, v, _row_stride(logits), k, values.data_ptr(),
                          index.data_ptr(), _stream_of(stream, logits)), "zg_topk")
     return values, index
@@ -680,7 +683,8 @@ def distill_loss(logits, t_logits, t_index, temperature: float, stream=None) -> 
     against the teacher's entries ``t_logits`` and ``t_index`` (rows, k; index
     -1 for none), and each row's log-sum-exp of logits / temperature."""
     a = _distill(logits, t_logits, t_index, temperature)
-    loss, lse = (logits.new_empty(a.rows, dtype=torch.float32) for _ in range(2))
+    loss = torch.empty(a.rows, dtype=torch.float32, device=logits.device)
+    lse = torch.empty(a.rows, dtype=torch.float32, device=logits.device)
     _check(lib().zg_distill_loss(ctypes.byref(a), loss.data_ptr(), lse.data_ptr(), _stream_of(stream, logits)),
            "zg_distill_loss")
     return loss, lse
@@ -708,7 +712,7 @@ def distill_loss_grad(logits, t_logits, t_index, temperature: float, scale: floa
     logits, in one pass over them. ``out`` may be the logits themselves."""
     a = _distill(logits, t_logits, t_index, temperature)
     out = _gradient_of(logits, out)
-    loss = logits.new_empty(a.rows, dtype=torch.float32)
+    loss = torch.empty(a.rows, dtype=torch.float32, device=logits.device)
     _check(lib().zg_distill_loss_grad(ctypes.byref(a), scale, _side(dloss, torch.float32, (a.rows,), logits, "dloss"),
                                       loss.data_ptr(), None, out.data_ptr(), _row_stride(out),
                                       _stream_of(stream, logits)), "zg_distill_loss_grad")
