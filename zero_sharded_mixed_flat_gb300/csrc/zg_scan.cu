@@ -98,9 +98,8 @@ constexpr float kKeepAtLowest = 2.71337577e-38f;  // exp(kLowest), less 4e-5 of 
 constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f;
 
 template <class T>
-__device__ __forceinline__ float2 decay(float2 f)
+__device__ __forceinline__ float2 decay(float2 f)  // f at least kLowest, or NaN
 {
-    f = make_float2(max_nan(f.x, kLowest), max_nan(f.y, kLowest));
     float2 e;
     if (sizeof(T) == 2) {
         const float2 t = mul_f32x2(f, make_float2(-kLog2e, -kLog2e));
@@ -225,34 +224,38 @@ __device__ __forceinline__ bool go_on(const Work &w, long long polls)
     return (polls & 63) != 63 || *reinterpret_cast<volatile int *>(w.status) == 0;
 }
 
-// Up to four maps of one slot, asked for together and composed in order.
+// Up to four maps of one slot, asked for together and composed in order. The
+// places past the last are filled with it again, which takes no branch and
+// counts for nothing; without any, nothing is asked for.
 struct Four {
     const ulonglong2 *p;
     int64_t step;
-    int count;
+    int count;  // the same in all lanes of a warp
     ulonglong2 v[4];
     __device__ __forceinline__ void ask()
     {
+        if (count <= 0) return;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < count) v[i] = look(p + i * step);
+        for (int i = 0; i < 4; ++i) v[i] = look(p + min(i, count - 1) * step);
     }
     // Where the wait runs out, what is not there is undefined.
     template <bool CUT>
     __device__ __forceinline__ float2 get(uint32_t tag, const Work &w)
     {
+        if (count <= 0) return make_float2(1.0f, 0.0f);
         for (long long polls = 0;; ++polls) {
-            bool ready = true;
+            uint32_t off = 0u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < count) ready = ready && there(v[i], tag);
-            if (ready || !go_on(w, polls)) break;
+            for (int i = 0; i < 4; ++i) off |= (uint32_t(v[i].x >> 32) ^ tag) | (uint32_t(v[i].y >> 32) ^ tag);
+            if (off == 0u || !go_on(w, polls)) break;
             ask();
         }
-        float2 m = make_float2(1.0f, 0.0f);
+        float2 m = values(v[0]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < count) m = then<CUT>(m, values(v[i]));
+        for (int i = 1; i < 4; ++i) {
+            const float2 n = values(v[i]), both = then<CUT>(m, n);
+            m = make_float2(i < count ? both.x : m.x, i < count ? both.y : m.y);
+        }
         return m;
     }
 };
@@ -443,11 +446,33 @@ __device__ __forceinline__ F4 read4(const uint16_t *row, int l)
     }
     return F4{make_float2(bf16_lo(row[l]), bf16_lo(row[l + 16])), make_float2(bf16_lo(row[l + 32]), bf16_lo(row[l + 48]))};
 }
+// The same of f, held above kLowest.
+template <bool VEC>
+__device__ __forceinline__ F4 read_f4(const uint16_t *row, int l)
+{
+    uint2 w;
+    if (VEC)
+        w = *reinterpret_cast<const uint2 *>(row + 4 * l);
+    else
+        w = make_uint2(row[l] | uint32_t(row[l + 16]) << 16, row[l + 32] | uint32_t(row[l + 48]) << 16);
+    constexpr uint32_t kLowest2 = 0xc2adc2adu;  // kLowest twice in bf16
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.x) : "r"(kLowest2));
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.y) : "r"(kLowest2));
+    return F4{make_float2(bf16_lo(w.x), bf16_hi(w.x)), make_float2(bf16_lo(w.y), bf16_hi(w.y))};
+}
 template <bool VEC>
 __device__ __forceinline__ F4 read4(const float *row, int l)
 {
     if (VEC) return lds4(row + 4 * l);
     return F4{make_float2(row[l], row[l + 16]), make_float2(row[l + 32], row[l + 48])};
+}
+
+template <bool VEC>
+__device__ __forceinline__ F4 read_f4(const float *row, int l)
+{
+    const F4 f = read4<VEC>(row, l);
+    return F4{make_float2(max_nan(f.lo.x, kLowest), max_nan(f.lo.y, kLowest)),
+              make_float2(max_nan(f.hi.x, kLowest), max_nan(f.hi.y, kLowest))};
 }
 
 // Lane l's four channels of a row of a tile, `n` of whose channels exist.
@@ -652,7 +677,11 @@ __device__ __forceinline__ void solve(Sh &sh, Before &before, const Work &w, con
     for (int i = 0; i < 4; ++i) h = apply<CUT>(sh.groups[i][slot], h);
 #pragma unroll
     for (int i = 0; i < 4; ++i) h = apply<CUT>(sh.chunks[i][slot], h);
-    for (int i = 0; i < part; ++i) h = apply<CUT>(sh.quarters[i][slot], h);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const float next = apply<CUT>(sh.quarters[i][slot], h);
+        h = i < part ? next : h;
+    }
     h = mine.run<CUT>(sh.runs, part, slot, h);
     if (part == 3 && ends_group && before.group == kGroup - 1) put(w.span + this_group / kGroup * step + at, h, h, tag);
     __syncthreads();
@@ -788,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
             F4 take;
-            gates(decay<T>(read4<VEC>(bf + (run * kRun + i) * kTile, l)), keep[i], take);
+            gates(decay<T>(read_f4<VEC>(bf + (run * kRun + i) * kTile, l)), keep[i], take);
             in[i] = mul(take, read4<VEC>(bx + (run * kRun + i) * kTile, l));
             if (PACKED && (mk.first >> i & 1)) {
                 m.b = fma(keep[i], initial(i), in[i]);
@@ -817,16 +846,24 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
         if (a.states && run == 0)
             put_state4<VEC>(a.states + (t.row * g.chunks + t.chunk) * a.channels + t.ch, l, n, h);
         T *py = static_cast<T *>(a.y.ptr) + t.row * a.y.sb + t0 * a.y.st + t.ch;
-        const bool plain = t0 + kRun < end && (!PACKED || !(mk.first | mk.last));
+        if (t0 + kRun < end && (!PACKED || !(mk.first | mk.last))) {
 #pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            if (PACKED && (mk.first >> i & 1)) h = initial(i);
-            h = fma(keep[i], h, in[i]);
-            if (plain || t0 + i < end) store4<VEC>(py, l, n, h);
-            py += a.y.st;
-            if (!plain && a.h_last && (PACKED ? mk.last >> i & 1 : t0 + i == end - 1))
-                put_state4<VEC>(a.h_last + (PACKED ? int64_t(sh.cuts.last[run * kRun + i]) : int64_t(t.row)) * a.channels + t.ch,
-                                l, n, h);
+            for (int i = 0; i < kRun; ++i) {
+                h = fma(keep[i], h, in[i]);
+                store4<VEC>(py, l, n, h);
+                py += a.y.st;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) {
+                if (PACKED && (mk.first >> i & 1)) h = initial(i);
+                h = fma(keep[i], h, in[i]);
+                if (t0 + i < end) store4<VEC>(py, l, n, h);
+                py += a.y.st;
+                if (a.h_last && (PACKED ? mk.last >> i & 1 : t0 + i == end - 1))
+                    put_state4<VEC>(a.h_last + (PACKED ? int64_t(sh.cuts.last[run * kRun + i]) : int64_t(t.row)) * a.channels + t.ch,
+                                    l, n, h);
+            }
         }
         if (EARLY) {
             ahead.done(u, g);
@@ -910,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
             F4 keep, take;
-            e[i] = decay<T>(read4<VEC>(bf + (run * kRun + i) * kTile, l));
+            e[i] = decay<T>(read_f4<VEC>(bf + (run * kRun + i) * kTile, l));
             gates(e[i], keep, take);
             const F4 in = mul(take, read4<VEC>(bx + (run * kRun + i) * kTile, l));
             if (PACKED && (mk.first >> i & 1)) {
@@ -969,23 +1006,34 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
         }
         T *px = static_cast<T *>(a.dx.ptr) + t.row * a.dx.sb + (t0 + kRun - 1) * a.dx.st + t.ch;
         T *pf = static_cast<T *>(a.df.ptr) + t.row * a.df.sb + (t0 + kRun - 1) * a.df.st + t.ch;
-        const bool plain = t0 + kRun <= end && (!PACKED || !(mk.first | mk.last));
+        auto back = [&](int i) {
+            F4 keep, take;
+            gates_again(e[i], keep, take);
+            gr = add(read4<VEC>(bx + kSize + (run * kRun + i) * kTile, l), gr);
+            const F4 dx = mul(take, gr);
+            store4<VEC>(px, l, n, dx);
+            gr = mul(keep, gr);
+            store4<VEC>(pf, l, n, mul(mul(over[i], keep), dx));
+        };
+        if (t0 + kRun <= end && (!PACKED || !(mk.first | mk.last))) {
 #pragma unroll
-        for (int i = kRun - 1; i >= 0; --i) {
-            if (plain || t0 + i < end) {
-                if (PACKED && (mk.last >> i & 1)) gr = side(a.dh_last, sh.cuts.last, i);
-                F4 keep, take;
-                gates_again(e[i], keep, take);
-                gr = add(read4<VEC>(bx + kSize + (run * kRun + i) * kTile, l), gr);
-                const F4 dx = mul(take, gr);
-                store4<VEC>(px, l, n, dx);
-                gr = mul(keep, gr);
-                store4<VEC>(pf, l, n, mul(mul(over[i], keep), dx));
-                if (PACKED && a.dh0 && (mk.first >> i & 1))
-                    put_state4<VEC>(a.dh0 + sh.cuts.first[run * kRun + i] * a.channels + t.ch, l, n, gr);
+            for (int i = kRun - 1; i >= 0; --i) {
+                back(i);
+                px -= a.dx.st;
+                pf -= a.df.st;
             }
-            px -= a.dx.st;
-            pf -= a.df.st;
+        } else {
+#pragma unroll
+            for (int i = kRun - 1; i >= 0; --i) {
+                if (t0 + i < end) {
+                    if (PACKED && (mk.last >> i & 1)) gr = side(a.dh_last, sh.cuts.last, i);
+                    back(i);
+                    if (PACKED && a.dh0 && (mk.first >> i & 1))
+                        put_state4<VEC>(a.dh0 + sh.cuts.first[run * kRun + i] * a.channels + t.ch, l, n, gr);
+                }
+                px -= a.dx.st;
+                pf -= a.df.st;
+            }
         }
         if (!PACKED && a.dh0 && t0 == 0) put_state4<VEC>(a.dh0 + t.row * a.channels + t.ch, l, n, gr);
         if (EARLY) {
@@ -1040,7 +1088,8 @@ __global__ void __launch_bounds__(128) few_kernel(ScanArgs a)
 #pragma unroll
     for (int t = 0; t < N; ++t) {
         float2 k, u;
-        gates(decay<T>(make_float2(f[t], f[t])), k, u);
+        const float ft = max_nan(f[t], kLowest);
+        gates(decay<T>(make_float2(ft, ft)), k, u);
         before[t] = h;
         f[t] = k.x;
         take[t] = u.x;
