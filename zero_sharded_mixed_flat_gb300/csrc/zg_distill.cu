@@ -137,14 +137,11 @@ __device__ __forceinline__ void read_shifted(const float *base, int i, Unit<floa
     x.w = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// KEEP: the part is copied into shared memory, in kStages groups, and both
-// passes read it there; else the one pass reads it from memory. Without LOSS,
-// lse is given. A row takes `blocks` blocks of `each` units: with LOSS a cluster,
-// in which they exchange sums.
-template <class T, class E, bool LOSS, bool GRAD, bool KEEP, int THREADS>
+// Without LOSS, lse is given. A row takes `blocks` blocks of `each` units: with
+// LOSS a cluster, in which they exchange sums.
+template <class T, class E, bool LOSS, bool GRAD, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(DistillArgs a, int blocks, int each)
 {
-    extern __shared__ __align__(16) unsigned char raw[];
     __shared__ Shared<THREADS> sh;
     constexpr int N = Unit<T>::kN, kWarps = THREADS / 32, kEntries = (ZG_TOPK_MAX + THREADS - 1) / THREADS;
     const int tid = threadIdx.x;
@@ -152,99 +149,68 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
     const int64_t r = number;
     const int rank = int(blockIdx.x - number * unsigned(blocks));
     const float rt = 1.0f / a.temperature, c = rt * kLog2e;
-    Unit<T> *const kept = reinterpret_cast<Unit<T> *>(raw);  // unit u0 + i at kept[i]
-    const Row<T> row(static_cast<const T *>(a.logits) + r * a.row_stride, a.vocab, each, rank, THREADS);
+    const Row<T> row(static_cast<const T *>(a.logits) + r * a.row_stride, a.vocab, each, rank);
     const Part &part = row.part;
     const T *const z = row.z, *const base = row.base;
     const uint4 *const from = row.from();
-    const int units = row.units, stage = row.stage;
+    const int units = row.units;
 
-    // The teacher's entries, one or two to a thread: asked for before the row, so
-    // as not to queue behind it.
+    // The teacher's entries, one or two to a thread, and the logits at them
+    // before anything is written over those.
     int at[kEntries];
-    E given[kEntries];
+    float te[kEntries], zt[kEntries];
     const bool entries = (tid & ~31) < a.k;  // of this warp
 #pragma unroll
     for (int n = 0; n < kEntries; ++n) {
         const int j = tid + n * THREADS;
         const bool in = entries && j < a.k;
         at[n] = in ? a.t_index[r * a.k + j] : -1;
-        given[n] = in ? static_cast<const E *>(a.t_logits)[r * a.k + j] : E(0);
+        te[n] = in ? load1(static_cast<const E *>(a.t_logits) + r * a.k + j) : -INFINITY;
     }
-    if (KEEP) {
-#pragma unroll
-        for (int g = 0; g < kStages; ++g) {
-            row.template start_copies<THREADS>(kept, g);
-            commit_copies();
-        }
-    }
-    // and the logits at them, before anything is written over those
-    float te[kEntries], zt[kEntries];
 #pragma unroll
     for (int n = 0; n < kEntries; ++n) {
-        if (at[n] < 0 || at[n] >= a.vocab) at[n] = -1;
-        te[n] = at[n] >= 0 ? load1(&given[n]) : -INFINITY;
+        if (at[n] < 0 || at[n] >= a.vocab) at[n] = -1, te[n] = -INFINITY;
         zt[n] = at[n] >= 0 ? load1(z + at[n]) : 0.0f;
     }
 
     Sum s = none();
-    if (LOSS && KEEP) {
-#pragma unroll
-        for (int g = 0; g < kStages; ++g) {
-            if (g == 0) wait_copies<1>();
-            if (g == 1) wait_copies<0>();
-            // a thread reads what it copied itself: first for its largest, then for the sum
-            const int begin = g * stage + tid, end = min((g + 1) * stage, units);
-            typename Unit<T>::Top top;
-#pragma unroll 2
-            for (int u = begin; u < end; u += THREADS) top.add(kept[u]);
-            raise(s, top.get(), c);
-            if (s.top != -INFINITY) {  // else nothing but masked logits so far
-                if (is_far(s.top * c)) {
-                    Under<T, true> under(s.top, c);
-                    for (int u = begin; u < end; u += THREADS) under.add(kept[u]);
-                    s.sum += under.get();
-                } else {
-                    Under<T, false> under(s.top, c);
-#pragma unroll 2
-                    for (int u = begin; u < end; u += THREADS) under.add(kept[u]);
-                    s.sum += under.get();
-                }
-            }
-        }
-    }
-    if (LOSS && !KEEP) {
-        for (int u = tid; u < units; u += kAhead * THREADS) {
-            Unit<T> x[kAhead];
+    if (LOSS) {
+        auto take_in = [&](const Unit<T> (&x)[kAhead], int u, bool whole) {
             typename Unit<T>::Top top;
 #pragma unroll
             for (int i = 0; i < kAhead; ++i)
-                if (u + i * THREADS < units) x[i].w = from[u + i * THREADS];
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (u + i * THREADS < units) top.add(x[i]);
+                if (whole || u + i * THREADS < units) top.add(x[i]);
             raise(s, top.get(), c);
-            if (s.top == -INFINITY) continue;
+            if (s.top == -INFINITY) return;  // nothing but masked logits so far
             if (is_far(s.top * c)) {
                 Under<T, true> under(s.top, c);
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i)
-                    if (u + i * THREADS < units) under.add(x[i]);
+                    if (whole || u + i * THREADS < units) under.add(x[i]);
                 s.sum += under.get();
             } else {
                 Under<T, false> under(s.top, c);
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i)
-                    if (u + i * THREADS < units) under.add(x[i]);
+                    if (whole || u + i * THREADS < units) under.add(x[i]);
                 s.sum += under.get();
             }
+        };
+        int u = tid;
+        for (; u + (kAhead - 1) * THREADS < units; u += kAhead * THREADS) {
+            Unit<T> x[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) x[i].w = GRAD ? from[u + i * THREADS] : __ldcs(from + u + i * THREADS);
+            take_in(x, u, true);
         }
-    }
-    if (LOSS) {  // the ragged ends: fewer elements than a unit each
-        const int head_end = min(part.u0 * N, part.last), tail = max(part.u1 * N, head_end);
-        int i = -1;
-        if (part.first + tid < head_end) i = part.first + tid;
-        if (tid >= 32 && tail + tid - 32 < part.last) i = tail + tid - 32;
+        if (u < units) {
+            Unit<T> x[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (u + i * THREADS < units) x[i].w = from[u + i * THREADS];
+            take_in(x, u, false);
+        }
+        const int i = row.ragged(tid);
         if (i >= 0) {
             const float v = load1(base + i);
             s = join(s, Sum{v, v == -INFINITY ? 0.0f : v - v + 1.0f}, c);
@@ -342,10 +308,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
         }
         auto pass = [&](auto is_far_too) {
             if (phase != 0) {
-                const T *const src = KEEP ? reinterpret_cast<const T *>(kept) - part.u0 * N : base;
                 for (int i = i0 + tid * N; i < i1; i += THREADS * N) {
                     Unit<T> x;
-                    read_shifted(src, i, x);
+                    read_shifted(base, i, x);
                     gradient(x, is_far_too);
                     __stcs(reinterpret_cast<uint4 *>(dz + i), x.w);
                 }
@@ -353,24 +318,19 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
             }
             uint4 *const to = reinterpret_cast<uint4 *>(dz) + part.u0;
             int u = tid;
-            if (!KEEP)
-                for (; u + (kAhead - 1) * THREADS < units; u += kAhead * THREADS) {
-                    Unit<T> x[kAhead];
+            for (; u + (kAhead - 1) * THREADS < units; u += kAhead * THREADS) {
+                Unit<T> x[kAhead];
 #pragma unroll
-                    for (int i = 0; i < kAhead; ++i) x[i].w = from[u + i * THREADS];
+                for (int i = 0; i < kAhead; ++i) x[i].w = __ldcs(from + u + i * THREADS);
 #pragma unroll
-                    for (int i = 0; i < kAhead; ++i) {
-                        gradient(x[i], is_far_too);
-                        __stcs(to + u + i * THREADS, x[i].w);
-                    }
+                for (int i = 0; i < kAhead; ++i) {
+                    gradient(x[i], is_far_too);
+                    __stcs(to + u + i * THREADS, x[i].w);
                 }
-#pragma unroll 2
+            }
             for (; u < units; u += THREADS) {
                 Unit<T> x;
-                if (KEEP)
-                    x = kept[u];
-                else
-                    x.w = from[u];
+                x.w = from[u];
                 gradient(x, is_far_too);
                 __stcs(to + u, x.w);
             }
@@ -421,21 +381,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
     if (LOSS && blocks > 1) cg::this_cluster().barrier_wait();
 }
 
-template <class T, class E, bool LOSS, bool GRAD, bool KEEP, int THREADS>
-cudaError_t launch(const DistillArgs &a, int blocks, int each, cudaStream_t st)
+template <class T, class E, bool LOSS, bool GRAD, int THREADS>
+cudaError_t launch(const DistillArgs &a, int64_t blocks, int64_t units, cudaStream_t st)
 {
-    auto *kernel = &distill_kernel<T, E, LOSS, GRAD, KEEP, THREADS>;
-    // a spare unit, which a read across units may touch
-    const size_t smem = KEEP ? size_t(each + 1) * 16 : 0;
-    if (smem) {
-        const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
-        if (e != cudaSuccess) return e;
-    }
     if (a.rows * blocks >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(a.rows * blocks));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -443,38 +395,41 @@ cudaError_t launch(const DistillArgs &a, int blocks, int each, cudaStream_t st)
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = LOSS && blocks > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, a, blocks, each);
+    return cudaLaunchKernelEx(&cfg, &distill_kernel<T, E, LOSS, GRAD, THREADS>, a, int(blocks),
+                              int((units + blocks - 1) / blocks));
 }
-
-#ifndef ZG_FEW
-#define ZG_FEW 152
-#endif
 
 template <class T, class E, bool LOSS, bool GRAD>
 cudaError_t by_size(const DistillArgs &a, cudaStream_t st)
 {
-    constexpr int64_t kEach = 27 * 1024;  // shared memory of 128 threads: eight such blocks to an SM
-    const int64_t units = (int64_t(a.vocab) * int64_t(sizeof(T)) + 30) / 16, bytes = units * 16;
-    auto each = [&](int64_t blocks) { return int((units + blocks - 1) / blocks); };
-    if constexpr (LOSS) {
-        // The smallest block that holds a row, or as few of the largest as do;
-        // more of them while rows are so few that SMs are left over.
-        const int threads = bytes <= kEach ? 128 : bytes <= 2 * kEach ? 256 : 512;
-        const int64_t most = kEach * threads / 128;
-        int64_t blocks = (bytes + most - 1) / most;
-        while (blocks < 8 && a.rows * blocks < ZG_FEW && bytes / blocks > 16384) blocks = blocks * 2 < 8 ? blocks * 2 : 8;
-        if (blocks > 8) blocks = 8;  // parts of up to 200 KB: one block to an SM
-        if (int64_t(each(blocks)) * 16 <= 200 * 1024) {
-            if (threads == 128) return launch<T, E, true, GRAD, true, 128>(a, int(blocks), each(blocks), st);
-            if (threads == 256) return launch<T, E, true, GRAD, true, 256>(a, int(blocks), each(blocks), st);
-            return launch<T, E, true, GRAD, true, 512>(a, int(blocks), each(blocks), st);
-        }
-        return launch<T, E, true, GRAD, false, 512>(a, 8, each(8), st);
+    const int64_t units = (int64_t(a.vocab) * int64_t(sizeof(T)) + 30) / 16;
+    if constexpr (!LOSS) {
+        // Nothing to exchange: as many small blocks as a row has parts for.
+        int64_t blocks = (units + 1727) / 1728;
+        if (a.rows * blocks < 152) blocks = (units + 1023) / 1024;
+        return launch<T, E, false, true, 128>(a, blocks, units, st);
     } else {
-        // nothing to exchange: as many small blocks as a row has parts for
-        int64_t blocks = (bytes + kEach - 1) / kEach;
-        if (a.rows * blocks < ZG_FEW) blocks = (bytes + 16383) / 16384;
-        return launch<T, E, false, true, false, 128>(a, int(blocks), each(blocks), st);
+        // The smallest blocks keep most rows in flight, at different places at
+        // once, so that the ends of some do not leave memory idle: for the loss
+        // of 4096 x 50257 in bf16, 128 threads to a row 70 us, 256 79, 512 98. A
+        // row that is read again for its gradient has to be in L2 still, so the
+        // rows in flight (1024 threads to an SM) have 64 MB together: 128
+        // threads 201 us, 256 159, 512 181; of 777 x 131075, 106, 112 and 91.
+        // Rows too few to fill half the GPU take more threads, then more blocks.
+        const int64_t held = GRAD ? (int64_t(64) << 20) / (152 * units * 16) : 8;  // rows to an SM
+        int threads = held >= 8 ? 128 : held >= 4 ? 256 : 512;
+        int64_t blocks = 1;
+        while (a.rows * blocks * threads < 152 * 512 && units / blocks > 4 * threads) {
+            if (threads < 512)
+                threads *= 2;
+            else if (blocks < 8)
+                blocks *= 2;
+            else
+                break;
+        }
+        if (threads == 128) return launch<T, E, true, GRAD, 128>(a, blocks, units, st);
+        if (threads == 256) return launch<T, E, true, GRAD, 256>(a, blocks, units, st);
+        return launch<T, E, true, GRAD, 512>(a, blocks, units, st);
     }
 }
 

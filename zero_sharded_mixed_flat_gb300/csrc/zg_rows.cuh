@@ -1,6 +1,5 @@
 // zg_rows.cuh -- rows of logits shared out over blocks: how a row of any
-// alignment is cut into parts of whole 16-byte units and ragged ends, and how a
-// part is copied into shared memory.
+// alignment is cut into parts of whole 16-byte units and ragged ends.
 #pragma once
 
 #include "zg_kernels.cuh"
@@ -99,42 +98,28 @@ __device__ __forceinline__ Part part_of(const T *row, int vocab, int each, int r
     return p;
 }
 
-__device__ __forceinline__ void copy_async(void *dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void wait_copies()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-constexpr int kStages = 2;
-
-// A block's part of row r, and how it lies in memory.
+// A block's part of a row, and how it lies in memory.
 template <class T>
 struct Row {
     const T *z;     // the row
     const T *base;  // element 0 of the part's count: only [head, head + vocab) is touched
     Part part;
-    int units, stage;  // whole units, and of them in each group of copies
-    __device__ __forceinline__ Row(const T *first, int vocab, int each, int rank, int threads)
+    int units;      // whole ones
+    __device__ __forceinline__ Row(const T *first, int vocab, int each, int rank)
     {
         z = first;
         part = part_of(z, vocab, each, rank);
         base = z - part.head;
         units = part.u1 - part.u0;
-        stage = (units + threads * kStages - 1) / (threads * kStages) * threads;
     }
     __device__ __forceinline__ const uint4 *from() const { return reinterpret_cast<const uint4 *>(base) + part.u0; }
-    __device__ __forceinline__ int stage_end(int g) const { return min((g + 1) * stage, units); }
-    template <int THREADS>
-    __device__ __forceinline__ void start_copies(Unit<T> *kept, int g) const
+    // A thread's one element of the part's ragged ends (less than a unit each), or -1.
+    __device__ __forceinline__ int ragged(int tid) const
     {
-        const int end = stage_end(g);
-        for (int u = g * stage + int(threadIdx.x); u < end; u += THREADS) copy_async(&kept[u], from() + u);
+        constexpr int N = Unit<T>::kN;
+        const int head_end = min(part.u0 * N, part.last), tail = max(part.u1 * N, head_end);
+        if (part.first + tid < head_end) return part.first + tid;
+        return tid >= 32 && tail + tid - 32 < part.last ? tail + tid - 32 : -1;
     }
 };
 

@@ -79,76 +79,70 @@ __device__ __forceinline__ int block_sum(int v, int *red)
     return v;
 }
 
-template <class T, bool KEEP, int THREADS>
+constexpr int kShares = 512;  // of a block's part: unit u belongs to share u mod kShares
+
+template <class T, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *logits, int vocab, int64_t row_stride, int k,
                                                                       T *values, int32_t *index, int blocks, int each)
 {
-    extern __shared__ __align__(16) unsigned char raw[];
+    extern __shared__ uint64_t lists[];  // the parts' lists, where a row has several
     __shared__ Shared sh;
     __shared__ T tops[ZG_TOPK_MAX];  // the logits at sh.top
-    constexpr int N = Unit<T>::kN, kWarps = THREADS / 32, kBits = 8 * int(sizeof(T));
+    constexpr int N = Unit<T>::kN, kWarps = THREADS / 32, kBits = 8 * int(sizeof(T)), kOwn = kShares / THREADS;
     const int tid = threadIdx.x;
     const unsigned number = blockIdx.x / unsigned(blocks);
     const int64_t r = number;
     const int rank = int(blockIdx.x - number * unsigned(blocks));
     const T *const z = logits + r * row_stride;
-    const Row<T> row(z, vocab, each, rank, THREADS);
+    const Row<T> row(z, vocab, each, rank);
     const Part &part = row.part;
-    Unit<T> *const kept = reinterpret_cast<Unit<T> *>(raw);
     const uint4 *const from = row.from();
     const int units = row.units;
     auto unit_at = [&](int u) {
         Unit<T> x;
-        if (KEEP)
-            x = kept[u];
-        else
-            x.w = from[u];
+        x.w = from[u];
         return x;
     };
-    // a thread's one element of the ragged ends, or -1
-    int ragged = -1;
-    {
-        const int head_end = min(part.u0 * N, part.last), tail = max(part.u1 * N, head_end);
-        if (part.first + tid < head_end) ragged = part.first + tid - part.head;
-        if (tid >= 32 && tail + tid - 32 < part.last) ragged = tail + tid - 32 - part.head;
-    }
-    const uint32_t ragged_key = ragged >= 0 ? key_of<T>(bits_at(z + ragged)) : 0u;
     const int base = part.u0 * N - part.head;  // vocabulary index of unit 0's first element
+    int ragged = row.ragged(tid);
+    if (ragged >= 0) ragged -= part.head;
+    const uint32_t ragged_key = ragged >= 0 ? key_of<T>(bits_at(z + ragged)) : 0u;
 
-    if (KEEP) {
-#pragma unroll
-        for (int g = 0; g < kStages; ++g) {
-            row.template start_copies<THREADS>(kept, g);
-            commit_copies();
-        }
-    }
-    typename Unit<T>::Top most;
-    if (KEEP) {
-#pragma unroll
-        for (int g = 0; g < kStages; ++g) {
-            if (g == 0) wait_copies<1>();
-            if (g == 1) wait_copies<0>();
-            const int end = row.stage_end(g);
-#pragma unroll 2
-            for (int u = g * row.stage + tid; u < end; u += THREADS) most.add(kept[u]);
-        }
-    } else {
+    // a thread has the shares tid, tid + THREADS, ...
+    typename Unit<T>::Top most[kOwn];
+    int u = tid;
+    if (kOwn == 1) {
 #pragma unroll 4
-        for (int u = tid; u < units; u += THREADS) most.add(unit_at(u));
+        for (; u < units; u += THREADS) most[0].add(unit_at(u));
+    } else {
+        for (; u + kShares - THREADS < units; u += kShares) {
+            Unit<T> x[kOwn];
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) x[i] = unit_at(u + i * THREADS);
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) most[i].add(x[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i)
+            if (u + i * THREADS < units) most[i].add(unit_at(u + i * THREADS));
     }
-    uint32_t best = ragged_key;
-    if (tid < units) best = max(best, key_of<T>(__float_as_uint(most.get())));
+    uint32_t best[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) best[i] = tid + i * THREADS < units ? key_of<T>(__float_as_uint(most[i].get())) : 0u;
+    const uint32_t units_best = best[0];  // without the ragged element
+    best[0] = max(best[0], ragged_key);
 
     // the largest bound, to 16 bits, that k of the threads' maxima reach: one
     // warp looks for it between the least and the largest of them
     uint32_t *const bests = reinterpret_cast<uint32_t *>(sh.list);
-    bests[tid] = best >> (kBits - 16);
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) bests[tid + i * THREADS] = best[i] >> (kBits - 16);
     __syncthreads();
     if (tid < 32) {
-        uint32_t v[kWarps], lo = 0xffffffffu, hi = 0u;
+        uint32_t v[kShares / 32], lo = 0xffffffffu, hi = 0u;
         int some = 0;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
+        for (int i = 0; i < kShares / 32; ++i) {
             v[i] = bests[tid + 32 * i];
             some += v[i] != 0u;
             lo = min(lo, v[i] ? v[i] : 0xffffffffu);
@@ -164,7 +158,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
                 const uint32_t mid = lo + (hi - lo + 1) / 2;
                 int n = 0;
 #pragma unroll
-                for (int i = 0; i < kWarps; ++i) n += v[i] >= mid;
+                for (int i = 0; i < kShares / 32; ++i) n += v[i] >= mid;
                 if (__reduce_add_sync(0xffffffffu, n) >= k)
                     lo = mid;
                 else
@@ -185,19 +179,20 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
         const int n = atomicAdd(&sh.count, 1);
         if (n < kMost) sh.list[n] = entry(key, v);
     };
-    if (best && best >= bound) {
-        if (ragged >= 0 && ragged_key >= bound) put(ragged_key, ragged);
-        if (tid < units) sh.hot[atomicAdd(&sh.hots, 1)] = uint16_t(tid);
-    }
+    if (ragged >= 0 && ragged_key >= bound) put(ragged_key, ragged);
+    best[0] = units_best;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+        if (best[i] && best[i] >= bound) sh.hot[atomicAdd(&sh.hots, 1)] = uint16_t(tid + i * THREADS);
     __syncthreads();
     {
-        const int hots = sh.hots, per = (units + THREADS - 1) / THREADS;
-        int side = 0;  // lanes to a hot thread: a power of two, at most a warp
+        const int hots = sh.hots, per = (units + kShares - 1) / kShares;
+        int side = 0;  // lanes to a share that reaches it: a power of two, at most a warp
         while (side < 5 && (1 << side) < per) ++side;
         for (int h = tid >> side; h < hots; h += THREADS >> side) {
             const int first = sh.hot[h];
             for (int i = tid & ((1 << side) - 1); i < per; i += 1 << side) {
-                const int u = first + i * THREADS;
+                const int u = first + i * kShares;
                 if (u >= units) break;
                 const Unit<T> x = unit_at(u);
                 typename Unit<T>::Top top;
@@ -210,7 +205,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
                     const int j = __ffs(int(hits)) - 1;
                     hits &= hits - 1;
                     const int v = base + u * N + j;
-                    put(key_of<T>(KEEP ? bits_at(reinterpret_cast<const T *>(&kept[u]) + j) : bits_at(z + v)), v);
+                    put(key_of<T>(bits_at(z + v)), v);
                 }
             }
         }
@@ -297,18 +292,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
         __syncthreads();
     }
     const int count = sh.count;
-    auto value_at = [&](int v) {
-        const int i = v - base;
-        return KEEP && i >= 0 && i < units * N ? reinterpret_cast<const T *>(kept)[i] : z[v];
-    };
     auto settle = [&](uint64_t e, int place) {
         const int v = index_of(e);
         if (blocks == 1) {
-            values[r * k + place] = value_at(v);
+            values[r * k + place] = z[v];
             index[r * k + place] = v;
         } else {
             sh.top[place] = e;
-            tops[place] = value_at(v);
+            tops[place] = z[v];
         }
     };
     if (count <= 128) {
@@ -359,13 +350,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
     if (blocks == 1) return;
 
     // Several parts: all their lists, each in order, into this block's shared
-    // memory (over the row, which is done with); an entry's place is then the sum
-    // of its places among them.
+    // memory; an entry's place is then the sum of its places among them.
     cg::cluster_group cluster = cg::this_cluster();
     const int mine = min(count, k);
     if (tid == 0) sh.tops = mine;
     cluster.sync();
-    uint64_t *const lists = reinterpret_cast<uint64_t *>(raw);
     __shared__ int counts[8];
     if (tid < blocks) counts[tid] = cluster.map_shared_rank(&sh, tid)->tops;
     for (int i = tid; i < blocks * k; i += THREADS) {
@@ -396,20 +385,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
     cluster.barrier_wait();
 }
 
-template <class T, bool KEEP, int THREADS>
-cudaError_t launch(const T *logits, int64_t rows, int vocab, int64_t stride, int k, T *values, int32_t *index, int blocks,
-                   int each, cudaStream_t st)
+template <class T, int THREADS>
+cudaError_t launch(const T *logits, int64_t rows, int vocab, int64_t stride, int k, T *values, int32_t *index,
+                   int64_t blocks, int64_t units, cudaStream_t st)
 {
-    auto *kernel = &topk_kernel<T, KEEP, THREADS>;
-    size_t smem = KEEP ? size_t(each + 1) * 16 : 16;
-    if (blocks > 1 && smem < size_t(blocks) * k * 8) smem = size_t(blocks) * k * 8;
-    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
-    if (e != cudaSuccess) return e;
+    auto *kernel = &topk_kernel<T, THREADS>;
     if (rows * blocks >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(rows * blocks));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = blocks > 1 ? size_t(blocks) * k * sizeof(uint64_t) : 0;  // at most 16 KB
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -417,28 +402,32 @@ cudaError_t launch(const T *logits, int64_t rows, int vocab, int64_t stride, int
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = blocks > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, logits, vocab, stride, k, values, index, blocks, each);
+    return cudaLaunchKernelEx(&cfg, kernel, logits, vocab, stride, k, values, index, int(blocks),
+                              int((units + blocks - 1) / blocks));
 }
 
 template <class T>
 cudaError_t by_size(const T *logits, int64_t rows, int vocab, int64_t stride, int k, T *values, int32_t *index, cudaStream_t st)
 {
-    // The smallest block that holds a row and has threads enough for a close
-    // bound, or as few of the largest as hold it; more of them while rows are so
-    // few that SMs are left over.
-    constexpr int64_t kEach = 25 * 1024 + 512;  // shared memory of 128 threads: eight such blocks to an SM
-    const int64_t units = (int64_t(vocab) * int64_t(sizeof(T)) + 30) / 16, bytes = units * 16;
-    auto each = [&](int64_t blocks) { return int((units + blocks - 1) / blocks); };
-    int threads = bytes <= kEach && k <= 64 ? 128 : bytes <= 2 * kEach && k <= 128 ? 256 : 512;
-    const int64_t most = kEach * threads / 128;
-    int64_t blocks = (bytes + most - 1) / most;
-    while (blocks < 8 && rows * blocks < 152 && bytes / blocks > 16384) blocks = blocks * 2 < 8 ? blocks * 2 : 8;
-    if (blocks > 8) blocks = 8;
-    if (int64_t(each(blocks)) * 16 > 200 * 1024)
-        return launch<T, false, 512>(logits, rows, vocab, stride, k, values, index, int(blocks), each(blocks), st);
-    if (threads == 128) return launch<T, true, 128>(logits, rows, vocab, stride, k, values, index, int(blocks), each(blocks), st);
-    if (threads == 256) return launch<T, true, 256>(logits, rows, vocab, stride, k, values, index, int(blocks), each(blocks), st);
-    return launch<T, true, 512>(logits, rows, vocab, stride, k, values, index, int(blocks), each(blocks), st);
+    // Small blocks keep most rows in flight, at different places at once, so that
+    // the ends of some do not leave memory idle; too small ones are long at the
+    // candidates: of 4096 x 50257 in bf16, k = 64, 128 threads to a row take
+    // 101 us, 256 90, 512 113; k = 256 206, 177 and 196. Short rows need fewer, and
+    // rows too few to fill half the GPU take more threads, then more blocks.
+    const int64_t units = (int64_t(vocab) * int64_t(sizeof(T)) + 30) / 16;
+    int threads = units <= 1024 ? 128 : 256;
+    int64_t blocks = 1;
+    while (rows * blocks * threads < 152 * 512 && units / blocks > 4 * threads) {
+        if (threads < 512)
+            threads *= 2;
+        else if (blocks < 8)
+            blocks *= 2;
+        else
+            break;
+    }
+    if (threads == 128) return launch<T, 128>(logits, rows, vocab, stride, k, values, index, blocks, units, st);
+    if (threads == 256) return launch<T, 256>(logits, rows, vocab, stride, k, values, index, blocks, units, st);
+    return launch<T, 512>(logits, rows, vocab, stride, k, values, index, blocks, units, st);
 }
 
 }  // namespace
