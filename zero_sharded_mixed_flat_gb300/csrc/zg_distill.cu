@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_kernel(Distil
             for (; u + (kAhead - 1) * THREADS < units; u += kAhead * THREADS) {
                 Unit<T> x[kAhead];
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) x[i].w = __ldcs(from + u + i * THREADS);
+                for (int i = 0; i < kAhead; ++i) x[i].w = LOSS ? __ldcs(from + u + i * THREADS) : from[u + i * THREADS];
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
                     gradient(x[i], is_far_too);

@@ -53,9 +53,34 @@ __device__ __forceinline__ uint32_t bits_in(const Unit<T> &x, int i)
     return (i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16;
 }
 
-// Larger keys first, then lower indices: one number, larger first.
-__device__ __forceinline__ uint64_t entry(uint32_t key, int v) { return (uint64_t(key) << 32) | uint32_t(0x7fffffff - v); }
-__device__ __forceinline__ int index_of(uint64_t e) { return 0x7fffffff - int(uint32_t(e)); }
+// The same for an i that is not known when compiling.
+template <class T>
+__device__ __forceinline__ uint32_t bits_of(const Unit<T> &x, int i)
+{
+    const int word = sizeof(T) == 2 ? i >> 1 : i;
+    const uint32_t lo = word & 1 ? x.w.y : x.w.x, hi = word & 1 ? x.w.w : x.w.z, w = word & 2 ? hi : lo;
+    if (sizeof(T) == 4) return w;
+    return i & 1 ? w & 0xffff0000u : w << 16;
+}
+
+// Larger keys first, then lower indices: one number, larger first. Its lowest
+// bit marks a -0, so that all but a NaN's bits can be had back from it.
+__device__ __forceinline__ uint64_t entry(uint32_t key, int v, uint32_t bits)
+{
+    return (uint64_t(key) << 32) | uint32_t(0x3fffffff - v) << 1 | uint32_t(bits == 0x80000000u);
+}
+__device__ __forceinline__ int index_of(uint64_t e) { return 0x3fffffff - int(uint32_t(e) >> 1); }
+template <class T>
+__device__ __forceinline__ T value_in(uint64_t e, const T *z)
+{
+    const uint32_t key = uint32_t(e >> 32), top = sizeof(T) == 2 ? 0x8000u : 0x80000000u;
+    if (key == top * 2u - 1u) return z[index_of(e)];  // a NaN
+    const uint32_t bits = (key & top) ? ((key & ~top) | ((e & 1u) ? top : 0u)) : ~key;
+    if constexpr (sizeof(T) == 2)
+        return T(bits);
+    else
+        return __uint_as_float(bits);
+}
 
 struct Shared {
     uint64_t list[kMost];
@@ -87,7 +112,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
 {
     extern __shared__ uint64_t lists[];  // the parts' lists, where a row has several
     __shared__ Shared sh;
-    __shared__ T tops[ZG_TOPK_MAX];  // the logits at sh.top
     constexpr int N = Unit<T>::kN, kWarps = THREADS / 32, kBits = 8 * int(sizeof(T)), kOwn = kShares / THREADS;
     const int tid = threadIdx.x;
     const unsigned number = blockIdx.x / unsigned(blocks);
@@ -106,7 +130,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
     const int base = part.u0 * N - part.head;  // vocabulary index of unit 0's first element
     int ragged = row.ragged(tid);
     if (ragged >= 0) ragged -= part.head;
-    const uint32_t ragged_key = ragged >= 0 ? key_of<T>(bits_at(z + ragged)) : 0u;
+    const uint32_t ragged_bits = ragged >= 0 ? bits_at(z + ragged) : 0u;
+    const uint32_t ragged_key = ragged >= 0 ? key_of<T>(ragged_bits) : 0u;
 
     // a thread has the shares tid, tid + THREADS, ...
     typename Unit<T>::Top most[kOwn];
@@ -175,11 +200,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
     const uint32_t bound = sh.bound;
     const float least = value_of<T>(bound);
     // what reaches it: the shares of the threads whose maximum does, spread over all threads
-    auto put = [&](uint32_t key, int v) {
+    auto put = [&](uint32_t bits, int v) {
         const int n = atomicAdd(&sh.count, 1);
-        if (n < kMost) sh.list[n] = entry(key, v);
+        if (n < kMost) sh.list[n] = entry(key_of<T>(bits), v, bits);
     };
-    if (ragged >= 0 && ragged_key >= bound) put(ragged_key, ragged);
+    if (ragged >= 0 && ragged_key >= bound) put(ragged_bits, ragged);
     best[0] = units_best;
 #pragma unroll
     for (int i = 0; i < kOwn; ++i)
@@ -203,9 +228,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
                 for (int j = 0; j < N; ++j) hits |= uint32_t(!(__uint_as_float(bits_in(x, j)) < least)) << j;
                 while (hits) {
                     const int j = __ffs(int(hits)) - 1;
-                    hits &= hits - 1;
-                    const int v = base + u * N + j;
-                    put(key_of<T>(bits_at(z + v)), v);
+                    hits &= hits - 1u;
+                    put(bits_of(x, j), base + u * N + j);
                 }
             }
         }
@@ -231,13 +255,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
         }
         if (tid == 0) sh.count = 0;
         __syncthreads();
-        if (ragged >= 0 && ragged_key > kth) put(ragged_key, ragged);
+        if (ragged >= 0 && ragged_key > kth) put(ragged_bits, ragged);
         for (int u = tid; u < units; u += THREADS) {
             const Unit<T> x = unit_at(u);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const uint32_t key = key_of<T>(bits_in(x, i));
-                if (key > kth) put(key, base + u * N + i);
+                const uint32_t bits = bits_in(x, i);
+                if (key_of<T>(bits) > kth) put(bits, base + u * N + i);
             }
         }
         __syncthreads();
@@ -264,7 +288,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
         };
         const bool head = ragged >= 0 && ragged < base, tail = ragged >= 0 && !head;
         equals(head && ragged_key == kth, [&](int at) {
-            if (at < want) sh.list[at] = entry(kth, ragged);
+            if (at < want) sh.list[at] = entry(kth, ragged, ragged_bits);
         });
         for (int u0 = 0; u0 < units && have < want; u0 += THREADS) {
             const int u = u0 + tid;
@@ -279,27 +303,25 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
 #pragma unroll
                 for (int i = 0; i < N; ++i)
                     if (key_of<T>(bits_in(x, i)) == kth) {
-                        if (at < want) sh.list[at] = entry(kth, base + u * N + i);
+                        if (at < want) sh.list[at] = entry(kth, base + u * N + i, bits_in(x, i));
                         ++at;
                     }
             });
         }
         if (have < want)
             equals(tail && ragged_key == kth, [&](int at) {
-                if (at < want) sh.list[at] = entry(kth, ragged);
+                if (at < want) sh.list[at] = entry(kth, ragged, ragged_bits);
             });
         if (tid == 0) sh.count = min(have, want);
         __syncthreads();
     }
     const int count = sh.count;
     auto settle = [&](uint64_t e, int place) {
-        const int v = index_of(e);
         if (blocks == 1) {
-            values[r * k + place] = z[v];
-            index[r * k + place] = v;
+            values[r * k + place] = value_in(e, z);
+            index[r * k + place] = index_of(e);
         } else {
             sh.top[place] = e;
-            tops[place] = z[v];
         }
     };
     if (count <= 128) {
@@ -378,7 +400,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
 #pragma unroll
         for (int o = 4; o; o >>= 1) lo += __shfl_xor_sync(0xffffffffu, lo, o);
         if (e < mine && b == 0 && lo < k) {
-            values[r * k + lo] = tops[e];
+            values[r * k + lo] = value_in(m, z);
             index[r * k + lo] = index_of(m);
         }
     }
@@ -415,7 +437,7 @@ cudaError_t by_size(const T *logits, int64_t rows, int vocab, int64_t stride, in
     // 101 us, 256 90, 512 113; k = 256 206, 177 and 196. Short rows need fewer, and
     // rows too few to fill half the GPU take more threads, then more blocks.
     const int64_t units = (int64_t(vocab) * int64_t(sizeof(T)) + 30) / 16;
-    int threads = units <= 1024 ? 128 : 256;
+    int threads = units <= 2048 ? 128 : 256;
     int64_t blocks = 1;
     while (rows * blocks * threads < 152 * 512 && units / blocks > 4 * threads) {
         if (threads < 512)
