@@ -107,7 +107,7 @@ __device__ __forceinline__ int block_sum(int v, int *red)
 constexpr int kShares = 512;  // of a block's part: unit u belongs to share u mod kShares
 
 template <class T, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *logits, int vocab, int64_t row_stride, int k,
+__global__ void __launch_bounds__(THREADS, 1536 / THREADS) topk_kernel(const T *logits, int vocab, int64_t row_stride, int k,
                                                                       T *values, int32_t *index, int blocks, int each)
 {
     extern __shared__ uint64_t lists[];  // the parts' lists, where a row has several
@@ -135,21 +135,23 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) topk_kernel(const T *
 
     // a thread has the shares tid, tid + THREADS, ...
     typename Unit<T>::Top most[kOwn];
+    constexpr int kRounds = 4 / kOwn;  // four units asked for before the first is looked at
     int u = tid;
-    if (kOwn == 1) {
-#pragma unroll 4
-        for (; u < units; u += THREADS) most[0].add(unit_at(u));
-    } else {
-        for (; u + kShares - THREADS < units; u += kShares) {
-            Unit<T> x[kOwn];
+    for (; u + kRounds * kShares - THREADS < units; u += kRounds * kShares) {
+        Unit<T> x[4];
 #pragma unroll
-            for (int i = 0; i < kOwn; ++i) x[i] = unit_at(u + i * THREADS);
+        for (int i = 0; i < 4; ++i) x[i] = unit_at(u + i * THREADS);
 #pragma unroll
-            for (int i = 0; i < kOwn; ++i) most[i].add(x[i]);
-        }
+        for (int i = 0; i < 4; ++i) most[i % kOwn].add(x[i]);
+    }
+    {
+        Unit<T> x[4];
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i)
-            if (u + i * THREADS < units) most[i].add(unit_at(u + i * THREADS));
+        for (int i = 0; i < 4; ++i)
+            if (u + i * THREADS < units) x[i] = unit_at(u + i * THREADS);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (u + i * THREADS < units) most[i % kOwn].add(x[i]);
     }
     uint32_t best[kOwn];
 #pragma unroll
@@ -434,7 +436,8 @@ cudaError_t by_size(const T *logits, int64_t rows, int vocab, int64_t stride, in
     // Small blocks keep most rows in flight, at different places at once, so that
     // the ends of some do not leave memory idle; too small ones are long at the
     // candidates: of 4096 x 50257 in bf16, k = 64, 128 threads to a row take
-    // 101 us, 256 90, 512 113; k = 256 206, 177 and 196. Short rows need fewer, and
+    // 101 us, 256 90, 512 113; k = 256 206, 177 and 196 (at 1024 threads to an SM;
+    // with 1536, as it is, 256 take 85 and 153). Short rows need fewer, and
     // rows too few to fill half the GPU take more threads, then more blocks.
     const int64_t units = (int64_t(vocab) * int64_t(sizeof(T)) + 30) / 16;
     int threads = units <= 2048 ? 128 : 256;
