@@ -14,14 +14,15 @@ from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-CSRC = os.path.join(PKG, "csrc")
+CSRC = os.path.join(PKG, "csrc")     # the optimizer step
+OPS = os.path.join(CSRC, "ops")      # the training operators
 INCLUDE = os.path.join(ROOT, "include")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libzg.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
-    "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
+    "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC, "-I", OPS,
     # IEEE division and square root, denormals kept: the step is defined with
     # correctly rounded binary32 operations.
     "-prec-div=true", "-prec-sqrt=true", "-ftz=false",
@@ -36,7 +37,7 @@ def nvcc() -> str:
 
 
 def sources() -> list[str]:
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
+    return sorted(os.path.join(d, f) for d in (CSRC, OPS) for f in os.listdir(d) if f.endswith(".cu"))
 
 
 def _stale(out: str, deps: list[str]) -> bool:
@@ -47,10 +48,10 @@ def _stale(out: str, deps: list[str]) -> bool:
 
 
 def build(verbose: bool = False, extra: list[str] | None = None, out_lib: str = LIB, obj_dir: str = OBJ) -> str:
-    """Compile every .cu under csrc/ and link ``out_lib``. ``extra`` adds nvcc
+    """Compile every .cu under csrc/ and csrc/ops/ and link ``out_lib``. ``extra`` adds nvcc
     flags (for instance -D tuning knobs); use a separate ``obj_dir`` then."""
     os.makedirs(obj_dir, exist_ok=True)
-    headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
+    headers = [os.path.join(d, f) for d in (CSRC, OPS) for f in os.listdir(d) if f.endswith((".h", ".cuh"))]
     headers.append(os.path.join(INCLUDE, "zg.h"))
     flags = NVCC_FLAGS + (extra or [])
     cc = nvcc()

@@ -38,6 +38,18 @@ int finish(cudaError_t e, const char *what)
     return fail(ZG_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
 }
 
+// A call's body. The pointer checks and the launch helpers keep what they know in
+// containers, whose allocations may throw: nothing of that crosses the C ABI.
+template <class Body>
+int guarded(Body body)
+{
+    try {
+        return body();
+    } catch (...) {
+        return fail(ZG_ERR_NO_MEMORY, "host allocation failed");
+    }
+}
+
 int element_size(int dtype) { return dtype == ZG_DTYPE_BF16 ? 2 : 4; }
 
 int check_dtype(int dtype, const char *what)
@@ -257,97 +269,109 @@ int zg_scan_status(zg_scan *s, zg_stream stream, int *status)
 int zg_gated_scan(zg_scan *scan, const zg_scan_shape *shape, const zg_view *x, const zg_view *f, const float *h0,
                   const zg_view *y, float *h_last, float *states, zg_stream stream)
 {
-    if (int rc = check_shape(scan, shape)) return rc;
-    if (int rc = check_view(x, shape, false, "x")) return rc;
-    if (int rc = check_view(f, shape, false, "f")) return rc;
-    if (int rc = check_view(y, shape, true, "y")) return rc;
-    if (int rc = check_ptr(h0, 4, true, "h0")) return rc;
-    if (int rc = check_ptr(h_last, 4, true, "h_last")) return rc;
-    if (int rc = check_ptr(states, 4, true, "states")) return rc;
-    zg::ScanArgs a = scan_args(shape);
-    a.x = view(x);
-    a.f = view(f);
-    a.y = view(y);
-    a.h0 = h0;
-    a.h_last = h_last;
-    a.states = states;
-    return finish(zg::launch_scan(a, work_of(scan), stream), "scan launch");
+    return guarded([&]() -> int {
+        if (int rc = check_shape(scan, shape)) return rc;
+        if (int rc = check_view(x, shape, false, "x")) return rc;
+        if (int rc = check_view(f, shape, false, "f")) return rc;
+        if (int rc = check_view(y, shape, true, "y")) return rc;
+        if (int rc = check_ptr(h0, 4, true, "h0")) return rc;
+        if (int rc = check_ptr(h_last, 4, true, "h_last")) return rc;
+        if (int rc = check_ptr(states, 4, true, "states")) return rc;
+        zg::ScanArgs a = scan_args(shape);
+        a.x = view(x);
+        a.f = view(f);
+        a.y = view(y);
+        a.h0 = h0;
+        a.h_last = h_last;
+        a.states = states;
+        return finish(zg::launch_scan(a, work_of(scan), stream), "scan launch");
+    });
 }
 
 int zg_gated_scan_bwd(zg_scan *scan, const zg_scan_shape *shape, const zg_view *x, const zg_view *f,
                       const zg_view *dy, const float *states, const float *h0, const float *dh_last,
                       const zg_view *dx, const zg_view *df, float *dh0, zg_stream stream)
 {
-    if (int rc = check_shape(scan, shape)) return rc;
-    if (int rc = check_view(x, shape, false, "x")) return rc;
-    if (int rc = check_view(f, shape, false, "f")) return rc;
-    if (int rc = check_view(dy, shape, false, "dy")) return rc;
-    if (int rc = check_view(dx, shape, true, "dx")) return rc;
-    if (int rc = check_view(df, shape, true, "df")) return rc;
-    if (int rc = check_ptr(states, 4, false, "states")) return rc;
-    if (int rc = check_ptr(h0, 4, true, "h0")) return rc;
-    if (int rc = check_ptr(dh_last, 4, true, "dh_last")) return rc;
-    if (int rc = check_ptr(dh0, 4, true, "dh0")) return rc;
-    zg::ScanArgs a = scan_args(shape);
-    a.x = view(x);
-    a.f = view(f);
-    a.y = view(dy);
-    a.h0 = h0;
-    a.states = const_cast<float *>(states);
-    a.dx = view(dx);
-    a.df = view(df);
-    a.dh_last = dh_last;
-    a.dh0 = dh0;
-    return finish(zg::launch_scan_bwd(a, work_of(scan), stream), "scan backward launch");
+    return guarded([&]() -> int {
+        if (int rc = check_shape(scan, shape)) return rc;
+        if (int rc = check_view(x, shape, false, "x")) return rc;
+        if (int rc = check_view(f, shape, false, "f")) return rc;
+        if (int rc = check_view(dy, shape, false, "dy")) return rc;
+        if (int rc = check_view(dx, shape, true, "dx")) return rc;
+        if (int rc = check_view(df, shape, true, "df")) return rc;
+        if (int rc = check_ptr(states, 4, false, "states")) return rc;
+        if (int rc = check_ptr(h0, 4, true, "h0")) return rc;
+        if (int rc = check_ptr(dh_last, 4, true, "dh_last")) return rc;
+        if (int rc = check_ptr(dh0, 4, true, "dh0")) return rc;
+        zg::ScanArgs a = scan_args(shape);
+        a.x = view(x);
+        a.f = view(f);
+        a.y = view(dy);
+        a.h0 = h0;
+        a.states = const_cast<float *>(states);
+        a.dx = view(dx);
+        a.df = view(df);
+        a.dh_last = dh_last;
+        a.dh0 = dh0;
+        return finish(zg::launch_scan_bwd(a, work_of(scan), stream), "scan backward launch");
+    });
 }
 
 int zg_topk(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride, int k, void *values,
             int32_t *index, zg_stream stream)
 {
-    if (int rc = check_rows(logits, dtype, rows, vocab, row_stride, k)) return rc;
-    if (k > vocab) return fail(ZG_ERR_INVALID_ARG, "k = %d is more than vocab = %lld", k, (long long)vocab);
-    if (rows == 0) return ZG_OK;
-    if (int rc = check_ptr(values, element_size(dtype), false, "values")) return rc;
-    if (int rc = check_ptr(index, 4, false, "index")) return rc;
-    return finish(zg::launch_topk(logits, dtype, rows, int(vocab), row_stride, k, values, index, stream), "top-k launch");
+    return guarded([&]() -> int {
+        if (int rc = check_rows(logits, dtype, rows, vocab, row_stride, k)) return rc;
+        if (k > vocab) return fail(ZG_ERR_INVALID_ARG, "k = %d is more than vocab = %lld", k, (long long)vocab);
+        if (rows == 0) return ZG_OK;
+        if (int rc = check_ptr(values, element_size(dtype), false, "values")) return rc;
+        if (int rc = check_ptr(index, 4, false, "index")) return rc;
+        return finish(zg::launch_topk(logits, dtype, rows, int(vocab), row_stride, k, values, index, stream), "top-k launch");
+    });
 }
 
 int zg_distill_loss(const zg_distill_args *args, float *loss, float *lse, zg_stream stream)
 {
-    zg::DistillArgs a;
-    if (int rc = check_distill(args, 0.0f, a)) return rc;
-    if (a.rows == 0) return ZG_OK;
-    if (int rc = check_ptr(loss, 4, false, "loss")) return rc;
-    if (int rc = check_ptr(lse, 4, true, "lse")) return rc;
-    a.loss = loss;
-    a.lse = lse;
-    return finish(zg::launch_distill(a, stream), "distillation loss launch");
+    return guarded([&]() -> int {
+        zg::DistillArgs a;
+        if (int rc = check_distill(args, 0.0f, a)) return rc;
+        if (a.rows == 0) return ZG_OK;
+        if (int rc = check_ptr(loss, 4, false, "loss")) return rc;
+        if (int rc = check_ptr(lse, 4, true, "lse")) return rc;
+        a.loss = loss;
+        a.lse = lse;
+        return finish(zg::launch_distill(a, stream), "distillation loss launch");
+    });
 }
 
 int zg_distill_grad(const zg_distill_args *args, const float *lse, float scale, const float *dloss, void *dlogits,
                     int64_t drow_stride, zg_stream stream)
 {
-    zg::DistillArgs a;
-    if (int rc = check_distill(args, scale, a)) return rc;
-    if (int rc = check_dlogits(args, dloss, dlogits, drow_stride, a)) return rc;
-    if (a.rows == 0) return ZG_OK;
-    if (int rc = check_ptr(lse, 4, false, "lse")) return rc;
-    a.lse_in = lse;
-    return finish(zg::launch_distill(a, stream), "distillation gradient launch");
+    return guarded([&]() -> int {
+        zg::DistillArgs a;
+        if (int rc = check_distill(args, scale, a)) return rc;
+        if (int rc = check_dlogits(args, dloss, dlogits, drow_stride, a)) return rc;
+        if (a.rows == 0) return ZG_OK;
+        if (int rc = check_ptr(lse, 4, false, "lse")) return rc;
+        a.lse_in = lse;
+        return finish(zg::launch_distill(a, stream), "distillation gradient launch");
+    });
 }
 
 int zg_distill_loss_grad(const zg_distill_args *args, float scale, const float *dloss, float *loss, float *lse,
                          void *dlogits, int64_t drow_stride, zg_stream stream)
 {
-    zg::DistillArgs a;
-    if (int rc = check_distill(args, scale, a)) return rc;
-    if (int rc = check_dlogits(args, dloss, dlogits, drow_stride, a)) return rc;
-    if (a.rows == 0) return ZG_OK;
-    if (int rc = check_ptr(loss, 4, false, "loss")) return rc;
-    if (int rc = check_ptr(lse, 4, true, "lse")) return rc;
-    a.loss = loss;
-    a.lse = lse;
-    return finish(zg::launch_distill(a, stream), "distillation launch");
+    return guarded([&]() -> int {
+        zg::DistillArgs a;
+        if (int rc = check_distill(args, scale, a)) return rc;
+        if (int rc = check_dlogits(args, dloss, dlogits, drow_stride, a)) return rc;
+        if (a.rows == 0) return ZG_OK;
+        if (int rc = check_ptr(loss, 4, false, "loss")) return rc;
+        if (int rc = check_ptr(lse, 4, true, "lse")) return rc;
+        a.loss = loss;
+        a.lse = lse;
+        return finish(zg::launch_distill(a, stream), "distillation launch");
+    });
 }
 
 }  // extern "C"

@@ -28,6 +28,8 @@
 // so nothing before it, a NaN included, is multiplied into what follows.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "zg_launch.h"
 #include "zg_ops.h"
 
@@ -1139,13 +1141,23 @@ Grid grid_of(const ScanArgs &a, int load_mode)
     return g;
 }
 
-template <class T, bool BWD, class Kernel>
-cudaError_t launch(Kernel *kernel, const ScanArgs &a, const ScanWork &sw, const Grid &g, cudaStream_t st)
+// (The kernel is a template argument: all of a direction have one type, and each
+// has a flag of its own for the shared memory that it was allowed.)
+template <class T, bool BWD, auto kernel>
+cudaError_t launch(const ScanArgs &a, const ScanWork &sw, const Grid &g, cudaStream_t st)
 {
     constexpr size_t smem = kTileBytes<T, BWD>;
     if (g.places >= int64_t(0xf0000000)) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
+    // the driver is asked once for each kernel and device
+    static std::atomic<bool> allowed[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev >= 64 || !allowed[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return e;
+        if (dev < 64) allowed[dev].store(true, std::memory_order_relaxed);
+    }
     Work w{};
     w.ctl = sw.ctl;
     w.status = sw.status;
@@ -1168,11 +1180,11 @@ cudaError_t choose(const ScanArgs &a, const ScanWork &sw, int load_mode, cudaStr
     const bool early = g.width >= 128;
     if constexpr (BWD) {
         if constexpr (kBuffers<T, true> == 2)
-            if (early) return launch<T, BWD>(&scan_bwd_kernel<T, VEC, PACKED, true>, a, sw, g, st);
-        return launch<T, BWD>(&scan_bwd_kernel<T, VEC, PACKED, false>, a, sw, g, st);
+            if (early) return launch<T, BWD, &scan_bwd_kernel<T, VEC, PACKED, true>>(a, sw, g, st);
+        return launch<T, BWD, &scan_bwd_kernel<T, VEC, PACKED, false>>(a, sw, g, st);
     } else {
-        if (early) return launch<T, BWD>(&scan_kernel<T, VEC, PACKED, true>, a, sw, g, st);
-        return launch<T, BWD>(&scan_kernel<T, VEC, PACKED, false>, a, sw, g, st);
+        if (early) return launch<T, BWD, &scan_kernel<T, VEC, PACKED, true>>(a, sw, g, st);
+        return launch<T, BWD, &scan_kernel<T, VEC, PACKED, false>>(a, sw, g, st);
     }
 }
 

@@ -145,21 +145,6 @@ int wave_blocks(const void *kernel, int threads, size_t smem)
     return blocks;
 }
 
-cudaError_t allow_smem(const void *kernel, size_t smem)
-{
-    static std::mutex mu;
-    static std::map<std::pair<int, const void *>, size_t> allowed;
-    int dev = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(mu);
-    size_t &most = allowed[std::make_pair(dev, kernel)];
-    if (smem <= most) return cudaSuccess;
-    const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (set == cudaSuccess) most = smem;
-    return set;
-}
-
 int norm_blocks_cap() { return kPartialsCap; }
 
 // What cudaPointerGetAttributes said about a pointer the library accepted:

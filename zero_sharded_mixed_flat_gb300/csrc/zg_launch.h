@@ -58,10 +58,6 @@ cudaError_t launch_step_kernel(const Src &src, int64_t n, float inv, StepK k, St
     return launch_dependent(kernel, blocks, kStepThreads, 0, st, src, n, inv, k, state, sc);
 }
 
-// Let `kernel` use `smem` bytes of dynamic shared memory on the current device
-// (the driver is asked once for each kernel, device and new largest size).
-cudaError_t allow_smem(const void *kernel, size_t smem);
-
 // Largest grid any norm launch may use (sizes the partials array).
 int norm_blocks_cap();
 
