@@ -87,6 +87,34 @@ def test_layouts(b, t, c, dtype, layout):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("c", [1, 63, 64, 68, 131])
+@pytest.mark.parametrize("off", range(8))
+def test_every_alignment_among_nans(off, c, dtype):
+    """Rows that begin at any place in a 16-byte unit, each operand's at another and with
+    another stride, between NaNs: the elements beside a row take no part."""
+    b, t, dt = 2, 140, DT[dtype]
+    x, f = views(b, t, c, dt, "plain", 70 + off)
+    dy = rand((b, t, c), 72).to(dt).cuda()
+
+    def placed(v, first, step):
+        wide = torch.full((b * t * step + 32,), math.nan, dtype=dt, device="cuda")
+        at = wide[first:first + b * t * step].view(b, t, step)[..., :c]
+        at.copy_(v)
+        return at
+
+    px, pf, pd = placed(x, off, c + off), placed(f, (3 * off + 1) % 8, c + 5), placed(dy, (5 * off + 2) % 8, c + 8 - off)
+    scan = zb.GatedScan(b, t, c)
+    y, _, kept = scan.forward(px, pf, keep=True)
+    dx, df, _ = scan.backward(px, pf, pd, kept)
+    X, F, bounds = x.double().cpu(), f.double().cpu(), [(r, 0, t) for r in range(b)]
+    zero = torch.zeros(b, c, dtype=torch.float64)
+    h, _, _, he, _, _ = ref.scan(X, F, zero, bounds)
+    wx, wf, _, xe, fe, _ = ref.scan_grad(X, F, zero, dy.double().cpu(), zero, bounds)
+    for got, want, err, what in ((y, h, he, "y"), (dx, wx, xe, "dx"), (df, wf, fe, "df")):
+        ref.check(got, want, ref.stored(want, err, dt), what)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("starts", [[0, 300], [0, 0, 0, 300], [0, 300, 300, 300], [0, 1, 2, 3, 300], [0, 128, 256, 300],
                                     [0, 127, 129, 129, 256, 299, 300], [0, 100, 100, 150], [0, 0, 0], [0, 250, 260],
                                     list(range(301))])

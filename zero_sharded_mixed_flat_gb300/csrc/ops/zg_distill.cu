@@ -7,11 +7,23 @@
 // gathered values, and for the gradient one exponential per logit again.
 //
 // Bound by memory: each logit is read once (2 bytes in bf16) and its gradient
-// written once. The row is shared out over a cluster of blocks, each of which
-// copies its part into shared memory, so that the second pass reads nothing
-// from memory: the blocks exchange their maximum and sum, no more. A part is
-// whole 16-byte units of the row but for its two ends, so any row, however it
-// is aligned, moves in wide copies.
+// written once. A row is read by one small block with a running maximum and sum;
+// for loss and gradient together it is read again, from L2, where the rows in
+// flight are kept few enough to stay. (Copies of the row in shared memory, with
+// the blocks large enough to hold it, took 92 us for the loss below and 156 for
+// both: the blocks' ends left memory idle.) Few rows take a cluster of blocks to
+// a row, which exchange their maximum and sum through distributed shared memory.
+// A part is whole 16-byte units of the row but for its two ends, so any row,
+// however it is aligned, moves in wide loads; a gradient whose rows are aligned
+// differently is stored in its own units, from words shifted into place.
+//
+// Measured at 4096 x 50257 in bf16, k = 64: the loss 64 us (6.5 TB/s), the
+// gradient 125 (6.6 TB/s), both in one launch 154 (5.3 TB/s of the once-read,
+// once-written bytes; what is left is the second read out of L2 and the phases
+// of a row). With gradient rows that are not aligned as the logits' are, 2048
+// rows: gradient 81, both 97 (a word more is
+// loaded for each unit). One row: 5 and 4 us, the latency of the launch and of
+// the row's three phases.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 

@@ -11,7 +11,6 @@ __device__ __forceinline__ float load1(const uint16_t *p) { return __uint_as_flo
 __device__ __forceinline__ void store1(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t *p, float v) { *p = uint16_t(pack_bf16x2(v, 0.0f)); }
 
-
 // max that keeps a NaN.
 __device__ __forceinline__ float max_nan(float a, float b)
 {

@@ -26,8 +26,18 @@
 // Packed sequences that begin inside a chunk cut the scan: a run that holds a
 // beginning has a constant map, marked by A = kConst (every real A is >= 0),
 // so nothing before it, a NaN included, is multiplied into what follows.
+//
+// Measured: 8 x 4096 x 1536 in bf16 forward 65 us (4.6 TB/s of x, f and y),
+// backward 103 (4.9 TB/s of five), where the SMs' issue of some 25 instructions
+// an element takes as long as the bytes do; rows at odd channels (1535 of them) 97
+// and 160, most of it in stores of two bytes; 1 x 65536 x 768 97 and 130 (twelve
+// tiles to a chunk, so a block waits for records that blocks beside it are only
+// writing); 8 x 1024 x 768 14 and 21, two tiles to a block; binary32, 1 x 20000 x
+// 768, 46 and 64, packed 9001 x 771 34 and 53. Three blocks to an SM instead of
+// two spill and are slower.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "zg_launch.h"
@@ -269,7 +279,6 @@ struct Grid {
     int64_t width;   // batch rows x tiles: the tiles of one chunk
     int64_t chunks;
     int64_t places;  // width x chunks
-    int load_mode;   // bytes of a copy into shared memory: 16, 4 or 2
 };
 
 // Places are taken in scan order, chunk by chunk, as blocks become free, and
@@ -335,23 +344,29 @@ struct Runs {
     float a[kRuns][kTile], b[kRuns][kTile];
 };
 
+// What composes a tile's maps. Maps of four runs, and of the chunks and groups
+// before, by fours: a, b.
 template <bool BWD>
-struct Shared {
+struct Maps {
     Runs runs;
-    Runs fwd;  // of h
-    float2 fwd_quarters[4][kTile];
-    // maps of four runs, and of the chunks and groups before, by fours: a, b
     float2 quarters[4][kTile], chunks[4][kTile], groups[4][kTile];
     float span[kTile];
-    Tile tile;
-    uint32_t tag;
-    Cuts cuts;
 };
 template <>
-struct Shared<false> {
+struct Maps<true> {
     Runs runs;
-    float2 quarters[4][kTile], chunks[4][kTile], groups[4][kTile];
+    union {
+        Runs fwd;  // of h; when the maps of chunks and groups come, its a has been read
+        struct {
+            float2 chunks[4][kTile], groups[4][kTile];
+        };
+    };
+    float2 quarters[4][kTile], fwd_quarters[4][kTile];
     float span[kTile];
+};
+static_assert(sizeof(Maps<true>::chunks) + sizeof(Maps<true>::groups) <= sizeof(Runs::a), "chunks and groups lie on fwd.a");
+
+struct Shared {
     Tile tile;
     uint32_t tag;
     Cuts cuts;
@@ -367,68 +382,123 @@ __device__ __forceinline__ void sts4(float *p, F4 v)
     *reinterpret_cast<float4 *>(p) = make_float4(v.lo.x, v.lo.y, v.hi.x, v.hi.y);
 }
 
+// N bytes, of which the first `bytes` are read and the others become zero.
 template <int N>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, int bytes)
 {
     if (N == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// Copies of N bytes of a tile of v into dst[token][channel]; what lies past the
-// tensor becomes zero.
-template <class T, int N>
-__device__ __forceinline__ void copy_tile(T *dst, const ScanView &v, const Tile &t, const ScanArgs &a)
+// How a tile's rows lie in memory, and how they are copied. WHOLE: all begin at
+// multiples of 16 bytes. ANY: anywhere. Copies are of 16 bytes from 16-byte
+// boundaries all the same, from the one at or before a row's first channel, which
+// so stands up to kUnit - 1 channels into its row of the buffer (copies of 4 bytes,
+// or plain loads of 2: 179 us for 8 x 4096 x 1535 in bf16 forward and 310 backward,
+// against 97 and 160). Rows of bf16 at multiples of 8 bytes are loaded and stored
+// four channels at a time as WHOLE is, and copied as ANY (FOURS, backward: 131 us
+// for 8 x 4096 x 1540 against 175) or in units of 8 bytes (EIGHTS, forward: 74
+// against 82; such copies pass through L1, for which backward's buffers leave no
+// room).
+enum { ANY, FOURS, EIGHTS, WHOLE };
+template <int ROWS>
+constexpr bool kShifted = ROWS <= FOURS;
+template <class T>
+constexpr int kUnit = 16 / int(sizeof(T));
+template <class T, int ROWS>
+constexpr int kPitch = kShifted<ROWS> ? kTile + kUnit<T> : kTile;
+// For ANY, whose lanes read single channels, every odd run stands another kSkew
+// channels on, so that the two half warps read different banks.
+template <int ROWS>
+constexpr int kSkew = ROWS == ANY ? 16 : 0;
+template <class T, int ROWS>
+constexpr int kBuffer = kChunk * kPitch<T, ROWS> + kRuns / 2 * kSkew<ROWS>;
+template <class T, int ROWS>
+__device__ __forceinline__ constexpr int place_of(int r)
 {
-    constexpr int kEach = N / int(sizeof(T)), kPerRow = kTile / kEach, kRows = kThreads / kPerRow;
+    return r * kPitch<T, ROWS> + (r / kRun + 1) / 2 * kSkew<ROWS>;
+}
+
+// Where the tokens of a run begin in their 16 bytes, one after another. A chunk's
+// first token, and every kRun-th, is at the same place, and so is every tile of a
+// row.
+static_assert(kRun % 8 == 0 && kTile % 8 == 0, "shifts repeat");
+template <class T, int ROWS>
+struct Walk {
+    uint32_t at;
+    __device__ __forceinline__ Walk(const ScanView &v, const Tile &t, int i)
+    {
+        if (!kShifted<ROWS>) return;
+        at = uint32_t(reinterpret_cast<uintptr_t>(v.ptr) / sizeof(T)) + t.row * uint32_t(v.sb) + uint32_t(i) * uint32_t(v.st);
+        asm volatile("" : "+r"(at));  // not formed again for every token
+    }
+    __device__ __forceinline__ int shift() const { return kShifted<ROWS> ? int(at % kUnit<T>) : 0; }
+    // Token i of a run in a buffer, then on to the next or the last token.
+    __device__ __forceinline__ const T *next(const T *buffer, const ScanView &v, int run, int i)
+    {
+        const T *const row = buffer + place_of<T, ROWS>(run * kRun) + i * kPitch<T, ROWS> + shift();
+        if (kShifted<ROWS>) at += uint32_t(v.st);
+        return row;
+    }
+    __device__ __forceinline__ const T *last(const T *buffer, const ScanView &v, int run, int i)
+    {
+        const T *const row = buffer + place_of<T, ROWS>(run * kRun) + i * kPitch<T, ROWS> + shift();
+        if (kShifted<ROWS>) at -= uint32_t(v.st);
+        return row;
+    }
+};
+
+// The unit of v's first element, for copies that read nothing.
+template <class T>
+__device__ __forceinline__ const T *unit_zero(const ScanView &v)
+{
+    return reinterpret_cast<const T *>(reinterpret_cast<uintptr_t>(v.ptr) & ~uintptr_t(15));
+}
+
+// Copies a tile of v into dst[token][shift + channel]; what lies past the tensor
+// becomes zero. Nothing is read past a row's last channel. Up to 15 bytes before
+// its first are, in the same 16: memory is allocated from such a boundary on.
+template <class T, int ROWS>
+__device__ __forceinline__ void start_copy(T *dst, const ScanView &v, const Tile &t, const ScanArgs &a)
+{
+    constexpr int N = ROWS == EIGHTS ? 8 : 16, kEach = N / int(sizeof(T)), kPerRow = kTile / kEach, kRows = kThreads / kPerRow;
+    constexpr int kStep = place_of<T, ROWS>(kRows) * int(sizeof(T));
+    static_assert(kRows % (2 * kRun) == 0, "each step is as far as the first");
     const int r0 = threadIdx.x / kPerRow, e = threadIdx.x % kPerRow * kEach;
     const int64_t c0 = int64_t(t.chunk) * kChunk;
-    const T *src = static_cast<const T *>(v.ptr) + t.row * v.sb + (c0 + r0) * v.st + t.ch + e;
-    const uint32_t to = uint32_t(__cvta_generic_to_shared(dst + r0 * kTile + e));
+    const int shift = Walk<T, ROWS>(v, t, r0).shift();
+    const T *const first = static_cast<const T *>(v.ptr) + t.row * v.sb + c0 * v.st + t.ch;
+    const T *src = first + r0 * v.st + e - shift;
+    const uint32_t base = uint32_t(__cvta_generic_to_shared(dst)), to = base + (place_of<T, ROWS>(r0) + e) * int(sizeof(T));
     const int64_t far = kRows * v.st;
-    if (c0 + kChunk <= a.tokens && t.ch + kTile <= a.channels) {
+    const bool inside = c0 + kChunk <= a.tokens && t.ch + kTile <= a.channels;
+    if (inside) {
 #pragma unroll
-        for (int r = 0; r < kChunk; r += kRows) {
-            copy_async<N>(to + r * kTile * int(sizeof(T)), src, N);
+        for (int i = 0; i < kChunk / kRows; ++i) {
+            copy_async<N>(to + i * kStep, src, N);
             src += far;
         }
-        return;
+        if (!kShifted<ROWS>) return;
     }
-    const int64_t left = (a.channels - t.ch - e) * int64_t(sizeof(T));
-    const int bytes = left <= 0 ? 0 : left < N ? int(left) : N;
+    const int wide = int(a.channels - t.ch < kTile ? a.channels - t.ch : kTile);
     const int rows = int(a.tokens - c0 < kChunk ? a.tokens - c0 : kChunk);
+    if (!inside) {
+        const int left = (shift + wide - e) * int(sizeof(T)), bytes = left <= 0 ? 0 : left < N ? left : N;
 #pragma unroll 1
-    for (int r = 0; r < kChunk; r += kRows) {
-        const int n = r0 + r < rows ? bytes : 0;
-        copy_async<N>(to + r * kTile * int(sizeof(T)), n ? src : static_cast<const T *>(v.ptr), n);
-        src += far;
+        for (int i = 0; i < kChunk / kRows; ++i) {
+            const int n = r0 + i * kRows < rows ? bytes : 0;
+            copy_async<N>(to + i * kStep, n ? src : unit_zero<T>(v), n);
+            src += far;
+        }
     }
-}
-// The same by plain loads, for bf16 rows that begin between words.
-__device__ __forceinline__ void copy_tile_2(uint16_t *dst, const ScanView &v, const Tile &t, const ScanArgs &a)
-{
-    const int r0 = threadIdx.x / kTile, e = threadIdx.x % kTile;
-    const int64_t c0 = int64_t(t.chunk) * kChunk;
-    const uint16_t *src = static_cast<const uint16_t *>(v.ptr) + t.row * v.sb + (c0 + r0) * v.st + t.ch + e;
-    const bool in = t.ch + e < a.channels;
-    const int rows = int(a.tokens - c0 < kChunk ? a.tokens - c0 : kChunk);
-    constexpr int kRows = kThreads / kTile;
-#pragma unroll 8
-    for (int r = 0; r < kChunk; r += kRows) {
-        dst[(r0 + r) * kTile + e] = in && r0 + r < rows ? *src : uint16_t(0);
-        src += kRows * v.st;
+    if (kShifted<ROWS> && threadIdx.x < kChunk) {  // what the shift moved past a row's last unit
+        const int r = threadIdx.x, over = Walk<T, ROWS>(v, t, r).shift() + wide - kTile;
+        const bool any = over > 0 && r < rows;
+        copy_async<16>(base + (place_of<T, ROWS>(r) + kTile) * int(sizeof(T)), any ? first + r * v.st + (wide - over) : unit_zero<T>(v),
+                       any ? over * int(sizeof(T)) : 0);
     }
-}
-template <class T>
-__device__ __forceinline__ void start_copy(T *dst, const ScanView &v, const Tile &t, const ScanArgs &a, int mode)
-{
-    if (mode == 16)
-        copy_tile<T, 16>(dst, v, t, a);
-    else if (sizeof(T) == 4 || mode == 4)
-        copy_tile<T, 4>(dst, v, t, a);
-    else
-        copy_tile_2(reinterpret_cast<uint16_t *>(dst), v, t, a);
 }
 __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
@@ -624,24 +694,24 @@ struct Before {
 };
 
 // Publishes this chunk's map, waits for the chunks before it, and leaves the
-// state before each run in sh.runs.b. The chunk's own map never waits for
+// state before each run in maps.runs.b. The chunk's own map never waits for
 // others, nor does the group's for earlier groups. `start` is the state before
 // the row's first token, at the thread's slot. The runs' maps are behind a
 // barrier; ends with one. Records of kTile slots lie by chunk (group, span) and
 // then by tile.
-template <bool CUT, class Sh>
-__device__ __forceinline__ void solve(Sh &sh, Before &before, const Work &w, const Tile &t, const Grid &g, uint32_t tag,
+template <bool CUT, class M>
+__device__ __forceinline__ void solve(M &maps, Before &before, const Work &w, const Tile &t, const Grid &g, uint32_t tag,
                                       float start)
 {
     const int slot = threadIdx.x % kTile, part = threadIdx.x / kTile;
     Quarter mine;
-    mine.load(sh.runs, part, slot);
-    sh.quarters[part][slot] = mine.whole<CUT>();
+    mine.load(maps.runs, part, slot);
+    maps.quarters[part][slot] = mine.whole<CUT>();
     if (g.chunks == 1) {
         __syncthreads();
         float h = start;
-        for (int i = 0; i < part; ++i) h = apply<CUT>(sh.quarters[i][slot], h);
-        mine.run<CUT>(sh.runs, part, slot, h);
+        for (int i = 0; i < part; ++i) h = apply<CUT>(maps.quarters[i][slot], h);
+        mine.run<CUT>(maps.runs, part, slot, h);
         __syncthreads();
         return;
     }
@@ -652,39 +722,39 @@ __device__ __forceinline__ void solve(Sh &sh, Before &before, const Work &w, con
     float2 all_runs = make_float2(1.0f, 0.0f);
     if (part == 0 && followed) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) all_runs = then<CUT>(all_runs, sh.quarters[i][slot]);
+        for (int i = 0; i < 4; ++i) all_runs = then<CUT>(all_runs, maps.quarters[i][slot]);
         if (!ends_group) put(w.chunk + t.k * step + at, all_runs.x, all_runs.y, tag);
     }
-    sh.chunks[part][slot] = before.chunks.get<CUT>(tag, w);
+    maps.chunks[part][slot] = before.chunks.get<CUT>(tag, w);
     if (ends_group && before.group < kGroup - 1) {
         __syncthreads();
         if (part == 0) {
             float2 m = make_float2(1.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m = then<CUT>(m, sh.chunks[i][slot]);
+            for (int i = 0; i < 4; ++i) m = then<CUT>(m, maps.chunks[i][slot]);
             m = then<CUT>(m, all_runs);
             put(w.group + this_group * step + at, m.x, m.y, tag);
         }
     }
-    sh.groups[part][slot] = before.groups.get<CUT>(tag, w);
+    maps.groups[part][slot] = before.groups.get<CUT>(tag, w);
     if (part == 3 && before.first_group > 0) {
         const ulonglong2 *p = w.span + (before.first_group / kGroup - 1) * step + at;
         ulonglong2 v = look(p);
         for (long long polls = 0; !there(v, tag) && go_on(w, polls); ++polls) v = look(p);
-        sh.span[slot] = values(v).x;
+        maps.span[slot] = values(v).x;
     }
     __syncthreads();
-    float h = before.first_group > 0 ? sh.span[slot] : start;
+    float h = before.first_group > 0 ? maps.span[slot] : start;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h = apply<CUT>(sh.groups[i][slot], h);
+    for (int i = 0; i < 4; ++i) h = apply<CUT>(maps.groups[i][slot], h);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h = apply<CUT>(sh.chunks[i][slot], h);
+    for (int i = 0; i < 4; ++i) h = apply<CUT>(maps.chunks[i][slot], h);
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        const float next = apply<CUT>(sh.quarters[i][slot], h);
+        const float next = apply<CUT>(maps.quarters[i][slot], h);
         h = i < part ? next : h;
     }
-    h = mine.run<CUT>(sh.runs, part, slot, h);
+    h = mine.run<CUT>(maps.runs, part, slot, h);
     if (part == 3 && ends_group && before.group == kGroup - 1) put(w.span + this_group / kGroup * step + at, h, h, tag);
     __syncthreads();
 }
@@ -715,11 +785,12 @@ __device__ __forceinline__ float state1(const float *p, int64_t row, const ScanA
 
 // Backward's buffers of x and dy per block: with two, the next tile's copies
 // start when a tile is begun; with one (binary32, where two would leave one block
-// to an SM) when it is done.
+// to an SM) when it is done. Then f's buffer, read once, gives way to the maps, or
+// they would leave one block to an SM all the same.
 template <class T, bool BWD>
 constexpr int kBuffers = BWD && sizeof(T) == 2 ? 2 : 1;
-template <class T, bool BWD>
-constexpr size_t kTileBytes = (BWD ? 2 * kBuffers<T, BWD> + 1 : 2) * kChunk * kTile * sizeof(T);
+template <class T, int ROWS, bool BWD>
+constexpr size_t kTileBytes = (BWD ? 2 * kBuffers<T, BWD> + 1 : 2) * kBuffer<T, ROWS> * sizeof(T);
 
 // A block's places. Where rows and tiles of channels alone fill the GPU
 // (EARLY) the next place is taken when a tile is begun, so that its copies can
@@ -727,13 +798,13 @@ constexpr size_t kTileBytes = (BWD ? 2 * kBuffers<T, BWD> + 1 : 2) * kChunk * kT
 // when all blocks have begun and taken their first. Where blocks work side by
 // side on few rows, a place that is taken but not begun holds up every block
 // after it, so the next one is taken only when a tile waits for nothing more.
-template <bool BWD, bool EARLY, class Sh>
+template <bool BWD, bool EARLY>
 struct Ahead {
-    Sh &sh;
+    Shared &sh;
     Places places;
     unsigned long long next;
     bool begun;
-    __device__ __forceinline__ Ahead(Sh &s, const Work &w, const Grid &g) : sh(s), places{w.ctl, int64_t(blockIdx.x)}, next(0), begun(false)
+    __device__ __forceinline__ Ahead(Shared &s, const Work &w, const Grid &g) : sh(s), places{w.ctl, int64_t(blockIdx.x)}, next(0), begun(false)
     {
         if (threadIdx.x == 0) {
             const unsigned long long taken = places.take(g);
@@ -771,21 +842,24 @@ struct Ahead {
     }
 };
 
-template <class T, bool VEC, bool PACKED, bool EARLY>
+template <class T, int ROWS, bool PACKED, bool EARLY>
 __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, Grid g)
 {
-    extern __shared__ __align__(16) unsigned char raw[];
-    constexpr int kSize = kChunk * kTile;
+    extern __shared__ __align__(128) unsigned char raw[];
+    constexpr bool VEC = ROWS != ANY;
+    constexpr int kSize = kBuffer<T, ROWS>;
     T *const bf = reinterpret_cast<T *>(raw), *const bx = bf + kSize;
-    __shared__ Shared<false> sh;
+    __shared__ struct { __align__(128) Maps<false> m; Shared s; } both;  // wide accesses to unaligned banks cost a tenth
+    Maps<false> &maps = both.m;
+    Shared &sh = both.s;
     const int l = threadIdx.x & 15, run = threadIdx.x / 16;
-    Ahead<false, EARLY, Shared<false>> ahead(sh, w, g);
+    Ahead<false, EARLY> ahead(sh, w, g);
     __syncthreads();
     Tile t = sh.tile;
     const uint32_t tag = sh.tag;
     if (t.valid) {
-        start_copy(bf, a.f, t, a, g.load_mode);
-        start_copy(bx, a.x, t, a, g.load_mode);
+        start_copy<T, ROWS>(bf, a.f, t, a);
+        start_copy<T, ROWS>(bx, a.x, t, a);
     }
     commit_copies();
     int64_t end = a.tokens;
@@ -815,12 +889,13 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
         };
 
         F4 keep[kRun], in[kRun];
+        Walk<T, ROWS> at_f(a.f, t, 0), at_x(a.x, t, 0);
         Map m;
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
             F4 take;
-            gates(decay<T>(read_f4<VEC>(bf + (run * kRun + i) * kTile, l)), keep[i], take);
-            in[i] = mul(take, read4<VEC>(bx + (run * kRun + i) * kTile, l));
+            gates(decay<T>(read_f4<VEC>(at_f.next(bf, a.f, run, i), l)), keep[i], take);
+            in[i] = mul(take, read4<VEC>(at_x.next(bx, a.x, run, i), l));
             if (PACKED && (mk.first >> i & 1)) {
                 m.b = fma(keep[i], initial(i), in[i]);
                 m.a = all(kConst);
@@ -832,19 +907,19 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
             }
         }
         if (!EARLY) before.ask(w, t, g);
-        sts4(&sh.runs.a[run][4 * l], m.a);
-        sts4(&sh.runs.b[run][4 * l], m.b);
+        sts4(&maps.runs.a[run][4 * l], m.a);
+        sts4(&maps.runs.b[run][4 * l], m.b);
         __syncthreads();
         if (EARLY) {
             if (u.valid) {
-                start_copy(bf, a.f, u, a, g.load_mode);
-                start_copy(bx, a.x, u, a, g.load_mode);
+                start_copy<T, ROWS>(bf, a.f, u, a);
+                start_copy<T, ROWS>(bx, a.x, u, a);
             }
             commit_copies();
         }
-        solve<PACKED>(sh, before, w, t, g, tag, start);
+        solve<PACKED>(maps, before, w, t, g, tag, start);
         ahead.ask(g);
-        F4 h = lds4(&sh.runs.b[run][4 * l]);
+        F4 h = lds4(&maps.runs.b[run][4 * l]);
         if (a.states && run == 0)
             put_state4<VEC>(a.states + (t.row * g.chunks + t.chunk) * a.channels + t.ch, l, n, h);
         T *py = static_cast<T *>(a.y.ptr) + t.row * a.y.sb + t0 * a.y.st + t.ch;
@@ -873,8 +948,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
         } else {
             t = ahead.close(g);
             if (t.valid) {
-                start_copy(bf, a.f, t, a, g.load_mode);
-                start_copy(bx, a.x, t, a, g.load_mode);
+                start_copy<T, ROWS>(bf, a.f, t, a);
+                start_copy<T, ROWS>(bx, a.x, t, a);
             }
             commit_copies();
         }
@@ -883,23 +958,27 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
 
 // ------------------------------------------------------------------ backward
 
-template <class T, bool VEC, bool PACKED, bool EARLY>
+template <class T, int ROWS, bool PACKED, bool EARLY>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work w, Grid g)
 {
-    extern __shared__ __align__(16) unsigned char raw[];
-    constexpr int kSize = kChunk * kTile;
+    extern __shared__ __align__(128) unsigned char raw[];
+    constexpr bool VEC = ROWS != ANY;
+    constexpr int kSize = kBuffer<T, ROWS>;
     constexpr bool kTwo = kBuffers<T, true> == 2;
     T *const bf = reinterpret_cast<T *>(raw), *bx = bf + kSize, *other = kTwo ? bx + 2 * kSize : bx;  // dy behind x
-    __shared__ Shared<true> sh;
+    static_assert(kTwo || sizeof(Maps<true>) <= kSize * sizeof(T), "the maps fit into f's buffer");
+    __shared__ struct { __align__(128) unsigned char own[kTwo ? sizeof(Maps<true>) : 16]; Shared s; } both;
+    Maps<true> &maps = *reinterpret_cast<Maps<true> *>(kTwo ? both.own : raw);
+    Shared &sh = both.s;
     const int l = threadIdx.x & 15, run = threadIdx.x / 16;
-    Ahead<true, EARLY, Shared<true>> ahead(sh, w, g);
+    Ahead<true, EARLY> ahead(sh, w, g);
     __syncthreads();
     Tile t = sh.tile;
     const uint32_t tag = sh.tag;
     if (t.valid) {
-        start_copy(bf, a.f, t, a, g.load_mode);
-        start_copy(bx, a.x, t, a, g.load_mode);
-        start_copy(bx + kSize, a.y, t, a, g.load_mode);
+        start_copy<T, ROWS>(bf, a.f, t, a);
+        start_copy<T, ROWS>(bx, a.x, t, a);
+        start_copy<T, ROWS>(bx + kSize, a.y, t, a);
     }
     commit_copies();
     int64_t end = a.tokens;
@@ -924,8 +1003,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
         if (EARLY) {
             u = ahead.after_open(g);
             if (u.valid) {
-                start_copy(other, a.x, u, a, g.load_mode);
-                start_copy(other + kSize, a.y, u, a, g.load_mode);
+                start_copy<T, ROWS>(other, a.x, u, a);
+                start_copy<T, ROWS>(other + kSize, a.y, u, a);
             }
         }
         Marks mk{0u, 0u};
@@ -942,6 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
         // kept of the gates, which are formed again from it where they are
         // needed (a reciprocal each), to hold the tile in 128 registers.
         F4 e[kRun];
+        Walk<T, ROWS> at_f(a.f, t, 0), at_x(a.x, t, 0), at_dy(a.y, t, 0);
         Map m, r;
         F4 weight = all(1.0f);  // of a token's dy in the run's gradient
         bool cut = false;       // a packed sequence ended: the later tokens do not count
@@ -949,9 +1029,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
             F4 keep, take;
-            e[i] = decay<T>(read_f4<VEC>(bf + (run * kRun + i) * kTile, l));
+            e[i] = decay<T>(read_f4<VEC>(at_f.next(bf, a.f, run, i), l));
             gates(e[i], keep, take);
-            const F4 in = mul(take, read4<VEC>(bx + (run * kRun + i) * kTile, l));
+            const F4 in = mul(take, read4<VEC>(at_x.next(bx, a.x, run, i), l));
             if (PACKED && (mk.first >> i & 1)) {
                 m.b = fma(keep, side(a.h0, sh.cuts.first, i), in);
                 m.a = all(kConst);
@@ -961,10 +1041,11 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
                 m.b = fma(keep, m.b, in);
                 if (!PACKED || m.a.lo.x >= 0.0f) m.a = mul(keep, m.a);
             }
+            const T *const row_dy = at_dy.next(bx + kSize, a.y, run, i);
             // tokens past the end have no gradient: what comes in there is zero or dh_last, unchanged
             if (PACKED ? !cut && t0 + i < end : t0 + i < a.tokens) {
                 weight = mul(weight, keep);
-                r.b = fma(weight, read4<VEC>(bx + kSize + (run * kRun + i) * kTile, l), r.b);
+                r.b = fma(weight, read4<VEC>(row_dy, l), r.b);
                 if (PACKED && (mk.last >> i & 1)) {
                     r.b = fma(weight, side(a.dh_last, sh.cuts.last, i), r.b);
                     cut = true;
@@ -973,45 +1054,48 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
         }
         r.a = cut ? all(kConst) : weight;
         if (!EARLY) before.ask(w, t, g);
-        sts4(&sh.fwd.a[run][4 * l], m.a);
-        sts4(&sh.fwd.b[run][4 * l], m.b);
-        sts4(&sh.runs.a[kRuns - 1 - run][4 * l], r.a);
-        sts4(&sh.runs.b[kRuns - 1 - run][4 * l], r.b);
+        if (!kTwo) __syncthreads();  // all of f has been read
+        sts4(&maps.fwd.a[run][4 * l], m.a);
+        sts4(&maps.fwd.b[run][4 * l], m.b);
+        sts4(&maps.runs.a[kRuns - 1 - run][4 * l], r.a);
+        sts4(&maps.runs.b[kRuns - 1 - run][4 * l], r.b);
         __syncthreads();
         if (EARLY) {
-            if (u.valid) start_copy(bf, a.f, u, a, g.load_mode);
+            if (u.valid) start_copy<T, ROWS>(bf, a.f, u, a);
             commit_copies();
         }
         {
             const int slot = threadIdx.x % kTile, part = threadIdx.x / kTile;
             Quarter q;
-            q.load(sh.fwd, part, slot);
-            sh.fwd_quarters[part][slot] = q.whole<PACKED>();
+            q.load(maps.fwd, part, slot);
+            maps.fwd_quarters[part][slot] = q.whole<PACKED>();
             __syncthreads();
             float h = h_start;
-            for (int i = 0; i < part; ++i) h = apply<PACKED>(sh.fwd_quarters[i][slot], h);
-            q.run<PACKED>(sh.fwd, part, slot, h);
+            for (int i = 0; i < part; ++i) h = apply<PACKED>(maps.fwd_quarters[i][slot], h);
+            q.run<PACKED>(maps.fwd, part, slot, h);
         }
-        solve<PACKED>(sh, before, w, t, g, tag, start);
+        solve<PACKED>(maps, before, w, t, g, tag, start);
         ahead.ask(g);
-        F4 h = lds4(&sh.fwd.b[run][4 * l]), gr = lds4(&sh.runs.b[kRuns - 1 - run][4 * l]);
+        F4 h = lds4(&maps.fwd.b[run][4 * l]), gr = lds4(&maps.runs.b[kRuns - 1 - run][4 * l]);
         // forward once more, for h_{t-1} - x_t
         F4 over[kRun];
+        Walk<T, ROWS> at_x2(a.x, t, 0);
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
             if (PACKED && (mk.first >> i & 1)) h = side(a.h0, sh.cuts.first, i);
             F4 keep, take;
             gates_again(e[i], keep, take);
-            const F4 xx = read4<VEC>(bx + (run * kRun + i) * kTile, l);
+            const F4 xx = read4<VEC>(at_x2.next(bx, a.x, run, i), l);
             over[i] = sub(h, xx);
             h = fma(keep, h, mul(take, xx));
         }
         T *px = static_cast<T *>(a.dx.ptr) + t.row * a.dx.sb + (t0 + kRun - 1) * a.dx.st + t.ch;
         T *pf = static_cast<T *>(a.df.ptr) + t.row * a.df.sb + (t0 + kRun - 1) * a.df.st + t.ch;
-        auto back = [&](int i) {
+        Walk<T, ROWS> at_dy2(a.y, t, kRun - 1);
+        auto back = [&](int i, const T *row_dy) {
             F4 keep, take;
             gates_again(e[i], keep, take);
-            gr = add(read4<VEC>(bx + kSize + (run * kRun + i) * kTile, l), gr);
+            gr = add(read4<VEC>(row_dy, l), gr);
             const F4 dx = mul(take, gr);
             store4<VEC>(px, l, n, dx);
             gr = mul(keep, gr);
@@ -1020,16 +1104,17 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
         if (t0 + kRun <= end && (!PACKED || !(mk.first | mk.last))) {
 #pragma unroll
             for (int i = kRun - 1; i >= 0; --i) {
-                back(i);
+                back(i, at_dy2.last(bx + kSize, a.y, run, i));
                 px -= a.dx.st;
                 pf -= a.df.st;
             }
         } else {
 #pragma unroll
             for (int i = kRun - 1; i >= 0; --i) {
+                const T *const row_dy = at_dy2.last(bx + kSize, a.y, run, i);
                 if (t0 + i < end) {
                     if (PACKED && (mk.last >> i & 1)) gr = side(a.dh_last, sh.cuts.last, i);
-                    back(i);
+                    back(i, row_dy);
                     if (PACKED && a.dh0 && (mk.first >> i & 1))
                         put_state4<VEC>(a.dh0 + sh.cuts.first[run * kRun + i] * a.channels + t.ch, l, n, gr);
                 }
@@ -1047,9 +1132,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
         } else {
             t = ahead.close(g);
             if (t.valid) {
-                start_copy(bf, a.f, t, a, g.load_mode);
-                start_copy(bx, a.x, t, a, g.load_mode);
-                start_copy(bx + kSize, a.y, t, a, g.load_mode);
+                start_copy<T, ROWS>(bf, a.f, t, a);
+                start_copy<T, ROWS>(bx, a.x, t, a);
+                start_copy<T, ROWS>(bx + kSize, a.y, t, a);
             }
             commit_copies();
         }
@@ -1065,7 +1150,12 @@ __device__ __forceinline__ void store1(uint16_t *p, float v) { *p = uint16_t(pac
 
 constexpr int kFew = 16;
 
-// Rows of at most kFew tokens: a thread to a channel, all its loads at once.
+// Rows of at most kFew tokens: a thread to a channel, all its loads at once, the
+// tokens one after another, so that a call for several tokens has the bits of
+// calls for each. One token of 32 rows of 768 channels takes 1.7 us, the launch's
+// own time. The scan would fill an eighth of its tiles' rows: 64 x 12 x 768 in
+// bf16 forward 4.1 us against 10.6 in the scan, backward 5.6 against 15.8;
+// 512 x 16 x 768 27 against 64, and 59 against 94.
 template <class T, int N, bool BWD>
 __global__ void __launch_bounds__(128) few_kernel(ScanArgs a)
 {
@@ -1118,35 +1208,29 @@ __global__ void __launch_bounds__(128) few_kernel(ScanArgs a)
 
 // ------------------------------------------------------------------ launches
 
-// The widest unit (16, 4 or 2 bytes) at whose multiples all rows of v begin.
-int unit_of(const ScanView &v, int size)
+// How the rows of v lie.
+int rows_of(const ScanView &v, int size, int64_t channels)
 {
     const uintptr_t bits = reinterpret_cast<uintptr_t>(v.ptr) | uintptr_t(v.sb * size) | uintptr_t(v.st * size);
-    return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
-}
-bool fours(const ScanView &v, int size, int64_t channels)
-{
-    const uintptr_t bits = reinterpret_cast<uintptr_t>(v.ptr) | uintptr_t(v.sb * size) | uintptr_t(v.st * size);
-    return channels % 4 == 0 && bits % (4 * size) == 0;
+    return bits % 16 == 0 && channels % 4 == 0 ? WHOLE : bits % (4 * size) == 0 && channels % 4 == 0 ? FOURS : ANY;
 }
 
-Grid grid_of(const ScanArgs &a, int load_mode)
+Grid grid_of(const ScanArgs &a)
 {
     Grid g{};
     g.tiles = (a.channels + kTile - 1) / kTile;
     g.width = a.batch * g.tiles;
     g.chunks = (a.tokens + kChunk - 1) / kChunk;
     g.places = g.width * g.chunks;
-    g.load_mode = load_mode;
     return g;
 }
 
 // (The kernel is a template argument: all of a direction have one type, and each
 // has a flag of its own for the shared memory that it was allowed.)
-template <class T, bool BWD, auto kernel>
+template <class T, int ROWS, bool BWD, auto kernel>
 cudaError_t launch(const ScanArgs &a, const ScanWork &sw, const Grid &g, cudaStream_t st)
 {
-    constexpr size_t smem = kTileBytes<T, BWD>;
+    constexpr size_t smem = kTileBytes<T, ROWS, BWD>;
     if (g.places >= int64_t(0xf0000000)) return cudaErrorInvalidConfiguration;
     // the driver is asked once for each kernel and device
     static std::atomic<bool> allowed[64];
@@ -1170,21 +1254,24 @@ cudaError_t launch(const ScanArgs &a, const ScanWork &sw, const Grid &g, cudaStr
     return cudaGetLastError();
 }
 
-template <class T, bool VEC, bool PACKED, bool BWD>
-cudaError_t choose(const ScanArgs &a, const ScanWork &sw, int load_mode, cudaStream_t st)
+template <class T, int ROWS, bool PACKED, bool BWD>
+cudaError_t choose(const ScanArgs &a, const ScanWork &sw, cudaStream_t st)
 {
-    const Grid g = grid_of(a, load_mode);
-    // Measured in bf16, places a tile ahead against at the end of a tile: 192
-    // tiles to a chunk (8 x 4096 x 1536) 78 against 95 us, 96 tiles
-    // (8 x 1024 x 768) the same, 12 tiles (1 x 65536 x 768) 138 against 115.
+    const Grid g = grid_of(a);
+    // A place taken a tile ahead has its copies in flight early, but others wait
+    // the longer for its records. Measured in bf16 forward, a tile ahead against at
+    // the end of a tile: 192 tiles to a chunk (8 x 4096 x 1536) 75 against 84 us,
+    // 96 (8 x 1024 x 768) 15.3 against 14.8, 48 (4 x 16384 x 768) 94 against 91, 12
+    // (1 x 65536 x 768) 127 against 104; backward 115 against 127, the same, the
+    // same, and 171 against 144.
     const bool early = g.width >= 128;
     if constexpr (BWD) {
         if constexpr (kBuffers<T, true> == 2)
-            if (early) return launch<T, BWD, &scan_bwd_kernel<T, VEC, PACKED, true>>(a, sw, g, st);
-        return launch<T, BWD, &scan_bwd_kernel<T, VEC, PACKED, false>>(a, sw, g, st);
+            if (early) return launch<T, ROWS, BWD, &scan_bwd_kernel<T, ROWS, PACKED, true>>(a, sw, g, st);
+        return launch<T, ROWS, BWD, &scan_bwd_kernel<T, ROWS, PACKED, false>>(a, sw, g, st);
     } else {
-        if (early) return launch<T, BWD, &scan_kernel<T, VEC, PACKED, true>>(a, sw, g, st);
-        return launch<T, BWD, &scan_kernel<T, VEC, PACKED, false>>(a, sw, g, st);
+        if (early) return launch<T, ROWS, BWD, &scan_kernel<T, ROWS, PACKED, true>>(a, sw, g, st);
+        return launch<T, ROWS, BWD, &scan_kernel<T, ROWS, PACKED, false>>(a, sw, g, st);
     }
 }
 
@@ -1204,16 +1291,16 @@ template <class T, bool BWD>
 cudaError_t pick(const ScanArgs &a, const ScanWork &w, cudaStream_t st)
 {
     if (!a.seq_start && a.tokens <= kFew) return launch_few<T, BWD>(a, st);
-    constexpr int size = int(sizeof(T));
-    int mode = unit_of(a.x, size);
-    mode = mode < unit_of(a.f, size) ? mode : unit_of(a.f, size);
-    bool vec = fours(a.x, size, a.channels) && fours(a.f, size, a.channels) && fours(a.y, size, a.channels);
-    if (BWD) {
-        mode = mode < unit_of(a.y, size) ? mode : unit_of(a.y, size);
-        vec = vec && fours(a.dx, size, a.channels) && fours(a.df, size, a.channels);
-    }
-    if (a.seq_start) return vec ? choose<T, true, true, BWD>(a, w, mode, st) : choose<T, false, true, BWD>(a, w, mode, st);
-    return vec ? choose<T, true, false, BWD>(a, w, mode, st) : choose<T, false, false, BWD>(a, w, mode, st);
+    auto lie = [&](const ScanView &v) { return rows_of(v, int(sizeof(T)), a.channels); };
+    int rows = std::min({lie(a.x), lie(a.f), lie(a.y)});
+    if (BWD) rows = std::min({rows, lie(a.dx), lie(a.df)});
+    if (rows == WHOLE) return a.seq_start ? choose<T, WHOLE, true, BWD>(a, w, st) : choose<T, WHOLE, false, BWD>(a, w, st);
+    if constexpr (sizeof(T) == 2)
+        if (rows == FOURS) {
+            constexpr int how = BWD ? FOURS : EIGHTS;
+            return a.seq_start ? choose<T, how, true, BWD>(a, w, st) : choose<T, how, false, BWD>(a, w, st);
+        }
+    return a.seq_start ? choose<T, ANY, true, BWD>(a, w, st) : choose<T, ANY, false, BWD>(a, w, st);
 }
 
 template <bool BWD>

@@ -1,15 +1,20 @@
 // The k largest of each row of logits, largest first, ties to the lowest index.
 //
-// Bound by memory: a row is read once. Each thread takes the maximum of its
-// share of the row while it arrives in shared memory. The k-th largest of these
+// Bound by memory: a row is read once. It is cut into kShares shares, whose
+// maxima are taken as it streams through registers. The k-th largest of these
 // maxima is no more than the row's k-th largest logit (k shares each hold one
 // at least as large), so it is a bound below which nothing has to be looked at:
-// only threads whose maximum reaches it go over their share again, and about k
+// only shares whose maximum reaches it are read again, out of L2, and about k
 // logits pass. Those are put in order by counting, for each, how many come
-// before it. Rows in which too many pass (many equal values) have their k-th
-// largest found bit by bit. A row of several parts (few rows, or a vocabulary
-// beyond one block's shared memory) takes a cluster of blocks, whose lists are
-// merged through distributed shared memory.
+// before it (a longer list by sorted runs, and searches in the others). Rows in
+// which too many pass (many equal values) have their k-th largest found bit by
+// bit. Few rows take a cluster of blocks to a row, whose lists are merged
+// through distributed shared memory.
+//
+// Measured at 4096 x 50257 in bf16: k = 64 87 us (4.7 TB/s), k = 256 154. What
+// is above the 61 us of the bytes is each row's end (bound, shares read again,
+// order), during which its block asks for nothing; other blocks of the SM fill
+// in for it. In binary32 188 us (4.4 TB/s); 7 rows, k = 100, 8 us, all latency.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
