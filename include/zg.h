@@ -363,6 +363,8 @@ void zg_destroy(zg_ctx *ctx);
  * scale. Each takes bf16 or binary32 data and computes in binary32, rounding
  * once where it stores; each is stream-ordered, allocates nothing and gives
  * the same bits for the same inputs every time.
+ * Inputs are read in units of up to 16 bytes from boundaries of as many, so what
+ * shares a unit with an input's element may be read; it takes no part.
  * ------------------------------------------------------------------------ */
 
 #define ZG_DTYPE_BF16 0

@@ -30,10 +30,10 @@
 // Measured: 8 x 4096 x 1536 in bf16 forward 65 us (4.6 TB/s of x, f and y),
 // backward 103 (4.9 TB/s of five), where the SMs' issue of some 25 instructions
 // an element takes as long as the bytes do; rows at odd channels (1535 of them) 97
-// and 160, most of it in stores of two bytes; 1 x 65536 x 768 97 and 130 (twelve
+// and 160, most of it in stores of two bytes; 1 x 65536 x 768 92 and 122 (twelve
 // tiles to a chunk, so a block waits for records that blocks beside it are only
-// writing); 8 x 1024 x 768 14 and 21, two tiles to a block; binary32, 1 x 20000 x
-// 768, 46 and 64, packed 9001 x 771 34 and 53. Three blocks to an SM instead of
+// writing); 8 x 1024 x 768 13 and 20, two tiles to a block; binary32, 1 x 20000 x
+// 768, 45 and 62, packed 9001 x 771 33 and 52. Three blocks to an SM instead of
 // two spill and are slower.
 #include <cuda_bf16.h>
 
@@ -500,6 +500,21 @@ __device__ __forceinline__ void start_copy(T *dst, const ScanView &v, const Tile
                        any ? over * int(sizeof(T)) : 0);
     }
 }
+// Asks for a tile of v to be brought into L2, a line for each row (two in
+// binary32). Blocks that take their places late cannot copy ahead, but where the
+// GPU's next tiles lie is known, whoever takes them: one grid on. Without this
+// memory idles while all wait for one another (in bf16, 1 x 65536 x 768 forward 92
+// against 97 us and backward 122 against 130; from two grids on, 93 and 126).
+template <class T>
+__device__ __forceinline__ void bring(const ScanView &v, const Tile &t, const ScanArgs &a)
+{
+    constexpr int kEach = 128 / int(sizeof(T)), kPieces = kTile / kEach;
+    const int64_t c0 = int64_t(t.chunk) * kChunk;
+    if (threadIdx.x >= kChunk * kPieces) return;
+    const int r = threadIdx.x / kPieces, e = threadIdx.x % kPieces * kEach;
+    if (c0 + r < a.tokens && t.ch + e < a.channels)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const T *>(v.ptr) + t.row * v.sb + (c0 + r) * v.st + t.ch + e));
+}
 __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
@@ -872,16 +887,24 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
         const int n = int(a.channels - t.ch < kTile ? a.channels - t.ch : kTile);
         const int64_t t0 = int64_t(t.chunk) * kChunk + run * kRun;
         const float start = PACKED ? 0.0f : state1<VEC>(a.h0, t.row, a, t);
+        if (PACKED && !EARLY) find_cuts(sh.cuts, a, t, n, a.h0, a.h_last);  // while the copies are under way
         wait_copies();
         ahead.open(g);
         __syncthreads();
+        if (!EARLY) {
+            const Tile soon = tile_at<false>(t.k * uint32_t(g.width) + t.rest + gridDim.x, g);
+            if (soon.valid) {
+                bring<T>(a.f, soon, a);
+                bring<T>(a.x, soon, a);
+            }
+        }
         Tile u;
         if (EARLY) u = ahead.after_open(g);
         Before before;
         if (EARLY) before.ask(w, t, g);
         Marks mk{0u, 0u};
         if (PACKED) {
-            find_cuts(sh.cuts, a, t, n, a.h0, a.h_last);
+            if (EARLY) find_cuts(sh.cuts, a, t, n, a.h0, a.h_last);
             mk = marks_of(sh.cuts);
         }
         auto initial = [&](int i) {
@@ -994,9 +1017,18 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
         const float h_start = t.chunk > 0 ? state1<VEC>(a.states, t.row * g.chunks + t.chunk, a, t)
                               : PACKED    ? 0.0f
                                           : state1<VEC>(a.h0, t.row, a, t);
+        if (PACKED && !EARLY) find_cuts(sh.cuts, a, t, n, a.dh_last, a.dh0);  // while the copies are under way
         wait_copies();
         ahead.open(g);
         __syncthreads();
+        if (!EARLY) {
+            const Tile soon = tile_at<true>(t.k * uint32_t(g.width) + t.rest + gridDim.x, g);
+            if (soon.valid) {
+                bring<T>(a.f, soon, a);
+                bring<T>(a.x, soon, a);
+                bring<T>(a.y, soon, a);
+            }
+        }
         Tile u;
         Before before;
         if (EARLY) before.ask(w, t, g);
@@ -1009,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
         }
         Marks mk{0u, 0u};
         if (PACKED) {
-            find_cuts(sh.cuts, a, t, n, a.dh_last, a.dh0);
+            if (EARLY) find_cuts(sh.cuts, a, t, n, a.dh_last, a.dh0);
             mk = marks_of(sh.cuts);
         }
         auto side = [&](const float *p, const int *table, int i) {
@@ -1259,12 +1291,15 @@ cudaError_t choose(const ScanArgs &a, const ScanWork &sw, cudaStream_t st)
 {
     const Grid g = grid_of(a);
     // A place taken a tile ahead has its copies in flight early, but others wait
-    // the longer for its records. Measured in bf16 forward, a tile ahead against at
-    // the end of a tile: 192 tiles to a chunk (8 x 4096 x 1536) 75 against 84 us,
-    // 96 (8 x 1024 x 768) 15.3 against 14.8, 48 (4 x 16384 x 768) 94 against 91, 12
-    // (1 x 65536 x 768) 127 against 104; backward 115 against 127, the same, the
-    // same, and 171 against 144.
-    const bool early = g.width >= 128;
+    // the longer for its records. Measured in bf16, a tile ahead against at the
+    // end of a tile, tiles of a chunk x chunks: 192 x 32 forward 65 against 68 us,
+    // backward 103 against 101; 768 x 2 19.5 against 20.3, 29.0 against 30.3;
+    // 96 x 16 22.7 against 21.1, 32.5 against 31.7; 48 x 32 24.6 against 22.6, 36
+    // against 34; 12 x 512 105 against 92, 153 against 122. In long rows forward
+    // gains from fewer tiles on: 64 x 512 367 against 400, 568 against 574;
+    // 32 x 512 208 against 222, 312 against 305; 24 x 512 168 against 172, 245
+    // against 232.
+    const bool early = g.width >= 128 || (!BWD && g.width >= 32 && g.chunks >= 256);
     if constexpr (BWD) {
         if constexpr (kBuffers<T, true> == 2)
             if (early) return launch<T, ROWS, BWD, &scan_bwd_kernel<T, ROWS, PACKED, true>>(a, sw, g, st);
