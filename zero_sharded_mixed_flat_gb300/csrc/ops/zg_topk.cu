@@ -11,10 +11,10 @@
 // bit. Few rows take a cluster of blocks to a row, whose lists are merged
 // through distributed shared memory.
 //
-// Measured at 4096 x 50257 in bf16: k = 64 87 us (4.7 TB/s), k = 256 154. What
+// Measured at 4096 x 50257 in bf16: k = 64 84 us (4.9 TB/s), k = 256 146. What
 // is above the 61 us of the bytes is each row's end (bound, shares read again,
 // order), during which its block asks for nothing; other blocks of the SM fill
-// in for it. In binary32 188 us (4.4 TB/s); 7 rows, k = 100, 8 us, all latency.
+// in for it. In binary32 186 us (4.4 TB/s); 7 rows, k = 100, 8 us, all latency.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -221,23 +221,34 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) topk_kernel(const T *
         const int hots = sh.hots, per = (units + kShares - 1) / kShares;
         int side = 0;  // lanes to a share that reaches it: a power of two, at most a warp
         while (side < 5 && (1 << side) < per) ++side;
-        for (int h = tid >> side; h < hots; h += THREADS >> side) {
-            const int first = sh.hot[h];
-            for (int i = tid & ((1 << side) - 1); i < per; i += 1 << side) {
-                const int u = first + i * kShares;
-                if (u >= units) break;
-                const Unit<T> x = unit_at(u);
-                typename Unit<T>::Top top;
-                top.add(x);
-                if (top.get() < least) continue;
-                uint32_t hits = 0u;
+        auto look = [&](const Unit<T> &x, int u) {
+            typename Unit<T>::Top top;
+            top.add(x);
+            if (top.get() < least) return;
+            uint32_t hits = 0u;
 #pragma unroll
-                for (int j = 0; j < N; ++j) hits |= uint32_t(!(__uint_as_float(bits_in(x, j)) < least)) << j;
-                while (hits) {
-                    const int j = __ffs(int(hits)) - 1;
-                    hits &= hits - 1u;
-                    put(bits_of(x, j), base + u * N + j);
+            for (int j = 0; j < N; ++j) hits |= uint32_t(!(__uint_as_float(bits_in(x, j)) < least)) << j;
+            while (hits) {
+                const int j = __ffs(int(hits)) - 1;
+                hits &= hits - 1u;
+                put(bits_of(x, j), base + u * N + j);
+            }
+        };
+        // two units asked for before the first is looked at (one: 85 us for 83 above, four: 85)
+        const int lanes = 1 << side;
+        for (int i = tid & (lanes - 1); i < per; i += lanes) {
+            for (int h = tid >> side; h < hots; h += 2 * THREADS >> side) {
+                Unit<T> x[2];
+                int at[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int share = h + (j * THREADS >> side);
+                    at[j] = share < hots ? sh.hot[share] + i * kShares : units;
+                    if (at[j] < units) x[j] = unit_at(at[j]);
                 }
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (at[j] < units) look(x[j], at[j]);
             }
         }
     }
