@@ -15,15 +15,14 @@
 // a row, which exchange their maximum and sum through distributed shared memory.
 // A part is whole 16-byte units of the row but for its two ends, so any row,
 // however it is aligned, moves in wide loads; a gradient whose rows are aligned
-// differently is stored in its own units, from words shifted into place.
+// differently is stored in its own units, each from the two that it lies across.
 //
 // Measured at 4096 x 50257 in bf16, k = 64: the loss 64 us (6.5 TB/s), the
 // gradient 125 (6.6 TB/s), both in one launch 154 (5.3 TB/s of the once-read,
 // once-written bytes; what is left is the second read out of L2 and the phases
 // of a row). With gradient rows that are not aligned as the logits' are, 2048
-// rows: gradient 81, both 97 (a word more is
-// loaded for each unit). One row: 5 and 4 us, the latency of the launch and of
-// the row's three phases.
+// rows: gradient 72, both 89. One row: 5 and 4 us, the latency of the launch and
+// of the row's three phases.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -131,22 +130,18 @@ struct Shared {
     __align__(16) int at[ZG_TOPK_MAX];
 };
 
-// Sixteen bytes from element i of `base`, which is aligned to its units only,
-// by whole words: up to one element before and after them is read too.
-__device__ __forceinline__ void read_shifted(const uint16_t *base, int i, Unit<uint16_t> &x)
+// Sixteen bytes that begin `at` elements into the first of two units.
+template <class T>
+__device__ __forceinline__ uint4 across(uint4 p, uint4 q, int at)
 {
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(base) + (i >> 1);
-    x.w = make_uint4(w[0], w[1], w[2], w[3]);
-    if (i & 1) {
-        const uint32_t last = w[4];
-        x.w = make_uint4(__funnelshift_r(x.w.x, x.w.y, 16), __funnelshift_r(x.w.y, x.w.z, 16),
-                         __funnelshift_r(x.w.z, x.w.w, 16), __funnelshift_r(x.w.w, last, 16));
-    }
-}
-__device__ __forceinline__ void read_shifted(const float *base, int i, Unit<float> &x)
-{
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(base) + i;
-    x.w = make_uint4(w[0], w[1], w[2], w[3]);
+    const int words = at * int(sizeof(T)) / 4, bits = sizeof(T) == 2 ? 16 * (at & 1) : 0;
+    const bool two = words & 2, one = words & 1;
+    const uint32_t a0 = two ? p.z : p.x, a1 = two ? p.w : p.y, a2 = two ? q.x : p.z, a3 = two ? q.y : p.w;
+    const uint32_t a4 = two ? q.z : q.x, a5 = two ? q.w : q.y;
+    const uint32_t b0 = one ? a1 : a0, b1 = one ? a2 : a1, b2 = one ? a3 : a2, b3 = one ? a4 : a3, b4 = one ? a5 : a4;
+    if (sizeof(T) == 4) return make_uint4(b0, b1, b2, b3);
+    return make_uint4(__funnelshift_r(b0, b1, bits), __funnelshift_r(b1, b2, bits), __funnelshift_r(b2, b3, bits),
+                      __funnelshift_r(b3, b4, bits));
 }
 
 // Threads to an SM: as many as registers allow without spilling what is asked
@@ -319,18 +314,35 @@ __global__ void __launch_bounds__(THREADS, (kToSm<LOSS, GRAD> / THREADS)) distil
             i0 = part.u0 * N;
             i1 = part.u1 * N;
         } else {
-            // the output's units lie across the input's: whole ones of the output,
-            // read a word at a time, with an element to spare at both ends
+            // the output's units lie across the input's: whole ones of the output
+            // that lie across whole ones of the part
             i0 = (part.u0 * N + 1 + phase + N - 1) / N * N - phase;
             i1 = max((part.u1 * N - 1 + phase) / N * N - phase, i0);
         }
         auto pass = [&](auto is_far_too) {
             if (phase != 0) {
-                for (int i = i0 + tid * N; i < i1; i += THREADS * N) {
-                    Unit<T> x;
-                    read_shifted(base, i, x);
-                    gradient(x, is_far_too);
-                    __stcs(reinterpret_cast<uint4 *>(dz + i), x.w);
+                // each from the two units that it lies across, the second of which a
+                // neighbour reads first; two at a time (one: 80 and 94 us for 72 and 89)
+                const uint4 *const in = reinterpret_cast<const uint4 *>(base);
+                const int at = (N - phase) % N;
+                for (int i = i0 + tid * N; i < i1; i += 2 * THREADS * N) {
+                    uint4 p[2], q[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int u = (i + j * THREADS * N) / N;
+                        if (i + j * THREADS * N < i1) {
+                            p[j] = in[u];
+                            q[j] = in[u + 1];
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (i + j * THREADS * N >= i1) break;
+                        Unit<T> x;
+                        x.w = across<T>(p[j], q[j], at);
+                        gradient(x, is_far_too);
+                        __stcs(reinterpret_cast<uint4 *>(dz + i + j * THREADS * N), x.w);
+                    }
                 }
                 return;
             }
