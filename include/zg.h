@@ -472,7 +472,8 @@ int zg_topk(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t 
  * A term with p_j = 0 counts as zero. A row without a present entry, or whose
  * present entries are all -inf, is empty (a padding row): its loss, lse and
  * gradient are zero, whatever its logits are. A logit of -inf has
- * q = 0. Entries may come in any order; a repeated index adds up. */
+ * q = 0, and so has one that any large finite number masks. Entries may come in
+ * any order; a repeated index adds up. */
 typedef struct {
     const void *logits; /* row r starts at logits + r * row_stride elements; aligned to its element */
     int64_t rows, vocab, row_stride; /* vocab <= 2^30, row_stride >= vocab */
@@ -487,7 +488,10 @@ typedef struct {
 /* The loss of each row and its lse (rows binary32 each; lse may be NULL). */
 int zg_distill_loss(const zg_distill_args *args, float *loss, float *lse, zg_stream stream);
 
-/* The gradient, from the lse that zg_distill_loss gave for the same logits.
+/* The gradient, from the lse that zg_distill_loss gave for the same logits. q has a
+ * relative error of some |lse| 2^-24; rows with |lse| above 2800, where that would
+ * begin to show (every logit a large mask value, say), have their sum taken again,
+ * which is slower.
  * scale (finite) is common to all rows: the loss scale over the number of
  * rows, say. dloss: one binary32 factor per row, or NULL for ones. dlogits has
  * the logits' dtype and row_stride drow_stride; it may be the logits
@@ -496,7 +500,7 @@ int zg_distill_grad(const zg_distill_args *args, const float *lse, float scale, 
                     int64_t drow_stride, zg_stream stream);
 
 /* Both in one pass that reads the logits once from memory. lse may be NULL.
- * The values are those of the two calls up to the order of the sums. */
+ * The values are those of the two calls up to roundings. */
 int zg_distill_loss_grad(const zg_distill_args *args, float scale, const float *dloss, float *loss, float *lse,
                          void *dlogits, int64_t drow_stride, zg_stream stream);
 

@@ -343,3 +343,72 @@ def test_refusals():
         zb.distill_loss(z[:1].expand(4, 100), t, index, 1.0)
     with pytest.raises(ValueError, match="out must have shape"):
         zb.distill_loss_grad(z, t, index, 1.0, out=z[:, :50])
+
+
+def check_rows_like(z, same, t, index, temperature, only_both=False):
+    """The outputs for z against the formulas for ``same``: logits with the same
+    probabilities (masked ones at -inf, or all moved by one number), whose smaller
+    values give the tight bounds. ``only_both``: not what goes through lse, which is
+    held to the formulas for z itself."""
+    d = rand(z.shape[0], 78).abs().float()
+    loss, lse, grad, loss_err, lse_err, grad_err = ref.distill(same, t.double().cpu(), index.cpu(), temperature, 64.0, d.double())
+    err, f32 = ref.stored(grad, grad_err, z.dtype), torch.float32
+    one_loss, one = zb.distill_loss_grad(z, t, index, temperature, 64.0, d.cuda())
+    ref.check(one_loss, loss, ref.stored(loss, loss_err, f32), "loss of both")
+    ref.check(one, grad, err, "grad of both")
+    got_loss, got_lse = zb.distill_loss(z, t, index, temperature)
+    ref.check(got_loss, loss, ref.stored(loss, loss_err, f32), "loss")
+    if only_both:
+        _, lse, grad, _, lse_err, grad_err = ref.distill(z.double().cpu(), t.double().cpu(), index.cpu(), temperature, 64.0,
+                                                         d.double())
+        err = ref.stored(grad, grad_err, z.dtype)
+    ref.check(got_lse, lse, ref.stored(lse, lse_err, f32), "lse")
+    ref.check(zb.distill_grad(z, got_lse, t, index, temperature, 64.0, d.cuda()), grad, err, "grad")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("temperature", [0.1, 0.25, 1.0, 2.0])
+@pytest.mark.parametrize("v", [90, 5003, 50257])
+def test_distill_finite_masks(v, temperature, dtype):
+    """Logits closed by a large finite number count for nothing, whatever the number and
+    however many a thread meets before its first open one."""
+    dt, lowest = DT[dtype], torch.finfo(DT[dtype]).min
+    t, index = teacher(6, v, 30, dt, 31, ragged=False)
+    at = torch.arange(v)
+    shut = torch.stack([at < v // 2, at >= v // 2, at % 16 < 8, at % 7 != 3, torch.ones(v, dtype=torch.bool), at < 0])
+    shut.scatter_(1, index.long().cpu(), False)  # the teacher's entries stay open
+    z = logits_of(6, v, dt, 32)
+    same = torch.where(shut, -math.inf, z.double().cpu())
+    for mask in (-1e4, -1e9, -1e10, -1e12, -1e15, -1e20, -1e29, lowest):
+        check_rows_like(z.masked_fill(shut.cuda(), mask), same, t, index, temperature)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_distill_finite_masks_in_many_rows(dtype):
+    """The same with a block to a row."""
+    n, v, dt = 610, 20011, DT[dtype]
+    t, index = teacher(n, v, 20, dt, 33)
+    shut = torch.arange(v).expand(n, v) < (torch.arange(n) * 37 % v)[:, None]
+    shut = shut.scatter(1, index.long().clamp(min=0).cpu(), False)
+    z = logits_of(n, v, dt, 34)
+    same = torch.where(shut, -math.inf, z.double().cpu())
+    for mask in (-1e10, -1e20):
+        check_rows_like(z.masked_fill(shut.cuda(), mask), same, t, index, 1.0)
+
+
+@pytest.mark.parametrize("temperature", [0.5, 2.0])
+@pytest.mark.parametrize("v", [90, 5003, 50257])
+def test_distill_rows_far_from_zero(v, temperature):
+    """A row moved by one number has the same probabilities, and so the same loss and, in
+    one pass, the same gradient: neither goes through the log-sum-exp, whose last place
+    grows with the move."""
+    t, index = teacher(6, v, 30, torch.float32, 35, ragged=False)
+    for move in (3e3, 1e5, -1e6, -1e10, 1e15, -1e30):
+        z = (logits_of(6, v, torch.float32, 36) + move).contiguous()
+        z[5] = move  # uniform
+        same = z.double().cpu() - z.double().cpu().max(1, keepdim=True).values
+        check_rows_like(z, same, t, index, temperature, only_both=True)
+    z = torch.full((6, v), torch.finfo(torch.bfloat16).min, dtype=torch.bfloat16, device="cuda")
+    d = torch.ones(6, device="cuda")
+    want = ref.distill(torch.zeros(6, v, dtype=torch.float64), t.double().cpu(), index.cpu(), temperature)
+    ref.check(zb.distill_loss_grad(z, t, index, temperature, 1.0, d)[1], want[2], ref.stored(want[2], want[5], torch.bfloat16))

@@ -18,10 +18,10 @@
 // differently is stored in its own units, each from the two that it lies across.
 //
 // Measured at 4096 x 50257 in bf16, k = 64: the loss 64 us (6.5 TB/s), the
-// gradient 125 (6.6 TB/s), both in one launch 154 (5.3 TB/s of the once-read,
+// gradient 126 (6.5 TB/s), both in one launch 154 (5.3 TB/s of the once-read,
 // once-written bytes; what is left is the second read out of L2 and the phases
 // of a row). With gradient rows that are not aligned as the logits' are, 2048
-// rows: gradient 72, both 89. One row: 5 and 4 us, the latency of the launch and
+// rows: gradient 74, both 90. One row: 5 and 4 us, the latency of the launch and
 // of the row's three phases.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -94,8 +94,8 @@ __device__ __forceinline__ void raise(Sum &s, float top, float c)
 }
 // sum 2^((v - top) c) over units, each element one packed multiply-add and an
 // exponential: top c is rounded once, and what that takes off every exponent
-// is given back to the sum. Where top c could overflow (rows of a type's lowest
-// value) differences come first.
+// is given back to the sum. Where that rounding is no longer small (a top that is
+// a mask, or rows far from zero) differences come first.
 template <class T, bool FAR>
 struct Under {
     float top, c, off;
@@ -118,7 +118,12 @@ struct Under {
         return FAR ? s : s * exp2_approx(-fmaf(top, c, -off));
     }
 };
-__device__ __forceinline__ bool is_far(float v) { return !(fabsf(v) < 1e30f); }
+// An exponent from which on differences come first. Below this its rounding is at most
+// 2^-17; from 2^31 on what has to be made good would pass the exponent's range and
+// give inf * 0.
+__device__ __forceinline__ bool is_far(float v) { return !(fabsf(v) < 256.0f); }
+// A given lse whose last place would show: half of it is 2^-13 of q from here on.
+__device__ __forceinline__ bool is_lost(float lse) { return !(fabsf(lse * kLog2e) < 4096.0f); }
 
 template <int THREADS>
 struct Shared {
@@ -151,7 +156,10 @@ template <bool LOSS, bool GRAD>
 constexpr int kToSm = !LOSS ? 1536 : GRAD ? 1024 : 1280;
 
 // Without LOSS, lse is given. A row takes `blocks` blocks of `each` units: with
-// LOSS a cluster, in which they exchange sums.
+// LOSS a cluster, in which they exchange sums. A row whose given lse is_lost has its
+// maximum and sum taken again, all of it by its first block alone: the logits may be
+// written over. (What that asks of the registers takes 1 % from the other rows'
+// gradient: 126 us for 125 of 4096 x 50257 in bf16.)
 template <class T, class E, bool LOSS, bool GRAD, int THREADS>
 __global__ void __launch_bounds__(THREADS, (kToSm<LOSS, GRAD> / THREADS)) distill_kernel(DistillArgs a, int blocks, int each)
 {
@@ -161,12 +169,9 @@ __global__ void __launch_bounds__(THREADS, (kToSm<LOSS, GRAD> / THREADS)) distil
     const unsigned number = blockIdx.x / unsigned(blocks);
     const int64_t r = number;
     const int rank = int(blockIdx.x - number * unsigned(blocks));
+    const float given = LOSS ? 0.0f : a.lse_in[r];
     const float rt = 1.0f / a.temperature, c = rt * kLog2e;
-    const Row<T> row(static_cast<const T *>(a.logits) + r * a.row_stride, a.vocab, each, rank);
-    const Part &part = row.part;
-    const T *const z = row.z, *const base = row.base;
-    const uint4 *const from = row.from();
-    const int units = row.units;
+    const T *const z = static_cast<const T *>(a.logits) + r * a.row_stride;
 
     // The teacher's entries, one or two to a thread, and the logits at them
     // before anything is written over those.
@@ -185,6 +190,16 @@ __global__ void __launch_bounds__(THREADS, (kToSm<LOSS, GRAD> / THREADS)) distil
         if (at[n] < 0 || at[n] >= a.vocab) at[n] = -1, te[n] = -INFINITY;
         zt[n] = at[n] >= 0 ? load1(z + at[n]) : 0.0f;
     }
+    const bool lost = !LOSS && is_lost(given);
+    if (lost) {
+        if (rank != 0) return;
+        each = a.vocab / N + 2;
+    }
+    const Row<T> row(z, a.vocab, each, rank);
+    const Part &part = row.part;
+    const T *const base = row.base;
+    const uint4 *const from = row.from();
+    const int units = row.units;
 
     Sum s = none();
     if (LOSS) {
@@ -223,6 +238,21 @@ __global__ void __launch_bounds__(THREADS, (kToSm<LOSS, GRAD> / THREADS)) distil
                 if (u + i * THREADS < units) x[i].w = from[u + i * THREADS];
             take_in(x, u, false);
         }
+    }
+    if (lost) {  // differences first throughout
+#pragma unroll 1
+        for (int u = tid; u < units; u += THREADS) {
+            Unit<T> x;
+            x.w = from[u];
+            typename Unit<T>::Top top;
+            top.add(x);
+            raise(s, top.get(), c);
+            Under<T, true> under(s.top, c);
+            under.add(x);
+            if (s.top != -INFINITY) s.sum += under.get();
+        }
+    }
+    if (LOSS || lost) {
         const int i = row.ragged(tid);
         if (i >= 0) {
             const float v = load1(base + i);
@@ -239,7 +269,7 @@ __global__ void __launch_bounds__(THREADS, (kToSm<LOSS, GRAD> / THREADS)) distil
             if (entries) t = join(t, Sum{te[n], te[n] == -INFINITY ? 0.0f : te[n] - te[n] + 1.0f}, c);
         }
         if (entries) t = across<32>(t, c);
-        if (LOSS) s = across<32>(s, c);
+        if (LOSS || lost) s = across<32>(s, c);
         if (tid % 32 == 0) {
             sh.teacher[tid / 32] = t;
             sh.student[tid / 32] = s;
@@ -278,8 +308,8 @@ __global__ void __launch_bounds__(THREADS, (kToSm<LOSS, GRAD> / THREADS)) distil
             if (tid % 32 == 0) sh.red[tid / 32] = term;
         }
         if (rank == 0 && tid == 0 && a.lse) a.lse[r] = empty ? 0.0f : lse;
-    } else if (!empty) {
-        lse = a.lse_in[r];
+    } else {
+        lse = given;
     }
     if (GRAD) {
 #pragma unroll
@@ -289,12 +319,14 @@ __global__ void __launch_bounds__(THREADS, (kToSm<LOSS, GRAD> / THREADS)) distil
         }
         const float g = a.scale * a.temperature * (a.dloss ? a.dloss[r] : 1.0f);
         T *const dz = static_cast<T *>(a.dlogits) + r * a.drow_stride - part.head;
-        // 2^(v c - low), low = lse log2(e) rounded once and made good in the factor
+        // 2^(v c - low), low = lse log2(e) rounded once and made good in the factor.
+        // For rows far from zero lse's own last place would show, and q is
+        // 2^((v - top) c) / sum.
         const float low = lse * kLog2e;
-        const bool far = is_far(low);
-        const float gg = far ? g : g * exp2_approx(-fmaf(lse, kLog2eRest, fmaf(lse, kLog2e, -low)));
+        const bool far = LOSS ? is_far(low) : lost;
+        const float gg = far ? g / s.sum : g * exp2_approx(-fmaf(lse, kLog2eRest, fmaf(lse, kLog2e, -low)));
         auto gradient1 = [&](float v) {
-            return empty ? 0.0f : exp2_approx(far ? fmaf(v, rt, -lse) * kLog2e : fmaf(v, c, -low)) * gg;
+            return empty ? 0.0f : exp2_approx(far ? (v - s.top) * c : fmaf(v, c, -low)) * gg;
         };
         auto gradient = [&](Unit<T> &x, auto is_far_too) {
             float2 v[N / 2];
@@ -302,7 +334,7 @@ __global__ void __launch_bounds__(THREADS, (kToSm<LOSS, GRAD> / THREADS)) distil
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) {
                 const float2 q = decltype(is_far_too)::value
-                                     ? mul_f32x2(fma_f32x2(v[i], make_float2(rt, rt), make_float2(-lse, -lse)), make_float2(kLog2e, kLog2e))
+                                     ? mul_f32x2(add_f32x2(v[i], make_float2(-s.top, -s.top)), make_float2(c, c))
                                      : fma_f32x2(v[i], make_float2(c, c), make_float2(-low, -low));
                 v[i] = mul_f32x2(make_float2(exp2_approx(q.x), exp2_approx(q.y)), make_float2(gg, gg));
             }
@@ -397,7 +429,10 @@ __global__ void __launch_bounds__(THREADS, (kToSm<LOSS, GRAD> / THREADS)) distil
                                        min(other.z == at[n] ? m + 2 : j, other.w == at[n] ? m + 3 : j)));
             }
             const bool write = first == j;
-            if (write) store1(dz + i, (exp2_approx(fmaf(zt[n], rt, -lse) * kLog2e) - sum / t.sum) * g);
+            const float p = sum / t.sum;
+            if (write)
+                store1(dz + i, far ? exp2_approx((zt[n] - s.top) * c) * gg - p * g
+                                   : (exp2_approx(fmaf(zt[n], rt, -lse) * kLog2e) - p) * g);
         }
     } else {
         __syncthreads();
