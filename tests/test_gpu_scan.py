@@ -337,3 +337,30 @@ def test_a_wait_that_runs_out_is_reported_and_forgotten():
     scan.set_wait_limit(4000000)
     assert torch.equal(scan.forward(x, f)[0], want)
     assert scan.status() == zb.ZG_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("c", [70, 64])
+def test_a_nan_leaves_the_other_channels_values_alone(c, dtype):
+    """What shares a lane, a run or a tile with a NaN has the bits that it has without it."""
+    t, dt = 700, DT[dtype]
+    starts = torch.tensor([0, 200, 450, 600], dtype=torch.int64).cuda()
+    x, f = (v[0] for v in views(1, t, c, dt, "plain", 29))
+    dy, h0, dh = rand((t, c), 30).to(dt).cuda(), rand((3, c), 31).float().cuda(), rand((3, c), 32).float().cuda()
+
+    def run(x, f, dy):
+        scan = zb.GatedScan(1, t, c)
+        y, last, kept = scan.forward(x, f, h0, starts, keep=True)
+        dx, df, dh0 = scan.backward(x, f, dy, kept, h0, dh, starts)
+        return [v[:600] for v in (y, dx, df)] + [last, kept[0], dh0]
+
+    want = run(x, f, dy)
+    for planted, (at, ch) in ((f, (300, 4)), (f, (0, 0)), (f, (211, 8)), (x, (303, 1)), (dy, (333, 12)), (f, (202, 3)),
+                              (f, (449, 0)), (f, (320, 32))):
+        was = planted[at, ch].clone()
+        planted[at, ch] = math.nan
+        got = run(x, f, dy)
+        planted[at, ch] = was
+        others = torch.arange(c, device="cuda") != ch
+        for g, w in zip(got, want):
+            assert torch.equal(g[:, others], w[:, others]), (at, ch)
