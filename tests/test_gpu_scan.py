@@ -364,3 +364,32 @@ def test_a_nan_leaves_the_other_channels_values_alone(c, dtype):
         others = torch.arange(c, device="cuda") != ch
         for g, w in zip(got, want):
             assert torch.equal(g[:, others], w[:, others]), (at, ch)
+
+
+def packed_starts(t, seed):
+    """Sequences within a run of tokens, across runs, warps and chunks, and empty ones."""
+    cuts, at = [0, 7, 9, 9, 18, 33, 128, 128, 140, 267, 300, 300, 301], 301
+    rng = np.random.default_rng(seed)
+    while at < t - 1:
+        at = min(t - 1, at + int(rng.integers(1, 300)))
+        cuts.append(at)
+    return [c for c in cuts if c < t] + [t]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t,c", [(300, 66), (1500, 771), (5000, 64), (700, 8256)])
+def test_packed_states_updated_in_place(t, c, dtype):
+    """h_last in h0's own memory: the same bits as apart, wherever a sequence begins and ends."""
+    starts = packed_starts(t, t + c)
+    x, f = (v[0] for v in views(1, t, c, DT[dtype], "plain", 83))
+    seq_start = torch.tensor(starts, dtype=torch.int64).cuda()
+    h0 = rand((len(starts) - 1, c), 84, 50.0).float().cuda()
+    scan = zb.GatedScan(1, t, c)
+    y, last, kept = scan.forward(x, f, h0, seq_start, keep=True)
+    for _ in range(3):
+        state = h0.clone()
+        y2, last2, kept2 = scan.forward(x, f, state, seq_start, keep=True, h_last=state)
+        assert last2 is state
+        for got, want in ((y2, y), (state, last), (kept2, kept)):
+            assert torch.equal(got, want)
+    assert scan.status() == zb.ZG_OK

@@ -922,8 +922,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
             gates(decay<T>(read_f4<VEC>(at_f.next(bf, a.f, run, i), l)), keep[i], take);
             in[i] = mul(take, read4<VEC>(at_x.next(bx, a.x, run, i), l));
             if (PACKED && (mk.first >> i & 1)) {
+                // the state after the first token stands for its input: h0 is not read
+                // again, since h_last may be the same memory, and the block that has the
+                // sequence's last token writes there once this tile's map is known
                 m.b = fma(keep[i], initial(i), in[i]);
                 m.a = all(kConst);
+                in[i] = m.b;
             } else if (i == 0) {
                 m = Map{keep[0], in[0]};
             } else {
@@ -958,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
         } else {
 #pragma unroll
             for (int i = 0; i < kRun; ++i) {
-                if (PACKED && (mk.first >> i & 1)) h = initial(i);
+                if (PACKED && (mk.first >> i & 1)) h = all(-0.0f);  // then in[i], to the bit
                 h = fma(keep[i], h, in[i]);
                 if (t0 + i < end) store4<VEC>(py, l, n, h);
                 py += a.y.st;
