@@ -393,3 +393,38 @@ def test_packed_states_updated_in_place(t, c, dtype):
         for got, want in ((y2, y), (state, last), (kept2, kept)):
             assert torch.equal(got, want)
     assert scan.status() == zb.ZG_OK
+
+
+def backward_in_place(scan, x, f, dy, kept, h0, d, seq_start):
+    """The C call with dh0 in dh_last's memory, ``d``; (tokens, channels) or (batch, tokens, channels)."""
+    import ctypes
+
+    dt = zb.ZG_DTYPE_BF16 if x.dtype is torch.bfloat16 else zb.ZG_DTYPE_F32
+    b, t, c = (1, *x.shape) if x.dim() == 2 else x.shape
+    shape = zb._ScanShape(b, t, c, None if seq_start is None else seq_start.data_ptr(), d.shape[0], dt)
+    view = lambda v: ctypes.byref(zb._View(v.data_ptr(), v.stride(0) if v.dim() == 3 else 0, v.stride(-2)))  # noqa: E731
+    dx, df = torch.empty_like(x), torch.empty_like(x)
+    assert zb.lib().zg_gated_scan_bwd(scan.handle, ctypes.byref(shape), view(x), view(f), view(dy), kept.data_ptr(),
+                                      h0.data_ptr(), d.data_ptr(), view(dx), view(df), d.data_ptr(),
+                                      torch.cuda.current_stream().cuda_stream) == 0
+    return dx, df
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t,c", [(300, 66), (1500, 771), (5000, 64), (700, 8256)])
+def test_packed_gradients_of_states_in_place(t, c, dtype):
+    """dh0 in dh_last's own memory: the same bits as apart."""
+    starts = packed_starts(t, t + c)
+    x, f = (v[0] for v in views(1, t, c, DT[dtype], "plain", 85))
+    dy = rand((t, c), 86).to(DT[dtype]).cuda()
+    seq_start = torch.tensor(starts, dtype=torch.int64).cuda()
+    h0, dh = (rand((len(starts) - 1, c), s, 50.0).float().cuda() for s in (87, 88))
+    scan = zb.GatedScan(1, t, c)
+    _, _, kept = scan.forward(x, f, h0, seq_start, keep=True)
+    want = scan.backward(x, f, dy, kept, h0, dh, seq_start)
+    for _ in range(3):
+        d = dh.clone()
+        got = (*backward_in_place(scan, x, f, dy, kept, h0, d, seq_start), d)
+        for p, q in zip(got, want):
+            assert torch.equal(p, q)
+    assert scan.status() == zb.ZG_OK

@@ -1054,6 +1054,18 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
             return state4<VEC>(p ? p + table[run * kRun + i] * a.channels + t.ch : nullptr, l, n);
         };
 
+        // dh_last of the sequences that end in the run, in order. It is not read after
+        // this tile's map is known, since dh0 may be the same memory, and the block that
+        // has a sequence's first token writes there then. Indexed when running, so that
+        // it lies in local memory and takes no registers where nothing ends.
+        F4 ends[PACKED ? kRun : 1];
+        if (PACKED) {
+            int ended = 0;
+#pragma unroll 1
+            for (uint32_t left = mk.last; left; left &= left - 1u)
+                ends[ended++] = side(a.dh_last, sh.cuts.last, __ffs(int(left)) - 1);
+        }
+
         // Both maps in one pass over the tokens: the later tokens' gradient
         // comes in through the product of the gates so far. exp(-f) alone is
         // kept of the gates, which are formed again from it where they are
@@ -1085,7 +1097,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
                 weight = mul(weight, keep);
                 r.b = fma(weight, read4<VEC>(row_dy, l), r.b);
                 if (PACKED && (mk.last >> i & 1)) {
-                    r.b = fma(weight, side(a.dh_last, sh.cuts.last, i), r.b);
+                    r.b = fma(weight, ends[0], r.b);
                     cut = true;
                 }
             }
@@ -1151,7 +1163,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
             for (int i = kRun - 1; i >= 0; --i) {
                 const T *const row_dy = at_dy2.last(bx + kSize, a.y, run, i);
                 if (t0 + i < end) {
-                    if (PACKED && (mk.last >> i & 1)) gr = side(a.dh_last, sh.cuts.last, i);
+                    if (PACKED && (mk.last >> i & 1)) gr = ends[__popc(mk.last & ((1u << i) - 1u))];
                     back(i, row_dy);
                     if (PACKED && a.dh0 && (mk.first >> i & 1))
                         put_state4<VEC>(a.dh0 + sh.cuts.first[run * kRun + i] * a.channels + t.ch, l, n, gr);
