@@ -428,3 +428,21 @@ def test_packed_gradients_of_states_in_place(t, c, dtype):
         for p, q in zip(got, want):
             assert torch.equal(p, q)
     assert scan.status() == zb.ZG_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("b,t,c", [(2, 9, 70), (2, 100, 66), (1, 5000, 130), (3, 700, 4160)])
+def test_rows_in_place(b, t, c, dtype):
+    """States and their gradients in place, in rows of few and of many chunks."""
+    x, f = views(b, t, c, DT[dtype], "plain", 89)
+    dy = rand((b, t, c), 90).to(DT[dtype]).cuda()
+    h0, dh = (rand((b, c), s, 50.0).float().cuda() for s in (91, 92))
+    scan = zb.GatedScan(b, t, c)
+    y, last, kept = scan.forward(x, f, h0, keep=True)
+    want = scan.backward(x, f, dy, kept, h0, dh)
+    for _ in range(3):
+        state, d = h0.clone(), dh.clone()
+        y2, _, kept2 = scan.forward(x, f, state, keep=True, h_last=state)
+        for p, q in zip((y2, state, kept2, *backward_in_place(scan, x, f, dy, kept, h0, d, None), d), (y, last, kept, *want)):
+            assert torch.equal(p, q)
+    assert scan.status() == zb.ZG_OK

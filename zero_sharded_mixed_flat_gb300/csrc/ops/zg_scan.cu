@@ -732,6 +732,9 @@ __device__ __forceinline__ void solve(M &maps, Before &before, const Work &w, co
         __syncthreads();
         return;
     }
+    // Through shared memory, so that it has been read before this chunk's map is
+    // published: the row's last block may write its final state over it after that.
+    maps.span[slot] = start;
     const bool followed = t.k + 1 < uint32_t(g.chunks), ends_group = before.in_group == kGroup - 1 && followed;
     const int64_t step = g.width * kTile, at = int64_t(t.rest) * kTile + slot;
     const uint32_t this_group = t.k / kGroup;
@@ -761,7 +764,7 @@ __device__ __forceinline__ void solve(M &maps, Before &before, const Work &w, co
         maps.span[slot] = values(v).x;
     }
     __syncthreads();
-    float h = before.first_group > 0 ? maps.span[slot] : start;
+    float h = maps.span[slot];
 #pragma unroll
     for (int i = 0; i < 4; ++i) h = apply<CUT>(maps.groups[i][slot], h);
 #pragma unroll
