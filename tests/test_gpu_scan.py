@@ -446,3 +446,20 @@ def test_rows_in_place(b, t, c, dtype):
         for p, q in zip((y2, state, kept2, *backward_in_place(scan, x, f, dy, kept, h0, d, None), d), (y, last, kept, *want)):
             assert torch.equal(p, q)
     assert scan.status() == zb.ZG_OK
+
+
+def test_a_new_handle_on_a_stream_that_waits_for_nothing():
+    """The handle's workspace is ready when it is made, whatever the default stream is busy with."""
+    b, t, c = 2, 1500, 130
+    x, f = views(b, t, c, torch.bfloat16, "plain", 93)
+    want = zb.GatedScan(b, t, c).forward(x, f)[0]
+    side = torch.cuda.Stream()  # does not wait for the default stream
+    torch.cuda.synchronize()
+    for _ in range(20):
+        torch.cuda._sleep(20_000_000)  # some 10 ms on the default stream
+        scan = zb.GatedScan(b, t, c)
+        with torch.cuda.stream(side):
+            got = scan.forward(x, f)[0]
+        assert scan.status(side) == zb.ZG_OK
+        assert torch.equal(got, want)
+    torch.cuda.synchronize()

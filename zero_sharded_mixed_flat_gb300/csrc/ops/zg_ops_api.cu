@@ -224,6 +224,9 @@ int zg_scan_init(int64_t batch, int64_t tokens, int64_t channels, zg_scan **out)
     // epoch 1: the cleared records belong to no launch
     const unsigned long long ctl = 1ull << 32;
     if (e == cudaSuccess) e = cudaMemcpy(s->d_mem, &ctl, sizeof ctl, cudaMemcpyHostToDevice);
+    // Both may return before they are done on the device, and a stream of the caller's
+    // that does not wait for the default stream could overtake them.
+    if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
     if (e != cudaSuccess) {
         const int rc = e == cudaErrorMemoryAllocation
                            ? fail(ZG_ERR_NO_MEMORY, "zg_scan_init: %lld bytes of workspace: %s",
