@@ -443,8 +443,9 @@ int zg_gated_scan_bwd(zg_scan *scan, const zg_scan_shape *shape, const zg_view *
                       const zg_view *dx, const zg_view *df, float *dh0, zg_stream stream);
 
 /* Wait for `stream`, then report and clear the handle's status: ZG_OK, or
- * ZG_ERR_DEVICE_TIMEOUT when a part of a scan waited for its predecessor's
- * state longer than the wait limit (its outputs are then unspecified). */
+ * ZG_ERR_DEVICE_TIMEOUT when since the last call a part of a scan waited for its
+ * predecessor's state longer than the wait limit (that scan's outputs are then
+ * unspecified; later scans on the handle are not concerned). */
 int zg_scan_status(zg_scan *scan, zg_stream stream, int *status);
 
 /* Bound, in polls, on that wait (default a few million, far above any healthy

@@ -463,3 +463,22 @@ def test_a_new_handle_on_a_stream_that_waits_for_nothing():
         assert scan.status(side) == zb.ZG_OK
         assert torch.equal(got, want)
     torch.cuda.synchronize()
+
+
+def test_a_wait_that_ran_out_does_not_concern_the_next_scan():
+    """Whether the status has been asked for or not: it is kept for the asking, and no more."""
+    b, t, c = 1, 40000, 130
+    x, f = views(b, t, c, torch.bfloat16, "plain", 95)
+    dy = rand((b, t, c), 96).to(torch.bfloat16).cuda()
+    scan = zb.GatedScan(b, t, c)
+    y, _, kept = scan.forward(x, f, keep=True)
+    want = (y, *scan.backward(x, f, dy, kept))
+    assert scan.status() == zb.ZG_OK
+    for _ in range(5):
+        scan.set_wait_limit(0)
+        scan.forward(x, f)
+        scan.set_wait_limit(4000000)
+        got = (scan.forward(x, f)[0], *scan.backward(x, f, dy, kept))
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+        assert scan.status() == zb.ZG_ERR_DEVICE_TIMEOUT
+        assert scan.status() == zb.ZG_OK

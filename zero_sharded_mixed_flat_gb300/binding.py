@@ -637,7 +637,9 @@ class GatedScan:
         _check(lib().zg_scan_set_wait_limit(self.handle, polls), "zg_scan_set_wait_limit")
 
     def status(self, stream=None) -> int:
-        """ZG_OK, or ZG_ERR_DEVICE_TIMEOUT when a scan's bounded wait ran out (waits for the stream)."""
+        """ZG_OK, or ZG_ERR_DEVICE_TIMEOUT when a bounded wait of a scan since the last call ran out, so
+        that its outputs are not valid; later scans are not concerned. Waits for the stream;
+        ``forward`` and ``backward`` do not look."""
         st = ctypes.c_int()
         _check(lib().zg_scan_status(self.handle, _stream(stream), ctypes.byref(st)), "zg_scan_status")
         return st.value

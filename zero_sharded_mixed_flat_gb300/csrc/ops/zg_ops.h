@@ -33,6 +33,7 @@ struct ScanArgs {
 struct ScanWork {
     unsigned long long *ctl;
     int *status;
+    uint32_t *gave_up;
     void *records;
     long long wait_limit;
 };

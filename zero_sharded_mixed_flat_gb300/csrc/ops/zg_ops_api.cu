@@ -16,7 +16,7 @@ struct zg_scan {
     int device;
     int64_t batch, tokens, channels;
     int64_t record_bytes;
-    char *d_mem;  // ctl (8 bytes), status (4 bytes), and from kHead on the records
+    char *d_mem;  // ctl (8 bytes), status and gave_up (4 bytes each), and from kHead on the records
     long long wait_limit;
 };
 
@@ -75,7 +75,7 @@ constexpr long long kScanWaitLimit = 4000000;
 zg::ScanWork work_of(const zg_scan *s)
 {
     return zg::ScanWork{reinterpret_cast<unsigned long long *>(s->d_mem), reinterpret_cast<int *>(s->d_mem + 8),
-                        s->d_mem + kHead, s->wait_limit};
+                        reinterpret_cast<uint32_t *>(s->d_mem + 12), s->d_mem + kHead, s->wait_limit};
 }
 
 // `out`: no two elements may share memory.

@@ -201,6 +201,7 @@ struct Work {
     ulonglong2 *group;  // the same per group
     ulonglong2 *span;   // per span, tile and slot: the state after it (twice)
     int *status;
+    uint32_t *gave_up;  // the epoch of the last launch in which a wait ran out
     long long wait_limit;
 };
 
@@ -227,14 +228,16 @@ __device__ __forceinline__ float2 values(ulonglong2 v)
 }
 
 // Whether to ask again for words that are not there yet; false when the wait ran
-// out, here or in another block (which then must not be waited for).
-__device__ __forceinline__ bool go_on(const Work &w, long long polls)
+// out, here or in another block of this launch (which then must not be waited for).
+// The status stays until it is asked for, over launches that are not concerned.
+__device__ __forceinline__ bool go_on(const Work &w, uint32_t tag, long long polls)
 {
     if (polls >= w.wait_limit) {
         atomicExch(w.status, kStatusTimeout);
+        atomicExch(w.gave_up, tag);
         return false;
     }
-    return (polls & 63) != 63 || *reinterpret_cast<volatile int *>(w.status) == 0;
+    return (polls & 63) != 63 || *reinterpret_cast<volatile uint32_t *>(w.gave_up) != tag;
 }
 
 // Up to four maps of one slot, asked for together and composed in order. The
@@ -260,7 +263,7 @@ struct Four {
             uint32_t off = 0u;
 #pragma unroll
             for (int i = 0; i < 4; ++i) off |= (uint32_t(v[i].x >> 32) ^ tag) | (uint32_t(v[i].y >> 32) ^ tag);
-            if (off == 0u || !go_on(w, polls)) break;
+            if (off == 0u || !go_on(w, tag, polls)) break;
             ask();
         }
         float2 m = values(v[0]);
@@ -760,7 +763,7 @@ __device__ __forceinline__ void solve(M &maps, Before &before, const Work &w, co
     if (part == 3 && before.first_group > 0) {
         const ulonglong2 *p = w.span + (before.first_group / kGroup - 1) * step + at;
         ulonglong2 v = look(p);
-        for (long long polls = 0; !there(v, tag) && go_on(w, polls); ++polls) v = look(p);
+        for (long long polls = 0; !there(v, tag) && go_on(w, tag, polls); ++polls) v = look(p);
         maps.span[slot] = values(v).x;
     }
     __syncthreads();
@@ -1298,6 +1301,7 @@ cudaError_t launch(const ScanArgs &a, const ScanWork &sw, const Grid &g, cudaStr
     Work w{};
     w.ctl = sw.ctl;
     w.status = sw.status;
+    w.gave_up = sw.gave_up;
     w.wait_limit = sw.wait_limit;
     w.chunk = reinterpret_cast<ulonglong2 *>(sw.records);
     w.group = w.chunk + kTile * g.width * g.chunks;
