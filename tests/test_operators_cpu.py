@@ -129,3 +129,44 @@ def test_reference_distillation_against_autograd():
     with torch.no_grad():
         got, _, grad, *_ = ref.distill(z, t, index, 1.7, 8.0, w)
     assert torch.allclose(got, loss, rtol=1e-11, atol=1e-13) and torch.allclose(grad, z.grad, rtol=1e-11, atol=1e-13)
+
+
+def test_two_threads_on_one_handle_pass_their_own_arguments(monkeypatch):
+    """A call's arguments are whole when the library reads them, whatever another thread
+    does with the same handle meanwhile (the interpreter's lock is free during the call)."""
+    import threading
+
+    both, seen = threading.Barrier(2, timeout=60), {}
+
+    class Library:  # in place of the C calls: looks at its arguments when both threads are in them
+        @staticmethod
+        def zg_gated_scan(handle, shape, x, f, h0, y, h_last, states, stream):
+            both.wait()
+            seen[threading.get_ident()] = (shape._obj.tokens, x._obj.ptr, f._obj.ptr, y._obj.ptr, y._obj.token_stride)
+            both.wait()
+            return zb.ZG_OK
+
+        @staticmethod
+        def zg_scan_destroy(handle):
+            pass
+
+    monkeypatch.setattr(zb, "_lib", Library)
+    monkeypatch.setattr(zb, "_like", lambda t, ref, what: t)
+    monkeypatch.setattr(zb, "_side", lambda t, *args: None if t is None else t.data_ptr())
+    monkeypatch.setattr(zb, "_stream_of", lambda *args: 0)
+    scan = zb.GatedScan.__new__(zb.GatedScan)
+    scan.handle = None
+    want, outs = {}, []
+
+    def call(tokens):
+        x, f, y = (torch.zeros(1, tokens, 8, dtype=torch.bfloat16) for _ in range(3))
+        outs.append((x, f, y))
+        want[threading.get_ident()] = (tokens, x.data_ptr(), f.data_ptr(), y.data_ptr(), 8)
+        scan.forward(x, f, out=y)
+
+    threads = [threading.Thread(target=call, args=(n,)) for n in (30, 50)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(want) == 2 and seen == want

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from dataclasses import dataclass
 
 import torch
@@ -506,6 +507,28 @@ def _stream_of(stream, ref: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(ref.get_device()) if stream is None else _stream(stream)
 
 
+class _Blocks(threading.local):
+    """A thread's argument blocks: filled anew by every call, kept only to spare their
+    construction. A thread has its own, since a call's are read by the library while other
+    threads may run, on the same handle too."""
+
+    def __init__(self):
+        self.shape = _ScanShape()
+        self.views = [_View() for _ in range(5)]
+        self.refs = [ctypes.byref(self.shape), *[ctypes.byref(v) for v in self.views]]
+
+
+_blocks = _Blocks()
+
+
+def _fill(v: _View, t: torch.Tensor) -> None:
+    v.ptr = t.data_ptr()
+    if t.dim() == 3:
+        v.batch_stride, v.token_stride, _ = t.stride()
+    else:
+        v.batch_stride, v.token_stride = 0, t.stride(0)
+
+
 class GatedScan:
     """The gated linear recurrence h_t = sigmoid(f_t) h_{t-1} + sigmoid(-f_t) x_t
     over time, channel by channel, with its backward pass, on a handle for up
@@ -515,7 +538,8 @@ class GatedScan:
     bfloat16 or float32, the channels contiguous (parts of a wider projection
     are fine). ``seq_start``: for one row that holds several sequences end to
     end, the int64 CUDA tensor of their starts and the last one's end. States
-    are float32 (sequences, channels). One handle serves one stream at a time.
+    are float32 (sequences, channels). One handle serves one stream at a time, and any
+    thread.
     """
 
     def __init__(self, batch: int, tokens: int, channels: int):
@@ -523,25 +547,19 @@ class GatedScan:
         self.handle = None
         _check(lib().zg_scan_init(batch, tokens, channels, ctypes.byref(out)), "zg_scan_init")
         self.handle = out.value
-        self._prepare()
-
-    def _prepare(self) -> None:
-        # filled anew by every call, kept only to spare their construction
-        self._shape = _ScanShape()
-        self._views = [_View() for _ in range(5)]
-        self._refs = [ctypes.byref(self._shape), *[ctypes.byref(v) for v in self._views]]
 
     def __del__(self):
         if getattr(self, "handle", None) and _lib is not None:
             _lib.zg_scan_destroy(self.handle)
             self.handle = None
 
-    def _describe(self, x, f, seq_start) -> int:
+    @staticmethod
+    def _describe(blocks, x, f, seq_start) -> int:
         """Fill the shape and the views of x and f; returns the number of sequences."""
         dtype = _dtype(x, "x")
         _like(x, x, "x")
         _like(f, x, "f")
-        s, dims = self._shape, x.dim()
+        s, views, dims = blocks.shape, blocks.views, x.dim()
         s.dtype = dtype
         if dims == 3:
             s.batch, s.tokens, s.channels = x.shape
@@ -550,8 +568,8 @@ class GatedScan:
             s.tokens, s.channels = x.shape
         else:
             raise ValueError(f"x must be (batch, tokens, channels) or (tokens, channels) (got {tuple(x.shape)})")
-        self._view(0, x)
-        self._view(1, f)
+        _fill(views[0], x)
+        _fill(views[1], f)
         if seq_start is None:
             s.seq_start, s.n_seq = None, 0
             return s.batch
@@ -561,29 +579,22 @@ class GatedScan:
         s.seq_start = _side(seq_start, torch.int64, (s.n_seq + 1,), x, "seq_start")
         return s.n_seq
 
-    def _view(self, n: int, t: torch.Tensor) -> None:
-        v = self._views[n]
-        v.ptr = t.data_ptr()
-        if t.dim() == 3:
-            v.batch_stride, v.token_stride, _ = t.stride()
-        else:
-            v.batch_stride, v.token_stride = 0, t.stride(0)
-
     def forward(self, x, f, h0=None, seq_start=None, keep: bool = False, out=None, h_last=None, stream=None):
         """y, the state after each sequence, and with ``keep`` the states that
         ``backward`` starts from (else None). ``out`` and ``h_last`` are
         allocated when None; h_last may be h0 itself."""
-        n = self._describe(x, f, seq_start)
-        s, side = self._shape, (n, self._shape.channels)
+        b = _blocks
+        n = self._describe(b, x, f, seq_start)
+        s, side = b.shape, (n, b.shape.channels)
         y = torch.empty_like(x, memory_format=torch.contiguous_format) if out is None else _like(out, x, "out")
-        self._view(2, y)
+        _fill(b.views[2], y)
         p0 = _side(h0, torch.float32, side, x, "h0")
         last = torch.empty(side, dtype=torch.float32, device=x.device) if h_last is None else h_last
         p1 = last.data_ptr() if h_last is None else _side(last, torch.float32, side, x, "h_last")
         kept = None
         if keep:
             kept = torch.empty((s.batch, -(-s.tokens // ZG_SCAN_CHUNK), s.channels), dtype=torch.float32, device=x.device)
-        r = self._refs
+        r = b.refs
         _check(_lib.zg_gated_scan(self.handle, r[0], r[1], r[2], p0, r[3], p1, kept.data_ptr() if keep else None,
                                   _stream_of(stream, x)), "zg_gated_scan")
         return y, last, kept
@@ -592,20 +603,21 @@ class GatedScan:
         """The gradients (dx, df, dh0) from dy and dh_last (None: zero), for the
         x, f and h0 of the forward call that gave ``kept``. ``out``: (dx, df)
         to write into, for instance the parts of one projection's gradient."""
-        n = self._describe(x, f, seq_start)
-        s, side = self._shape, (n, self._shape.channels)
-        self._view(2, _like(dy, x, "dy"))
+        b = _blocks
+        n = self._describe(b, x, f, seq_start)
+        s, side = b.shape, (n, b.shape.channels)
+        _fill(b.views[2], _like(dy, x, "dy"))
         if kept is None:
             raise ValueError("kept is None: call forward with keep=True")
         if out is None:
             dx, df = (torch.empty_like(x, memory_format=torch.contiguous_format) for _ in range(2))
         else:
             dx, df = _like(out[0], x, "dx"), _like(out[1], x, "df")
-        self._view(3, dx)
-        self._view(4, df)
+        _fill(b.views[3], dx)
+        _fill(b.views[4], df)
         dh0 = torch.empty(side, dtype=torch.float32, device=x.device)
         pk = _side(kept, torch.float32, (s.batch, -(-s.tokens // ZG_SCAN_CHUNK), s.channels), x, "kept")
-        r = self._refs
+        r = b.refs
         _check(_lib.zg_gated_scan_bwd(self.handle, r[0], r[1], r[2], r[3], pk, _side(h0, torch.float32, side, x, "h0"),
                                       _side(dh_last, torch.float32, side, x, "dh_last"), r[4], r[5], dh0.data_ptr(),
                                       _stream_of(stream, x)), "zg_gated_scan_bwd")
@@ -616,18 +628,19 @@ class GatedScan:
         state, written to ``out_state`` (``state`` itself to update it in place)."""
         if not isinstance(x, torch.Tensor) or x.dim() != 2:
             raise ValueError("x must be (batch, channels)")
-        self._describe(x, f, None)
+        b = _blocks
+        self._describe(b, x, f, None)
         y = torch.empty_like(x, memory_format=torch.contiguous_format) if out is None else _like(out, x, "out")
-        self._view(2, y)
+        _fill(b.views[2], y)
         # each row is a sequence of one token: what was the token stride leads from row to row
-        s, side = self._shape, tuple(x.shape)
+        s, side = b.shape, tuple(x.shape)
         s.batch, s.tokens = s.tokens, 1
-        for v in self._views[:3]:
+        for v in b.views[:3]:
             v.batch_stride = v.token_stride
         p0 = _side(state, torch.float32, side, x, "state")
         last = torch.empty(side, dtype=torch.float32, device=x.device) if out_state is None else out_state
         p1 = last.data_ptr() if out_state is None else _side(last, torch.float32, side, x, "out_state")
-        r = self._refs
+        r = b.refs
         _check(_lib.zg_gated_scan(self.handle, r[0], r[1], r[2], p0, r[3], p1, None, _stream_of(stream, x)),
                "zg_gated_scan")
         return y, last
