@@ -483,7 +483,7 @@ typedef struct {
     const int32_t *t_index;          /* rows x k, contiguous */
     int t_dtype;                     /* of t_logits */
     int k;                           /* 1 <= k <= ZG_TOPK_MAX */
-    float temperature;               /* finite, > 0 */
+    float temperature;               /* finite, above 4.3e-39 */
 } zg_distill_args;
 
 /* The loss of each row and its lse (rows binary32 each; lse may be NULL). */

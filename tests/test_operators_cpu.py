@@ -170,3 +170,14 @@ def test_two_threads_on_one_handle_pass_their_own_arguments(monkeypatch):
     for t in threads:
         t.join()
     assert len(want) == 2 and seen == want
+
+
+def test_temperatures_whose_exponents_overflow_are_refused(lib):
+    """z / T is taken as z * (log2(e) / T): the factor has to be finite."""
+    a = zb._Distill(None, 0, 10, 10, 0, None, None, 0, 3, 1.0)
+    for bad, fine in ((3e-39, 4.5e-39), (4.2e-39, 1e-30)):
+        a.temperature = bad
+        assert lib.zg_distill_loss(ctypes.byref(a), None, None, None) == zb.ZG_ERR_INVALID_ARG, bad
+        assert b"temperature" in lib.zg_last_error()
+        a.temperature = fine
+        assert lib.zg_distill_loss(ctypes.byref(a), None, None, None) == zb.ZG_OK, fine

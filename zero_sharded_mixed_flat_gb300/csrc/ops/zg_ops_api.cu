@@ -159,8 +159,9 @@ int check_distill(const zg_distill_args *d, float scale, zg::DistillArgs &a)
     if (!d) return fail(ZG_ERR_INVALID_ARG, "args is NULL");
     if (int rc = check_rows(d->logits, d->dtype, d->rows, d->vocab, d->row_stride, d->k)) return rc;
     if (int rc = check_dtype(d->t_dtype, "t_dtype")) return rc;
-    if (!(d->temperature > 0.0f) || !isfinite(d->temperature) || !isfinite(1.0f / d->temperature))
-        return fail(ZG_ERR_INVALID_ARG, "temperature must be finite and > 0, and its reciprocal finite (got %g)",
+    // the kernels scale by log2(e) / T
+    if (!(d->temperature > 0.0f) || !isfinite(d->temperature) || !isfinite(1.0f / d->temperature * 1.44269504f))
+        return fail(ZG_ERR_INVALID_ARG, "temperature must be finite and > 0, and log2(e) over it finite (got %g)",
                     double(d->temperature));
     if (!isfinite(scale)) return fail(ZG_ERR_INVALID_ARG, "scale must be finite");
     if (d->rows) {
