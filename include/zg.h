@@ -392,14 +392,15 @@ typedef struct {
  * [seq_start[s], seq_start[s+1]), where seq_start is a device array of
  * n_seq + 1 non-decreasing int64 from 0 up to at most `tokens`; a sequence
  * may be empty. Tokens at or past seq_start[n_seq] belong to no sequence:
- * what they hold does not matter, and nothing of theirs is written. (Values
- * that break this give unspecified results, but no access outside the
- * buffers.) */
+ * what they hold does not matter, and nothing of theirs is written, or, with
+ * clear_rest not 0, zeros to y, dx and df. (Starts that break this give
+ * unspecified results, but no access outside the buffers.) */
 typedef struct {
     int64_t batch, tokens, channels;
     const int64_t *seq_start;
     int64_t n_seq;
     int dtype;
+    int clear_rest; /* of packed sequences alone */
 } zg_scan_shape;
 
 /* Tokens per saved state: forward saves, and backward starts from, the state

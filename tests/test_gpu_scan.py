@@ -482,3 +482,33 @@ def test_a_wait_that_ran_out_does_not_concern_the_next_scan():
         assert all(torch.equal(p, q) for p, q in zip(got, want))
         assert scan.status() == zb.ZG_ERR_DEVICE_TIMEOUT
         assert scan.status() == zb.ZG_OK
+
+
+def remember_nan(shape, dtype, n=8):
+    """Leaves NaNs in the memory that the next allocations of this size are given."""
+    kept = [torch.full(shape, math.nan, dtype=dtype, device="cuda") for _ in range(n)]
+    torch.cuda.synchronize()
+    del kept
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t,end,c", [(5, 4, 67), (300, 290, 64), (300, 0, 68), (1100, 130, 71), (700, 513, 8256), (260, 257, 8257)])
+def test_outputs_past_the_last_sequence_are_zero(t, end, c, dtype):
+    """What forward and backward allocate is whole: a weight's gradient multiplies all its rows."""
+    dt = DT[dtype]
+    x, f = (v[0] for v in views(1, t, c, dt, "plain", 97))
+    dy = rand((t, c), 98).to(dt).cuda()
+    x[end:], f[end:], dy[end:] = math.nan, math.nan, math.nan
+    starts = torch.tensor([0, end // 2, end], dtype=torch.int64).cuda()
+    scan = zb.GatedScan(1, t, c)
+    remember_nan((t, c), dt)
+    y, _, kept = scan.forward(x, f, None, starts, keep=True)
+    dx, df, _ = scan.backward(x, f, dy, kept, None, None, starts)
+    for got in (y, dx, df):
+        assert bool((got[end:] == 0).all()) and bool(torch.isfinite(got).all())
+    # and the rest has the bits that it has in the caller's own memory, whose tail stays
+    mine = [torch.full((t, c), 7.0, dtype=dt, device="cuda") for _ in range(3)]
+    scan.forward(x, f, None, starts, out=mine[0])
+    scan.backward(x, f, dy, kept, None, None, starts, out=(mine[1], mine[2]))
+    for got, want in zip(mine, (y, dx, df)):
+        assert torch.equal(got[:end], want[:end]) and bool((got[end:] == 7.0).all())

@@ -73,7 +73,7 @@ class _View(ctypes.Structure):
 
 class _ScanShape(ctypes.Structure):
     _fields_ = [("batch", _I64), ("tokens", _I64), ("channels", _I64), ("seq_start", _P), ("n_seq", _I64),
-                ("dtype", ctypes.c_int)]
+                ("dtype", ctypes.c_int), ("clear_rest", ctypes.c_int)]
 
 
 class _Distill(ctypes.Structure):
@@ -554,13 +554,13 @@ class GatedScan:
             self.handle = None
 
     @staticmethod
-    def _describe(blocks, x, f, seq_start) -> int:
+    def _describe(blocks, x, f, seq_start, clear_rest) -> int:
         """Fill the shape and the views of x and f; returns the number of sequences."""
         dtype = _dtype(x, "x")
         _like(x, x, "x")
         _like(f, x, "f")
         s, views, dims = blocks.shape, blocks.views, x.dim()
-        s.dtype = dtype
+        s.dtype, s.clear_rest = dtype, clear_rest
         if dims == 3:
             s.batch, s.tokens, s.channels = x.shape
         elif dims == 2:
@@ -582,9 +582,10 @@ class GatedScan:
     def forward(self, x, f, h0=None, seq_start=None, keep: bool = False, out=None, h_last=None, stream=None):
         """y, the state after each sequence, and with ``keep`` the states that
         ``backward`` starts from (else None). ``out`` and ``h_last`` are
-        allocated when None; h_last may be h0 itself."""
+        allocated when None; h_last may be h0 itself. Rows of y past the last
+        packed sequence are zero, or in an ``out`` of yours left as they are."""
         b = _blocks
-        n = self._describe(b, x, f, seq_start)
+        n = self._describe(b, x, f, seq_start, out is None)
         s, side = b.shape, (n, b.shape.channels)
         y = torch.empty_like(x, memory_format=torch.contiguous_format) if out is None else _like(out, x, "out")
         _fill(b.views[2], y)
@@ -602,9 +603,11 @@ class GatedScan:
     def backward(self, x, f, dy, kept, h0=None, dh_last=None, seq_start=None, out=None, stream=None):
         """The gradients (dx, df, dh0) from dy and dh_last (None: zero), for the
         x, f and h0 of the forward call that gave ``kept``. ``out``: (dx, df)
-        to write into, for instance the parts of one projection's gradient."""
+        to write into, for instance the parts of one projection's gradient.
+        Rows of dx and df past the last packed sequence are zero, or in an
+        ``out`` of yours left as they are."""
         b = _blocks
-        n = self._describe(b, x, f, seq_start)
+        n = self._describe(b, x, f, seq_start, out is None)
         s, side = b.shape, (n, b.shape.channels)
         _fill(b.views[2], _like(dy, x, "dy"))
         if kept is None:
@@ -629,7 +632,7 @@ class GatedScan:
         if not isinstance(x, torch.Tensor) or x.dim() != 2:
             raise ValueError("x must be (batch, channels)")
         b = _blocks
-        self._describe(b, x, f, None)
+        self._describe(b, x, f, None, False)
         y = torch.empty_like(x, memory_format=torch.contiguous_format) if out is None else _like(out, x, "out")
         _fill(b.views[2], y)
         # each row is a sequence of one token: what was the token stride leads from row to row

@@ -19,6 +19,7 @@ struct ScanArgs {
     const int64_t *seq_start;  // device, or null
     int64_t n_seq;             // sequences: batch when seq_start is null
     int dtype;
+    bool clear_rest;           // zeros to the outputs of tokens past the last packed sequence
     ScanView x, f, y;          // y: forward's output; dy in backward
     const float *h0;           // or null
     float *h_last;             // or null

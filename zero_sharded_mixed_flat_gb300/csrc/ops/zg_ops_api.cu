@@ -135,6 +135,7 @@ zg::ScanArgs scan_args(const zg_scan_shape *s)
     a.seq_start = s->seq_start;
     a.n_seq = s->seq_start ? s->n_seq : s->batch;
     a.dtype = s->dtype;
+    a.clear_rest = s->clear_rest != 0;
     return a;
 }
 

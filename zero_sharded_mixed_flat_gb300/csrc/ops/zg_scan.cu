@@ -615,6 +615,16 @@ __device__ __forceinline__ void put_state4(float *row, int l, int n, F4 v)
     if (channel_of<VEC>(l, 3) < n) row[channel_of<VEC>(l, 3)] = v.hi.y;
 }
 
+// Zeros to a run's tokens of an output past `end`, where no sequence lies.
+template <class T, bool VEC>
+__device__ __forceinline__ void clear_rest(const ScanView &v, const Tile &t, int64_t t0, int64_t end, const ScanArgs &a, int l, int n)
+{
+    T *const p = static_cast<T *>(v.ptr) + t.row * v.sb + t.ch;
+    const int64_t stop = t0 + kRun < a.tokens ? t0 + kRun : a.tokens;
+#pragma unroll 1
+    for (int64_t i = t0 > end ? t0 : end; i < stop; ++i) store4<VEC>(p + i * v.st, l, n, all(0.0f));
+}
+
 // ------------------------------------------------------------------ packed sequences
 
 // First index in the non-decreasing v[0, n) whose value is at least `key` (n
@@ -888,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
     int64_t end = a.tokens;
     if (PACKED) {
         end = a.seq_start[a.n_seq];
-        end = end < a.tokens ? end : a.tokens;
+        end = end < 0 ? 0 : end < a.tokens ? end : a.tokens;
     }
     __syncthreads();
     while (t.valid) {
@@ -976,6 +986,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
                     put_state4<VEC>(a.h_last + (PACKED ? int64_t(sh.cuts.last[run * kRun + i]) : int64_t(t.row)) * a.channels + t.ch,
                                     l, n, h);
             }
+            if (PACKED && a.clear_rest) clear_rest<T, VEC>(a.y, t, t0, end, a, l, n);
         }
         if (EARLY) {
             ahead.done(u, g);
@@ -1019,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
     int64_t end = a.tokens;
     if (PACKED) {
         end = a.seq_start[a.n_seq];
-        end = end < a.tokens ? end : a.tokens;
+        end = end < 0 ? 0 : end < a.tokens ? end : a.tokens;
     }
     __syncthreads();
     while (t.valid) {
@@ -1176,6 +1187,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
                 }
                 px -= a.dx.st;
                 pf -= a.df.st;
+            }
+            if (PACKED && a.clear_rest) {
+                clear_rest<T, VEC>(a.dx, t, t0, end, a, l, n);
+                clear_rest<T, VEC>(a.df, t, t0, end, a, l, n);
             }
         }
         if (!PACKED && a.dh0 && t0 == 0) put_state4<VEC>(a.dh0 + t.row * a.channels + t.ch, l, n, gr);
