@@ -512,3 +512,34 @@ def test_outputs_past_the_last_sequence_are_zero(t, end, c, dtype):
     scan.backward(x, f, dy, kept, None, None, starts, out=(mine[1], mine[2]))
     for got, want in zip(mine, (y, dx, df)):
         assert torch.equal(got[:end], want[:end]) and bool((got[end:] == 7.0).all())
+
+
+def test_outputs_belong_to_the_given_stream():
+    """What a call allocates is of the stream that it is given, as under torch.cuda.stream: memory
+    given back goes to that stream's calls, not to the current one's while the other still writes."""
+    b, t, c = 2, 300, 64
+    x, f = views(b, t, c, torch.bfloat16, "plain", 99)
+    scan = zb.GatedScan(b, t, c)
+    y, last, kept = scan.forward(x, f, keep=True)
+    want = [y, last, kept, *scan.backward(x, f, x, kept), *scan.step(x[:, 0], f[:, 0], last)]
+    z = rand((40, 1003), 100).to(torch.bfloat16).cuda()
+    values, index = zb.topk_logits(z, 20)
+    loss, lse = zb.distill_loss(z, values, index, 1.0)
+    want += [values, index, loss, lse, zb.distill_grad(z, lse, values, index, 1.0), *zb.distill_loss_grad(z, values, index, 1.0)]
+    torch.cuda.synchronize()
+    for side in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        got = [*scan.forward(x, f, keep=True, stream=side), *scan.backward(x, f, x, kept, stream=side),
+               *scan.step(x[:, 0], f[:, 0], last, stream=side), *zb.topk_logits(z, 20, stream=side),
+               *zb.distill_loss(z, values, index, 1.0, stream=side),
+               zb.distill_grad(z, lse, values, index, 1.0, stream=side),
+               *zb.distill_loss_grad(z, values, index, 1.0, stream=side)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want)) and len(got) == len(want)
+        sizes = [(v.numel() * v.element_size(), v.data_ptr()) for v in got]
+        del got
+        for size, ptr in sizes:  # none of it is handed out for the current stream
+            assert torch.empty(size, dtype=torch.uint8, device="cuda").data_ptr() != ptr
+    # and the default stream by its address
+    got = scan.forward(x, f, stream=0)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(got, y)

@@ -459,6 +459,10 @@ class ShardedAdamW:
 
 
 # ----------------------------------------------------------------- training operators
+#
+# Each runs on ``stream``, or on the current one, and allocates its outputs there, as under
+# ``torch.cuda.stream``: inputs, and outputs used elsewhere, are the caller's to order and to
+# keep. None is recorded by autograd: of tensors that require gradients the values are taken.
 
 _DTYPES = {torch.bfloat16: ZG_DTYPE_BF16, torch.float32: ZG_DTYPE_F32}
 
@@ -502,9 +506,21 @@ def _side(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, ref: torch.T
     return _dev_ptr(t, dtype, 0, what)
 
 
-def _stream_of(stream, ref: torch.Tensor) -> int:
-    """The given stream's address, or that of ref's device's current stream."""
-    return torch._C._cuda_getCurrentRawStream(ref.get_device()) if stream is None else _stream(stream)
+def _stream_of(ref: torch.Tensor) -> int:
+    """The address of ref's device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(ref.get_device())
+
+
+def _on(stream, ref, call, *args):
+    """``call(*args)`` with ``stream`` (a stream or its address) as the current one, so that
+    what it allocates is that stream's too: memory of the current stream's could be given
+    out again there while the other still writes."""
+    if not isinstance(stream, torch.cuda.Stream):
+        device = ref.device if isinstance(ref, torch.Tensor) and ref.is_cuda else None
+        address = _stream(stream)
+        stream = torch.cuda.ExternalStream(address, device) if address > 1 else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return call(*args)
 
 
 class _Blocks(threading.local):
@@ -584,6 +600,8 @@ class GatedScan:
         ``backward`` starts from (else None). ``out`` and ``h_last`` are
         allocated when None; h_last may be h0 itself. Rows of y past the last
         packed sequence are zero, or in an ``out`` of yours left as they are."""
+        if stream is not None:
+            return _on(stream, x, self.forward, x, f, h0, seq_start, keep, out, h_last)
         b = _blocks
         n = self._describe(b, x, f, seq_start, out is None)
         s, side = b.shape, (n, b.shape.channels)
@@ -597,7 +615,7 @@ class GatedScan:
             kept = torch.empty((s.batch, -(-s.tokens // ZG_SCAN_CHUNK), s.channels), dtype=torch.float32, device=x.device)
         r = b.refs
         _check(_lib.zg_gated_scan(self.handle, r[0], r[1], r[2], p0, r[3], p1, kept.data_ptr() if keep else None,
-                                  _stream_of(stream, x)), "zg_gated_scan")
+                                  _stream_of(x)), "zg_gated_scan")
         return y, last, kept
 
     def backward(self, x, f, dy, kept, h0=None, dh_last=None, seq_start=None, out=None, stream=None):
@@ -606,6 +624,8 @@ class GatedScan:
         to write into, for instance the parts of one projection's gradient.
         Rows of dx and df past the last packed sequence are zero, or in an
         ``out`` of yours left as they are."""
+        if stream is not None:
+            return _on(stream, x, self.backward, x, f, dy, kept, h0, dh_last, seq_start, out)
         b = _blocks
         n = self._describe(b, x, f, seq_start, out is None)
         s, side = b.shape, (n, b.shape.channels)
@@ -623,12 +643,14 @@ class GatedScan:
         r = b.refs
         _check(_lib.zg_gated_scan_bwd(self.handle, r[0], r[1], r[2], r[3], pk, _side(h0, torch.float32, side, x, "h0"),
                                       _side(dh_last, torch.float32, side, x, "dh_last"), r[4], r[5], dh0.data_ptr(),
-                                      _stream_of(stream, x)), "zg_gated_scan_bwd")
+                                      _stream_of(x)), "zg_gated_scan_bwd")
         return dx, df, dh0
 
     def step(self, x, f, state, out_state=None, out=None, stream=None):
         """One token for each of x's rows (batch, channels): y and the new
         state, written to ``out_state`` (``state`` itself to update it in place)."""
+        if stream is not None:
+            return _on(stream, x, self.step, x, f, state, out_state, out)
         if not isinstance(x, torch.Tensor) or x.dim() != 2:
             raise ValueError("x must be (batch, channels)")
         b = _blocks
@@ -644,7 +666,7 @@ class GatedScan:
         last = torch.empty(side, dtype=torch.float32, device=x.device) if out_state is None else out_state
         p1 = last.data_ptr() if out_state is None else _side(last, torch.float32, side, x, "out_state")
         r = b.refs
-        _check(_lib.zg_gated_scan(self.handle, r[0], r[1], r[2], p0, r[3], p1, None, _stream_of(stream, x)),
+        _check(_lib.zg_gated_scan(self.handle, r[0], r[1], r[2], p0, r[3], p1, None, _stream_of(x)),
                "zg_gated_scan")
         return y, last
 
@@ -675,12 +697,14 @@ def _row_stride(t: torch.Tensor) -> int:
 def topk_logits(logits, k: int, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """The k largest of each row of ``logits`` (rows, vocab), largest first,
     ties to the lowest index: values (rows, k) and int32 indices."""
+    if stream is not None:
+        return _on(stream, logits, topk_logits, logits, k)
     _rows(logits, "logits")
     n, v = logits.shape
     values = torch.empty((n, k), dtype=logits.dtype, device=logits.device)
     index = torch.empty((n, k), dtype=torch.int32, device=logits.device)
     _check(lib().zg_topk(logits.data_ptr(), _DTYPES[logits.dtype], n, v, _row_stride(logits), k, values.data_ptr(),
-                         index.data_ptr(), _stream_of(stream, logits)), "zg_topk")
+                         index.data_ptr(), _stream_of(logits)), "zg_topk")
     return values, index
 
 
@@ -700,10 +724,12 @@ def distill_loss(logits, t_logits, t_index, temperature: float, stream=None) -> 
     """The distillation loss of each row of student ``logits`` (rows, vocab)
     against the teacher's entries ``t_logits`` and ``t_index`` (rows, k; index
     -1 for none), and each row's log-sum-exp of logits / temperature."""
+    if stream is not None:
+        return _on(stream, logits, distill_loss, logits, t_logits, t_index, temperature)
     a = _distill(logits, t_logits, t_index, temperature)
     loss = torch.empty(a.rows, dtype=torch.float32, device=logits.device)
     lse = torch.empty(a.rows, dtype=torch.float32, device=logits.device)
-    _check(lib().zg_distill_loss(ctypes.byref(a), loss.data_ptr(), lse.data_ptr(), _stream_of(stream, logits)),
+    _check(lib().zg_distill_loss(ctypes.byref(a), loss.data_ptr(), lse.data_ptr(), _stream_of(logits)),
            "zg_distill_loss")
     return loss, lse
 
@@ -716,11 +742,13 @@ def distill_grad(logits, lse, t_logits, t_index, temperature: float, scale: floa
                  stream=None) -> torch.Tensor:
     """The gradient of sum(scale * dloss * loss) by the logits, from the lse of
     ``distill_loss`` (dloss None: ones). ``out`` may be the logits themselves."""
+    if stream is not None:
+        return _on(stream, logits, distill_grad, logits, lse, t_logits, t_index, temperature, scale, dloss, out)
     a = _distill(logits, t_logits, t_index, temperature)
     out = _gradient_of(logits, out)
     _check(lib().zg_distill_grad(ctypes.byref(a), _side(lse, torch.float32, (a.rows,), logits, "lse"), scale,
                                  _side(dloss, torch.float32, (a.rows,), logits, "dloss"), out.data_ptr(),
-                                 _row_stride(out), _stream_of(stream, logits)), "zg_distill_grad")
+                                 _row_stride(out), _stream_of(logits)), "zg_distill_grad")
     return out
 
 
@@ -728,10 +756,12 @@ def distill_loss_grad(logits, t_logits, t_index, temperature: float, scale: floa
                       stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """The loss of each row and the gradient of sum(scale * dloss * loss) by the
     logits, in one pass over them. ``out`` may be the logits themselves."""
+    if stream is not None:
+        return _on(stream, logits, distill_loss_grad, logits, t_logits, t_index, temperature, scale, dloss, out)
     a = _distill(logits, t_logits, t_index, temperature)
     out = _gradient_of(logits, out)
     loss = torch.empty(a.rows, dtype=torch.float32, device=logits.device)
     _check(lib().zg_distill_loss_grad(ctypes.byref(a), scale, _side(dloss, torch.float32, (a.rows,), logits, "dloss"),
                                       loss.data_ptr(), None, out.data_ptr(), _row_stride(out),
-                                      _stream_of(stream, logits)), "zg_distill_loss_grad")
+                                      _stream_of(logits)), "zg_distill_loss_grad")
     return loss, out
