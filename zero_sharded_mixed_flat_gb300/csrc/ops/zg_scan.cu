@@ -825,11 +825,11 @@ constexpr int kBuffers = BWD && sizeof(T) == 2 ? 2 : 1;
 template <class T, int ROWS, bool BWD>
 constexpr size_t kTileBytes = (BWD ? 2 * kBuffers<T, BWD> + 1 : 2) * kBuffer<T, ROWS> * sizeof(T);
 
-// A block's places. Where rows and tiles of channels alone fill the GPU
-// (EARLY) the next place is taken when a tile is begun, so that its copies can
-// start at once; a block's second place then waits for its first tile's copies,
-// when all blocks have begun and taken their first. Where blocks work side by
-// side on few rows, a place that is taken but not begun holds up every block
+// A block's places. Where rows and tiles of channels alone fill the GPU (EARLY; not
+// with packed sequences) the next place is taken when a tile is begun, so that its
+// copies can start at once; a block's second place then waits for its first tile's
+// copies, when all blocks have begun and taken their first. Where blocks work side
+// by side on few rows, a place that is taken but not begun holds up every block
 // after it, so the next one is taken only when a tile waits for nothing more.
 template <bool BWD, bool EARLY>
 struct Ahead {
@@ -879,6 +879,7 @@ template <class T, int ROWS, bool PACKED, bool EARLY>
 __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, Grid g)
 {
     extern __shared__ __align__(128) unsigned char raw[];
+    static_assert(!(PACKED && EARLY), "the cuts are found between two tiles");
     constexpr bool VEC = ROWS != ANY;
     constexpr int kSize = kBuffer<T, ROWS>;
     T *const bf = reinterpret_cast<T *>(raw), *const bx = bf + kSize;
@@ -905,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
         const int n = int(a.channels - t.ch < kTile ? a.channels - t.ch : kTile);
         const int64_t t0 = int64_t(t.chunk) * kChunk + run * kRun;
         const float start = PACKED ? 0.0f : state1<VEC>(a.h0, t.row, a, t);
-        if (PACKED && !EARLY) find_cuts(sh.cuts, a, t, n, a.h0, a.h_last);  // while the copies are under way
+        if (PACKED) find_cuts(sh.cuts, a, t, n, a.h0, a.h_last);  // while the copies are under way
         wait_copies();
         ahead.open(g);
         __syncthreads();
@@ -921,10 +922,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(ScanArgs a, Work w, G
         Before before;
         if (EARLY) before.ask(w, t, g);
         Marks mk{0u, 0u};
-        if (PACKED) {
-            if (EARLY) find_cuts(sh.cuts, a, t, n, a.h0, a.h_last);
-            mk = marks_of(sh.cuts);
-        }
+        if (PACKED) mk = marks_of(sh.cuts);
         auto initial = [&](int i) {
             return state4<VEC>(a.h0 ? a.h0 + sh.cuts.first[run * kRun + i] * a.channels + t.ch : nullptr, l, n);
         };
@@ -1008,6 +1006,7 @@ template <class T, int ROWS, bool PACKED, bool EARLY>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work w, Grid g)
 {
     extern __shared__ __align__(128) unsigned char raw[];
+    static_assert(!(PACKED && EARLY), "the cuts are found between two tiles");
     constexpr bool VEC = ROWS != ANY;
     constexpr int kSize = kBuffer<T, ROWS>;
     constexpr bool kTwo = kBuffers<T, true> == 2;
@@ -1040,7 +1039,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
         const float h_start = t.chunk > 0 ? state1<VEC>(a.states, t.row * g.chunks + t.chunk, a, t)
                               : PACKED    ? 0.0f
                                           : state1<VEC>(a.h0, t.row, a, t);
-        if (PACKED && !EARLY) find_cuts(sh.cuts, a, t, n, a.dh_last, a.dh0);  // while the copies are under way
+        if (PACKED) find_cuts(sh.cuts, a, t, n, a.dh_last, a.dh0);  // while the copies are under way
         wait_copies();
         ahead.open(g);
         __syncthreads();
@@ -1063,10 +1062,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, Work 
             }
         }
         Marks mk{0u, 0u};
-        if (PACKED) {
-            if (EARLY) find_cuts(sh.cuts, a, t, n, a.dh_last, a.dh0);
-            mk = marks_of(sh.cuts);
-        }
+        if (PACKED) mk = marks_of(sh.cuts);
         auto side = [&](const float *p, const int *table, int i) {
             return state4<VEC>(p ? p + table[run * kRun + i] * a.channels + t.ch : nullptr, l, n);
         };
@@ -1338,16 +1334,26 @@ cudaError_t choose(const ScanArgs &a, const ScanWork &sw, cudaStream_t st)
     // against 34; 12 x 512 105 against 92, 153 against 122. In long rows forward
     // gains from fewer tiles on: 64 x 512 367 against 400, 568 against 574;
     // 32 x 512 208 against 222, 312 against 305; 24 x 512 168 against 172, 245
-    // against 232.
-    const bool early = g.width >= 128 || (!BWD && g.width >= 32 && g.chunks >= 256);
-    if constexpr (BWD) {
-        if constexpr (kBuffers<T, true> == 2)
+    // against 232. Forward in binary32: 192 x 32 97 against 99; 768 x 3 38.5 against
+    // 40.8; 96 x 16 32.6 against 30.5; 48 x 32 35.4 against 35.0; 12 x 512 143 against
+    // 124; 64 x 256 266 against 287; 32 x 256 151 against 158. Packed sequences never
+    // gain, since finding the cuts then has no copies to hide behind: in bf16, 192 x 32
+    // 99.7 against 93.4, backward 189 against 166; 64 x 256 267 against 246, 552
+    // against 418; 32 x 512 285 against 254, 575 against 416; 12 x 512 141 against 106,
+    // 244 against 178; binary32, 192 x 64 forward 244 against 235; 32 x 512 364 against
+    // 327.
+    if constexpr (!PACKED && (!BWD || kBuffers<T, true> == 2)) {
+        const bool early = g.width >= 128 || (!BWD && g.width >= 32 && g.chunks >= 256);
+        if constexpr (BWD) {
             if (early) return launch<T, ROWS, BWD, &scan_bwd_kernel<T, ROWS, PACKED, true>>(a, sw, g, st);
-        return launch<T, ROWS, BWD, &scan_bwd_kernel<T, ROWS, PACKED, false>>(a, sw, g, st);
-    } else {
-        if (early) return launch<T, ROWS, BWD, &scan_kernel<T, ROWS, PACKED, true>>(a, sw, g, st);
-        return launch<T, ROWS, BWD, &scan_kernel<T, ROWS, PACKED, false>>(a, sw, g, st);
+        } else {
+            if (early) return launch<T, ROWS, BWD, &scan_kernel<T, ROWS, PACKED, true>>(a, sw, g, st);
+        }
     }
+    if constexpr (BWD)
+        return launch<T, ROWS, BWD, &scan_bwd_kernel<T, ROWS, PACKED, false>>(a, sw, g, st);
+    else
+        return launch<T, ROWS, BWD, &scan_kernel<T, ROWS, PACKED, false>>(a, sw, g, st);
 }
 
 template <class T, bool BWD>
