@@ -412,3 +412,18 @@ def test_distill_rows_far_from_zero(v, temperature):
     d = torch.ones(6, device="cuda")
     want = ref.distill(torch.zeros(6, v, dtype=torch.float64), t.double().cpu(), index.cpu(), temperature)
     ref.check(zb.distill_loss_grad(z, t, index, temperature, 1.0, d)[1], want[2], ref.stored(want[2], want[5], torch.bfloat16))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,v", [(3, 90), (3, 50257), (200, 20011)])
+def test_distill_gradient_of_rows_far_from_zero_in_place(n, v, dtype):
+    """Where lse does not do, the row is read twice, and its own memory is written over after that."""
+    dt = DT[dtype]
+    t, index = teacher(n, v, 20, dt, 37)
+    z = logits_of(n, v, dt, 38)
+    z[::2] = -1e10
+    loss, lse = zb.distill_loss(z, t, index, 1.0)
+    want = zb.distill_grad(z, lse, t, index, 1.0)
+    mine = z.clone()
+    assert zb.distill_grad(mine, lse, t, index, 1.0, out=mine) is mine
+    assert torch.equal(mine, want) and bool(torch.isfinite(want).all())
