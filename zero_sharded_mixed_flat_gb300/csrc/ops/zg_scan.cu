@@ -28,14 +28,19 @@
 // NaN), so nothing before it, a NaN included, is multiplied into what follows.
 // (The mark is asked for as A < 0, which a NaN is not.)
 //
-// Measured: 8 x 4096 x 1536 in bf16 forward 65 us (4.6 TB/s of x, f and y),
-// backward 103 (4.9 TB/s of five), where the SMs' issue of some 25 instructions
-// an element takes as long as the bytes do; rows at odd channels (1535 of them) 97
-// and 160, most of it in stores of two bytes; 1 x 65536 x 768 92 and 122 (twelve
-// tiles to a chunk, so a block waits for records that blocks beside it are only
-// writing); 8 x 1024 x 768 13 and 20, two tiles to a block; binary32, 1 x 20000 x
-// 768, 45 and 62, packed 9001 x 771 33 and 52. Three blocks to an SM instead of
-// two spill and are slower.
+// Measured: 8 x 4096 x 1536 in bf16 forward 66 us (4.6 TB/s of x, f and y),
+// backward 104 (4.9 TB/s of five). Neither the bytes (44.5 and 74 us) nor the issue
+// of 25 and 45 instructions an element (31 and 55 us) is the limit: with two blocks
+// of eight warps to an SM, which is what 128 registers allow, issue is active in 50
+// and 56 % of the cycles and DRAM in 41 and 48 %, and warps wait at barriers most of
+// all (profile of 8 x 2048 x 1536). Three blocks to an SM, tried with what is kept in
+// registers now, spill and are slower. Rows at odd channels (1535 of them) 97 and
+// 160, with stores of two bytes; 1 x 65536 x 768 90 and 123 (twelve tiles to a chunk,
+// so a block waits for records that blocks beside it are only writing); 8 x 1024 x
+// 768 13.5 and 19.6, two tiles to a block; binary32, 1 x 20000 x 768 45 and 62, 8 x
+// 4096 x 1536 98 and 159. Packed: 9001 x 771 in binary32 31 and 48, in bf16 24 and 40
+// (three full waves of blocks and a part of a fourth, and a last tile of 3 channels);
+// bf16 65536 x 768 107 and 180, 32768 x 4096 247 and 420.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -102,10 +107,11 @@ __device__ __forceinline__ float rcp_approx(float v)
 // e = exp(-f): neither is a difference, so both hold to a few units in the
 // last place however near to one the other is. f is held above kLowest, where
 // e and its sum are still finite, and keep is taken down by just less than its
-// value there (far below any other keep's last place), so that it ends at zero,
-// never below; a NaN stays. For binary32 data the exponent's argument is reduced first, which
-// keeps its rounding out of e; for bf16 data that rounding (|f| 2^-24 of e)
-// is far below the data's own.
+// value there, so that it ends at zero, never below; a NaN stays. That is an error
+// below 3e-38, which shows in keep itself where f is below about -70 (its last
+// place there, 1.5e-3 of it at -80). For binary32 data the exponent's argument is reduced first
+// (as Cody and Waite do it: n log 2 taken off in two parts), which keeps its rounding
+// out of e; for bf16 data that rounding (|f| 2^-24 of e) is far below the data's own.
 constexpr float kLowest = -86.5f;
 constexpr float kKeepAtLowest = 2.71337577e-38f;  // exp(kLowest), less 4e-5 of itself for the roundings on the way
 constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f;

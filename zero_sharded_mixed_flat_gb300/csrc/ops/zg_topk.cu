@@ -14,7 +14,10 @@
 // Measured at 4096 x 50257 in bf16: k = 64 84 us (4.9 TB/s), k = 256 146. What
 // is above the 61 us of the bytes is each row's end (bound, shares read again,
 // order), during which its block asks for nothing; other blocks of the SM fill
-// in for it. In binary32 186 us (4.4 TB/s); 7 rows, k = 100, 8 us, all latency.
+// in for it. At k = 256 the bound is the median share's maximum, and half of the row
+// is looked at again. In binary32 186 us (4.4 TB/s) for 121: the rows in flight, 183
+// MB, do not fit L2, and a third of the logits comes from DRAM again. 7 rows, k = 100,
+// 8 us, all latency.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
