@@ -506,6 +506,145 @@ int zg_distill_grad(const zg_distill_args *args, const float *lse, float scale, 
 int zg_distill_loss_grad(const zg_distill_args *args, float scale, const float *dloss, float *loss, float *lse,
                          void *dlogits, int64_t drow_stride, zg_stream stream);
 
+/* Token embedding. out row i = scale * table row tokens[i], rounded once; a token
+ * outside [0, vocab) is absent (padding) and gives a row of zeros. table and out
+ * have one dtype (ZG_DTYPE_*) and rows of `width` elements whose starts lie
+ * table_stride and out_stride elements apart (at least width). tokens: n values of
+ * token_bytes 4 (int32) or 8 (int64), contiguous. out must not overlap the table.
+ * Any row alignment works; pointers and strides that are multiples of 16 bytes are
+ * read fastest. width <= ZG_EMBED_MAX_WIDTH, vocab and n below 2^31. */
+#define ZG_EMBED_MAX_WIDTH (1 << 20)
+int zg_embed(const void *table, int dtype, int64_t vocab, int64_t width, int64_t table_stride, const void *tokens,
+             int token_bytes, int64_t n, float scale, void *out, int64_t out_stride, zg_stream stream);
+
+/* The embedding's gradient: dtable row v = add row v + scale * sum over the tokens
+ * i = v of drows row i, summed in binary32 in an order that the tokens alone
+ * decide (the same bits for the same inputs), rounded once. add NULL: zeros. Every
+ * row of dtable is written; where add is dtable itself (same pointer and stride, a
+ * tied table's gradient taken further) only rows with a token are read and
+ * written. drows has `dtype`, add and dtable table_dtype. Absent tokens take no part.
+ * work: at least zg_embed_grad_workspace(n, vocab, width) bytes, 16-byte
+ * aligned, the call's alone until it is done; -1 says that the sizes are out of
+ * range. dtable overlaps neither drows nor (in part) add. */
+int64_t zg_embed_grad_workspace(int64_t n, int64_t vocab, int64_t width);
+int zg_embed_grad(const void *drows, int dtype, int64_t drow_stride, const void *tokens, int token_bytes, int64_t n,
+                  int64_t vocab, int64_t width, float scale, const void *add, int64_t add_stride, void *dtable,
+                  int table_dtype, int64_t dtable_stride, void *work, int64_t work_bytes, zg_stream stream);
+
+/* The norms around a block, with its gate and the residual's scale. For each of
+ * `rows` rows of `width` elements, x the residual stream and o the block's output:
+ *   b     = w_post * o * s_o,  s_o = 1 / sqrt(mean(o^2) + eps)   (w_post NULL: b = o)
+ *   x_new = res_scale * x + gate * b                             (gate NULL: ones)
+ *   n     = w_pre * x_new * s_x,  s_x = 1 / sqrt(mean(x_new^2) + eps)
+ * n is of x_new before its rounding. All tensors have one dtype (ZG_DTYPE_*).
+ * gate is `groups` contiguous rows: row r takes the gate of group r / (rows /
+ * groups), so 1 is a gate of the channels, the number of sequences one for each of
+ * them, and `rows` one for each token. o NULL: there is no block yet (x_new =
+ * res_scale * x; w_post and gate are NULL too). w_pre NULL: there is no norm after. */
+#define ZG_BLOCK_MAX_WIDTH 16384
+typedef struct {
+    int64_t rows, width, groups; /* width <= ZG_BLOCK_MAX_WIDTH; groups >= 1 divides rows */
+    int dtype;
+    const void *x, *o; /* rows start x_stride and o_stride elements apart, at least width */
+    int64_t x_stride, o_stride;
+    const void *w_post, *gate, *w_pre; /* contiguous */
+    float res_scale, eps;              /* finite; eps >= 0 */
+} zg_block;
+
+/* x_new (may be NULL where o is NULL; may be x itself, same pointer and stride),
+ * n (NULL exactly where w_pre is; may be o itself) and, for the gradient, kept:
+ * 2 x rows binary32, s_o of all rows and then s_x (NULL: not kept). */
+int zg_block_norm(const zg_block *block, void *x_new, int64_t x_new_stride, void *n, int64_t n_stride, float *kept,
+                  zg_stream stream);
+
+/* Backward, from the same block (x and o as they were) and its `kept`. dn is the
+ * gradient of n (NULL exactly where w_pre is), dx_new that of x_new (NULL: zero).
+ * Writes dx (may be dx_new itself), d_o (of o; may be dn itself; NULL exactly where
+ * o is) and the gradients of the weights, in the dtype, contiguous, summed over
+ * rows in binary32 in a fixed order: dw_pre, dw_post and dgate (groups x width),
+ * each NULL exactly where its weight is. work: at least
+ * zg_block_norm_workspace(rows, width, groups) bytes (groups 1 without a gate),
+ * 16-byte aligned, the call's alone until it is done. Outputs overlap no input (but as said) nor each other. */
+int64_t zg_block_norm_workspace(int64_t rows, int64_t width, int64_t groups);
+int zg_block_norm_grad(const zg_block *block, const float *kept, const void *dn, int64_t dn_stride,
+                       const void *dx_new, int64_t dx_new_stride, void *dx, int64_t dx_stride, void *d_o,
+                       int64_t d_o_stride, void *dw_pre, void *dw_post, void *dgate, void *work, int64_t work_bytes,
+                       zg_stream stream);
+
+/* The log-probability of each row's token under softmax(logits / temperature), and
+ * (lse not NULL) the row's log sum exp(logits / temperature): rows binary32
+ * each. A row whose token is outside [0, vocab) is a padding row: zeros, whatever
+ * its logits are. Rows of logits as for the distillation above; tokens as for
+ * zg_embed. The log-probabilities of a behaviour or a reference policy. */
+int zg_token_logp(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride, const void *tokens,
+                  int token_bytes, float temperature, float *logp, float *lse, zg_stream stream);
+
+/* The clipped policy loss of sampled tokens with a KL term, and its gradient by
+ * the logits. For each row, with logp as zg_token_logp gives it:
+ *   ratio = exp(logp - old_logp),  A = advantage,  d = ref_logp - logp,
+ *   loss  = -min(ratio A, min(max(ratio, 1 - clip_low), 1 + clip_high) A)
+ *           + kl (exp(d) - 1 - d),
+ *   slope = dloss/dlogp = -(ratio A, or 0 where the ratio is cut off: above
+ *           1 + clip_high with A > 0, or below 1 - clip_low with A < 0) + kl (1 - exp(d)),
+ *   dlogits_v = scale * dloss * slope / temperature * ([v = token] - softmax_v).
+ * ref_logp NULL: no KL term. A row whose token is outside [0, vocab) is a padding
+ * row: its loss, logp and gradient are zero, whatever else it holds. Logits may be
+ * masked by -inf or any large negative number; a row of nothing but -inf gives NaN. */
+typedef struct {
+    const void *logits; /* row r starts at logits + r * row_stride elements; aligned to its element */
+    int64_t rows, vocab, row_stride; /* vocab <= 2^30, row_stride >= vocab */
+    int dtype;                       /* of logits and dlogits */
+    int token_bytes;                 /* 4 or 8 */
+    const void *tokens;              /* rows int32 or int64 */
+    const float *old_logp, *advantage, *ref_logp; /* rows each; ref_logp may be NULL */
+    float clip_low, clip_high;       /* finite, >= 0; clip_low <= 1 */
+    float kl;                        /* finite; without effect where ref_logp is NULL */
+    float temperature;               /* finite, above 4.3e-39 */
+} zg_policy_args;
+
+/* The loss and logp of each row, and (NULL: not kept) what zg_policy_grad takes:
+ * rows x 2 binary32, the row's largest logit and the sum of exp((z - it) / T). */
+int zg_policy_loss(const zg_policy_args *args, float *loss, float *logp, float *kept, zg_stream stream);
+
+/* The gradient, from what zg_policy_loss kept for the same arguments. scale
+ * (finite) is common to all rows: the loss scale over the number of tokens, say.
+ * dloss: one binary32 factor per row, or NULL for ones. dlogits has the logits'
+ * dtype and row_stride drow_stride; it may be the logits themselves (same pointer
+ * and stride), else it must not overlap them. */
+int zg_policy_grad(const zg_policy_args *args, const float *kept, float scale, const float *dloss, void *dlogits,
+                   int64_t drow_stride, zg_stream stream);
+
+/* Both, reading the logits once from memory. The values are those of the two calls
+ * up to roundings. */
+int zg_policy_loss_grad(const zg_policy_args *args, float scale, const float *dloss, float *loss, float *logp,
+                        void *dlogits, int64_t drow_stride, zg_stream stream);
+
+/* The gradients of a model's tensors, clipped by their common norm. A list is made
+ * once for the tensors' addresses; its calls read what is there then. */
+typedef struct {
+    const void *grad; /* n contiguous elements, aligned to the element */
+    void *out;        /* n elements of out_dtype: the gradient itself (then of the same dtype), or memory
+                         that overlaps no gradient and no other output (a part of the flat gradient, say) */
+    int64_t n;        /* >= 0 (pointers of an empty tensor may be NULL); below 2^40 */
+    int dtype, out_dtype;
+} zg_grad;
+typedef struct zg_grads zg_grads; /* opaque: the list on the current device; read alone by the calls below */
+int zg_grads_init(const zg_grad *list, int64_t count, zg_grads **out); /* waits for the device's default stream */
+void zg_grads_destroy(zg_grads *grads); /* after the calls on it are done */
+int64_t zg_grads_workspace(const zg_grads *grads); /* bytes, for either call */
+
+/* norm = sqrt(sum over all elements of (scale * g)^2), squares in binary32 and their
+ * sums in a fixed order; stats[0] = norm, stats[1] = the coefficient
+ * min(1, max_norm / (norm + eps)), or 1 where the norm is not finite. zg_grads_norm
+ * has 1 there always. zg_grads_clip writes out = (scale * coefficient) * g, rounded
+ * once. A norm that is not finite clips nothing, so that an infinite or NaN element
+ * reaches the step that takes the gradients, which then skips. work: 16-byte aligned, the
+ * call's alone until it is done. max_norm > 0 and scale > 0 finite (max_norm may
+ * be infinite), eps >= 0 finite. */
+int zg_grads_norm(const zg_grads *grads, float scale, float *stats, void *work, int64_t work_bytes, zg_stream stream);
+int zg_grads_clip(const zg_grads *grads, float max_norm, float eps, float scale, float *stats, void *work,
+                  int64_t work_bytes, zg_stream stream);
+
 const char *zg_strerror(int code);
 const char *zg_last_error(void); /* this thread's last detailed message */
 int zg_version(void);

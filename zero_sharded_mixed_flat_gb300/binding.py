@@ -12,6 +12,7 @@ fails loudly.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -41,6 +42,8 @@ ZG_DTYPE_BF16 = 0
 ZG_DTYPE_F32 = 1
 ZG_SCAN_CHUNK = 128
 ZG_TOPK_MAX = 256
+ZG_EMBED_MAX_WIDTH = 1 << 20
+ZG_BLOCK_MAX_WIDTH = 16384
 
 
 class ZgError(RuntimeError):
@@ -80,6 +83,23 @@ class _Distill(ctypes.Structure):
     _fields_ = [("logits", _P), ("rows", _I64), ("vocab", _I64), ("row_stride", _I64), ("dtype", ctypes.c_int),
                 ("t_logits", _P), ("t_index", _P), ("t_dtype", ctypes.c_int), ("k", ctypes.c_int),
                 ("temperature", ctypes.c_float)]
+
+
+class _Block(ctypes.Structure):
+    _fields_ = [("rows", _I64), ("width", _I64), ("groups", _I64), ("dtype", ctypes.c_int), ("x", _P), ("o", _P),
+                ("x_stride", _I64), ("o_stride", _I64), ("w_post", _P), ("gate", _P), ("w_pre", _P),
+                ("res_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class _Policy(ctypes.Structure):
+    _fields_ = [("logits", _P), ("rows", _I64), ("vocab", _I64), ("row_stride", _I64), ("dtype", ctypes.c_int),
+                ("token_bytes", ctypes.c_int), ("tokens", _P), ("old_logp", _P), ("advantage", _P), ("ref_logp", _P),
+                ("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float), ("kl", ctypes.c_float),
+                ("temperature", ctypes.c_float)]
+
+
+class _Grad(ctypes.Structure):
+    _fields_ = [("grad", _P), ("out", _P), ("n", _I64), ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int)]
 
 
 @dataclass(frozen=True)
@@ -149,6 +169,24 @@ def lib() -> ctypes.CDLL:
             "zg_distill_loss": (ctypes.c_int, [_P, _P, _P, _P]),
             "zg_distill_grad": (ctypes.c_int, [_P, _P, ctypes.c_float, _P, _P, _I64, _P]),
             "zg_distill_loss_grad": (ctypes.c_int, [_P, ctypes.c_float, _P, _P, _P, _P, _I64, _P]),
+            "zg_embed": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, ctypes.c_int, _I64, ctypes.c_float, _P, _I64,
+                                        _P]),
+            "zg_embed_grad_workspace": (_I64, [_I64, _I64, _I64]),
+            "zg_embed_grad": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P, ctypes.c_int, _I64, _I64, _I64, ctypes.c_float, _P,
+                                             _I64, _P, ctypes.c_int, _I64, _P, _I64, _P]),
+            "zg_block_norm": (ctypes.c_int, [_P, _P, _I64, _P, _I64, _P, _P]),
+            "zg_block_norm_workspace": (_I64, [_I64, _I64, _I64]),
+            "zg_block_norm_grad": (ctypes.c_int, [_P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P]),
+            "zg_token_logp": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, ctypes.c_int, ctypes.c_float, _P, _P,
+                                             _P]),
+            "zg_policy_loss": (ctypes.c_int, [_P, _P, _P, _P, _P]),
+            "zg_policy_grad": (ctypes.c_int, [_P, _P, ctypes.c_float, _P, _P, _I64, _P]),
+            "zg_policy_loss_grad": (ctypes.c_int, [_P, ctypes.c_float, _P, _P, _P, _P, _I64, _P]),
+            "zg_grads_init": (ctypes.c_int, [_P, _I64, ctypes.POINTER(_P)]),
+            "zg_grads_destroy": (None, [_P]),
+            "zg_grads_workspace": (_I64, [_P]),
+            "zg_grads_norm": (ctypes.c_int, [_P, ctypes.c_float, _P, _P, _I64, _P]),
+            "zg_grads_clip": (ctypes.c_int, [_P, ctypes.c_float, ctypes.c_float, ctypes.c_float, _P, _P, _I64, _P]),
             "zg_strerror": (ctypes.c_char_p, [ctypes.c_int]),
             "zg_last_error": (ctypes.c_char_p, []),
             "zg_version": (ctypes.c_int, []),
@@ -488,7 +526,7 @@ def _like(t: torch.Tensor, ref: torch.Tensor, what: str) -> torch.Tensor:
             raise TypeError(f"{what} must have dtype {ref.dtype} (got {t.dtype})")
         if t.shape != ref.shape:
             raise ValueError(f"{what} must have shape {tuple(ref.shape)} (got {tuple(t.shape)})")
-    if t.stride(-1) != 1 and t.shape[-1] != 1:
+    if t.stride(-1) != 1 and t.shape[-1] != 1 and t.numel():
         raise ValueError(f"the last dimension of {what} must be contiguous")
     return t
 
@@ -765,3 +803,335 @@ def distill_loss_grad(logits, t_logits, t_index, temperature: float, scale: floa
                                       loss.data_ptr(), None, out.data_ptr(), _row_stride(out),
                                       _stream_of(logits)), "zg_distill_loss_grad")
     return loss, out
+
+
+# ----------------------------------------------------------------- around a block
+
+_TOKEN_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+def _tokens(t, ref: torch.Tensor, shape=None) -> int:
+    """The size in bytes of a contiguous CUDA tensor of token ids (of ``shape``, if given)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("tokens must be a tensor")
+    if t.dtype not in _TOKEN_BYTES:
+        raise TypeError(f"tokens must be int32 or int64 (got {t.dtype})")
+    if not t.is_cuda:
+        raise TypeError("tokens must be a CUDA tensor")
+    if t.get_device() != ref.get_device():
+        raise ValueError(f"tokens is on {t.device}, not on {ref.device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"tokens must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if not t.is_contiguous():
+        raise ValueError("tokens must be contiguous")
+    return _TOKEN_BYTES[t.dtype]
+
+
+def _stride_of_rows(t: torch.Tensor, what: str) -> int:
+    """The distance of the rows (the last dimension) of a tensor that are evenly spaced."""
+    if t.dim() == 2:
+        return _row_stride(t)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous, or (rows, width)")
+    return t.shape[-1]
+
+
+def _workspace(size: int, ref: torch.Tensor) -> torch.Tensor | None:
+    return torch.empty(size, dtype=torch.uint8, device=ref.device) if size else None
+
+
+def embed(table, tokens, scale: float = 1.0, out=None, stream=None) -> torch.Tensor:
+    """Rows of ``table`` (vocab, width) times ``scale``, for int32 or int64 ``tokens`` of any shape:
+    (*tokens.shape, width). A token outside [0, vocab) gives a row of zeros."""
+    if stream is not None:
+        return _on(stream, table, embed, table, tokens, scale, out)
+    dtype = _dtype(table, "table")
+    if table.dim() != 2:
+        raise ValueError(f"table must be (vocab, width) (got {tuple(table.shape)})")
+    _like(table, table, "table")
+    size = _tokens(tokens, table)
+    vocab, width = table.shape
+    if out is None:
+        out = torch.empty((*tokens.shape, width), dtype=table.dtype, device=table.device)
+        stride = width
+    else:
+        _beside(out, table, (*tokens.shape, width), "out")
+        stride = _stride_of_rows(out, "out")
+    _check(lib().zg_embed(table.data_ptr(), dtype, vocab, width, _row_stride(table), tokens.data_ptr(), size,
+                          tokens.numel(), scale, out.data_ptr(), stride, _stream_of(table)), "zg_embed")
+    return out
+
+
+def _beside(t, ref: torch.Tensor, shape, what: str, dtype=None) -> torch.Tensor:
+    """A CUDA tensor of ref's device, of ``dtype`` (or ref's) and ``shape``, its last dimension contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a tensor")
+    if not t.is_cuda:
+        raise TypeError(f"{what} must be a CUDA tensor")
+    if t.get_device() != ref.get_device():
+        raise ValueError(f"{what} is on {t.device}, not on {ref.device}")
+    if t.dtype != (dtype or ref.dtype):
+        raise TypeError(f"{what} must have dtype {dtype or ref.dtype} (got {t.dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"the last dimension of {what} must be contiguous")
+    return t
+
+
+def embed_grad(drows, tokens, vocab: int, scale: float = 1.0, add=None, out=None, dtype=None, stream=None) -> torch.Tensor:
+    """The gradient by the table (vocab, width) from that of ``embed``'s rows, plus ``add`` (the table's gradient
+    from elsewhere). Allocated in ``dtype`` (add's, else drows' own) when ``out`` is None; ``out`` may be
+    ``add`` itself, of which then only rows with a token are touched. The same bits for the same inputs."""
+    if stream is not None:
+        return _on(stream, drows, embed_grad, drows, tokens, vocab, scale, add, out, dtype)
+    rows_dtype = _dtype(drows, "drows")
+    if drows.dim() < 1:
+        raise ValueError("drows must be (*tokens.shape, width)")
+    width = drows.shape[-1]
+    _like(drows, drows, "drows")
+    size = _tokens(tokens, drows, drows.shape[:-1])
+    if out is None:
+        out = torch.empty((vocab, width), dtype=dtype or (drows if add is None else add).dtype, device=drows.device)
+    _beside(out, drows, (vocab, width), "out", dtype or out.dtype)
+    if add is not None:
+        _beside(add, drows, (vocab, width), "add", out.dtype)
+    L, n = lib(), tokens.numel()
+    work_bytes = L.zg_embed_grad_workspace(n, vocab, width)
+    _check(min(work_bytes, 0), "zg_embed_grad_workspace")
+    work = _workspace(work_bytes, drows)
+    _check(L.zg_embed_grad(drows.data_ptr(), rows_dtype, _stride_of_rows(drows, "drows"), tokens.data_ptr(), size, n,
+                           vocab, width, scale, None if add is None else add.data_ptr(),
+                           0 if add is None else _row_stride(add), out.data_ptr(), _dtype(out, "out"), _row_stride(out),
+                           None if work is None else work.data_ptr(), work_bytes, _stream_of(drows)), "zg_embed_grad")
+    return out
+
+
+def _weight_ptr(w, x: torch.Tensor, shape, what: str) -> int | None:
+    if w is None:
+        return None
+    _beside(w, x, shape, what)
+    if not w.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return w.data_ptr()
+
+
+def _block(x, w_pre, o, w_post, gate, res_scale: float, eps: float) -> _Block:
+    dtype = _dtype(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have rows")
+    _like(x, x, "x")
+    width = x.shape[-1]
+    groups = 1
+    if gate is not None and isinstance(gate, torch.Tensor) and gate.dim() == 2:
+        groups = gate.shape[0]
+    return _Block(x.numel() // width if width else 0, width, groups, dtype, x.data_ptr(),
+                  None if o is None else _like(o, x, "o").data_ptr(), _stride_of_rows(x, "x"),
+                  0 if o is None else _stride_of_rows(o, "o"), _weight_ptr(w_post, x, (width,), "w_post"),
+                  None if gate is None else _weight_ptr(gate, x, (groups, width) if gate.dim() == 2 else (width,), "gate"),
+                  _weight_ptr(w_pre, x, (width,), "w_pre"), res_scale, eps)
+
+
+def _rows_like(t, x: torch.Tensor, what: str) -> tuple:
+    """Address and row stride of an optional tensor like x."""
+    if t is None:
+        return None, 0
+    _like(t, x, what)
+    return t.data_ptr(), _stride_of_rows(t, what)
+
+
+def block_norm(x, w_pre=None, o=None, w_post=None, gate=None, res_scale: float = 1.0, eps: float = 1e-6,
+               keep: bool = False, out=None, n_out=None, stream=None):
+    """x_new = res_scale * x + gate * b, with b = w_post * o / rms(o) (o itself without w_post), and
+    n = w_pre * x_new / rms(x_new): the residual stream after a block and the next one's input. x, o are
+    (..., width); w_post and w_pre (width,); gate (width,), or (groups, width) for as many equal runs of rows.
+    Returns x_new (``out``, which may be x; without o only if asked for), n (``n_out``, which may be o; None
+    without w_pre) and, with ``keep``, what ``block_norm_grad`` takes (else None)."""
+    if stream is not None:
+        return _on(stream, x, block_norm, x, w_pre, o, w_post, gate, res_scale, eps, keep, out, n_out)
+    b = _block(x, w_pre, o, w_post, gate, res_scale, eps)
+    if out is None and o is not None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if n_out is None and w_pre is not None:
+        n_out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    kept = torch.empty((2, b.rows), dtype=torch.float32, device=x.device) if keep else None
+    _check(lib().zg_block_norm(ctypes.byref(b), *_rows_like(out, x, "out"), *_rows_like(n_out, x, "n_out"),
+                               kept.data_ptr() if keep else None, _stream_of(x)), "zg_block_norm")
+    return out, n_out, kept
+
+
+def block_norm_grad(x, kept, dn=None, dx_new=None, w_pre=None, o=None, w_post=None, gate=None, res_scale: float = 1.0,
+                    eps: float = 1e-6, out=None, stream=None):
+    """The gradients (dx, do, dw_pre, dw_post, dgate) from those of n and of x_new (None: zero), for the x and o of
+    the ``block_norm`` call that gave ``kept``; None for what that call did not have. ``out``: (dx, do) to
+    write into; they may be dx_new and dn themselves."""
+    if stream is not None:
+        return _on(stream, x, block_norm_grad, x, kept, dn, dx_new, w_pre, o, w_post, gate, res_scale, eps, out)
+    if kept is None:
+        raise ValueError("kept is None: call block_norm with keep=True")
+    b = _block(x, w_pre, o, w_post, gate, res_scale, eps)
+    new = functools.partial(torch.empty_like, memory_format=torch.contiguous_format)
+    dx, do = out if out is not None else (new(x), None if o is None else new(x))
+    dw_pre, dw_post, dgate = (None if w is None else new(w) for w in (w_pre, w_post, gate))
+    L = lib()
+    work_bytes = L.zg_block_norm_workspace(b.rows, b.width, b.groups)
+    _check(min(work_bytes, 0), "zg_block_norm_workspace")
+    work = _workspace(work_bytes, x)
+    _check(L.zg_block_norm_grad(ctypes.byref(b), _side(kept, torch.float32, (2, b.rows), x, "kept"),
+                                *_rows_like(dn, x, "dn"), *_rows_like(dx_new, x, "dx_new"), *_rows_like(dx, x, "dx"),
+                                *_rows_like(do, x, "do"),
+                                *(None if w is None else w.data_ptr() for w in (dw_pre, dw_post, dgate)),
+                                None if work is None else work.data_ptr(), work_bytes, _stream_of(x)), "zg_block_norm_grad")
+    return dx, do, dw_pre, dw_post, dgate
+
+
+# ----------------------------------------------------------------- policies
+
+def token_logp(logits, tokens, temperature: float = 1.0, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The log-probability of each row's token (rows,) under softmax(logits / temperature), and each row's
+    log-sum-exp of logits / temperature. Zeros for a token outside [0, vocab)."""
+    if stream is not None:
+        return _on(stream, logits, token_logp, logits, tokens, temperature)
+    _rows(logits, "logits")
+    n, v = logits.shape
+    size = _tokens(tokens, logits, (n,))
+    logp, lse = (torch.empty(n, dtype=torch.float32, device=logits.device) for _ in range(2))
+    _check(lib().zg_token_logp(logits.data_ptr(), _DTYPES[logits.dtype], n, v, _row_stride(logits), tokens.data_ptr(), size,
+                               temperature, logp.data_ptr(), lse.data_ptr(), _stream_of(logits)), "zg_token_logp")
+    return logp, lse
+
+
+def _policy(logits, tokens, old_logp, advantage, ref_logp, clip, kl: float, temperature: float) -> _Policy:
+    _rows(logits, "logits")
+    n, v = logits.shape
+    size = _tokens(tokens, logits, (n,))
+    low, high = clip
+    return _Policy(logits.data_ptr(), n, v, _row_stride(logits), _DTYPES[logits.dtype], size, tokens.data_ptr(),
+                   *(_side(t, torch.float32, (n,), logits, what) for t, what in
+                     ((old_logp, "old_logp"), (advantage, "advantage"), (ref_logp, "ref_logp"))),
+                   low, high, kl, temperature)
+
+
+def policy_loss(logits, tokens, old_logp, advantage, ref_logp=None, clip=(0.2, 0.2), kl: float = 0.0,
+                temperature: float = 1.0, stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The clipped policy loss of each row's token, -min(r A, clamp(r, 1 - clip[0], 1 + clip[1]) A) with
+    r = exp(logp - old_logp), plus kl (exp(d) - 1 - d) with d = ref_logp - logp where there is a reference; the
+    rows' logp; and what ``policy_grad`` takes. Zeros for a token outside [0, vocab)."""
+    if stream is not None:
+        return _on(stream, logits, policy_loss, logits, tokens, old_logp, advantage, ref_logp, clip, kl, temperature)
+    a = _policy(logits, tokens, old_logp, advantage, ref_logp, clip, kl, temperature)
+    loss, logp = (torch.empty(a.rows, dtype=torch.float32, device=logits.device) for _ in range(2))
+    kept = torch.empty((a.rows, 2), dtype=torch.float32, device=logits.device)
+    _check(lib().zg_policy_loss(ctypes.byref(a), loss.data_ptr(), logp.data_ptr(), kept.data_ptr(), _stream_of(logits)),
+           "zg_policy_loss")
+    return loss, logp, kept
+
+
+def policy_grad(logits, kept, tokens, old_logp, advantage, ref_logp=None, clip=(0.2, 0.2), kl: float = 0.0,
+                temperature: float = 1.0, scale: float = 1.0, dloss=None, out=None, stream=None) -> torch.Tensor:
+    """The gradient of sum(scale * dloss * loss) by the logits, from what ``policy_loss`` kept for the same
+    arguments (dloss None: ones). ``out`` may be the logits themselves."""
+    if stream is not None:
+        return _on(stream, logits, policy_grad, logits, kept, tokens, old_logp, advantage, ref_logp, clip, kl, temperature,
+                   scale, dloss, out)
+    a = _policy(logits, tokens, old_logp, advantage, ref_logp, clip, kl, temperature)
+    out = _gradient_of(logits, out)
+    _check(lib().zg_policy_grad(ctypes.byref(a), _side(kept, torch.float32, (a.rows, 2), logits, "kept"), scale,
+                                _side(dloss, torch.float32, (a.rows,), logits, "dloss"), out.data_ptr(), _row_stride(out),
+                                _stream_of(logits)), "zg_policy_grad")
+    return out
+
+
+def policy_loss_grad(logits, tokens, old_logp, advantage, ref_logp=None, clip=(0.2, 0.2), kl: float = 0.0,
+                     temperature: float = 1.0, scale: float = 1.0, dloss=None, out=None,
+                     stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The loss and logp of each row and the gradient of sum(scale * dloss * loss) by the logits, in one pass over
+    them. ``out`` may be the logits themselves."""
+    if stream is not None:
+        return _on(stream, logits, policy_loss_grad, logits, tokens, old_logp, advantage, ref_logp, clip, kl, temperature,
+                   scale, dloss, out)
+    a = _policy(logits, tokens, old_logp, advantage, ref_logp, clip, kl, temperature)
+    out = _gradient_of(logits, out)
+    loss, logp = (torch.empty(a.rows, dtype=torch.float32, device=logits.device) for _ in range(2))
+    _check(lib().zg_policy_loss_grad(ctypes.byref(a), scale, _side(dloss, torch.float32, (a.rows,), logits, "dloss"),
+                                     loss.data_ptr(), logp.data_ptr(), out.data_ptr(), _row_stride(out),
+                                     _stream_of(logits)), "zg_policy_loss_grad")
+    return loss, logp, out
+
+
+# ----------------------------------------------------------------- many gradients
+
+class GradClip:
+    """The common norm of many gradients, and their clipping: for contiguous bf16 or float32 tensors, whose
+    memory this object keeps (make another when they get new memory). ``out``: None to clip them
+    where they are; a flat tensor, bf16 or float32, that receives them end to end in their order (the flat
+    gradient of ``ShardedAdamW.step``, say; elements past them are left as they were); or a list of tensors of
+    their sizes. Calls may run on any stream; two that write at once must be ordered by the caller."""
+
+    def __init__(self, tensors, out=None):
+        self.handle = None
+        tensors = list(tensors)
+        for i, t in enumerate(tensors):
+            _dtype(t, f"tensors[{i}]")
+            _dev_ptr(t, t.dtype, 0, f"tensors[{i}]")
+            if t.get_device() != tensors[0].get_device():
+                raise ValueError(f"tensors[{i}] is on {t.device}, not on {tensors[0].device}")
+        if not tensors:
+            raise ValueError("there are no tensors")
+        if out is None:
+            outs = tensors
+        elif isinstance(out, torch.Tensor):
+            _dtype(out, "out")
+            _dev_ptr(out, out.dtype, sum(t.numel() for t in tensors), "out")
+            outs, at = [], 0
+            flat = out.view(-1)
+            for t in tensors:
+                outs.append(flat[at:at + t.numel()])
+                at += t.numel()
+        else:
+            outs = list(out)
+            if len(outs) != len(tensors):
+                raise ValueError(f"out has {len(outs)} tensors for {len(tensors)}")
+        for i, (t, o) in enumerate(zip(tensors, outs)):
+            _dtype(o, f"out[{i}]")
+            _dev_ptr(o, o.dtype, 0, f"out[{i}]")
+            if o.numel() != t.numel():
+                raise ValueError(f"out[{i}] holds {o.numel()} elements, not {t.numel()}")
+            if o.get_device() != tensors[0].get_device():
+                raise ValueError(f"out[{i}] is on {o.device}, not on {tensors[0].device}")
+        rows = (_Grad * len(tensors))(*(_Grad(t.data_ptr(), o.data_ptr(), t.numel(), _DTYPES[t.dtype], _DTYPES[o.dtype])
+                                        for t, o in zip(tensors, outs)))
+        self.tensors, self.out, self._outs = tensors, out, outs  # the memory stays while the list has its addresses
+        handle = ctypes.c_void_p()
+        with torch.cuda.device(tensors[0].device):
+            _check(lib().zg_grads_init(rows, len(tensors), ctypes.byref(handle)), "zg_grads_init")
+        self.handle = handle.value
+        self._work_bytes = _lib.zg_grads_workspace(self.handle)
+
+    def __del__(self):
+        if getattr(self, "handle", None) and _lib is not None:
+            _lib.zg_grads_destroy(self.handle)
+            self.handle = None
+
+    def norm(self, scale: float = 1.0, stream=None) -> torch.Tensor:
+        """A float32 CUDA tensor of two: the norm of ``scale`` times all gradients, and 1."""
+        ref = self.tensors[0]
+        if stream is not None:
+            return _on(stream, ref, self.norm, scale)
+        stats = torch.empty(2, dtype=torch.float32, device=ref.device)
+        work = _workspace(self._work_bytes, ref)
+        _check(_lib.zg_grads_norm(self.handle, scale, stats.data_ptr(), work.data_ptr(), self._work_bytes,
+                                  _stream_of(ref)), "zg_grads_norm")
+        return stats
+
+    def clip(self, max_norm: float, eps: float = 1e-6, scale: float = 1.0, stream=None) -> torch.Tensor:
+        """Write scale * min(1, max_norm / (norm + eps)) times the gradients (scale times them where the norm is
+        not finite): a float32 CUDA tensor of the norm, of ``scale`` times them, and the coefficient."""
+        ref = self.tensors[0]
+        if stream is not None:
+            return _on(stream, ref, self.clip, max_norm, eps, scale)
+        stats = torch.empty(2, dtype=torch.float32, device=ref.device)
+        work = _workspace(self._work_bytes, ref)
+        _check(_lib.zg_grads_clip(self.handle, max_norm, eps, scale, stats.data_ptr(), work.data_ptr(), self._work_bytes,
+                                  _stream_of(ref)), "zg_grads_clip")
+        return stats

@@ -68,4 +68,79 @@ struct DistillArgs {
 
 cudaError_t launch_distill(const DistillArgs &a, cudaStream_t st);
 
+struct EmbedArgs {
+    const void *table;  // of the lookup, or add of the gradient (or null)
+    int dtype;          // of table and out
+    int64_t vocab, width, table_stride;
+    const void *tokens;
+    int token_bytes;
+    int64_t n;
+    float scale;
+    void *out;  // rows, or dtable
+    int64_t out_stride;
+    const void *drows;  // of the gradient
+    int drow_dtype;
+    int64_t drow_stride;
+    void *work;
+};
+
+cudaError_t launch_embed(const EmbedArgs &a, cudaStream_t st);
+int64_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t width);
+cudaError_t launch_embed_grad(const EmbedArgs &a, cudaStream_t st);
+
+// One tensor of a block's norms: element (r, c) at ptr[r * stride + c].
+struct RowsView {
+    void *ptr;
+    int64_t stride;
+};
+
+struct BlockArgs {
+    int64_t rows, groups;
+    int width, dtype;
+    RowsView x, o;  // o.ptr may be null, as the weights
+    const void *w_post, *gate, *w_pre;
+    float res_scale, eps;
+    float *kept;         // 2 x rows: written by forward (or null), read by backward
+    RowsView x_new, n;   // forward's outputs (either may be null); dx_new (or null) and dn of backward
+    RowsView dx, d_o;    // backward only, as the rest
+    void *dw_pre, *dw_post, *dgate;
+    float *work;
+};
+
+cudaError_t launch_block_norm(const BlockArgs &a, cudaStream_t st);
+int64_t block_norm_workspace(int64_t rows, int64_t width, int64_t groups);
+cudaError_t launch_block_norm_grad(const BlockArgs &a, cudaStream_t st);
+
+// loss alone, gradient alone (from kept), or both; with old_logp null the
+// log-probabilities alone.
+struct PolicyArgs {
+    const void *logits;
+    int64_t rows, row_stride;
+    int vocab, dtype, token_bytes;
+    const void *tokens;
+    const float *old_logp, *advantage, *ref_logp;
+    float clip_low, clip_high, kl, temperature;
+    float *loss, *logp, *lse;  // written where not null
+    float *kept;               // rows x 2: written with the loss (or null)
+    const float *kept_in;      // the gradient alone starts from these
+    float scale;
+    const float *dloss;
+    void *dlogits;
+    int64_t drow_stride;
+};
+
+cudaError_t launch_policy(const PolicyArgs &a, cudaStream_t st);
+
+// A share of one tensor of a gradient list.
+struct GradPart {
+    const void *grad;
+    void *out;
+    int n;
+    uint8_t dtype, out_dtype;
+};
+constexpr int kGradPart = 16384;  // elements of a part
+
+cudaError_t launch_grads_norm(const GradPart *parts, int64_t count, double *sums, float scale, float max_norm, float eps,
+                              float *stats, bool write, cudaStream_t st);
+
 }  // namespace zg

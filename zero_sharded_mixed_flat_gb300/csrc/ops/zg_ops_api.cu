@@ -6,7 +6,9 @@
 #include <stdint.h>
 #include <stdio.h>
 
+#include <algorithm>
 #include <new>
+#include <vector>
 
 #include "zg.h"
 #include "zg_launch.h"
@@ -18,6 +20,12 @@ struct zg_scan {
     int64_t record_bytes;
     char *d_mem;  // ctl (8 bytes), status and gave_up (4 bytes each), and from kHead on the records
     long long wait_limit;
+};
+
+struct zg_grads {
+    int device;
+    int64_t parts;
+    zg::GradPart *d_parts;
 };
 
 namespace {
@@ -201,6 +209,203 @@ int check_dlogits(const zg_distill_args *d, const float *dloss, void *dlogits, i
     return ZG_OK;
 }
 
+// ------------------------------------------------------------------ tokens, blocks, policies, gradients
+
+// Rows of `width` elements, `stride` apart.
+int check_stride(int64_t rows, int64_t width, int64_t stride, const char *what)
+{
+    if (stride < width || stride >= kFar || double(rows) * double(stride) >= double(kFar))
+        return fail(ZG_ERR_INVALID_ARG, "%s %lld is not at least the row's %lld, or out of range", what, (long long)stride,
+                    (long long)width);
+    return ZG_OK;
+}
+
+int check_tokens(const void *tokens, int token_bytes, int64_t n)
+{
+    if (token_bytes != 4 && token_bytes != 8) return fail(ZG_ERR_INVALID_ARG, "token_bytes must be 4 or 8 (got %d)", token_bytes);
+    return n ? check_ptr(tokens, token_bytes, false, "tokens") : ZG_OK;
+}
+
+int check_work(const void *work, int64_t have, int64_t need)
+{
+    if (have < need) return fail(ZG_ERR_INVALID_ARG, "work has %lld bytes, needs %lld", (long long)have, (long long)need);
+    return need ? check_ptr(work, 16, false, "work") : ZG_OK;
+}
+
+int check_embed(int64_t n, int64_t vocab, int64_t width, float scale)
+{
+    constexpr int64_t kMost = (int64_t(1) << 31) - 1;
+    if (n < 0 || n > kMost) return fail(ZG_ERR_INVALID_ARG, "n must be in [0, 2^31) (got %lld)", (long long)n);
+    if (vocab < 1 || vocab > kMost) return fail(ZG_ERR_INVALID_ARG, "vocab must be in [1, 2^31) (got %lld)", (long long)vocab);
+    if (width < 1 || width > ZG_EMBED_MAX_WIDTH)
+        return fail(ZG_ERR_INVALID_ARG, "width must be in [1, %d] (got %lld)", ZG_EMBED_MAX_WIDTH, (long long)width);
+    if (!isfinite(scale)) return fail(ZG_ERR_INVALID_ARG, "scale must be finite");
+    return ZG_OK;
+}
+
+// One of a block's tensors of rows, of which `there` says whether it takes part.
+int check_block_rows(const zg_block *b, const void *p, int64_t stride, bool there, const char *what, zg::RowsView &v)
+{
+    v = zg::RowsView{nullptr, 0};
+    if (!b->rows) return ZG_OK;
+    if (!there) return p ? fail(ZG_ERR_INVALID_ARG, "%s must be NULL here", what) : ZG_OK;
+    if (!p) return fail(ZG_ERR_INVALID_ARG, "%s is NULL", what);
+    if (int rc = check_stride(b->rows, b->width, stride, what)) return rc;
+    if (int rc = check_ptr(p, element_size(b->dtype), false, what)) return rc;
+    v = zg::RowsView{const_cast<void *>(p), stride};
+    return ZG_OK;
+}
+
+int check_block_shape(int64_t rows, int64_t width, int64_t groups)
+{
+    if (rows < 0 || rows >= kFar) return fail(ZG_ERR_INVALID_ARG, "rows is out of range (got %lld)", (long long)rows);
+    if (width < 1 || width > ZG_BLOCK_MAX_WIDTH)
+        return fail(ZG_ERR_INVALID_ARG, "width must be in [1, %d] (got %lld)", ZG_BLOCK_MAX_WIDTH, (long long)width);
+    if (groups < 1 || rows % groups || (rows && groups > rows))
+        return fail(ZG_ERR_INVALID_ARG, "groups must divide rows (got %lld and %lld)", (long long)groups, (long long)rows);
+    return ZG_OK;
+}
+
+int check_block(const zg_block *b, zg::BlockArgs &a)
+{
+    if (!b) return fail(ZG_ERR_INVALID_ARG, "block is NULL");
+    if (int rc = check_dtype(b->dtype, "dtype")) return rc;
+    if (int rc = check_block_shape(b->rows, b->width, b->groups)) return rc;
+    if (!isfinite(b->res_scale)) return fail(ZG_ERR_INVALID_ARG, "res_scale must be finite");
+    if (!(b->eps >= 0.0f) || !isfinite(b->eps)) return fail(ZG_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (b->rows && !b->o && (b->w_post || b->gate))
+        return fail(ZG_ERR_INVALID_ARG, "w_post and gate must be NULL where o is");
+    a = zg::BlockArgs{};
+    a.rows = b->rows;
+    a.width = int(b->width);
+    a.groups = b->gate ? b->groups : 1;
+    a.dtype = b->dtype;
+    a.res_scale = b->res_scale;
+    a.eps = b->eps;
+    const int size = element_size(b->dtype);
+    if (int rc = check_block_rows(b, b->x, b->x_stride, true, "x", a.x)) return rc;
+    if (int rc = check_block_rows(b, b->o, b->o_stride, b->o != nullptr, "o", a.o)) return rc;
+    if (int rc = check_ptr(b->w_post, size, true, "w_post")) return rc;
+    if (int rc = check_ptr(b->gate, size, true, "gate")) return rc;
+    if (int rc = check_ptr(b->w_pre, size, true, "w_pre")) return rc;
+    a.w_post = b->w_post;
+    a.gate = b->gate;
+    a.w_pre = b->w_pre;
+    return ZG_OK;
+}
+
+// A weight's gradient, there exactly where the weight is.
+int check_weight(const void *w, const void *dw, int dtype, const char *what)
+{
+    if (!w) return dw ? fail(ZG_ERR_INVALID_ARG, "%s must be NULL here", what) : ZG_OK;
+    return check_ptr(dw, element_size(dtype), false, what);
+}
+
+int check_temperature(float t)
+{
+    // the kernels scale by log2(e) / T
+    if (t > 0.0f && isfinite(t) && isfinite(1.0f / t * 1.44269504f)) return ZG_OK;
+    return fail(ZG_ERR_INVALID_ARG, "temperature must be finite and > 0, and log2(e) over it finite (got %g)", double(t));
+}
+
+int check_policy(const zg_policy_args *p, float scale, zg::PolicyArgs &a)
+{
+    if (!p) return fail(ZG_ERR_INVALID_ARG, "args is NULL");
+    if (int rc = check_rows(p->logits, p->dtype, p->rows, p->vocab, p->row_stride, 1)) return rc;
+    if (int rc = check_tokens(p->tokens, p->token_bytes, p->rows)) return rc;
+    if (int rc = check_temperature(p->temperature)) return rc;
+    if (!(p->clip_low >= 0.0f && p->clip_low <= 1.0f))
+        return fail(ZG_ERR_INVALID_ARG, "clip_low must be in [0, 1] (got %g)", double(p->clip_low));
+    if (!(p->clip_high >= 0.0f) || !isfinite(p->clip_high))
+        return fail(ZG_ERR_INVALID_ARG, "clip_high must be finite and >= 0 (got %g)", double(p->clip_high));
+    if (!isfinite(p->kl)) return fail(ZG_ERR_INVALID_ARG, "kl must be finite");
+    if (!isfinite(scale)) return fail(ZG_ERR_INVALID_ARG, "scale must be finite");
+    if (p->rows) {
+        if (int rc = check_ptr(p->old_logp, 4, false, "old_logp")) return rc;
+        if (int rc = check_ptr(p->advantage, 4, false, "advantage")) return rc;
+        if (int rc = check_ptr(p->ref_logp, 4, true, "ref_logp")) return rc;
+    }
+    a = zg::PolicyArgs{};
+    a.logits = p->logits;
+    a.rows = p->rows;
+    a.row_stride = p->row_stride;
+    a.vocab = int(p->vocab);
+    a.dtype = p->dtype;
+    a.token_bytes = p->token_bytes;
+    a.tokens = p->tokens;
+    a.old_logp = p->old_logp;
+    a.advantage = p->advantage;
+    a.ref_logp = p->ref_logp;
+    a.clip_low = p->clip_low;
+    a.clip_high = p->clip_high;
+    a.kl = p->kl;
+    a.temperature = p->temperature;
+    a.scale = scale;
+    return ZG_OK;
+}
+
+int check_policy_gradient(const zg_policy_args *p, const float *dloss, void *dlogits, int64_t stride, zg::PolicyArgs &a)
+{
+    if (int rc = check_stride(p->rows, p->vocab, stride, "drow_stride")) return rc;
+    if (p->rows) {
+        if (dlogits == p->logits && stride != p->row_stride)
+            return fail(ZG_ERR_INVALID_ARG, "a gradient in the logits' own memory needs their row_stride");
+        if (int rc = check_ptr(dloss, 4, true, "dloss")) return rc;
+        if (int rc = check_ptr(dlogits, element_size(p->dtype), false, "dlogits")) return rc;
+    }
+    a.dloss = dloss;
+    a.dlogits = dlogits;
+    a.drow_stride = stride;
+    return ZG_OK;
+}
+
+// No output overlaps another, or a gradient that is not its own.
+int check_apart(const zg_grad *list, int64_t count)
+{
+    struct Span {
+        uintptr_t lo, hi;
+        int64_t of;
+    };
+    std::vector<Span> outs;
+    for (int64_t i = 0; i < count; ++i) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(list[i].out);
+        if (list[i].n) outs.push_back(Span{lo, lo + uintptr_t(list[i].n) * element_size(list[i].out_dtype), i});
+    }
+    std::sort(outs.begin(), outs.end(), [](const Span &a, const Span &b) { return a.lo < b.lo; });
+    for (size_t i = 1; i < outs.size(); ++i)
+        if (outs[i].lo < outs[i - 1].hi)
+            return fail(ZG_ERR_INVALID_ARG, "the outputs of list[%lld] and list[%lld] overlap", (long long)outs[i - 1].of,
+                        (long long)outs[i].of);
+    for (int64_t i = 0; i < count; ++i) {
+        if (!list[i].n) continue;
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(list[i].grad);
+        const uintptr_t hi = lo + uintptr_t(list[i].n) * element_size(list[i].dtype);
+        auto it = std::upper_bound(outs.begin(), outs.end(), lo, [](uintptr_t v, const Span &s) { return v < s.hi; });
+        for (; it != outs.end() && it->lo < hi; ++it)
+            if (it->of != i || list[i].grad != list[i].out)
+                return fail(ZG_ERR_INVALID_ARG, "list[%lld] overlaps the output of list[%lld]", (long long)i, (long long)it->of);
+    }
+    return ZG_OK;
+}
+
+int grads_call(const zg_grads *g, float max_norm, float eps, float scale, float *stats, void *work, int64_t work_bytes,
+               bool write, cudaStream_t stream)
+{
+    if (!g) return fail(ZG_ERR_INVALID_ARG, "list is NULL");
+    if (!(scale > 0.0f) || !isfinite(scale)) return fail(ZG_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (write && !(max_norm > 0.0f)) return fail(ZG_ERR_INVALID_ARG, "max_norm must be > 0");
+    if (write && (!(eps >= 0.0f) || !isfinite(eps))) return fail(ZG_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    int dev = 0;
+    if (int rc = finish(cudaGetDevice(&dev), "zg_grads")) return rc;
+    if (dev != g->device)
+        return fail(ZG_ERR_INVALID_ARG, "the list belongs to device %d, but the current device is %d", g->device, dev);
+    if (int rc = check_ptr(stats, 4, false, "stats")) return rc;
+    if (int rc = check_work(work, work_bytes, zg_grads_workspace(g))) return rc;
+    return finish(zg::launch_grads_norm(g->d_parts, g->parts, static_cast<double *>(work), scale, max_norm, eps, stats, write,
+                                        stream),
+                  "gradient list launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -377,6 +582,289 @@ int zg_distill_loss_grad(const zg_distill_args *args, float scale, const float *
         a.lse = lse;
         return finish(zg::launch_distill(a, stream), "distillation launch");
     });
+}
+
+int zg_embed(const void *table, int dtype, int64_t vocab, int64_t width, int64_t table_stride, const void *tokens,
+             int token_bytes, int64_t n, float scale, void *out, int64_t out_stride, zg_stream stream)
+{
+    return guarded([&]() -> int {
+        if (int rc = check_dtype(dtype, "dtype")) return rc;
+        if (int rc = check_embed(n, vocab, width, scale)) return rc;
+        if (int rc = check_stride(vocab, width, table_stride, "table_stride")) return rc;
+        if (int rc = check_stride(n, width, out_stride, "out_stride")) return rc;
+        if (int rc = check_tokens(tokens, token_bytes, n)) return rc;
+        if (n == 0) return ZG_OK;
+        if (int rc = check_ptr(table, element_size(dtype), false, "table")) return rc;
+        if (int rc = check_ptr(out, element_size(dtype), false, "out")) return rc;
+        zg::EmbedArgs a{};
+        a.table = table;
+        a.dtype = dtype;
+        a.vocab = vocab;
+        a.width = width;
+        a.table_stride = table_stride;
+        a.tokens = tokens;
+        a.token_bytes = token_bytes;
+        a.n = n;
+        a.scale = scale;
+        a.out = out;
+        a.out_stride = out_stride;
+        return finish(zg::launch_embed(a, stream), "embedding launch");
+    });
+}
+
+int64_t zg_embed_grad_workspace(int64_t n, int64_t vocab, int64_t width)
+{
+    if (check_embed(n, vocab, width, 1.0f)) return -1;
+    return zg::embed_grad_workspace(n, vocab, width);
+}
+
+int zg_embed_grad(const void *drows, int dtype, int64_t drow_stride, const void *tokens, int token_bytes, int64_t n,
+                  int64_t vocab, int64_t width, float scale, const void *add, int64_t add_stride, void *dtable,
+                  int table_dtype, int64_t dtable_stride, void *work, int64_t work_bytes, zg_stream stream)
+{
+    return guarded([&]() -> int {
+        if (int rc = check_dtype(dtype, "dtype")) return rc;
+        if (int rc = check_dtype(table_dtype, "table_dtype")) return rc;
+        if (int rc = check_embed(n, vocab, width, scale)) return rc;
+        if (int rc = check_stride(n, width, drow_stride, "drow_stride")) return rc;
+        if (int rc = check_stride(vocab, width, dtable_stride, "dtable_stride")) return rc;
+        if (add)
+            if (int rc = check_stride(vocab, width, add_stride, "add_stride")) return rc;
+        if (add && add == dtable && add_stride != dtable_stride)
+            return fail(ZG_ERR_INVALID_ARG, "a gradient in add's own memory needs its stride");
+        if (int rc = check_tokens(tokens, token_bytes, n)) return rc;
+        if (n)
+            if (int rc = check_ptr(drows, element_size(dtype), false, "drows")) return rc;
+        if (int rc = check_ptr(add, element_size(table_dtype), true, "add")) return rc;
+        if (int rc = check_ptr(dtable, element_size(table_dtype), false, "dtable")) return rc;
+        if (int rc = check_work(work, work_bytes, zg::embed_grad_workspace(n, vocab, width))) return rc;
+        zg::EmbedArgs a{};
+        a.table = add;
+        a.dtype = table_dtype;
+        a.vocab = vocab;
+        a.width = width;
+        a.table_stride = add_stride;
+        a.tokens = tokens;
+        a.token_bytes = token_bytes;
+        a.n = n;
+        a.scale = scale;
+        a.out = dtable;
+        a.out_stride = dtable_stride;
+        a.drows = drows;
+        a.drow_dtype = dtype;
+        a.drow_stride = drow_stride;
+        a.work = work;
+        return finish(zg::launch_embed_grad(a, stream), "embedding gradient launch");
+    });
+}
+
+int zg_block_norm(const zg_block *block, void *x_new, int64_t x_new_stride, void *n, int64_t n_stride, float *kept,
+                  zg_stream stream)
+{
+    return guarded([&]() -> int {
+        zg::BlockArgs a;
+        if (int rc = check_block(block, a)) return rc;
+        if (int rc = check_block_rows(block, x_new, x_new_stride, x_new || block->o, "x_new", a.x_new)) return rc;
+        if (int rc = check_block_rows(block, n, n_stride, block->w_pre != nullptr, "n", a.n)) return rc;
+        if (a.rows == 0) return ZG_OK;
+        if (!x_new && !n) return fail(ZG_ERR_INVALID_ARG, "neither x_new nor n is asked for");
+        if (x_new && ((x_new == block->x && x_new_stride != block->x_stride) || x_new == block->o || x_new == n))
+            return fail(ZG_ERR_INVALID_ARG, "x_new must not overlap o or n, and in x's own memory it needs x's stride");
+        if (n && ((n == block->o && n_stride != block->o_stride) || n == block->x))
+            return fail(ZG_ERR_INVALID_ARG, "n must not overlap x, and in o's own memory it needs o's stride");
+        if (int rc = check_ptr(kept, 4, true, "kept")) return rc;
+        a.kept = kept;
+        return finish(zg::launch_block_norm(a, stream), "block norm launch");
+    });
+}
+
+int64_t zg_block_norm_workspace(int64_t rows, int64_t width, int64_t groups)
+{
+    if (check_block_shape(rows, width, groups)) return -1;
+    return rows ? zg::block_norm_workspace(rows, width, groups) : 0;
+}
+
+int zg_block_norm_grad(const zg_block *block, const float *kept, const void *dn, int64_t dn_stride,
+                       const void *dx_new, int64_t dx_new_stride, void *dx, int64_t dx_stride, void *d_o,
+                       int64_t d_o_stride, void *dw_pre, void *dw_post, void *dgate, void *work, int64_t work_bytes,
+                       zg_stream stream)
+{
+    return guarded([&]() -> int {
+        zg::BlockArgs a;
+        if (int rc = check_block(block, a)) return rc;
+        if (int rc = check_block_rows(block, dn, dn_stride, block->w_pre != nullptr, "dn", a.n)) return rc;
+        if (int rc = check_block_rows(block, dx_new, dx_new_stride, dx_new != nullptr, "dx_new", a.x_new)) return rc;
+        if (int rc = check_block_rows(block, dx, dx_stride, true, "dx", a.dx)) return rc;
+        if (int rc = check_block_rows(block, d_o, d_o_stride, block->o != nullptr, "d_o", a.d_o)) return rc;
+        if (int rc = check_weight(block->w_pre, dw_pre, block->dtype, "dw_pre")) return rc;
+        if (int rc = check_weight(block->w_post, dw_post, block->dtype, "dw_post")) return rc;
+        if (int rc = check_weight(block->gate, dgate, block->dtype, "dgate")) return rc;
+        const int size = element_size(block->dtype);
+        if (a.rows == 0) {  // sums over nothing
+            const size_t row = size_t(a.width) * size;
+            cudaError_t e = dw_pre ? cudaMemsetAsync(dw_pre, 0, row, stream) : cudaSuccess;
+            if (e == cudaSuccess && dw_post) e = cudaMemsetAsync(dw_post, 0, row, stream);
+            if (e == cudaSuccess && dgate) e = cudaMemsetAsync(dgate, 0, row * size_t(a.groups), stream);
+            return finish(e, "block norm gradient of no rows");
+        }
+        if (dx == d_o || dx == block->x || dx == block->o || (d_o && (d_o == block->x || d_o == block->o)) ||
+            (dx == dx_new && dx_stride != dx_new_stride) || (d_o && d_o == dn && d_o_stride != dn_stride) || dx == dn ||
+            (d_o && d_o == dx_new))
+            return fail(ZG_ERR_INVALID_ARG, "dx and d_o overlap an input or each other");
+        if (int rc = check_ptr(kept, 4, false, "kept")) return rc;
+        if (int rc = check_work(work, work_bytes, zg::block_norm_workspace(a.rows, a.width, a.groups))) return rc;
+        a.kept = const_cast<float *>(kept);
+        a.dw_pre = dw_pre;
+        a.dw_post = dw_post;
+        a.dgate = dgate;
+        a.work = static_cast<float *>(work);
+        return finish(zg::launch_block_norm_grad(a, stream), "block norm gradient launch");
+    });
+}
+
+int zg_token_logp(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride, const void *tokens,
+                  int token_bytes, float temperature, float *logp, float *lse, zg_stream stream)
+{
+    return guarded([&]() -> int {
+        if (int rc = check_rows(logits, dtype, rows, vocab, row_stride, 1)) return rc;
+        if (int rc = check_tokens(tokens, token_bytes, rows)) return rc;
+        if (int rc = check_temperature(temperature)) return rc;
+        if (rows == 0) return ZG_OK;
+        if (int rc = check_ptr(logp, 4, false, "logp")) return rc;
+        if (int rc = check_ptr(lse, 4, true, "lse")) return rc;
+        zg::PolicyArgs a{};
+        a.logits = logits;
+        a.rows = rows;
+        a.row_stride = row_stride;
+        a.vocab = int(vocab);
+        a.dtype = dtype;
+        a.token_bytes = token_bytes;
+        a.tokens = tokens;
+        a.temperature = temperature;
+        a.logp = logp;
+        a.lse = lse;
+        return finish(zg::launch_policy(a, stream), "token log-probability launch");
+    });
+}
+
+int zg_policy_loss(const zg_policy_args *args, float *loss, float *logp, float *kept, zg_stream stream)
+{
+    return guarded([&]() -> int {
+        zg::PolicyArgs a;
+        if (int rc = check_policy(args, 0.0f, a)) return rc;
+        if (a.rows == 0) return ZG_OK;
+        if (int rc = check_ptr(loss, 4, false, "loss")) return rc;
+        if (int rc = check_ptr(logp, 4, true, "logp")) return rc;
+        if (int rc = check_ptr(kept, 4, true, "kept")) return rc;
+        a.loss = loss;
+        a.logp = logp;
+        a.kept = kept;
+        return finish(zg::launch_policy(a, stream), "policy loss launch");
+    });
+}
+
+int zg_policy_grad(const zg_policy_args *args, const float *kept, float scale, const float *dloss, void *dlogits,
+                   int64_t drow_stride, zg_stream stream)
+{
+    return guarded([&]() -> int {
+        zg::PolicyArgs a;
+        if (int rc = check_policy(args, scale, a)) return rc;
+        if (int rc = check_policy_gradient(args, dloss, dlogits, drow_stride, a)) return rc;
+        if (a.rows == 0) return ZG_OK;
+        if (int rc = check_ptr(kept, 4, false, "kept")) return rc;
+        a.kept_in = kept;
+        return finish(zg::launch_policy(a, stream), "policy gradient launch");
+    });
+}
+
+int zg_policy_loss_grad(const zg_policy_args *args, float scale, const float *dloss, float *loss, float *logp,
+                        void *dlogits, int64_t drow_stride, zg_stream stream)
+{
+    return guarded([&]() -> int {
+        zg::PolicyArgs a;
+        if (int rc = check_policy(args, scale, a)) return rc;
+        if (int rc = check_policy_gradient(args, dloss, dlogits, drow_stride, a)) return rc;
+        if (a.rows == 0) return ZG_OK;
+        if (int rc = check_ptr(loss, 4, false, "loss")) return rc;
+        if (int rc = check_ptr(logp, 4, true, "logp")) return rc;
+        a.loss = loss;
+        a.logp = logp;
+        return finish(zg::launch_policy(a, stream), "policy launch");
+    });
+}
+
+int zg_grads_init(const zg_grad *list, int64_t count, zg_grads **out)
+{
+    if (!out) return fail(ZG_ERR_INVALID_ARG, "out is NULL");
+    *out = nullptr;
+    return guarded([&]() -> int {
+        if (count < 0 || (count && !list)) return fail(ZG_ERR_INVALID_ARG, "list is NULL or count negative");
+        std::vector<zg::GradPart> parts;
+        for (int64_t i = 0; i < count; ++i) {
+            const zg_grad &g = list[i];
+            char what[48];
+            snprintf(what, sizeof what, "list[%lld]", (long long)i);
+            if (int rc = check_dtype(g.dtype, what)) return rc;
+            if (int rc = check_dtype(g.out_dtype, what)) return rc;
+            if (g.n < 0 || g.n >= (int64_t(1) << 40))
+                return fail(ZG_ERR_INVALID_ARG, "%s: n must be in [0, 2^40) (got %lld)", what, (long long)g.n);
+            if (g.n == 0) continue;
+            if (int rc = check_ptr(g.grad, element_size(g.dtype), false, what)) return rc;
+            if (int rc = check_ptr(g.out, element_size(g.out_dtype), false, what)) return rc;
+            if (g.grad == g.out && g.dtype != g.out_dtype)
+                return fail(ZG_ERR_INVALID_ARG, "%s: a gradient clipped in its own memory keeps its dtype", what);
+            for (int64_t at = 0; at < g.n; at += zg::kGradPart) {
+                zg::GradPart p{};
+                p.grad = static_cast<const char *>(g.grad) + at * element_size(g.dtype);
+                p.out = static_cast<char *>(g.out) + at * element_size(g.out_dtype);
+                p.n = int(g.n - at < zg::kGradPart ? g.n - at : zg::kGradPart);
+                p.dtype = uint8_t(g.dtype);
+                p.out_dtype = uint8_t(g.out_dtype);
+                parts.push_back(p);
+            }
+        }
+        if (int rc = check_apart(list, count)) return rc;
+        if (parts.size() >= (size_t(1) << 31)) return fail(ZG_ERR_INVALID_ARG, "the list has too many elements");
+        zg_grads *g = new zg_grads();
+        g->parts = int64_t(parts.size());
+        const size_t bytes = parts.size() * sizeof(zg::GradPart);
+        cudaError_t e = cudaGetDevice(&g->device);
+        if (e == cudaSuccess) e = cudaMalloc(&g->d_parts, bytes ? bytes : 16);
+        if (e == cudaSuccess && bytes) e = cudaMemcpy(g->d_parts, parts.data(), bytes, cudaMemcpyHostToDevice);
+        // The copy may return before it is done on the device, and a stream of the caller's
+        // that does not wait for the default stream could overtake it.
+        if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
+        if (e != cudaSuccess) {
+            const int rc = e == cudaErrorMemoryAllocation
+                               ? fail(ZG_ERR_NO_MEMORY, "zg_grads_init: %zu bytes: %s", bytes, cudaGetErrorString(e))
+                               : finish(e, "zg_grads_init");
+            cudaGetLastError();
+            zg_grads_destroy(g);
+            return rc;
+        }
+        *out = g;
+        return ZG_OK;
+    });
+}
+
+void zg_grads_destroy(zg_grads *g)
+{
+    if (!g) return;
+    if (g->d_parts) cudaFree(g->d_parts);
+    delete g;
+}
+
+int64_t zg_grads_workspace(const zg_grads *g) { return g ? (g->parts + 2) / 2 * 16 : -1; }
+
+int zg_grads_norm(const zg_grads *grads, float scale, float *stats, void *work, int64_t work_bytes, zg_stream stream)
+{
+    return guarded([&]() -> int { return grads_call(grads, 1.0f, 0.0f, scale, stats, work, work_bytes, false, stream); });
+}
+
+int zg_grads_clip(const zg_grads *grads, float max_norm, float eps, float scale, float *stats, void *work,
+                  int64_t work_bytes, zg_stream stream)
+{
+    return guarded([&]() -> int { return grads_call(grads, max_norm, eps, scale, stats, work, work_bytes, true, stream); });
 }
 
 }  // extern "C"
