@@ -91,6 +91,21 @@ def test_gradient(n, vocab, width, kind, dtype, drow_dtype):
     assert torch.equal(got, again)
 
 
+@pytest.mark.parametrize("kind", ["zipf", "one", "two", "even"])
+@pytest.mark.parametrize("n,vocab,width", [(65536, 300000, 16), (65537, 511, 9), (150001, 40000, 8), (70000, 1, 16),
+                                           (300000, 1 << 20, 1), (9000, 1 << 24, 2)])
+def test_gradient_of_many_tokens(n, vocab, width, kind):
+    """Several tiles to a sorting block; more tokens than the filling blocks look through; tables of up to four
+    digits; runs of one token over thousands of tiles."""
+    d, tokens = rand((n, width), 21, torch.bfloat16), ids(n, vocab, 22, kind)
+    want, err = ref.embed_grad(d, tokens, vocab, 1.0)
+    got = zb.embed_grad(d.cuda(), tokens.cuda(), vocab, dtype=torch.float32)
+    ref.check(got, want, ref.stored(want, err, torch.float32), "gradient")
+    mine = torch.ones(vocab, width, device="cuda")
+    zb.embed_grad(d.cuda(), tokens.cuda(), vocab, add=mine, out=mine)
+    ref.check(mine, want + 1, ref.stored(want + 1, err + ref.ULP * (want + 1).abs(), torch.float32), "in place")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n,vocab,width", [(7, 50257, 8), (100, 997, 771), (3000, 300, 64)])
 def test_gradient_added_to_another(n, vocab, width, dtype):
