@@ -10,6 +10,13 @@
 // so a row takes one joint sum of three values. Of the weights' gradients
 // dw2 = Q = sum dn xh, and with P = sum of dX oh over a gate's rows, dgate = w1 P
 // and dw1 = sum over gates of gate P: two sums to a column.
+//
+// Bound by memory: forward reads two rows and writes two, backward reads four and
+// writes two, of which each is moved once. A team of warps works on a row; it copies its next
+// rows into shared memory while it computes (cp.async: an aligned row's units are
+// copied and read by the same thread, so they need no barrier), and goes over the
+// row in shared memory again where a sum has to be known first.
+#include "zg_launch.h"
 #include "zg_ops.h"
 #include "zg_rows.cuh"
 
@@ -17,53 +24,28 @@ namespace zg {
 namespace {
 
 constexpr int kMost = 512;     // threads of a block
-constexpr int kBlocks = 304;   // blocks that share the rows of the backward pass
+constexpr int kBlocks = 152;   // blocks that share the rows of backward, one to an SM
+constexpr int kStages = 4;     // rows of a team in shared memory, at most
+constexpr int kTeams = 8;      // of a block, at most
 
-// VEC neighbouring elements, `n` of which are there.
-template <class T, int VEC>
-__device__ __forceinline__ void load(const T *p, int n, float (&v)[VEC])
+__device__ __forceinline__ void copy16(uint32_t to, const void *from)
 {
-    if constexpr (VEC == 1) {
-        v[0] = n > 0 ? load1(p) : 0.0f;
-    } else {
-        if (n >= VEC) {
-            Unit<T> u;
-            u.w = *reinterpret_cast<const uint4 *>(p);
-            float2 f[VEC / 2];
-            u.get(f);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] = i & 1 ? f[i / 2].y : f[i / 2].x;
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] = i < n ? load1(p + i) : 0.0f;
-        }
-    }
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
-template <class T, int VEC>
-__device__ __forceinline__ void store(T *p, int n, const float (&v)[VEC])
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest `later` groups are here.
+__device__ __forceinline__ void wait_copies(int later)
 {
-    if constexpr (VEC == 1) {
-        if (n > 0) store1(p, v[0]);
-    } else {
-        if (n >= VEC) {
-            float2 f[VEC / 2];
-#pragma unroll
-            for (int i = 0; i < VEC / 2; ++i) f[i] = make_float2(v[2 * i], v[2 * i + 1]);
-            Unit<T> u;
-            u.set(f);
-            *reinterpret_cast<uint4 *>(p) = u.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                if (i < n) store1(p + i, v[i]);
-        }
-    }
+    if (later == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (later == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    if (later == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    if (later >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
 
 // The threads that share a row: whole warps of a block.
 struct Team {
-    int id, count;       // of the block's teams
-    int tid, threads;    // of the team's threads
+    int id, count;     // of the block's teams
+    int tid, threads;  // of the team's threads
     int parity = 0;
     __device__ __forceinline__ Team(int team_threads)
     {
@@ -72,8 +54,16 @@ struct Team {
         id = threadIdx.x / team_threads;
         tid = threadIdx.x - id * team_threads;
     }
+    __device__ __forceinline__ void sync() const
+    {
+        if (threads == 32)
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
+    }
     // Sums over the team, the same in all of its threads. Two buffers, so that one
-    // barrier is enough: nobody is two sums ahead of another.
+    // barrier is enough: nobody is two sums ahead of another. A team has 16 places of each,
+    // those that it has no warp for zero, which are read all at once.
     template <int N>
     __device__ __forceinline__ void sum(float (&v)[N], float *sh)
     {
@@ -82,102 +72,319 @@ struct Team {
 #pragma unroll
             for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
         if (threads == 32) return;
-        float *const mine = sh + parity * (kMost / 32 * N) + id * (threads / 32) * N;
+        float *const mine = sh + (id * 2 + parity) * (kMost / 32 * N);
         parity ^= 1;
         if (tid % 32 == 0)
 #pragma unroll
-            for (int i = 0; i < N; ++i) mine[tid / 32 * N + i] = v[i];
-        asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
+            for (int i = 0; i < N; ++i) mine[i * (kMost / 32) + tid / 32] = v[i];
+        sync();
+        // a lane takes its half's place of one value, and 16 lanes add up
+        float x[(N + 1) / 2];
+        const int lane = tid % 32;
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = 0.0f;
-        for (int w = 0; w < threads / 32; ++w)
+        for (int i = 0; i < (N + 1) / 2; ++i) x[i] = mine[min(2 * i + lane / 16, N - 1) * 16 + lane % 16];
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += mine[w * N + i];
+        for (int o = 8; o; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < (N + 1) / 2; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, x[i / 2], i % 2 * 16);
+    }
+};
+// Before the first sum.
+template <int N>
+__device__ __forceinline__ void clear_sums(float *sh)
+{
+    for (int i = threadIdx.x; i < N; i += blockDim.x) sh[i] = 0.0f;
+    __syncthreads();
+}
+
+// How a block's teams keep rows in shared memory: `stages` of them, each of some tensors
+// whose rows take `slot` bytes. Without stages rows are read from memory itself.
+struct Ring {
+    int stages, slot;
+};
+
+// A thread has K chunks of E columns: chunk k is VEC = E neighbouring columns of a row whose
+// tensors all lie on 16 bytes, or (VEC = 1) E columns one team apart.
+template <int VEC, int E>
+__device__ __forceinline__ int column(const Team &team, int k, int i)
+{
+    return VEC == 1 ? team.tid + (k * E + i) * team.threads : (team.tid + k * team.threads) * VEC + i;
+}
+
+__device__ __forceinline__ float2 pair(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float total(float2 v) { return v.x + v.y; }
+
+// The rows of one tensor as a team reads them.
+template <class T, int VEC, int E>
+struct Source {
+    const T *ptr;
+    int64_t stride;
+    uint32_t at;  // shared address of the team's first stage; stages are `step` bytes apart
+    int step;
+    __device__ __forceinline__ Source(const RowsView &v, uint32_t first, int tensor, const Ring &ring, int tensors)
+        : ptr(static_cast<const T *>(v.ptr)), stride(v.stride), at(first + tensor * ring.slot), step(ring.slot * tensors)
+    {
+    }
+    __device__ __forceinline__ int head(int64_t r) const  // elements between a 16-byte boundary and the row
+    {
+        return VEC == 1 ? int((reinterpret_cast<uintptr_t>(ptr + r * stride) & 15u) / sizeof(T)) : 0;
+    }
+    // Row r on its way into a stage. Of aligned rows a thread copies what it reads itself.
+    template <int K>
+    __device__ __forceinline__ void copy(const Team &team, int64_t r, int stage, int width) const
+    {
+        const T *const row = ptr + r * stride;
+        const uint32_t to = at + stage * step;
+        if constexpr (VEC == 1) {
+            constexpr int N = Unit<T>::kN;
+            const int h = head(r), units = (h + width + N - 1) / N;
+            for (int u = team.tid; u < units; u += team.threads) copy16(to + u * 16, reinterpret_cast<const char *>(row - h) + u * 16);
+        } else {
+            const T *const mine = row + team.tid * VEC;
+            const uint32_t there = to + team.tid * 16;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (column<VEC, E>(team, k, 0) < width) copy16(there + k * team.threads * 16, mine + k * team.threads * VEC);
+        }
+    }
+    // Chunk k of row r. Columns past the width are column 0 again, or (behind a row's end in its last
+    // unit) zero.
+    __device__ __forceinline__ void get(const Team &team, int64_t r, int stage, bool staged, int k, int width,
+                                        float2 (&v)[E / 2]) const
+    {
+        if constexpr (VEC == 1) {
+            const int h = staged ? head(r) : 0;
+            float e[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const int c = column<VEC, E>(team, k, i), at_c = c < width ? c : 0;
+                if (!staged) {
+                    e[i] = load1(ptr + r * stride + at_c);
+                } else if constexpr (sizeof(T) == 2) {
+                    uint16_t w;
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(at + stage * step + (h + at_c) * 2));
+                    e[i] = __uint_as_float(uint32_t(w) << 16);
+                } else {
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(e[i]) : "r"(at + stage * step + (h + at_c) * 4));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) v[i] = make_float2(e[2 * i], e[2 * i + 1]);
+        } else {
+            const int c = column<VEC, E>(team, k, 0), at_c = c < width ? c : 0;
+            Unit<T> u;
+            if (!staged)
+                u.w = *reinterpret_cast<const uint4 *>(ptr + r * stride + at_c);
+            else
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(u.w.x), "=r"(u.w.y), "=r"(u.w.z), "=r"(u.w.w)
+                             : "r"(at + stage * step + at_c * int(sizeof(T))));
+            u.get(v);
+            if (at_c + VEC > width) {
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) {
+                    if (at_c + 2 * i >= width) v[i].x = 0.0f;
+                    if (at_c + 2 * i + 1 >= width) v[i].y = 0.0f;
+                }
+            }
+        }
     }
 };
 
-template <class T>
-__device__ __forceinline__ const T *row_of(const RowsView &v, int64_t r)
+// Chunk k of a row of an output.
+template <class T, int VEC, int E>
+__device__ __forceinline__ void store(const Team &team, T *row, int k, int width, const float2 (&v)[E / 2])
 {
-    return static_cast<const T *>(v.ptr) + r * v.stride;
+    if constexpr (VEC != 1) {
+        const int c = column<VEC, E>(team, k, 0);
+        if (c + VEC <= width) {
+            Unit<T> u;
+            u.set(v);
+            *reinterpret_cast<uint4 *>(row + c) = u.w;
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const int c = column<VEC, E>(team, k, i);
+        if (c < width) store1(row + c, i & 1 ? v[i / 2].y : v[i / 2].x);
+    }
 }
 template <class T>
 __device__ __forceinline__ T *out_row(const RowsView &v, int64_t r)
 {
     return static_cast<T *>(v.ptr) + r * v.stride;
 }
-// A weight's unit at column c, or ones.
-template <class T, int VEC>
-__device__ __forceinline__ void weight(const void *w, int64_t at, int n, float (&v)[VEC])
+
+// A thread's columns of a weight: ones without one, zeros past the width.
+template <class T, int VEC, int E, int K>
+__device__ __forceinline__ void weights(const void *w, int64_t at, const Team &team, int width, float2 (&v)[K][E / 2])
 {
-    if (w) {
-        load<T, VEC>(static_cast<const T *>(w) + at, n, v);
-        return;
-    }
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = 1.0f;
+    for (int k = 0; k < K; ++k) {
+        float e[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int c = column<VEC, E>(team, k, i);
+            e[i] = c >= width ? 0.0f : w ? load1(static_cast<const T *>(w) + at + c) : 1.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) v[k][i] = make_float2(e[2 * i], e[2 * i + 1]);
+    }
 }
 
-template <class T, int VEC, int K>
-__global__ void __launch_bounds__(kMost) forward_kernel(BlockArgs a, int team_threads)
+// A weight of the block's, binary32 in shared memory, laid out so that a warp's loads of 16 bytes
+// are neighbours: of chunks of eight columns the first halves come before the second ones.
+template <int VEC, int E>
+struct Wide {
+    uint32_t at;
+    int chunks;  // of a row
+    __device__ __forceinline__ static int size(int width) { return VEC == 1 ? (width + 3) / 4 * 4 : (width + VEC - 1) / VEC * VEC; }
+    __device__ __forceinline__ Wide(const float *p, int width)
+        : at(uint32_t(__cvta_generic_to_shared(p))), chunks(VEC == 1 ? 0 : (width + VEC - 1) / VEC)
+    {
+    }
+    __device__ __forceinline__ int index(int c) const
+    {
+        return VEC == 8 ? ((c % 8 / 4) * chunks + c / 8) * 4 + c % 4 : c;
+    }
+    __device__ __forceinline__ void get(const Team &team, int k, int width, float2 (&v)[E / 2]) const
+    {
+        if constexpr (VEC == 1) {
+            float e[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const int c = column<VEC, E>(team, k, i);
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(e[i]) : "r"(at + (c < width ? c : 0) * 4));
+                if (c >= width) e[i] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) v[i] = make_float2(e[2 * i], e[2 * i + 1]);
+        } else {
+            const int n = team.tid + k * team.threads, chunk = n < chunks ? n : 0;
+#pragma unroll
+            for (int h = 0; h < E / 4; ++h) {
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(v[2 * h].x), "=f"(v[2 * h].y), "=f"(v[2 * h + 1].x), "=f"(v[2 * h + 1].y)
+                             : "r"(at + (h * chunks + chunk) * 16));
+            }
+            if (n >= chunks)  // a chunk that is none of the row's counts for nothing
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) v[i] = make_float2(0.0f, 0.0f);
+        }
+    }
+};
+
+// A chunk's sum of squares, of the columns that are the row's.
+template <int VEC, int E>
+__device__ __forceinline__ float squares(const Team &team, int k, int width, const float2 (&v)[E / 2])
 {
-    __shared__ float sh[2 * kMost / 32];
+    float2 s = pair(0.0f);
+    if constexpr (VEC == 1) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const float x = i & 1 ? v[i / 2].y : v[i / 2].x;
+            sum = column<VEC, E>(team, k, i) < width ? fmaf(x, x, sum) : sum;
+        }
+        return sum;
+    } else {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) s = fma_f32x2(v[i], v[i], s);
+        return column<VEC, E>(team, k, 0) < width ? total(s) : 0.0f;
+    }
+}
+
+template <class T, int VEC, int E, int K>
+__global__ void __launch_bounds__(kMost, 1) forward_kernel(BlockArgs a, int team_threads, Ring ring)
+{
+    __shared__ __align__(16) float sh[kTeams * 2 * kMost / 32];
+    extern __shared__ __align__(16) char rows[];
     Team team(team_threads);
-    const int64_t r = int64_t(blockIdx.x) * team.count + team.id;
-    if (r >= a.rows) return;
-    const int64_t group = r / (a.rows / a.groups);
-    const int width = a.width;
-    float x[K][VEC], o[K][VEC];
-    float s[1] = {0.0f};
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = (team.tid + k * team.threads) * VEC;
-        load<T, VEC>(row_of<T>(a.x, r) + c, width - c, x[k]);
-        if (!a.o.ptr) continue;
-        load<T, VEC>(row_of<T>(a.o, r) + c, width - c, o[k]);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) s[0] = fmaf(o[k][i], o[k][i], s[0]);
-    }
-    float s1 = 1.0f;
-    if (a.w_post) {
-        team.sum<1>(s, sh);
-        s1 = 1.0f / sqrtf(s[0] / float(width) + a.eps);
-    }
-    s[0] = 0.0f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = (team.tid + k * team.threads) * VEC, n = width - c;
-        float w[VEC], g[VEC];
-        if (a.o.ptr) {
-            weight<T, VEC>(a.w_post, c, n, w);
-            weight<T, VEC>(a.gate, group * width + c, n, g);
+    clear_sums<kTeams * 2 * kMost / 32>(sh);
+    const int width = a.width, stages = ring.stages > 0 ? ring.stages : 1;
+    const bool staged = ring.stages > 0, block = a.o.ptr != nullptr;
+    const uint32_t mine = uint32_t(__cvta_generic_to_shared(rows)) + team.id * (2 * ring.slot * ring.stages);
+    const Source<T, VEC, E> x_in(a.x, mine, 0, ring, 2), o_in(a.o, mine, 1, ring, 2);
+    const int64_t teams = int64_t(gridDim.x) * team.count, each = (a.rows + teams - 1) / teams;
+    const int64_t lo = min((int64_t(blockIdx.x) * team.count + team.id) * each, a.rows), hi = min(lo + each, a.rows);
+    const int64_t in_group = a.rows / a.groups;
+    auto ask = [&](int64_t r, int stage) {
+        if (staged && r < hi) {
+            x_in.template copy<K>(team, r, stage, width);
+            if (block) o_in.template copy<K>(team, r, stage, width);
         }
+        commit_copies();
+    };
+    for (int i = 0; i < stages; ++i) ask(lo + i, i);
+    float2 u[K][E / 2], w2[K][E / 2];
+    weights<T, VEC, E, K>(a.w_pre, 0, team, width, w2);
+    int64_t next_group = lo;  // where u changes
+    const float mean = 1.0f / float(width);
+    int stage = 0;
+    for (int64_t r = lo; r < hi; ++r) {
+        if (r == next_group && block) {
+            const int64_t g = r / in_group;
+            float2 gate[K][E / 2];
+            weights<T, VEC, E, K>(a.w_post, 0, team, width, u);
+            weights<T, VEC, E, K>(a.gate, g * width, team, width, gate);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            x[k][i] *= a.res_scale;
-            if (a.o.ptr) x[k][i] = i < n ? fmaf(g[i] * w[i], o[k][i] * s1, x[k][i]) : 0.0f;
-            s[0] = fmaf(x[k][i], x[k][i], s[0]);
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) u[k][i] = mul_f32x2(u[k][i], gate[k][i]);
+            next_group = (g + 1) * in_group;
         }
-        if (a.x_new.ptr) store<T, VEC>(out_row<T>(a.x_new, r) + c, n, x[k]);
-    }
-    float s2 = 1.0f;
-    if (a.w_pre) {
-        team.sum<1>(s, sh);
-        s2 = 1.0f / sqrtf(s[0] / float(width) + a.eps);
+        wait_copies(stages - 1);
+        if (VEC == 1) team.sync();
+        float s[1] = {0.0f}, s1 = 1.0f, s2 = 1.0f;
+        float2 y[K][E / 2];
+        if (a.w_post) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float2 o[E / 2];
+                o_in.get(team, r, stage, staged, k, width, o);
+                s[0] += squares<VEC, E>(team, k, width, o);
+            }
+            team.sum<1>(s, sh);
+            s1 = rsqrtf(fmaf(s[0], mean, a.eps));
+            s[0] = 0.0f;
+        }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (team.tid + k * team.threads) * VEC, n = width - c;
-            float w[VEC];
-            weight<T, VEC>(a.w_pre, c, n, w);
+            float2 o[E / 2];
+            x_in.get(team, r, stage, staged, k, width, y[k]);
+            if (block) o_in.get(team, r, stage, staged, k, width, o);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) x[k][i] *= s2 * w[i];
-            store<T, VEC>(out_row<T>(a.n, r) + c, n, x[k]);
+            for (int i = 0; i < E / 2; ++i) {
+                y[k][i] = mul_f32x2(y[k][i], pair(a.res_scale));
+                if (block) y[k][i] = fma_f32x2(mul_f32x2(u[k][i], pair(s1)), o[i], y[k][i]);
+            }
+            s[0] += squares<VEC, E>(team, k, width, y[k]);
         }
+        if (VEC == 1) team.sync();  // the row has been read
+        ask(r + stages, stage);
+        if (a.x_new.ptr)
+#pragma unroll
+            for (int k = 0; k < K; ++k) store<T, VEC, E>(team, out_row<T>(a.x_new, r), k, width, y[k]);
+        if (a.w_pre) {
+            team.sum<1>(s, sh);
+            s2 = rsqrtf(fmaf(s[0], mean, a.eps));
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) y[k][i] = mul_f32x2(y[k][i], mul_f32x2(w2[k][i], pair(s2)));
+                store<T, VEC, E>(team, out_row<T>(a.n, r), k, width, y[k]);
+            }
+        }
+        if (a.kept && team.tid == 0) {
+            a.kept[r] = s1;
+            a.kept[a.rows + r] = s2;
+        }
+        stage = stage + 1 == stages ? 0 : stage + 1;
     }
-    if (a.kept && team.tid == 0) {
-        a.kept[r] = s1;
-        a.kept[a.rows + r] = s2;
-    }
+    wait_copies(0);
 }
 
 // How the rows are shared out: `segments` blocks to each gate, a block's teams taking
@@ -205,18 +412,18 @@ __host__ __device__ inline Shares shares_of(int64_t rows, int64_t groups)
 }
 
 // A thread's sums over its columns, added up over the block's teams in their order.
-template <int VEC, int K>
-__device__ __forceinline__ void hand_in(const Team &team, float (&v)[K][VEC], float *sh, float *out, int width)
+template <int VEC, int E, int K>
+__device__ __forceinline__ void hand_in(const Team &team, const float2 (&v)[K][E / 2], float *sh, float *out, int width)
 {
     for (int t = 0; t < team.count; ++t) {
         if (team.id == t) {
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const int c = (team.tid + k * team.threads) * VEC + i;
+                for (int i = 0; i < E; ++i) {
+                    const int c = column<VEC, E>(team, k, i);
                     if (c >= width) continue;
-                    const float sum = t ? sh[c] + v[k][i] : v[k][i];
+                    const float mine = i & 1 ? v[k][i / 2].y : v[k][i / 2].x, sum = t ? sh[c] + mine : mine;
                     if (t == team.count - 1)
                         out[c] = sum;
                     else
@@ -227,107 +434,221 @@ __device__ __forceinline__ void hand_in(const Team &team, float (&v)[K][VEC], fl
     }
 }
 
-template <class T, int VEC, int K>
-__global__ void __launch_bounds__(kMost) backward_kernel(BlockArgs a, int team_threads, Shares shares)
+// MANY: whole gates to a team (segments is 0), whose sums it finishes itself. ALL: every tensor and
+// weight is there, and rows are staged, which leaves a fifth of the instructions out.
+template <class T, int VEC, int E, int K, bool MANY, bool ALL>
+__global__ void __launch_bounds__(kMost, 1) backward_kernel(BlockArgs a, int team_threads, Ring ring, Shares shares)
 {
-    __shared__ float sh[6 * kMost / 32];
-    extern __shared__ float joint[];
+    __shared__ __align__(16) float sh[kTeams * 6 * kMost / 32];
+    extern __shared__ __align__(16) char rows[];
     Team team(team_threads);
-    const int width = a.width;
-    const int64_t in_group = a.rows / a.groups;
-    float q[K][VEC], p[K][VEC], dw1[K][VEC];
+    pdl_trigger();
+    clear_sums<kTeams * 6 * kMost / 32>(sh);
+    const int width = a.width, stages = ring.stages > 0 ? ring.stages : 1;
+    const bool staged = ALL || ring.stages > 0, block = ALL || a.o.ptr, has_n = ALL || a.w_pre, has_y = ALL || a.x_new.ptr,
+               has_w1 = ALL || a.w_post;
+    const uint32_t mine = uint32_t(__cvta_generic_to_shared(rows)) + team.id * (4 * ring.slot * ring.stages);
+    float *const wide = reinterpret_cast<float *>(rows + team.count * (4 * ring.slot * ring.stages));
+    const Wide<VEC, E> u_of(wide, width), w2_of(wide + Wide<VEC, E>::size(width), width);
+    const Source<T, VEC, E> x_in(a.x, mine, 0, ring, 4), o_in(a.o, mine, 1, ring, 4), dn_in(a.n, mine, 2, ring, 4),
+        y_in(a.x_new, mine, 3, ring, 4);
+    const int64_t in_group = a.rows / a.groups, group_step = int64_t(gridDim.x) * team.count;
+    // The team's rows, one after another: of one gate's segment every count-th, or all of
+    // every gate that is the team's.
+    struct At {
+        int64_t row, end, group;
+    } now;
+    if (MANY) {
+        now.group = int64_t(blockIdx.x) * team.count + team.id;
+        now.row = now.group * in_group;
+        now.end = now.group < a.groups ? now.row + in_group : now.row;
+    } else {
+        now.group = blockIdx.x / shares.segments;
+        const int64_t lo = (blockIdx.x - now.group * shares.segments) * shares.each;
+        now.end = now.group * in_group + min(lo + shares.each, in_group);
+        now.row = now.group * in_group + lo + team.id;
+    }
+    auto advance = [&](At &p) {
+        p.row += MANY ? 1 : team.count;
+        if (MANY && p.row >= p.end && p.group < a.groups) {
+            p.group += group_step;
+            p.row = p.group * in_group;
+            p.end = p.group < a.groups ? p.row + in_group : p.row;
+        }
+    };
+    At asked = now;
+    auto ask = [&](int stage) {
+        if (staged && asked.row < asked.end) {
+            x_in.template copy<K>(team, asked.row, stage, width);
+            if (block) o_in.template copy<K>(team, asked.row, stage, width);
+            if (has_n) dn_in.template copy<K>(team, asked.row, stage, width);
+            if (has_y) y_in.template copy<K>(team, asked.row, stage, width);
+            advance(asked);
+        }
+        commit_copies();
+    };
+    for (int i = 0; i < stages; ++i) ask(i);
+    constexpr int R = MANY ? K : 1;  // what a gate's change or end concerns is a team's own, in registers
+    float2 q[K][E / 2], p[K][E / 2], dw1[R][E / 2], u_here[R][E / 2], w2_here[R][E / 2];
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) q[k][i] = p[k][i] = dw1[k][i] = 0.0f;
-
-    auto one_row = [&](int64_t r, int64_t group) {
-        float xh[K][VEC], oh[K][VEC], e[K][VEC], y[K][VEC];
-        const float s1 = a.kept[r], s2 = a.kept[a.rows + r];
-        float s[3] = {0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < E / 2; ++i) q[k][i] = p[k][i] = pair(0.0f);
+    if constexpr (MANY) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = (team.tid + k * team.threads) * VEC, n = width - c;
-            float u[VEC], w[VEC], dn[VEC];
-            load<T, VEC>(row_of<T>(a.x, r) + c, n, xh[k]);
+        for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) oh[k][i] = y[k][i] = e[k][i] = 0.0f;
-            if (a.o.ptr) load<T, VEC>(row_of<T>(a.o, r) + c, n, oh[k]);
-            if (a.x_new.ptr) load<T, VEC>(row_of<T>(a.x_new, r) + c, n, y[k]);
-            weight<T, VEC>(a.w_post, c, n, u);
-            weight<T, VEC>(a.gate, group * width + c, n, w);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                u[i] *= w[i];
-                oh[k][i] *= s1;
-                xh[k][i] = fmaf(u[i], oh[k][i], a.res_scale * xh[k][i]) * s2;
-            }
-            if (a.w_pre) {
-                load<T, VEC>(row_of<T>(a.n, r) + c, n, dn);
-                weight<T, VEC>(a.w_pre, c, n, w);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    q[k][i] = fmaf(dn[i], xh[k][i], q[k][i]);
-                    e[k][i] = dn[i] * w[i];
-                    s[0] = fmaf(e[k][i], xh[k][i], s[0]);
-                }
-            }
-            if (a.w_post)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float uo = u[i] * oh[k][i];
-                    s[1] = fmaf(uo, fmaf(s2, e[k][i], y[k][i]), s[1]);
-                    s[2] = fmaf(uo, xh[k][i], s[2]);
-                }
+            for (int i = 0; i < E / 2; ++i) dw1[k][i] = pair(0.0f);
+        weights<T, VEC, E, K>(a.w_pre, 0, team, width, w2_here);
+    } else {
+        // gate w1 and w2 are the block's: in registers they cost a team its place beside another
+        for (int c = threadIdx.x; c < Wide<VEC, E>::size(width); c += blockDim.x) {
+            const bool in = c < width;
+            const float w1 = in && a.w_post ? load1(static_cast<const T *>(a.w_post) + c) : 1.0f;
+            const float g = in && a.gate ? load1(static_cast<const T *>(a.gate) + now.group * width + c) : 1.0f;
+            wide[u_of.index(c)] = in ? w1 * g : 0.0f;
+            (wide + Wide<VEC, E>::size(width))[w2_of.index(c)] = in ? (a.w_pre ? load1(static_cast<const T *>(a.w_pre) + c) : 1.0f) : 0.0f;
         }
-        team.sum<3>(s, sh);
-        const float mean = 1.0f / float(width), c2 = a.w_pre ? s[0] * mean : 0.0f;
-        const float c1 = a.w_post ? (s[1] - s2 * c2 * s[2]) * mean : 0.0f;
+        __syncthreads();
+    }
+    auto u_at = [&](int k, float2 (&v)[E / 2]) {
+        if constexpr (MANY) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = (team.tid + k * team.threads) * VEC, n = width - c;
-            float u[VEC], w[VEC], dx[VEC];
-            weight<T, VEC>(a.w_post, c, n, u);
-            weight<T, VEC>(a.gate, group * width + c, n, w);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float d = a.w_pre ? fmaf(s2, fmaf(-xh[k][i], c2, e[k][i]), y[k][i]) : y[k][i];
-                p[k][i] = fmaf(d, oh[k][i], p[k][i]);
-                dx[i] = a.res_scale * d;
-                e[k][i] = s1 * fmaf(u[i] * w[i], d, -oh[k][i] * c1);
-            }
-            store<T, VEC>(out_row<T>(a.dx, r) + c, n, dx);
-            if (a.o.ptr) store<T, VEC>(out_row<T>(a.d_o, r) + c, n, e[k]);
+            for (int i = 0; i < E / 2; ++i) v[i] = u_here[k][i];
+        } else {
+            u_of.get(team, k, width, v);
         }
     };
-
-    if (shares.segments) {
-        const int64_t group = blockIdx.x / shares.segments;
-        const int64_t lo = (blockIdx.x - group * shares.segments) * shares.each;
-        const int64_t hi = min(lo + shares.each, in_group);
-        for (int64_t i = lo + team.id; i < hi; i += team.count) one_row(group * in_group + i, group);
-    } else {
-        for (int64_t g = int64_t(blockIdx.x) * team.count + team.id; g < a.groups; g += int64_t(gridDim.x) * team.count) {
-            for (int64_t i = 0; i < in_group; ++i) one_row(g * in_group + i, g);
+    auto w2_at = [&](int k, float2 (&v)[E / 2]) {
+        if constexpr (MANY) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int c = (team.tid + k * team.threads) * VEC, n = width - c;
-                float w[VEC], gate[VEC];
-                weight<T, VEC>(a.w_post, c, n, w);
-                weight<T, VEC>(a.gate, g * width + c, n, gate);
+            for (int i = 0; i < E / 2; ++i) v[i] = w2_here[k][i];
+        } else {
+            w2_of.get(team, k, width, v);
+        }
+    };
+    const float mean = 1.0f / float(width);
+    float s1 = now.row < now.end ? a.kept[now.row] : 0.0f, s2 = now.row < now.end ? a.kept[a.rows + now.row] : 0.0f;
+    int64_t of = -1;  // the gate that u is of
+    int stage = 0;
+    while (now.row < now.end) {
+        if constexpr (MANY) {
+            if (now.group != of && block) {
+                float2 gate[K][E / 2];
+                weights<T, VEC, E, K>(a.w_post, 0, team, width, u_here);
+                weights<T, VEC, E, K>(a.gate, now.group * width, team, width, gate);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    dw1[k][i] = fmaf(gate[i], p[k][i], dw1[k][i]);
-                    w[i] *= p[k][i];
-                    p[k][i] = 0.0f;
-                }
-                if (a.dgate) store<T, VEC>(static_cast<T *>(a.dgate) + g * width + c, n, w);
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int i = 0; i < E / 2; ++i) u_here[k][i] = mul_f32x2(u_here[k][i], gate[k][i]);
             }
         }
+        of = now.group;
+        const int64_t r = now.row;
+        advance(now);
+        // of the row after this one, before they are needed
+        const float next1 = now.row < now.end ? a.kept[now.row] : 0.0f;
+        const float next2 = now.row < now.end ? a.kept[a.rows + now.row] : 0.0f;
+        wait_copies(stages - 1);
+        if (VEC == 1) team.sync();
+        // x' s2, o s1, dn and y of a chunk
+        auto chunk = [&](int k, float2 (&xh)[E / 2], float2 (&oh)[E / 2], float2 (&dn)[E / 2], float2 (&y)[E / 2],
+                         float2 (&u)[E / 2], float2 (&w2)[E / 2]) {
+            if (block) u_at(k, u);
+            if (has_n) w2_at(k, w2);
+            x_in.get(team, r, stage, staged, k, width, xh);
+            if (!ALL)
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) oh[i] = dn[i] = y[i] = pair(0.0f);
+            if (!block)
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) u[i] = pair(0.0f);
+            if (!has_n)
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) w2[i] = pair(0.0f);
+            if (block) o_in.get(team, r, stage, staged, k, width, oh);
+            if (has_n) dn_in.get(team, r, stage, staged, k, width, dn);
+            if (has_y) y_in.get(team, r, stage, staged, k, width, y);
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+                xh[i] = mul_f32x2(xh[i], pair(a.res_scale * s2));
+                if (block) {
+                    oh[i] = mul_f32x2(oh[i], pair(s1));
+                    xh[i] = fma_f32x2(mul_f32x2(u[i], pair(s2)), oh[i], xh[i]);
+                }
+            }
+        };
+        float s[3] = {0.0f, 0.0f, 0.0f};
+        if (has_n || has_w1) {
+            float2 sum[3] = {pair(0.0f), pair(0.0f), pair(0.0f)};
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float2 xh[E / 2], oh[E / 2], dn[E / 2], y[E / 2], u[E / 2], w2[E / 2];
+                chunk(k, xh, oh, dn, y, u, w2);
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) {
+                    q[k][i] = fma_f32x2(dn[i], xh[i], q[k][i]);
+                    const float2 e = mul_f32x2(dn[i], w2[i]), uo = mul_f32x2(u[i], oh[i]);
+                    sum[0] = fma_f32x2(e, xh[i], sum[0]);
+                    if (has_w1) {
+                        sum[1] = fma_f32x2(uo, fma_f32x2(pair(s2), e, y[i]), sum[1]);
+                        sum[2] = fma_f32x2(uo, xh[i], sum[2]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 3; ++i) s[i] = total(sum[i]);
+            team.sum<3>(s, sh);
+        }
+        const float c2 = has_n ? s[0] * mean : 0.0f, c1 = has_w1 ? (s[1] - s2 * c2 * s[2]) * mean : 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float2 xh[E / 2], oh[E / 2], dn[E / 2], y[E / 2], u[E / 2], w2[E / 2];
+            chunk(k, xh, oh, dn, y, u, w2);
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+                const float2 d = fma_f32x2(pair(s2), fma_f32x2(xh[i], pair(-c2), mul_f32x2(dn[i], w2[i])), y[i]);
+                p[k][i] = fma_f32x2(d, oh[i], p[k][i]);
+                xh[i] = mul_f32x2(d, pair(a.res_scale));
+                if (block) oh[i] = mul_f32x2(pair(s1), fma_f32x2(oh[i], pair(-c1), mul_f32x2(u[i], d)));
+            }
+            store<T, VEC, E>(team, out_row<T>(a.dx, r), k, width, xh);
+            if (block) store<T, VEC, E>(team, out_row<T>(a.d_o, r), k, width, oh);
+        }
+        if (VEC == 1) team.sync();  // the row has been read
+        ask(stage);
+        stage = stage + 1 == stages ? 0 : stage + 1;
+        s1 = next1;
+        s2 = next2;
+        if constexpr (MANY) {
+            if (now.row < now.end && now.group == of) continue;
+            float2 w[K][E / 2], gate[K][E / 2];
+            weights<T, VEC, E, K>(a.w_post, 0, team, width, w);
+            weights<T, VEC, E, K>(a.gate, of * width, team, width, gate);
+            T *const dgate = static_cast<T *>(a.dgate) + of * width;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) {
+                    dw1[k][i] = fma_f32x2(gate[k][i], p[k][i], dw1[k][i]);
+                    w[k][i] = mul_f32x2(w[k][i], p[k][i]);
+                    p[k][i] = pair(0.0f);
+                    const int c0 = column<VEC, E>(team, k, 2 * i), c1 = column<VEC, E>(team, k, 2 * i + 1);
+                    if (c0 < width) store1(dgate + c0, w[k][i].x);
+                    if (c1 < width) store1(dgate + c1, w[k][i].y);
+                }
+        }
     }
-    if (a.w_pre) hand_in<VEC, K>(team, q, joint, a.work + int64_t(blockIdx.x) * width, width);
-    if (a.w_post || (a.gate && shares.segments))
-        hand_in<VEC, K>(team, shares.segments ? p : dw1, joint, a.work + (shares.blocks + blockIdx.x) * width, width);
+    wait_copies(0);
+    __syncthreads();  // the rows' memory is free
+    float *const joint = reinterpret_cast<float *>(rows);
+    float *const out = a.work + int64_t(blockIdx.x) * width;
+    if (a.w_pre) hand_in<VEC, E, K>(team, q, joint, out, width);
+    if constexpr (MANY) {
+        if (a.w_post) hand_in<VEC, E, K>(team, dw1, joint, out + shares.blocks * width, width);
+    } else {
+        if (a.w_post || a.gate) hand_in<VEC, E, K>(team, p, joint, out + shares.blocks * width, width);
+    }
 }
 
 // The sums of the weights' gradients over the blocks.
@@ -335,6 +656,7 @@ template <class T>
 __global__ void __launch_bounds__(512) weights_kernel(BlockArgs a, Shares shares)
 {
     __shared__ float sh[16][33];
+    pdl_wait();
     const int lane = threadIdx.x % 32, row = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
     const bool there = c < a.width;
     auto total = [&](float v) {
@@ -389,52 +711,84 @@ bool whole(const RowsView &v, int size)
 {
     return (reinterpret_cast<uintptr_t>(v.ptr) | uintptr_t(v.stride * size)) % 16 == 0;
 }
-bool aligned(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // Every row of every tensor starts on 16 bytes.
 bool in_units(const BlockArgs &a, bool backward)
 {
     const int size = a.dtype == ZG_DTYPE_BF16 ? 2 : 4;
-    bool ok = whole(a.x, size) && whole(a.o, size) && whole(a.x_new, size) && whole(a.n, size) && aligned(a.w_post) &&
-              aligned(a.w_pre) && aligned(a.gate) && (a.groups == 1 || a.width * size % 16 == 0);
-    if (backward) ok = ok && whole(a.dx, size) && whole(a.d_o, size) && aligned(a.dgate);
-    return ok;
+    const bool ok = whole(a.x, size) && whole(a.o, size) && whole(a.x_new, size) && whole(a.n, size);
+    return ok && (!backward || (whole(a.dx, size) && whole(a.d_o, size)));
 }
 
-int team_of(int width, int vec, int k) { return ((width + vec * k - 1) / (vec * k) + 31) / 32 * 32; }
+// Threads of a team, teams of a block (an SM has one), and the rows that its shared memory holds.
+struct Shape {
+    int team, teams;
+    Ring ring;
+    size_t bytes;
+};
+Shape shape_of(const BlockArgs &a, int vec, int columns, int tensors, bool wide)
+{
+    const int size = a.dtype == ZG_DTYPE_BF16 ? 2 : 4;
+    Shape s;
+    s.team = ((a.width + columns - 1) / columns + 31) / 32 * 32;
+    s.teams = kMost / s.team;
+    if (s.teams > kTeams) s.teams = kTeams;
+    s.ring.slot = (a.width * size + (vec == 1 ? 16 : 0) + 15) / 16 * 16;
+    const size_t row = size_t(s.teams) * tensors * s.ring.slot;
+    const size_t beside = wide ? size_t(a.width + 7) / 8 * 64 : 0;  // two weights in binary32
+    s.ring.stages = int((size_t(224 * 1024) - beside) / row);
+    if (s.ring.stages > kStages) s.ring.stages = kStages;
+    s.bytes = row * s.ring.stages + beside;
+    const size_t joint = s.teams > 1 ? size_t(a.width) * 4 : 0;  // of the weights' sums
+    if (s.bytes < joint) s.bytes = joint;
+    return s;
+}
 
-template <class T, int VEC, int K>
+template <class F>
+cudaError_t allow(F *kernel, size_t bytes)
+{
+    return bytes > 46 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) : cudaSuccess;
+}
+
+template <class T, int VEC, int E, int K>
 cudaError_t forward(const BlockArgs &a, cudaStream_t st)
 {
-    const int team = team_of(a.width, VEC, K), teams = team >= 128 ? 1 : 128 / team;
-    const int64_t blocks = (a.rows + teams - 1) / teams;
-    if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
-    forward_kernel<T, VEC, K><<<unsigned(blocks), team * teams, 0, st>>>(a, team);
+    const Shape s = shape_of(a, VEC, E * K, 2, false);
+    auto *kernel = &forward_kernel<T, VEC, E, K>;
+    if (cudaError_t e = allow(kernel, s.bytes)) return e;
+    const int64_t want = (a.rows + s.teams - 1) / s.teams;
+    const int wave = wave_blocks(reinterpret_cast<const void *>(kernel), s.team * s.teams, s.bytes);
+    kernel<<<unsigned(want < wave ? want : wave), s.team * s.teams, s.bytes, st>>>(a, s.team, s.ring);
     return cudaGetLastError();
 }
 
-template <class T, int VEC, int K>
+template <class T, int VEC, int E, int K>
 cudaError_t backward(const BlockArgs &a, cudaStream_t st)
 {
-    const int team = team_of(a.width, VEC, K), teams = kMost / team > 8 ? 8 : kMost / team;
-    const Shares s = shares_of(a.rows, a.groups);
-    const size_t joint = teams > 1 ? size_t(a.width) * 4 : 0;
-    backward_kernel<T, VEC, K><<<unsigned(s.blocks), team * teams, joint, st>>>(a, team, s);
+    const Shares shares = shares_of(a.rows, a.groups);
+    const Shape s = shape_of(a, VEC, E * K, 4, shares.segments > 0);
+    const bool all = s.ring.stages > 0 && a.o.ptr && a.n.ptr && a.x_new.ptr && a.w_post;
+    auto *kernel = !shares.segments ? &backward_kernel<T, VEC, E, K, true, false>
+                   : all            ? &backward_kernel<T, VEC, E, K, false, true>
+                                    : &backward_kernel<T, VEC, E, K, false, false>;
+    if (cudaError_t e = allow(kernel, s.bytes)) return e;
+    kernel<<<unsigned(shares.blocks), s.team * s.teams, s.bytes, st>>>(a, s.team, s.ring, shares);
     if (cudaError_t e = cudaGetLastError()) return e;
-    if (a.w_pre || a.w_post || (a.gate && s.segments)) weights_kernel<T><<<(a.width + 31) / 32, 512, 0, st>>>(a, s);
-    return cudaGetLastError();
+    if (!a.w_pre && !a.w_post && !(a.gate && shares.segments)) return cudaSuccess;
+    return launch_dependent(&weights_kernel<T>, (a.width + 31) / 32, 512, 0, st, a, shares);
 }
 
 template <class T, bool BACK>
 cudaError_t of_type(const BlockArgs &a, cudaStream_t st)
 {
-#define ZG_CASE(VEC, K) \
-    if (a.width <= (VEC) * (K) * kMost) return BACK ? backward<T, VEC, K>(a, st) : forward<T, VEC, K>(a, st);
+    // chunks of E columns, K of them to a thread, and at most MOST threads to a row
+#define ZG_CASE(MOST, VEC, E, K) \
+    if (a.width <= (E) * (K) * (MOST)) return BACK ? backward<T, VEC, E, K>(a, st) : forward<T, VEC, E, K>(a, st);
     constexpr int N = Unit<T>::kN;
     if (in_units(a, BACK)) {
-        ZG_CASE(N, 1) ZG_CASE(N, 2) ZG_CASE(N, 4) ZG_CASE(N, 8)
+        ZG_CASE(256, N, N, 8 / N) ZG_CASE(kMost, N, N, 16 / N) ZG_CASE(kMost, N, N, 32 / N)
     } else {
-        ZG_CASE(1, 2) ZG_CASE(1, 8) ZG_CASE(1, 32)
+        ZG_CASE(kMost, 1, 8, 1) ZG_CASE(kMost, 1, 8, 2) ZG_CASE(kMost, 1, 8, 4)
     }
 #undef ZG_CASE
     return cudaErrorInvalidValue;
