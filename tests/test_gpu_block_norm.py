@@ -144,6 +144,30 @@ def test_rows_apart_and_in_place(d, pad, offset, dtype):
         assert bool((whole[:-1, d:] == 7.0).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [511, 512, 513, 1021, 1024, 2047, 2048, 4095, 4096, 4100, 8191, 12000, 16383])
+def test_widths_that_fill_a_team_at_any_alignment(d, dtype):
+    """Rows one element apart from their neighbours, NaN between them, at widths of whole teams and one off."""
+    n = 11
+    c, up = make(n, d, dtype, seed=70)
+    fwd, back = formulas(c, up, DT[dtype])
+    k, u = cuda(c), cuda(up)
+
+    def apart(t):
+        flat = torch.full((n * (d + 1) + 1,), math.nan, dtype=t.dtype, device="cuda")
+        view = flat[1:].view(n, d + 1)[:, :d]
+        view.copy_(t)
+        return view
+
+    x, k["o"] = apart(k.pop("x")), apart(k["o"])
+    u = {name: apart(t) for name, t in u.items()}
+    x_new, nn, kept = zb.block_norm(x, **k, res_scale=R, eps=EPS, keep=True)
+    held(x_new, fwd["x_new"], "x_new")
+    held(nn, fwd["n"], "n")
+    for g, w, name in zip(zb.block_norm_grad(x, kept, **u, **k, res_scale=R, eps=EPS), back, NAMES):
+        held(g, w, name)
+
+
 def test_more_dimensions_and_a_gate_of_one():
     c, up = make(24, 48, "f32", seed=80)
     k, u = cuda(c), cuda(up)

@@ -106,18 +106,21 @@ struct Ring {
 };
 
 // A thread has K chunks of E columns: chunk k is VEC = E neighbouring columns of a row whose
-// tensors all lie on 16 bytes, or (VEC = 1) E columns one team apart.
-template <int VEC, int E>
+// tensors all lie on 16 bytes, or (VEC = 1) E columns one team apart. With TEAM, the
+// team's size is known, and a row in shared memory has zeros behind it up to the last column of
+// the team, so that nothing but the stores asks whether a column is the row's.
+template <int VEC, int E, int TEAM>
 __device__ __forceinline__ int column(const Team &team, int k, int i)
 {
-    return VEC == 1 ? team.tid + (k * E + i) * team.threads : (team.tid + k * team.threads) * VEC + i;
+    const int threads = TEAM ? TEAM : team.threads;
+    return VEC == 1 ? team.tid + (k * E + i) * threads : (team.tid + k * threads) * VEC + i;
 }
 
 __device__ __forceinline__ float2 pair(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float total(float2 v) { return v.x + v.y; }
 
 // The rows of one tensor as a team reads them.
-template <class T, int VEC, int E>
+template <class T, int VEC, int E, int K, int TEAM>
 struct Source {
     const T *ptr;
     int64_t stride;
@@ -132,7 +135,6 @@ struct Source {
         return VEC == 1 ? int((reinterpret_cast<uintptr_t>(ptr + r * stride) & 15u) / sizeof(T)) : 0;
     }
     // Row r on its way into a stage. Of aligned rows a thread copies what it reads itself.
-    template <int K>
     __device__ __forceinline__ void copy(const Team &team, int64_t r, int stage, int width) const
     {
         const T *const row = ptr + r * stride;
@@ -140,40 +142,58 @@ struct Source {
         if constexpr (VEC == 1) {
             constexpr int N = Unit<T>::kN;
             const int h = head(r), units = (h + width + N - 1) / N;
-            for (int u = team.tid; u < units; u += team.threads) copy16(to + u * 16, reinterpret_cast<const char *>(row - h) + u * 16);
+            const char *const from = reinterpret_cast<const char *>(row - h);
+            for (int u = team.tid; u < units; u += TEAM ? TEAM : team.threads) copy16(to + u * 16, from + u * 16);
         } else {
             const T *const mine = row + team.tid * VEC;
             const uint32_t there = to + team.tid * 16;
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (column<VEC, E>(team, k, 0) < width) copy16(there + k * team.threads * 16, mine + k * team.threads * VEC);
+                if (column<VEC, E, TEAM>(team, k, 0) < width) copy16(there + k * team.threads * 16, mine + k * team.threads * VEC);
         }
     }
-    // Chunk k of row r. Columns past the width are column 0 again, or (behind a row's end in its last
-    // unit) zero.
+    // Once its own copies are here, and before the team's barrier: zeros from a row's end on, over what
+    // its last unit has behind it and the unit after that, which an earlier row may have reached.
+    __device__ __forceinline__ void close(const Team &team, int64_t r, int stage, int width) const
+    {
+        if constexpr (TEAM != 0) {
+            constexpr int N = Unit<T>::kN;
+            const int end = head(r) + width, units = (end + N - 1) / N;
+            if (team.tid != (units - 1) % TEAM) return;  // the thread that copied the last unit
+            const uint32_t to = at + stage * step;
+            for (int i = end; i < (units + 1) * N; ++i) {
+                if constexpr (sizeof(T) == 2)
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + i * 2), "h"(uint16_t(0)) : "memory");
+                else
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + i * 4), "r"(0u) : "memory");
+            }
+        }
+    }
+    // Chunk k of row r. Without TEAM, columns past the width are column 0 again, or (behind a row's end in its
+    // last unit) zero.
     __device__ __forceinline__ void get(const Team &team, int64_t r, int stage, bool staged, int k, int width,
                                         float2 (&v)[E / 2]) const
     {
         if constexpr (VEC == 1) {
-            const int h = staged ? head(r) : 0;
+            const uint32_t row = at + stage * step + head(r) * uint32_t(sizeof(T));
             float e[E];
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const int c = column<VEC, E>(team, k, i), at_c = c < width ? c : 0;
-                if (!staged) {
+                const int c = column<VEC, E, TEAM>(team, k, i), at_c = TEAM || c < width ? c : 0;
+                if (!TEAM && !staged) {
                     e[i] = load1(ptr + r * stride + at_c);
                 } else if constexpr (sizeof(T) == 2) {
                     uint16_t w;
-                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(at + stage * step + (h + at_c) * 2));
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(row + at_c * 2));
                     e[i] = __uint_as_float(uint32_t(w) << 16);
                 } else {
-                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(e[i]) : "r"(at + stage * step + (h + at_c) * 4));
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(e[i]) : "r"(row + at_c * 4));
                 }
             }
 #pragma unroll
             for (int i = 0; i < E / 2; ++i) v[i] = make_float2(e[2 * i], e[2 * i + 1]);
         } else {
-            const int c = column<VEC, E>(team, k, 0), at_c = c < width ? c : 0;
+            const int c = column<VEC, E, TEAM>(team, k, 0), at_c = c < width ? c : 0;
             Unit<T> u;
             if (!staged)
                 u.w = *reinterpret_cast<const uint4 *>(ptr + r * stride + at_c);
@@ -194,11 +214,11 @@ struct Source {
 };
 
 // Chunk k of a row of an output.
-template <class T, int VEC, int E>
+template <class T, int VEC, int E, int TEAM>
 __device__ __forceinline__ void store(const Team &team, T *row, int k, int width, const float2 (&v)[E / 2])
 {
     if constexpr (VEC != 1) {
-        const int c = column<VEC, E>(team, k, 0);
+        const int c = column<VEC, E, TEAM>(team, k, 0);
         if (c + VEC <= width) {
             Unit<T> u;
             u.set(v);
@@ -208,8 +228,8 @@ __device__ __forceinline__ void store(const Team &team, T *row, int k, int width
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-        const int c = column<VEC, E>(team, k, i);
-        if (c < width) store1(row + c, i & 1 ? v[i / 2].y : v[i / 2].x);
+        const int c = column<VEC, E, TEAM>(team, k, i);
+        if ((TEAM && (k * E + i + 1) * TEAM <= width) || c < width) store1(row + c, i & 1 ? v[i / 2].y : v[i / 2].x);
     }
 }
 template <class T>
@@ -219,7 +239,7 @@ __device__ __forceinline__ T *out_row(const RowsView &v, int64_t r)
 }
 
 // A thread's columns of a weight: ones without one, zeros past the width.
-template <class T, int VEC, int E, int K>
+template <class T, int VEC, int E, int K, int TEAM>
 __device__ __forceinline__ void weights(const void *w, int64_t at, const Team &team, int width, float2 (&v)[K][E / 2])
 {
 #pragma unroll
@@ -227,7 +247,7 @@ __device__ __forceinline__ void weights(const void *w, int64_t at, const Team &t
         float e[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            const int c = column<VEC, E>(team, k, i);
+            const int c = column<VEC, E, TEAM>(team, k, i);
             e[i] = c >= width ? 0.0f : w ? load1(static_cast<const T *>(w) + at + c) : 1.0f;
         }
 #pragma unroll
@@ -237,11 +257,14 @@ __device__ __forceinline__ void weights(const void *w, int64_t at, const Team &t
 
 // A weight of the block's, binary32 in shared memory, laid out so that a warp's loads of 16 bytes
 // are neighbours: of chunks of eight columns the first halves come before the second ones.
-template <int VEC, int E>
+template <int VEC, int E, int K, int TEAM>
 struct Wide {
     uint32_t at;
     int chunks;  // of a row
-    __device__ __forceinline__ static int size(int width) { return VEC == 1 ? (width + 3) / 4 * 4 : (width + VEC - 1) / VEC * VEC; }
+    __host__ __device__ __forceinline__ static int size(int width)
+    {
+        return TEAM ? TEAM * E * K : VEC == 1 ? (width + 3) / 4 * 4 : (width + VEC - 1) / VEC * VEC;
+    }
     __device__ __forceinline__ Wide(const float *p, int width)
         : at(uint32_t(__cvta_generic_to_shared(p))), chunks(VEC == 1 ? 0 : (width + VEC - 1) / VEC)
     {
@@ -256,9 +279,9 @@ struct Wide {
             float e[E];
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const int c = column<VEC, E>(team, k, i);
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(e[i]) : "r"(at + (c < width ? c : 0) * 4));
-                if (c >= width) e[i] = 0.0f;
+                const int c = column<VEC, E, TEAM>(team, k, i);
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(e[i]) : "r"(at + (TEAM || c < width ? c : 0) * 4));
+                if (!TEAM && c >= width) e[i] = 0.0f;
             }
 #pragma unroll
             for (int i = 0; i < E / 2; ++i) v[i] = make_float2(e[2 * i], e[2 * i + 1]);
@@ -278,49 +301,57 @@ struct Wide {
 };
 
 // A chunk's sum of squares, of the columns that are the row's.
-template <int VEC, int E>
+template <int VEC, int E, int TEAM>
 __device__ __forceinline__ float squares(const Team &team, int k, int width, const float2 (&v)[E / 2])
 {
     float2 s = pair(0.0f);
-    if constexpr (VEC == 1) {
+    if constexpr (VEC == 1 && !TEAM) {
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < E; ++i) {
             const float x = i & 1 ? v[i / 2].y : v[i / 2].x;
-            sum = column<VEC, E>(team, k, i) < width ? fmaf(x, x, sum) : sum;
+            sum = column<VEC, E, TEAM>(team, k, i) < width ? fmaf(x, x, sum) : sum;
         }
         return sum;
     } else {
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) s = fma_f32x2(v[i], v[i], s);
-        return column<VEC, E>(team, k, 0) < width ? total(s) : 0.0f;
+        return TEAM || column<VEC, E, TEAM>(team, k, 0) < width ? total(s) : 0.0f;
     }
 }
 
-template <class T, int VEC, int E, int K>
+// Shared memory cleared, so that with TEAM there are zeros behind every row.
+__device__ __forceinline__ void clear(char *p, int bytes)
+{
+    for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16) *reinterpret_cast<uint4 *>(p + i) = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+}
+
+template <class T, int VEC, int E, int K, int TEAM>
 __global__ void __launch_bounds__(kMost, 1) forward_kernel(BlockArgs a, int team_threads, Ring ring)
 {
     __shared__ __align__(16) float sh[kTeams * 2 * kMost / 32];
     extern __shared__ __align__(16) char rows[];
-    Team team(team_threads);
+    Team team(TEAM ? TEAM : team_threads);
+    if (TEAM) clear(rows, team.count * 2 * ring.slot * ring.stages);
     clear_sums<kTeams * 2 * kMost / 32>(sh);
     const int width = a.width, stages = ring.stages > 0 ? ring.stages : 1;
-    const bool staged = ring.stages > 0, block = a.o.ptr != nullptr;
+    const bool staged = TEAM || ring.stages > 0, block = a.o.ptr != nullptr;
     const uint32_t mine = uint32_t(__cvta_generic_to_shared(rows)) + team.id * (2 * ring.slot * ring.stages);
-    const Source<T, VEC, E> x_in(a.x, mine, 0, ring, 2), o_in(a.o, mine, 1, ring, 2);
+    const Source<T, VEC, E, K, TEAM> x_in(a.x, mine, 0, ring, 2), o_in(a.o, mine, 1, ring, 2);
     const int64_t teams = int64_t(gridDim.x) * team.count, each = (a.rows + teams - 1) / teams;
     const int64_t lo = min((int64_t(blockIdx.x) * team.count + team.id) * each, a.rows), hi = min(lo + each, a.rows);
     const int64_t in_group = a.rows / a.groups;
     auto ask = [&](int64_t r, int stage) {
         if (staged && r < hi) {
-            x_in.template copy<K>(team, r, stage, width);
-            if (block) o_in.template copy<K>(team, r, stage, width);
+            x_in.copy(team, r, stage, width);
+            if (block) o_in.copy(team, r, stage, width);
         }
         commit_copies();
     };
     for (int i = 0; i < stages; ++i) ask(lo + i, i);
     float2 u[K][E / 2], w2[K][E / 2];
-    weights<T, VEC, E, K>(a.w_pre, 0, team, width, w2);
+    weights<T, VEC, E, K, TEAM>(a.w_pre, 0, team, width, w2);
     int64_t next_group = lo;  // where u changes
     const float mean = 1.0f / float(width);
     int stage = 0;
@@ -328,8 +359,8 @@ __global__ void __launch_bounds__(kMost, 1) forward_kernel(BlockArgs a, int team
         if (r == next_group && block) {
             const int64_t g = r / in_group;
             float2 gate[K][E / 2];
-            weights<T, VEC, E, K>(a.w_post, 0, team, width, u);
-            weights<T, VEC, E, K>(a.gate, g * width, team, width, gate);
+            weights<T, VEC, E, K, TEAM>(a.w_post, 0, team, width, u);
+            weights<T, VEC, E, K, TEAM>(a.gate, g * width, team, width, gate);
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -337,7 +368,11 @@ __global__ void __launch_bounds__(kMost, 1) forward_kernel(BlockArgs a, int team
             next_group = (g + 1) * in_group;
         }
         wait_copies(stages - 1);
-        if (VEC == 1) team.sync();
+        if (VEC == 1) {
+            x_in.close(team, r, stage, width);
+            if (block) o_in.close(team, r, stage, width);
+            team.sync();
+        }
         float s[1] = {0.0f}, s1 = 1.0f, s2 = 1.0f;
         float2 y[K][E / 2];
         if (a.w_post) {
@@ -345,7 +380,7 @@ __global__ void __launch_bounds__(kMost, 1) forward_kernel(BlockArgs a, int team
             for (int k = 0; k < K; ++k) {
                 float2 o[E / 2];
                 o_in.get(team, r, stage, staged, k, width, o);
-                s[0] += squares<VEC, E>(team, k, width, o);
+                s[0] += squares<VEC, E, TEAM>(team, k, width, o);
             }
             team.sum<1>(s, sh);
             s1 = rsqrtf(fmaf(s[0], mean, a.eps));
@@ -361,13 +396,13 @@ __global__ void __launch_bounds__(kMost, 1) forward_kernel(BlockArgs a, int team
                 y[k][i] = mul_f32x2(y[k][i], pair(a.res_scale));
                 if (block) y[k][i] = fma_f32x2(mul_f32x2(u[k][i], pair(s1)), o[i], y[k][i]);
             }
-            s[0] += squares<VEC, E>(team, k, width, y[k]);
+            s[0] += squares<VEC, E, TEAM>(team, k, width, y[k]);
         }
         if (VEC == 1) team.sync();  // the row has been read
         ask(r + stages, stage);
         if (a.x_new.ptr)
 #pragma unroll
-            for (int k = 0; k < K; ++k) store<T, VEC, E>(team, out_row<T>(a.x_new, r), k, width, y[k]);
+            for (int k = 0; k < K; ++k) store<T, VEC, E, TEAM>(team, out_row<T>(a.x_new, r), k, width, y[k]);
         if (a.w_pre) {
             team.sum<1>(s, sh);
             s2 = rsqrtf(fmaf(s[0], mean, a.eps));
@@ -375,7 +410,7 @@ __global__ void __launch_bounds__(kMost, 1) forward_kernel(BlockArgs a, int team
             for (int k = 0; k < K; ++k) {
 #pragma unroll
                 for (int i = 0; i < E / 2; ++i) y[k][i] = mul_f32x2(y[k][i], mul_f32x2(w2[k][i], pair(s2)));
-                store<T, VEC, E>(team, out_row<T>(a.n, r), k, width, y[k]);
+                store<T, VEC, E, TEAM>(team, out_row<T>(a.n, r), k, width, y[k]);
             }
         }
         if (a.kept && team.tid == 0) {
@@ -412,7 +447,7 @@ __host__ __device__ inline Shares shares_of(int64_t rows, int64_t groups)
 }
 
 // A thread's sums over its columns, added up over the block's teams in their order.
-template <int VEC, int E, int K>
+template <int VEC, int E, int K, int TEAM>
 __device__ __forceinline__ void hand_in(const Team &team, const float2 (&v)[K][E / 2], float *sh, float *out, int width)
 {
     for (int t = 0; t < team.count; ++t) {
@@ -421,7 +456,7 @@ __device__ __forceinline__ void hand_in(const Team &team, const float2 (&v)[K][E
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
-                    const int c = column<VEC, E>(team, k, i);
+                    const int c = column<VEC, E, TEAM>(team, k, i);
                     if (c >= width) continue;
                     const float mine = i & 1 ? v[k][i / 2].y : v[k][i / 2].x, sum = t ? sh[c] + mine : mine;
                     if (t == team.count - 1)
@@ -434,23 +469,25 @@ __device__ __forceinline__ void hand_in(const Team &team, const float2 (&v)[K][E
     }
 }
 
-// MANY: whole gates to a team (segments is 0), whose sums it finishes itself. ALL: every tensor and
-// weight is there, and rows are staged, which leaves a fifth of the instructions out.
-template <class T, int VEC, int E, int K, bool MANY, bool ALL>
+// MANY: whole gates to a team (segments is 0), whose sums it finishes itself. ALL: every tensor of
+// rows is there and staged, which leaves a third of the instructions out.
+template <class T, int VEC, int E, int K, int TEAM, bool MANY, bool ALL>
 __global__ void __launch_bounds__(kMost, 1) backward_kernel(BlockArgs a, int team_threads, Ring ring, Shares shares)
 {
     __shared__ __align__(16) float sh[kTeams * 6 * kMost / 32];
     extern __shared__ __align__(16) char rows[];
-    Team team(team_threads);
+    static_assert(!TEAM || (ALL && !MANY), "a known team has all of its rows");
+    Team team(TEAM ? TEAM : team_threads);
     pdl_trigger();
+    if (TEAM) clear(rows, team.count * 4 * ring.slot * ring.stages);
     clear_sums<kTeams * 6 * kMost / 32>(sh);
     const int width = a.width, stages = ring.stages > 0 ? ring.stages : 1;
     const bool staged = ALL || ring.stages > 0, block = ALL || a.o.ptr, has_n = ALL || a.w_pre, has_y = ALL || a.x_new.ptr,
-               has_w1 = ALL || a.w_post;
+               has_w1 = a.w_post != nullptr;
     const uint32_t mine = uint32_t(__cvta_generic_to_shared(rows)) + team.id * (4 * ring.slot * ring.stages);
     float *const wide = reinterpret_cast<float *>(rows + team.count * (4 * ring.slot * ring.stages));
-    const Wide<VEC, E> u_of(wide, width), w2_of(wide + Wide<VEC, E>::size(width), width);
-    const Source<T, VEC, E> x_in(a.x, mine, 0, ring, 4), o_in(a.o, mine, 1, ring, 4), dn_in(a.n, mine, 2, ring, 4),
+    const Wide<VEC, E, K, TEAM> u_of(wide, width), w2_of(wide + Wide<VEC, E, K, TEAM>::size(width), width);
+    const Source<T, VEC, E, K, TEAM> x_in(a.x, mine, 0, ring, 4), o_in(a.o, mine, 1, ring, 4), dn_in(a.n, mine, 2, ring, 4),
         y_in(a.x_new, mine, 3, ring, 4);
     const int64_t in_group = a.rows / a.groups, group_step = int64_t(gridDim.x) * team.count;
     // The team's rows, one after another: of one gate's segment every count-th, or all of
@@ -479,10 +516,10 @@ __global__ void __launch_bounds__(kMost, 1) backward_kernel(BlockArgs a, int tea
     At asked = now;
     auto ask = [&](int stage) {
         if (staged && asked.row < asked.end) {
-            x_in.template copy<K>(team, asked.row, stage, width);
-            if (block) o_in.template copy<K>(team, asked.row, stage, width);
-            if (has_n) dn_in.template copy<K>(team, asked.row, stage, width);
-            if (has_y) y_in.template copy<K>(team, asked.row, stage, width);
+            x_in.copy(team, asked.row, stage, width);
+            if (block) o_in.copy(team, asked.row, stage, width);
+            if (has_n) dn_in.copy(team, asked.row, stage, width);
+            if (has_y) y_in.copy(team, asked.row, stage, width);
             advance(asked);
         }
         commit_copies();
@@ -499,15 +536,15 @@ __global__ void __launch_bounds__(kMost, 1) backward_kernel(BlockArgs a, int tea
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int i = 0; i < E / 2; ++i) dw1[k][i] = pair(0.0f);
-        weights<T, VEC, E, K>(a.w_pre, 0, team, width, w2_here);
+        weights<T, VEC, E, K, TEAM>(a.w_pre, 0, team, width, w2_here);
     } else {
         // gate w1 and w2 are the block's: in registers they cost a team its place beside another
-        for (int c = threadIdx.x; c < Wide<VEC, E>::size(width); c += blockDim.x) {
+        for (int c = threadIdx.x; c < Wide<VEC, E, K, TEAM>::size(width); c += blockDim.x) {
             const bool in = c < width;
             const float w1 = in && a.w_post ? load1(static_cast<const T *>(a.w_post) + c) : 1.0f;
             const float g = in && a.gate ? load1(static_cast<const T *>(a.gate) + now.group * width + c) : 1.0f;
             wide[u_of.index(c)] = in ? w1 * g : 0.0f;
-            (wide + Wide<VEC, E>::size(width))[w2_of.index(c)] = in ? (a.w_pre ? load1(static_cast<const T *>(a.w_pre) + c) : 1.0f) : 0.0f;
+            (wide + Wide<VEC, E, K, TEAM>::size(width))[w2_of.index(c)] = in ? (a.w_pre ? load1(static_cast<const T *>(a.w_pre) + c) : 1.0f) : 0.0f;
         }
         __syncthreads();
     }
@@ -535,8 +572,8 @@ __global__ void __launch_bounds__(kMost, 1) backward_kernel(BlockArgs a, int tea
         if constexpr (MANY) {
             if (now.group != of && block) {
                 float2 gate[K][E / 2];
-                weights<T, VEC, E, K>(a.w_post, 0, team, width, u_here);
-                weights<T, VEC, E, K>(a.gate, now.group * width, team, width, gate);
+                weights<T, VEC, E, K, TEAM>(a.w_post, 0, team, width, u_here);
+                weights<T, VEC, E, K, TEAM>(a.gate, now.group * width, team, width, gate);
 #pragma unroll
                 for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -550,7 +587,15 @@ __global__ void __launch_bounds__(kMost, 1) backward_kernel(BlockArgs a, int tea
         const float next1 = now.row < now.end ? a.kept[now.row] : 0.0f;
         const float next2 = now.row < now.end ? a.kept[a.rows + now.row] : 0.0f;
         wait_copies(stages - 1);
-        if (VEC == 1) team.sync();
+        if (VEC == 1) {
+            if (TEAM) {
+                x_in.close(team, r, stage, width);
+                o_in.close(team, r, stage, width);
+                dn_in.close(team, r, stage, width);
+                y_in.close(team, r, stage, width);
+            }
+            team.sync();
+        }
         // x' s2, o s1, dn and y of a chunk
         auto chunk = [&](int k, float2 (&xh)[E / 2], float2 (&oh)[E / 2], float2 (&dn)[E / 2], float2 (&y)[E / 2],
                          float2 (&u)[E / 2], float2 (&w2)[E / 2]) {
@@ -590,7 +635,7 @@ __global__ void __launch_bounds__(kMost, 1) backward_kernel(BlockArgs a, int tea
                     q[k][i] = fma_f32x2(dn[i], xh[i], q[k][i]);
                     const float2 e = mul_f32x2(dn[i], w2[i]), uo = mul_f32x2(u[i], oh[i]);
                     sum[0] = fma_f32x2(e, xh[i], sum[0]);
-                    if (has_w1) {
+                    if (ALL || has_w1) {
                         sum[1] = fma_f32x2(uo, fma_f32x2(pair(s2), e, y[i]), sum[1]);
                         sum[2] = fma_f32x2(uo, xh[i], sum[2]);
                     }
@@ -612,8 +657,8 @@ __global__ void __launch_bounds__(kMost, 1) backward_kernel(BlockArgs a, int tea
                 xh[i] = mul_f32x2(d, pair(a.res_scale));
                 if (block) oh[i] = mul_f32x2(pair(s1), fma_f32x2(oh[i], pair(-c1), mul_f32x2(u[i], d)));
             }
-            store<T, VEC, E>(team, out_row<T>(a.dx, r), k, width, xh);
-            if (block) store<T, VEC, E>(team, out_row<T>(a.d_o, r), k, width, oh);
+            store<T, VEC, E, TEAM>(team, out_row<T>(a.dx, r), k, width, xh);
+            if (block) store<T, VEC, E, TEAM>(team, out_row<T>(a.d_o, r), k, width, oh);
         }
         if (VEC == 1) team.sync();  // the row has been read
         ask(stage);
@@ -623,8 +668,8 @@ __global__ void __launch_bounds__(kMost, 1) backward_kernel(BlockArgs a, int tea
         if constexpr (MANY) {
             if (now.row < now.end && now.group == of) continue;
             float2 w[K][E / 2], gate[K][E / 2];
-            weights<T, VEC, E, K>(a.w_post, 0, team, width, w);
-            weights<T, VEC, E, K>(a.gate, of * width, team, width, gate);
+            weights<T, VEC, E, K, TEAM>(a.w_post, 0, team, width, w);
+            weights<T, VEC, E, K, TEAM>(a.gate, of * width, team, width, gate);
             T *const dgate = static_cast<T *>(a.dgate) + of * width;
 #pragma unroll
             for (int k = 0; k < K; ++k)
@@ -633,7 +678,7 @@ __global__ void __launch_bounds__(kMost, 1) backward_kernel(BlockArgs a, int tea
                     dw1[k][i] = fma_f32x2(gate[k][i], p[k][i], dw1[k][i]);
                     w[k][i] = mul_f32x2(w[k][i], p[k][i]);
                     p[k][i] = pair(0.0f);
-                    const int c0 = column<VEC, E>(team, k, 2 * i), c1 = column<VEC, E>(team, k, 2 * i + 1);
+                    const int c0 = column<VEC, E, TEAM>(team, k, 2 * i), c1 = column<VEC, E, TEAM>(team, k, 2 * i + 1);
                     if (c0 < width) store1(dgate + c0, w[k][i].x);
                     if (c1 < width) store1(dgate + c1, w[k][i].y);
                 }
@@ -643,11 +688,11 @@ __global__ void __launch_bounds__(kMost, 1) backward_kernel(BlockArgs a, int tea
     __syncthreads();  // the rows' memory is free
     float *const joint = reinterpret_cast<float *>(rows);
     float *const out = a.work + int64_t(blockIdx.x) * width;
-    if (a.w_pre) hand_in<VEC, E, K>(team, q, joint, out, width);
+    if (a.w_pre) hand_in<VEC, E, K, TEAM>(team, q, joint, out, width);
     if constexpr (MANY) {
-        if (a.w_post) hand_in<VEC, E, K>(team, dw1, joint, out + shares.blocks * width, width);
+        if (a.w_post) hand_in<VEC, E, K, TEAM>(team, dw1, joint, out + shares.blocks * width, width);
     } else {
-        if (a.w_post || a.gate) hand_in<VEC, E, K>(team, p, joint, out + shares.blocks * width, width);
+        if (a.w_post || a.gate) hand_in<VEC, E, K, TEAM>(team, p, joint, out + shares.blocks * width, width);
     }
 }
 
@@ -726,16 +771,17 @@ struct Shape {
     Ring ring;
     size_t bytes;
 };
-Shape shape_of(const BlockArgs &a, int vec, int columns, int tensors, bool wide)
+Shape shape_of(const BlockArgs &a, int vec, int columns, int team, int tensors, bool wide)
 {
     const int size = a.dtype == ZG_DTYPE_BF16 ? 2 : 4;
     Shape s;
-    s.team = ((a.width + columns - 1) / columns + 31) / 32 * 32;
+    s.team = team ? team : ((a.width + columns - 1) / columns + 31) / 32 * 32;
     s.teams = kMost / s.team;
     if (s.teams > kTeams) s.teams = kTeams;
-    s.ring.slot = (a.width * size + (vec == 1 ? 16 : 0) + 15) / 16 * 16;
+    const int held = team ? team * columns : a.width;  // columns of a stage
+    s.ring.slot = (held * size + (vec == 1 ? 48 : 0) + 15) / 16 * 16;  // a head, and two units that are cleared
     const size_t row = size_t(s.teams) * tensors * s.ring.slot;
-    const size_t beside = wide ? size_t(a.width + 7) / 8 * 64 : 0;  // two weights in binary32
+    const size_t beside = wide ? size_t(held + 7) / 8 * 64 : 0;  // two weights in binary32
     s.ring.stages = int((size_t(224 * 1024) - beside) / row);
     if (s.ring.stages > kStages) s.ring.stages = kStages;
     s.bytes = row * s.ring.stages + beside;
@@ -750,11 +796,11 @@ cudaError_t allow(F *kernel, size_t bytes)
     return bytes > 46 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) : cudaSuccess;
 }
 
-template <class T, int VEC, int E, int K>
+template <class T, int VEC, int E, int K, int TEAM>
 cudaError_t forward(const BlockArgs &a, cudaStream_t st)
 {
-    const Shape s = shape_of(a, VEC, E * K, 2, false);
-    auto *kernel = &forward_kernel<T, VEC, E, K>;
+    const Shape s = shape_of(a, VEC, E * K, TEAM, 2, false);
+    auto *kernel = &forward_kernel<T, VEC, E, K, TEAM>;
     if (cudaError_t e = allow(kernel, s.bytes)) return e;
     const int64_t want = (a.rows + s.teams - 1) / s.teams;
     const int wave = wave_blocks(reinterpret_cast<const void *>(kernel), s.team * s.teams, s.bytes);
@@ -762,15 +808,19 @@ cudaError_t forward(const BlockArgs &a, cudaStream_t st)
     return cudaGetLastError();
 }
 
-template <class T, int VEC, int E, int K>
+template <class T, int VEC, int E, int K, int TEAM>
 cudaError_t backward(const BlockArgs &a, cudaStream_t st)
 {
     const Shares shares = shares_of(a.rows, a.groups);
-    const Shape s = shape_of(a, VEC, E * K, 4, shares.segments > 0);
-    const bool all = s.ring.stages > 0 && a.o.ptr && a.n.ptr && a.x_new.ptr && a.w_post;
-    auto *kernel = !shares.segments ? &backward_kernel<T, VEC, E, K, true, false>
-                   : all            ? &backward_kernel<T, VEC, E, K, false, true>
-                                    : &backward_kernel<T, VEC, E, K, false, false>;
+    const bool all = a.o.ptr && a.n.ptr && a.x_new.ptr && shares.segments;
+    Shape s = shape_of(a, VEC, E * K, all ? TEAM : 0, 4, shares.segments > 0);
+    auto *kernel = &backward_kernel<T, VEC, E, K, 0, false, false>;
+    if (!shares.segments)
+        kernel = &backward_kernel<T, VEC, E, K, 0, true, false>;
+    else if (all && s.ring.stages > 0)
+        kernel = &backward_kernel<T, VEC, E, K, TEAM, false, true>;
+    else if (all && TEAM)
+        s = shape_of(a, VEC, E * K, 0, 4, true);
     if (cudaError_t e = allow(kernel, s.bytes)) return e;
     kernel<<<unsigned(shares.blocks), s.team * s.teams, s.bytes, st>>>(a, s.team, s.ring, shares);
     if (cudaError_t e = cudaGetLastError()) return e;
@@ -782,13 +832,14 @@ template <class T, bool BACK>
 cudaError_t of_type(const BlockArgs &a, cudaStream_t st)
 {
     // chunks of E columns, K of them to a thread, and at most MOST threads to a row
-#define ZG_CASE(MOST, VEC, E, K) \
-    if (a.width <= (E) * (K) * (MOST)) return BACK ? backward<T, VEC, E, K>(a, st) : forward<T, VEC, E, K>(a, st);
+#define ZG_CASE(MOST, VEC, E, K, TEAM) \
+    if (a.width <= (E) * (K) * (MOST)) return BACK ? backward<T, VEC, E, K, TEAM>(a, st) : forward<T, VEC, E, K, TEAM>(a, st);
     constexpr int N = Unit<T>::kN;
     if (in_units(a, BACK)) {
-        ZG_CASE(256, N, N, 8 / N) ZG_CASE(kMost, N, N, 16 / N) ZG_CASE(kMost, N, N, 32 / N)
+        ZG_CASE(256, N, N, 8 / N, 0) ZG_CASE(kMost, N, N, 16 / N, 0) ZG_CASE(kMost, N, N, 32 / N, 0)
     } else {
-        ZG_CASE(kMost, 1, 8, 1) ZG_CASE(kMost, 1, 8, 2) ZG_CASE(kMost, 1, 8, 4)
+        ZG_CASE(64, 1, 8, 1, 64) ZG_CASE(128, 1, 8, 1, 128) ZG_CASE(256, 1, 8, 1, 256) ZG_CASE(512, 1, 8, 1, 512)
+        ZG_CASE(kMost, 1, 8, 2, 0) ZG_CASE(kMost, 1, 8, 4, 0)
     }
 #undef ZG_CASE
     return cudaErrorInvalidValue;
