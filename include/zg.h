@@ -603,7 +603,7 @@ typedef struct {
 } zg_policy_args;
 
 /* The loss and logp of each row, and (NULL: not kept) what zg_policy_grad takes:
- * rows x 2 binary32, the row's largest logit and the sum of exp((z - it) / T). */
+ * rows x 3 binary32, the row's largest logit, the sum of exp((z - it) / T), and logp. */
 int zg_policy_loss(const zg_policy_args *args, float *loss, float *logp, float *kept, zg_stream stream);
 
 /* The gradient, from what zg_policy_loss kept for the same arguments. scale

@@ -66,9 +66,13 @@ def check_policy(z, tokens, old, adv, refl, temperature, clip=CLIP, kl=KL, seed=
     narrow = (how[0].clamp(-(1 << 31), (1 << 31) - 1).to(torch.int32), *how[1:])
     again = zb.policy_loss_grad(z, *narrow, 64.0, dloss.cuda())
     assert all(torch.equal(p, q) for p, q in zip(again, (one_loss, one_logp, one)))
+    # in the logits' own memory: the bits of another output's on the same memory (of a row that lies
+    # differently the sum is taken in another order)
     mine = z.clone()
+    want = zb.policy_loss_grad(mine, *how, 64.0, dloss.cuda())[2]
     zb.policy_loss_grad(mine, *how, 64.0, dloss.cuda(), out=mine)
-    assert torch.equal(mine, one)
+    assert torch.equal(mine, want)
+    ref.check(mine, grad, ref.stored(grad, e_grad, dt), "gradient in place")
     mine = z.clone()
     zb.policy_grad(mine, kept, *how, 64.0, dloss.cuda(), out=mine)
     assert torch.equal(mine, two)
@@ -248,7 +252,7 @@ def test_only_outputs_are_written(v, dtype):
     n, dt = 3, DT[dtype]
     z = logits_of(n, v, dt, 18)
     tokens, old, adv, refl = (t.cuda() for t in sample(z, 1.0, 19))
-    grad, loss, kept = Guarded(n * v, dt), Guarded(n, torch.float32), Guarded(2 * n, torch.float32)
+    grad, loss, kept = Guarded(n * v, dt), Guarded(n, torch.float32), Guarded(3 * n, torch.float32)
     a = zb._policy(z, tokens, old, adv, refl, CLIP, KL, 1.0)
     st = torch.cuda.current_stream().cuda_stream
     L = zb.lib()
@@ -265,7 +269,7 @@ def test_no_rows():
     z = torch.empty(0, 100, dtype=torch.bfloat16, device="cuda")
     t, f = torch.empty(0, dtype=torch.int64, device="cuda"), torch.empty(0, device="cuda")
     assert zb.token_logp(z, t)[0].shape == (0,)
-    assert zb.policy_loss(z, t, f, f)[2].shape == (0, 2)
+    assert zb.policy_loss(z, t, f, f)[2].shape == (0, 3)
     assert zb.policy_loss_grad(z, t, f, f)[2].shape == (0, 100)
 
 

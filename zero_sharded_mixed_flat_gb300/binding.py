@@ -1021,7 +1021,7 @@ def policy_loss(logits, tokens, old_logp, advantage, ref_logp=None, clip=(0.2, 0
         return _on(stream, logits, policy_loss, logits, tokens, old_logp, advantage, ref_logp, clip, kl, temperature)
     a = _policy(logits, tokens, old_logp, advantage, ref_logp, clip, kl, temperature)
     loss, logp = (torch.empty(a.rows, dtype=torch.float32, device=logits.device) for _ in range(2))
-    kept = torch.empty((a.rows, 2), dtype=torch.float32, device=logits.device)
+    kept = torch.empty((a.rows, 3), dtype=torch.float32, device=logits.device)
     _check(lib().zg_policy_loss(ctypes.byref(a), loss.data_ptr(), logp.data_ptr(), kept.data_ptr(), _stream_of(logits)),
            "zg_policy_loss")
     return loss, logp, kept
@@ -1036,7 +1036,7 @@ def policy_grad(logits, kept, tokens, old_logp, advantage, ref_logp=None, clip=(
                    scale, dloss, out)
     a = _policy(logits, tokens, old_logp, advantage, ref_logp, clip, kl, temperature)
     out = _gradient_of(logits, out)
-    _check(lib().zg_policy_grad(ctypes.byref(a), _side(kept, torch.float32, (a.rows, 2), logits, "kept"), scale,
+    _check(lib().zg_policy_grad(ctypes.byref(a), _side(kept, torch.float32, (a.rows, 3), logits, "kept"), scale,
                                 _side(dloss, torch.float32, (a.rows,), logits, "dloss"), out.data_ptr(), _row_stride(out),
                                 _stream_of(logits)), "zg_policy_grad")
     return out

@@ -1,0 +1,32 @@
+// zg_async.cuh -- copies from memory into shared memory that a thread does not wait
+// for, and teams: the warps of a block that share a row.
+#pragma once
+
+#include <stdint.h>
+
+namespace zg {
+
+__device__ __forceinline__ void copy16(uint32_t to, const void *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest `later` groups are here.
+__device__ __forceinline__ void wait_copies(int later)
+{
+    if (later == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (later == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    if (later == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    if (later >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+// Whole warps of a block, at most 15 teams of more than one.
+__device__ __forceinline__ void team_sync(int id, int threads)
+{
+    if (threads == 32)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
+}
+
+}  // namespace zg

@@ -16,6 +16,7 @@
 // rows into shared memory while it computes (cp.async: an aligned row's units are
 // copied and read by the same thread, so they need no barrier), and goes over the
 // row in shared memory again where a sum has to be known first.
+#include "zg_async.cuh"
 #include "zg_launch.h"
 #include "zg_ops.h"
 #include "zg_rows.cuh"
@@ -27,20 +28,6 @@ constexpr int kMost = 512;     // threads of a block
 constexpr int kBlocks = 152;   // blocks that share the rows of backward, one to an SM
 constexpr int kStages = 4;     // rows of a team in shared memory, at most
 constexpr int kTeams = 8;      // of a block, at most
-
-__device__ __forceinline__ void copy16(uint32_t to, const void *from)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but the newest `later` groups are here.
-__device__ __forceinline__ void wait_copies(int later)
-{
-    if (later == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (later == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    if (later == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    if (later >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
-}
 
 // The threads that share a row: whole warps of a block.
 struct Team {
@@ -56,10 +43,7 @@ struct Team {
     }
     __device__ __forceinline__ void sync() const
     {
-        if (threads == 32)
-            __syncwarp();
-        else
-            asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
+        team_sync(id, threads);
     }
     // Sums over the team, the same in all of its threads. Two buffers, so that one
     // barrier is enough: nobody is two sums ahead of another. A team has 16 places of each,

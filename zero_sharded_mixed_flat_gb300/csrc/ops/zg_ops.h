@@ -121,7 +121,7 @@ struct PolicyArgs {
     const float *old_logp, *advantage, *ref_logp;
     float clip_low, clip_high, kl, temperature;
     float *loss, *logp, *lse;  // written where not null
-    float *kept;               // rows x 2: written with the loss (or null)
+    float *kept;               // rows x 3: written with the loss (or null)
     const float *kept_in;      // the gradient alone starts from these
     float scale;
     const float *dloss;
