@@ -14,10 +14,16 @@ __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_
 // All but the newest `later` groups are here.
 __device__ __forceinline__ void wait_copies(int later)
 {
-    if (later == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (later == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    if (later == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    if (later >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    switch (later) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+    }
 }
 
 // Whole warps of a block, at most 15 teams of more than one.
