@@ -12,7 +12,6 @@ fails loudly.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -846,13 +845,14 @@ def embed(table, tokens, scale: float = 1.0, out=None, stream=None) -> torch.Ten
     if stream is not None:
         return _on(stream, table, embed, table, tokens, scale, out)
     dtype = _dtype(table, "table")
-    if table.dim() != 2:
-        raise ValueError(f"table must be (vocab, width) (got {tuple(table.shape)})")
+    shape = table.shape
+    if len(shape) != 2:
+        raise ValueError(f"table must be (vocab, width) (got {tuple(shape)})")
     _like(table, table, "table")
     size = _tokens(tokens, table)
-    vocab, width = table.shape
+    vocab, width = shape
     if out is None:
-        out = torch.empty((*tokens.shape, width), dtype=table.dtype, device=table.device)
+        out = table.new_empty((*tokens.shape, width))
         stride = width
     else:
         _beside(out, table, (*tokens.shape, width), "out")
@@ -918,18 +918,24 @@ def _weight_ptr(w, x: torch.Tensor, shape, what: str) -> int | None:
 
 def _block(x, w_pre, o, w_post, gate, res_scale: float, eps: float) -> _Block:
     dtype = _dtype(x, "x")
-    if x.dim() < 1:
+    shape = x.shape
+    if not shape:
         raise ValueError("x must have rows")
     _like(x, x, "x")
-    width = x.shape[-1]
-    groups = 1
-    if gate is not None and isinstance(gate, torch.Tensor) and gate.dim() == 2:
-        groups = gate.shape[0]
-    return _Block(x.numel() // width if width else 0, width, groups, dtype, x.data_ptr(),
-                  None if o is None else _like(o, x, "o").data_ptr(), _stride_of_rows(x, "x"),
-                  0 if o is None else _stride_of_rows(o, "o"), _weight_ptr(w_post, x, (width,), "w_post"),
-                  None if gate is None else _weight_ptr(gate, x, (groups, width) if gate.dim() == 2 else (width,), "gate"),
-                  _weight_ptr(w_pre, x, (width,), "w_pre"), res_scale, eps)
+    width = shape[-1]
+    vector = (width,)
+    groups, p_gate, p_o, o_stride = 1, None, None, 0
+    if gate is not None:
+        if isinstance(gate, torch.Tensor) and gate.dim() == 2:
+            groups = gate.shape[0]
+            p_gate = _weight_ptr(gate, x, (groups, width), "gate")
+        else:
+            p_gate = _weight_ptr(gate, x, vector, "gate")
+    if o is not None:
+        p_o, o_stride = _rows_like(o, x, "o")
+    rows = shape[0] if len(shape) == 2 else x.numel() // width if width else 0
+    return _Block(rows, width, groups, dtype, x.data_ptr(), p_o, _stride_of_rows(x, "x"), o_stride,
+                  _weight_ptr(w_post, x, vector, "w_post"), p_gate, _weight_ptr(w_pre, x, vector, "w_pre"), res_scale, eps)
 
 
 def _rows_like(t, x: torch.Tensor, what: str) -> tuple:
@@ -938,6 +944,10 @@ def _rows_like(t, x: torch.Tensor, what: str) -> tuple:
         return None, 0
     _like(t, x, what)
     return t.data_ptr(), _stride_of_rows(t, what)
+
+
+def _new_rows(x: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 def block_norm(x, w_pre=None, o=None, w_post=None, gate=None, res_scale: float = 1.0, eps: float = 1e-6,
@@ -950,13 +960,23 @@ def block_norm(x, w_pre=None, o=None, w_post=None, gate=None, res_scale: float =
     if stream is not None:
         return _on(stream, x, block_norm, x, w_pre, o, w_post, gate, res_scale, eps, keep, out, n_out)
     b = _block(x, w_pre, o, w_post, gate, res_scale, eps)
-    if out is None and o is not None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    if n_out is None and w_pre is not None:
-        n_out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if out is not None:
+        p_out, out_stride = _rows_like(out, x, "out")
+    elif o is not None:
+        out = _new_rows(x)
+        p_out, out_stride = out.data_ptr(), b.width
+    else:
+        p_out, out_stride = None, 0
+    if n_out is not None:
+        p_n, n_stride = _rows_like(n_out, x, "n_out")
+    elif w_pre is not None:
+        n_out = _new_rows(x)
+        p_n, n_stride = n_out.data_ptr(), b.width
+    else:
+        p_n, n_stride = None, 0
     kept = torch.empty((2, b.rows), dtype=torch.float32, device=x.device) if keep else None
-    _check(lib().zg_block_norm(ctypes.byref(b), *_rows_like(out, x, "out"), *_rows_like(n_out, x, "n_out"),
-                               kept.data_ptr() if keep else None, _stream_of(x)), "zg_block_norm")
+    _check(lib().zg_block_norm(ctypes.byref(b), p_out, out_stride, p_n, n_stride, kept.data_ptr() if keep else None,
+                               _stream_of(x)), "zg_block_norm")
     return out, n_out, kept
 
 
@@ -970,9 +990,8 @@ def block_norm_grad(x, kept, dn=None, dx_new=None, w_pre=None, o=None, w_post=No
     if kept is None:
         raise ValueError("kept is None: call block_norm with keep=True")
     b = _block(x, w_pre, o, w_post, gate, res_scale, eps)
-    new = functools.partial(torch.empty_like, memory_format=torch.contiguous_format)
-    dx, do = out if out is not None else (new(x), None if o is None else new(x))
-    dw_pre, dw_post, dgate = (None if w is None else new(w) for w in (w_pre, w_post, gate))
+    dx, do = out if out is not None else (_new_rows(x), None if o is None else _new_rows(x))
+    dw_pre, dw_post, dgate = (None if w is None else _new_rows(w) for w in (w_pre, w_post, gate))
     L = lib()
     work_bytes = L.zg_block_norm_workspace(b.rows, b.width, b.groups)
     _check(min(work_bytes, 0), "zg_block_norm_workspace")

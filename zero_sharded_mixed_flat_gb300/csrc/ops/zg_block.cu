@@ -16,6 +16,8 @@
 // rows into shared memory while it computes (cp.async: an aligned row's units are
 // copied and read by the same thread, so they need no barrier), and goes over the
 // row in shared memory again where a sum has to be known first.
+#include <atomic>
+
 #include "zg_async.cuh"
 #include "zg_launch.h"
 #include "zg_ops.h"
@@ -25,9 +27,10 @@ namespace zg {
 namespace {
 
 constexpr int kMost = 512;     // threads of a block
-constexpr int kBlocks = 152;   // blocks that share the rows of backward, one to an SM
+constexpr int kBlocks = 152;   // blocks that share the rows, one to an SM
 constexpr int kStages = 4;     // rows of a team in shared memory, at most
 constexpr int kTeams = 8;      // of a block, at most
+constexpr int kMemory = 224 * 1024;  // bytes of a block, an SM's one
 
 // The threads that share a row: whole warps of a block.
 struct Team {
@@ -762,11 +765,12 @@ Shape shape_of(const BlockArgs &a, int vec, int columns, int team, int tensors, 
     s.team = team ? team : ((a.width + columns - 1) / columns + 31) / 32 * 32;
     s.teams = kMost / s.team;
     if (s.teams > kTeams) s.teams = kTeams;
+    if (a.rows < int64_t(s.teams) * kBlocks) s.teams = int((a.rows + kBlocks - 1) / kBlocks);  // few rows: all SMs
     const int held = team ? team * columns : a.width;  // columns of a stage
     s.ring.slot = (held * size + (vec == 1 ? 48 : 0) + 15) / 16 * 16;  // a head, and two units that are cleared
     const size_t row = size_t(s.teams) * tensors * s.ring.slot;
     const size_t beside = wide ? size_t(held + 7) / 8 * 64 : 0;  // two weights in binary32
-    s.ring.stages = int((size_t(224 * 1024) - beside) / row);
+    s.ring.stages = int((size_t(kMemory) - beside) / row);
     if (s.ring.stages > kStages) s.ring.stages = kStages;
     s.bytes = row * s.ring.stages + beside;
     const size_t joint = s.teams > 1 ? size_t(a.width) * 4 : 0;  // of the weights' sums
@@ -774,10 +778,17 @@ Shape shape_of(const BlockArgs &a, int vec, int columns, int team, int tensors, 
     return s;
 }
 
+// The most shared memory that any shape takes is allowed once for each kernel and device.
 template <class F>
-cudaError_t allow(F *kernel, size_t bytes)
+cudaError_t allow(F *kernel, std::atomic<uint64_t> &devices)
 {
-    return bytes > 46 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) : cudaSuccess;
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (devices.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMemory)) return e;
+    devices.fetch_or(bit, std::memory_order_release);
+    return cudaSuccess;
 }
 
 template <class T, int VEC, int E, int K, int TEAM>
@@ -785,10 +796,10 @@ cudaError_t forward(const BlockArgs &a, cudaStream_t st)
 {
     const Shape s = shape_of(a, VEC, E * K, TEAM, 2, false);
     auto *kernel = &forward_kernel<T, VEC, E, K, TEAM>;
-    if (cudaError_t e = allow(kernel, s.bytes)) return e;
+    static std::atomic<uint64_t> allowed{0};
+    if (cudaError_t e = allow(kernel, allowed)) return e;
     const int64_t want = (a.rows + s.teams - 1) / s.teams;
-    const int wave = wave_blocks(reinterpret_cast<const void *>(kernel), s.team * s.teams, s.bytes);
-    kernel<<<unsigned(want < wave ? want : wave), s.team * s.teams, s.bytes, st>>>(a, s.team, s.ring);
+    kernel<<<unsigned(want < kBlocks ? want : kBlocks), s.team * s.teams, s.bytes, st>>>(a, s.team, s.ring);
     return cudaGetLastError();
 }
 
@@ -798,14 +809,19 @@ cudaError_t backward(const BlockArgs &a, cudaStream_t st)
     const Shares shares = shares_of(a.rows, a.groups);
     const bool all = a.o.ptr && a.n.ptr && a.x_new.ptr && shares.segments;
     Shape s = shape_of(a, VEC, E * K, all ? TEAM : 0, 4, shares.segments > 0);
+    static std::atomic<uint64_t> allowed[3];
     auto *kernel = &backward_kernel<T, VEC, E, K, 0, false, false>;
-    if (!shares.segments)
+    int which = 0;
+    if (!shares.segments) {
         kernel = &backward_kernel<T, VEC, E, K, 0, true, false>;
-    else if (all && s.ring.stages > 0)
+        which = 1;
+    } else if (all && s.ring.stages > 0) {
         kernel = &backward_kernel<T, VEC, E, K, TEAM, false, true>;
-    else if (all && TEAM)
+        which = 2;
+    } else if (all && TEAM) {
         s = shape_of(a, VEC, E * K, 0, 4, true);
-    if (cudaError_t e = allow(kernel, s.bytes)) return e;
+    }
+    if (cudaError_t e = allow(kernel, allowed[which])) return e;
     kernel<<<unsigned(shares.blocks), s.team * s.teams, s.bytes, st>>>(a, s.team, s.ring, shares);
     if (cudaError_t e = cudaGetLastError()) return e;
     if (!a.w_pre && !a.w_post && !(a.gate && shares.segments)) return cudaSuccess;

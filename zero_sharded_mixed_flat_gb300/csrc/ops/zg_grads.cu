@@ -17,17 +17,37 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kAhead = 8;
 
-template <int THREADS>
-__device__ __forceinline__ double sum_of_block(double x)
+__device__ __forceinline__ double sum_of_warp(double x)
 {
-    __shared__ double part[THREADS / 32];
 #pragma unroll
     for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = x;
+    return x;
+}
+
+// The sum of all parts, of any number of threads in the order of 1,024 of them: each adds up every
+// 1024-th sum, then 32 neighbours, then those 32.
+__device__ double total_of(const double *sums, int64_t count)
+{
+    __shared__ double part[32];
+    for (int64_t t = threadIdx.x; t < 1024; t += blockDim.x) {
+        double s = 0.0;
+        int64_t i = t;
+        for (; i + 3 * 1024 < count; i += 4 * 1024) s += (sums[i] + sums[i + 1024]) + (sums[i + 2048] + sums[i + 3072]);
+        for (; i < count; i += 1024) s += sums[i];
+        s = sum_of_warp(s);
+        if (t % 32 == 0) part[t / 32] = s;
+    }
     __syncthreads();
     double s = 0.0;
-    for (int i = 0; i < THREADS / 32; ++i) s += part[i];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += part[i];
     return s;
+}
+__device__ __forceinline__ float2 stats_of(double sum, float max_norm, float eps, bool write)
+{
+    const double norm = sqrt(sum);
+    return make_float2(float(norm),
+                       write && isfinite(norm) ? float(fmin(1.0, double(max_norm) / (norm + double(eps)))) : 1.0f);
 }
 
 // The squares of a part, in units from the 16-byte boundary at or before it; what a unit has
@@ -76,8 +96,14 @@ __global__ void __launch_bounds__(kThreads) squares_kernel(const GradPart *parts
 {
     pdl_trigger();
     const GradPart p = parts[blockIdx.x];
-    const double total = sum_of_block<kThreads>(p.dtype == ZG_DTYPE_BF16 ? squares<uint16_t>(p, scale) : squares<float>(p, scale));
-    if (threadIdx.x == 0) sums[blockIdx.x] = total;
+    __shared__ double part[kThreads / 32];
+    const double mine = sum_of_warp(p.dtype == ZG_DTYPE_BF16 ? squares<uint16_t>(p, scale) : squares<float>(p, scale));
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = mine;
+    __syncthreads();
+    if (threadIdx.x) return;
+    double total = 0.0;
+    for (int i = 0; i < kThreads / 32; ++i) total += part[i];
+    sums[blockIdx.x] = total;
 }
 
 __global__ void __launch_bounds__(1024) finish_kernel(const double *sums, int64_t count, float max_norm, float eps,
@@ -85,15 +111,11 @@ __global__ void __launch_bounds__(1024) finish_kernel(const double *sums, int64_
 {
     pdl_trigger();
     pdl_wait();
-    double s = 0.0;
-    int64_t i = threadIdx.x;
-    for (; i + 3 * 1024 < count; i += 4 * 1024) s += (sums[i] + sums[i + 1024]) + (sums[i + 2048] + sums[i + 3072]);
-    for (; i < count; i += 1024) s += sums[i];
-    s = sum_of_block<1024>(s);
+    const double s = total_of(sums, count);
     if (threadIdx.x) return;
-    const double norm = sqrt(s);
-    stats[0] = float(norm);
-    stats[1] = write && isfinite(norm) ? float(fmin(1.0, double(max_norm) / (norm + double(eps)))) : 1.0f;
+    const float2 found = stats_of(s, max_norm, eps, write);
+    stats[0] = found.x;
+    stats[1] = found.y;
 }
 
 // Eight neighbouring elements of either type.
@@ -172,11 +194,24 @@ __device__ __forceinline__ void write_part(const GradPart &p, float k)
     for (; i < first; i += kThreads) one(i);
 }
 
-__global__ void __launch_bounds__(kThreads) write_kernel(const GradPart *parts, const float *stats, float scale)
+// `sums`: every block adds the parts up itself, and the first writes stats; otherwise they are known.
+__global__ void __launch_bounds__(kThreads) write_kernel(const GradPart *parts, const double *sums, int64_t count, float max_norm,
+                                                         float eps, float *stats, float scale)
 {
     const GradPart p = parts[gridDim.x - 1 - blockIdx.x];
     pdl_wait();
-    const float k = scale * stats[1];
+    float coefficient;
+    if (sums) {
+        const float2 found = stats_of(total_of(sums, count), max_norm, eps, true);
+        coefficient = found.y;
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            stats[0] = found.x;
+            stats[1] = found.y;
+        }
+    } else {
+        coefficient = stats[1];
+    }
+    const float k = scale * coefficient;
     if (p.dtype == ZG_DTYPE_BF16) {
         if (p.out_dtype == ZG_DTYPE_BF16)
             write_part<uint16_t, uint16_t>(p, k);
@@ -197,9 +232,15 @@ cudaError_t launch_grads_norm(const GradPart *parts, int64_t count, double *sums
 {
     if (count) squares_kernel<<<unsigned(count), kThreads, 0, st>>>(parts, sums, scale);
     if (cudaError_t e = cudaGetLastError()) return e;
-    if (cudaError_t e = launch_dependent(&finish_kernel, 1, 1024, 0, st, sums, count, max_norm, eps, write, stats)) return e;
+    // up to 1,024 parts are added up by each block that writes: a launch less (54 parts: 14.5 us for 10.5)
+    const bool alone = write && count > 0 && count <= 1024;
+    if (!alone)
+        if (cudaError_t e = launch_dependent(&finish_kernel, 1, 1024, 0, st, sums, count, max_norm, eps,
+                                             write, stats))
+            return e;
     if (!write || !count) return cudaSuccess;
-    return launch_dependent(&write_kernel, int(count), kThreads, 0, st, parts, static_cast<const float *>(stats), scale);
+    return launch_dependent(&write_kernel, int(count), kThreads, 0, st, parts, static_cast<const double *>(alone ? sums : nullptr),
+                            count, max_norm, eps, stats, scale);
 }
 
 }  // namespace zg
