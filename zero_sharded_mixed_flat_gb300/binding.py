@@ -852,7 +852,7 @@ def embed(table, tokens, scale: float = 1.0, out=None, stream=None) -> torch.Ten
     size = _tokens(tokens, table)
     vocab, width = shape
     if out is None:
-        out = table.new_empty((*tokens.shape, width))
+        out = torch.empty((*tokens.shape, width), dtype=table.dtype, device=table.device)
         stride = width
     else:
         _beside(out, table, (*tokens.shape, width), "out")

@@ -1,4 +1,4 @@
-// The norms before and after a block, with its gate and the residual's scale.
+// zg_block.cuh -- the norms before and after a block, with its gate and the residual's scale.
 //
 // Forward, for a row: b = w1 o s1, x' = r x + gate b, n = w2 x' s2, where s1 and s2
 // are 1 / sqrt(mean square + eps) of o and of x'.
@@ -16,6 +16,8 @@
 // rows into shared memory while it computes (cp.async: an aligned row's units are
 // copied and read by the same thread, so they need no barrier), and goes over the
 // row in shared memory again where a sum has to be known first.
+#pragma once
+
 #include <atomic>
 
 #include "zg_async.cuh"
@@ -846,20 +848,4 @@ cudaError_t of_type(const BlockArgs &a, cudaStream_t st)
 }
 
 }  // namespace
-
-int64_t block_norm_workspace(int64_t rows, int64_t width, int64_t groups)
-{
-    return 2 * shares_of(rows, groups).blocks * width * 4;
-}
-
-cudaError_t launch_block_norm(const BlockArgs &a, cudaStream_t st)
-{
-    return a.dtype == ZG_DTYPE_BF16 ? of_type<uint16_t, false>(a, st) : of_type<float, false>(a, st);
-}
-
-cudaError_t launch_block_norm_grad(const BlockArgs &a, cudaStream_t st)
-{
-    return a.dtype == ZG_DTYPE_BF16 ? of_type<uint16_t, true>(a, st) : of_type<float, true>(a, st);
-}
-
 }  // namespace zg

@@ -1,0 +1,15 @@
+// The norms around a block in bf16.
+#include "zg_block.cuh"
+
+namespace zg {
+
+int64_t block_norm_workspace(int64_t rows, int64_t width, int64_t groups)
+{
+    return 2 * shares_of(rows, groups).blocks * width * 4;
+}
+
+cudaError_t launch_block_norm_bf16(const BlockArgs &a, cudaStream_t st) { return of_type<uint16_t, false>(a, st); }
+
+cudaError_t launch_block_norm_grad_bf16(const BlockArgs &a, cudaStream_t st) { return of_type<uint16_t, true>(a, st); }
+
+}  // namespace zg

@@ -107,9 +107,12 @@ struct BlockArgs {
     float *work;
 };
 
-cudaError_t launch_block_norm(const BlockArgs &a, cudaStream_t st);
+// A translation unit to each dtype.
+cudaError_t launch_block_norm_bf16(const BlockArgs &a, cudaStream_t st);
+cudaError_t launch_block_norm_f32(const BlockArgs &a, cudaStream_t st);
+cudaError_t launch_block_norm_grad_bf16(const BlockArgs &a, cudaStream_t st);
+cudaError_t launch_block_norm_grad_f32(const BlockArgs &a, cudaStream_t st);
 int64_t block_norm_workspace(int64_t rows, int64_t width, int64_t groups);
-cudaError_t launch_block_norm_grad(const BlockArgs &a, cudaStream_t st);
 
 // loss alone, gradient alone (from kept), or both; with old_logp null the
 // log-probabilities alone.

@@ -674,7 +674,8 @@ int zg_block_norm(const zg_block *block, void *x_new, int64_t x_new_stride, void
             return fail(ZG_ERR_INVALID_ARG, "n must not overlap x, and in o's own memory it needs o's stride");
         if (int rc = check_ptr(kept, 4, true, "kept")) return rc;
         a.kept = kept;
-        return finish(zg::launch_block_norm(a, stream), "block norm launch");
+        return finish(a.dtype == ZG_DTYPE_BF16 ? zg::launch_block_norm_bf16(a, stream) : zg::launch_block_norm_f32(a, stream),
+                      "block norm launch");
     });
 }
 
@@ -718,7 +719,9 @@ int zg_block_norm_grad(const zg_block *block, const float *kept, const void *dn,
         a.dw_post = dw_post;
         a.dgate = dgate;
         a.work = static_cast<float *>(work);
-        return finish(zg::launch_block_norm_grad(a, stream), "block norm gradient launch");
+        return finish(a.dtype == ZG_DTYPE_BF16 ? zg::launch_block_norm_grad_bf16(a, stream)
+                                               : zg::launch_block_norm_grad_f32(a, stream),
+                      "block norm gradient launch");
     });
 }
 
