@@ -316,7 +316,8 @@ __device__ __forceinline__ void clear(char *p, int bytes)
     __syncthreads();
 }
 
-template <class T, int VEC, int E, int K, int TEAM>
+// ALL: x_new, o and w_pre are there, and rows are staged.
+template <class T, int VEC, int E, int K, int TEAM, bool ALL>
 __global__ void __launch_bounds__(kMost, 1) forward_kernel(BlockArgs a, int team_threads, Ring ring)
 {
     __shared__ __align__(16) float sh[kTeams * 2 * kMost / 32];
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(kMost, 1) forward_kernel(BlockArgs a, int team
     if (TEAM) clear(rows, team.count * 2 * ring.slot * ring.stages);
     clear_sums<kTeams * 2 * kMost / 32>(sh);
     const int width = a.width, stages = ring.stages > 0 ? ring.stages : 1;
-    const bool staged = TEAM || ring.stages > 0, block = a.o.ptr != nullptr;
+    const bool staged = TEAM || ALL || ring.stages > 0, block = ALL || a.o.ptr, has_n = ALL || a.w_pre, has_x = ALL || a.x_new.ptr;
     const uint32_t mine = uint32_t(__cvta_generic_to_shared(rows)) + team.id * (2 * ring.slot * ring.stages);
     const Source<T, VEC, E, K, TEAM> x_in(a.x, mine, 0, ring, 2), o_in(a.o, mine, 1, ring, 2);
     const int64_t teams = int64_t(gridDim.x) * team.count, each = (a.rows + teams - 1) / teams;
@@ -389,10 +390,10 @@ __global__ void __launch_bounds__(kMost, 1) forward_kernel(BlockArgs a, int team
         }
         if (VEC == 1) team.sync();  // the row has been read
         ask(r + stages, stage);
-        if (a.x_new.ptr)
+        if (has_x)
 #pragma unroll
             for (int k = 0; k < K; ++k) store<T, VEC, E, TEAM>(team, out_row<T>(a.x_new, r), k, width, y[k]);
-        if (a.w_pre) {
+        if (has_n) {
             team.sum<1>(s, sh);
             s2 = rsqrtf(fmaf(s[0], mean, a.eps));
 #pragma unroll
@@ -686,6 +687,20 @@ __global__ void __launch_bounds__(kMost, 1) backward_kernel(BlockArgs a, int tea
 }
 
 // The sums of the weights' gradients over the blocks.
+// Every step-th of `count` rows from `first` on, eight loads at a time.
+__device__ __forceinline__ float sum_rows(const float *p, int width, int first, int count, int step)
+{
+    float s = 0.0f;
+    for (int b = first; b < count; b += 8 * step) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = p[int64_t(min(b + i * step, count - 1)) * width];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += b + i * step < count ? v[i] : 0.0f;
+    }
+    return s;
+}
+
 template <class T>
 __global__ void __launch_bounds__(512) weights_kernel(BlockArgs a, Shares shares)
 {
@@ -693,6 +708,7 @@ __global__ void __launch_bounds__(512) weights_kernel(BlockArgs a, Shares shares
     pdl_wait();
     const int lane = threadIdx.x % 32, row = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
     const bool there = c < a.width;
+    const int blocks = int(shares.blocks);
     auto total = [&](float v) {
         sh[row][lane] = v;
         __syncthreads();
@@ -704,7 +720,7 @@ __global__ void __launch_bounds__(512) weights_kernel(BlockArgs a, Shares shares
     if (a.w_pre) {
         float s = 0.0f;
         if (there)
-            for (int64_t b = row; b < shares.blocks; b += 16) s += a.work[b * a.width + c];
+            s = sum_rows(a.work + c, a.width, row, blocks, 16);
         s = total(s);
         if (there && row == 0) store1(static_cast<T *>(a.dw_pre) + c, s);
     }
@@ -713,7 +729,7 @@ __global__ void __launch_bounds__(512) weights_kernel(BlockArgs a, Shares shares
         if (!a.w_post) return;
         float s = 0.0f;
         if (there)
-            for (int64_t b = row; b < shares.blocks; b += 16) s += sums[b * a.width + c];
+            s = sum_rows(sums + c, a.width, row, blocks, 16);
         s = total(s);
         if (there && row == 0) store1(static_cast<T *>(a.dw_post) + c, s);
         return;
@@ -723,7 +739,7 @@ __global__ void __launch_bounds__(512) weights_kernel(BlockArgs a, Shares shares
     if (a.groups == 1) {
         float s = 0.0f;
         if (there)
-            for (int64_t b = row; b < shares.blocks; b += 16) s += sums[b * a.width + c];
+            s = sum_rows(sums + c, a.width, row, blocks, 16);
         s = total(s);
         if (there && row == 0) {
             store1(static_cast<T *>(a.dgate) + c, w * s);
@@ -733,7 +749,7 @@ __global__ void __launch_bounds__(512) weights_kernel(BlockArgs a, Shares shares
     }
     for (int64_t g = row; there && g < a.groups; g += 16) {
         float s = 0.0f;
-        for (int i = 0; i < shares.segments; ++i) s += sums[(g * shares.segments + i) * a.width + c];
+        s = sum_rows(sums + (g * shares.segments) * a.width + c, a.width, 0, shares.segments, 1);
         store1(static_cast<T *>(a.dgate) + g * a.width + c, w * s);
         dw1 = fmaf(s, load1(static_cast<const T *>(a.gate) + g * a.width + c), dw1);
     }
@@ -797,9 +813,10 @@ template <class T, int VEC, int E, int K, int TEAM>
 cudaError_t forward(const BlockArgs &a, cudaStream_t st)
 {
     const Shape s = shape_of(a, VEC, E * K, TEAM, 2, false);
-    auto *kernel = &forward_kernel<T, VEC, E, K, TEAM>;
-    static std::atomic<uint64_t> allowed{0};
-    if (cudaError_t e = allow(kernel, allowed)) return e;
+    const bool all = s.ring.stages > 0 && a.o.ptr && a.x_new.ptr && a.w_pre;
+    auto *kernel = all ? &forward_kernel<T, VEC, E, K, TEAM, true> : &forward_kernel<T, VEC, E, K, TEAM, false>;
+    static std::atomic<uint64_t> allowed[2];
+    if (cudaError_t e = allow(kernel, allowed[all])) return e;
     const int64_t want = (a.rows + s.teams - 1) / s.teams;
     kernel<<<unsigned(want < kBlocks ? want : kBlocks), s.team * s.teams, s.bytes, st>>>(a, s.team, s.ring);
     return cudaGetLastError();

@@ -1,6 +1,6 @@
 // The gradients of many tensors, clipped by their common norm.
 //
-// A list is cut into parts of at most kGradPart elements of one tensor, a block to
+// A list is cut into parts of some thousand elements of one tensor, a block to
 // each: the first pass leaves the sum of a part's squares, one block adds the
 // sums up in a fixed order, and the second pass writes (scale * coefficient) * g.
 //
@@ -15,32 +15,37 @@ namespace zg {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 8;
+constexpr int kAhead = 8;   // units of a thread at a time in the first pass
+constexpr int kEights = 4;  // eights of elements in the second
 
-__device__ __forceinline__ double sum_of_warp(double x)
+template <class F>
+__device__ __forceinline__ F sum_of_warp(F x)
 {
 #pragma unroll
     for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
-// The sum of all parts, of any number of threads in the order of 1,024 of them: each adds up every
-// 1024-th sum, then 32 neighbours, then those 32.
+// The sum of all parts, for the block's first thread, in one order: a thread adds up every kThreads-th, then
+// warps, then those. (binary64 is slow here: what every thread repeats of it shows.)
 __device__ double total_of(const double *sums, int64_t count)
 {
-    __shared__ double part[32];
-    for (int64_t t = threadIdx.x; t < 1024; t += blockDim.x) {
-        double s = 0.0;
-        int64_t i = t;
-        for (; i + 3 * 1024 < count; i += 4 * 1024) s += (sums[i] + sums[i + 1024]) + (sums[i + 2048] + sums[i + 3072]);
-        for (; i < count; i += 1024) s += sums[i];
-        s = sum_of_warp(s);
-        if (t % 32 == 0) part[t / 32] = s;
-    }
-    __syncthreads();
+    __shared__ double part[kThreads / 32];
     double s = 0.0;
+    int64_t i = threadIdx.x;
+    for (; i + 7 * kThreads < count; i += 8 * kThreads) {
+        double v[8];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s += part[i];
+        for (int j = 0; j < 8; ++j) v[j] = sums[i + j * kThreads];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += v[j];
+    }
+    for (; i < count; i += kThreads) s += sums[i];
+    s = sum_of_warp(s);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = s;
+    __syncthreads();
+    if (threadIdx.x) return 0.0;
+    for (int w = 1; w < kThreads / 32; ++w) s += part[w];
     return s;
 }
 __device__ __forceinline__ float2 stats_of(double sum, float max_norm, float eps, bool write)
@@ -80,15 +85,14 @@ __device__ __forceinline__ float squares(const GradPart &p, float scale)
             sum = fma_f32x2(v[i], v[i], sum);
         }
     };
-    int u = threadIdx.x;
-    for (; u + (kAhead - 1) * kThreads < units; u += kAhead * kThreads) {
+    for (int u = threadIdx.x; u < units; u += kAhead * kThreads) {
         uint4 w[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) w[i] = from[u + i * kThreads];
+        for (int i = 0; i < kAhead; ++i) w[i] = from[min(u + i * kThreads, units - 1)];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) add(w[i], u + i * kThreads);
+        for (int i = 0; i < kAhead; ++i)
+            if (u + i * kThreads < units) add(w[i], u + i * kThreads);
     }
-    for (; u < units; u += kThreads) add(from[u], u);
     return sum.x + sum.y;
 }
 
@@ -96,18 +100,19 @@ __global__ void __launch_bounds__(kThreads) squares_kernel(const GradPart *parts
 {
     pdl_trigger();
     const GradPart p = parts[blockIdx.x];
-    __shared__ double part[kThreads / 32];
-    const double mine = sum_of_warp(p.dtype == ZG_DTYPE_BF16 ? squares<uint16_t>(p, scale) : squares<float>(p, scale));
+    __shared__ float part[kThreads / 32];
+    const float mine = sum_of_warp(p.dtype == ZG_DTYPE_BF16 ? squares<uint16_t>(p, scale) : squares<float>(p, scale));
     if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = mine;
     __syncthreads();
     if (threadIdx.x) return;
     double total = 0.0;
+#pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) total += part[i];
     sums[blockIdx.x] = total;
 }
 
-__global__ void __launch_bounds__(1024) finish_kernel(const double *sums, int64_t count, float max_norm, float eps,
-                                                      bool write, float *stats)
+__global__ void __launch_bounds__(kThreads) finish_kernel(const double *sums, int64_t count, float max_norm, float eps,
+                                                          bool write, float *stats)
 {
     pdl_trigger();
     pdl_wait();
@@ -160,38 +165,28 @@ __device__ __forceinline__ void write_part(const GradPart &p, float k)
     const bool alike = (reinterpret_cast<uintptr_t>(out + head) & 15u) == 0;
     const int first = alike ? min(head, p.n) : p.n, eights = (p.n - first) / 8;
     auto one = [&](int i) { store1(out + i, load1(g + i) * k); };
-    int u = threadIdx.x;
-    for (; u + kThreads < eights; u += 2 * kThreads) {
-        Eight<T> x, y;
-        x.load(g + first + u * 8);
-        y.load(g + first + (u + kThreads) * 8);
-        Eight<O> a, b;
+    for (int u = threadIdx.x; u < eights; u += kEights * kThreads) {
+        Eight<T> x[kEights];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a.v[i] = mul_f32x2(x.v[i], make_float2(k, k));
-            b.v[i] = mul_f32x2(y.v[i], make_float2(k, k));
+        for (int i = 0; i < kEights; ++i) x[i].load(g + first + min(u + i * kThreads, eights - 1) * 8);
+#pragma unroll
+        for (int i = 0; i < kEights; ++i) {
+            if (u + i * kThreads >= eights) break;
+            Eight<O> y;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y.v[j] = mul_f32x2(x[i].v[j], make_float2(k, k));
+            y.store(out + first + (u + i * kThreads) * 8);
         }
-        a.store(out + first + u * 8);
-        b.store(out + first + (u + kThreads) * 8);
-    }
-    for (; u < eights; u += kThreads) {
-        Eight<T> x;
-        x.load(g + first + u * 8);
-        Eight<O> a;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a.v[i] = mul_f32x2(x.v[i], make_float2(k, k));
-        a.store(out + first + u * 8);
     }
     for (int i = first + eights * 8 + threadIdx.x; i < p.n; i += kThreads) one(i);
-    int i = threadIdx.x;
-    for (; i + 7 * kThreads < first; i += 8 * kThreads) {
+    for (int i = threadIdx.x; i < first; i += 8 * kThreads) {
         float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = load1(g + i + j * kThreads);
+        for (int j = 0; j < 8; ++j) v[j] = load1(g + min(i + j * kThreads, first - 1));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) store1(out + i + j * kThreads, v[j] * k);
+        for (int j = 0; j < 8; ++j)
+            if (i + j * kThreads < first) store1(out + i + j * kThreads, v[j] * k);
     }
-    for (; i < first; i += kThreads) one(i);
 }
 
 // `sums`: every block adds the parts up itself, and the first writes stats; otherwise they are known.
@@ -200,16 +195,21 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const GradPart *parts, 
 {
     const GradPart p = parts[gridDim.x - 1 - blockIdx.x];
     pdl_wait();
-    float coefficient;
+    __shared__ float coefficient;
     if (sums) {
-        const float2 found = stats_of(total_of(sums, count), max_norm, eps, true);
-        coefficient = found.y;
-        if (blockIdx.x == 0 && threadIdx.x == 0) {
-            stats[0] = found.x;
-            stats[1] = found.y;
+        const double s = total_of(sums, count);
+        if (threadIdx.x == 0) {
+            const float2 found = stats_of(s, max_norm, eps, true);
+            coefficient = found.y;
+            if (blockIdx.x == 0) {
+                stats[0] = found.x;
+                stats[1] = found.y;
+            }
         }
+        __syncthreads();
     } else {
-        coefficient = stats[1];
+        if (threadIdx.x == 0) coefficient = stats[1];
+        __syncthreads();
     }
     const float k = scale * coefficient;
     if (p.dtype == ZG_DTYPE_BF16) {
@@ -232,10 +232,10 @@ cudaError_t launch_grads_norm(const GradPart *parts, int64_t count, double *sums
 {
     if (count) squares_kernel<<<unsigned(count), kThreads, 0, st>>>(parts, sums, scale);
     if (cudaError_t e = cudaGetLastError()) return e;
-    // up to 1,024 parts are added up by each block that writes: a launch less (54 parts: 14.5 us for 10.5)
+    // up to 1,024 parts are added up by each block that writes: a launch less
     const bool alone = write && count > 0 && count <= 1024;
     if (!alone)
-        if (cudaError_t e = launch_dependent(&finish_kernel, 1, 1024, 0, st, sums, count, max_norm, eps,
+        if (cudaError_t e = launch_dependent(&finish_kernel, 1, kThreads, 0, st, sums, count, max_norm, eps,
                                              write, stats))
             return e;
     if (!write || !count) return cudaSuccess;

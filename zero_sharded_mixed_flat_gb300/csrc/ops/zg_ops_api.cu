@@ -803,6 +803,10 @@ int zg_grads_init(const zg_grad *list, int64_t count, zg_grads **out)
     return guarded([&]() -> int {
         if (count < 0 || (count && !list)) return fail(ZG_ERR_INVALID_ARG, "list is NULL or count negative");
         std::vector<zg::GradPart> parts;
+        double total = 0.0;
+        for (int64_t i = 0; i < count; ++i) total += double(list[i].n > 0 ? list[i].n : 0);
+        int64_t each = zg::kGradPartLeast;
+        while (each < zg::kGradPartMost && total > 1024.0 * double(each)) each *= 2;
         for (int64_t i = 0; i < count; ++i) {
             const zg_grad &g = list[i];
             char what[48];
@@ -816,11 +820,11 @@ int zg_grads_init(const zg_grad *list, int64_t count, zg_grads **out)
             if (int rc = check_ptr(g.out, element_size(g.out_dtype), false, what)) return rc;
             if (g.grad == g.out && g.dtype != g.out_dtype)
                 return fail(ZG_ERR_INVALID_ARG, "%s: a gradient clipped in its own memory keeps its dtype", what);
-            for (int64_t at = 0; at < g.n; at += zg::kGradPart) {
+            for (int64_t at = 0; at < g.n; at += each) {
                 zg::GradPart p{};
                 p.grad = static_cast<const char *>(g.grad) + at * element_size(g.dtype);
                 p.out = static_cast<char *>(g.out) + at * element_size(g.out_dtype);
-                p.n = int(g.n - at < zg::kGradPart ? g.n - at : zg::kGradPart);
+                p.n = int(g.n - at < each ? g.n - at : each);
                 p.dtype = uint8_t(g.dtype);
                 p.out_dtype = uint8_t(g.out_dtype);
                 parts.push_back(p);
