@@ -143,6 +143,50 @@ def test_many_rows(n, v, dtype):
             ref.check(g[cut], want, ref.stored(want, err, DT[dtype]), "gradient")
 
 
+def on_the_gpu(n, v, dtype, pad=0):
+    """Both gradients and all values of n rows against the formulas in 64 bits on the GPU."""
+    gen = torch.Generator("cuda").manual_seed(7)
+    z = torch.randn(n, v + pad, generator=gen, device="cuda").mul_(2.5).to(DT[dtype])[:, :v]
+    tokens = torch.randint(0, v, (n,), generator=gen, device="cuda")
+    tokens[0], tokens[n // 2] = v - 1, 0
+    logq = torch.cat([torch.log_softmax(p.double(), 1) for p in z.split(8)])
+    logp = logq.gather(1, tokens[:, None])[:, 0]
+    old, adv = (logp + 0.05).float(), torch.linspace(-1, 1.1, n, device="cuda")
+    loss, got, grad = zb.policy_loss_grad(z, tokens, old, adv)
+    two_loss, two_logp, kept = zb.policy_loss(z, tokens, old, adv)
+    two = zb.policy_grad(z, kept, tokens, old, adv)
+    alone = zb.token_logp(z, tokens)[0]
+    slope = -torch.exp(logp - old.double()) * adv.double()
+    bound = ref.DEEP + 4 * ref.EPS * 30
+    for b in (got, two_logp, alone):
+        ref.check(b, logp, bound * (1 + logp.abs()), "logp")
+    for a in (loss, two_loss):
+        ref.check(a, slope, 2 * bound * (1 + logp.abs()) * adv.double().abs() + ref.TINY, "loss")
+    for r in range(n):
+        q = torch.exp(logq[r])
+        hot = torch.zeros_like(q)
+        hot[tokens[r]] = 1.0
+        want, err = slope[r] * (hot - q), 4 * bound * slope[r].abs() * (hot + q)
+        for g in (grad, two):
+            ref.check(g[r], want, ref.stored(want, err, DT[dtype]), "gradient")
+    mine = z.clone()
+    want = zb.policy_loss_grad(mine, tokens, old, adv)[2]
+    zb.policy_loss_grad(mine, tokens, old, adv, out=mine)
+    assert torch.equal(mine, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 2, 38, 43, 50, 60, 76, 77, 100, 152])
+def test_rows_shared_out_over_clusters_of_every_size(n, dtype):
+    on_the_gpu(n, 20011, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,v,pad", [(2, 500003, 0), (3, 1000001, 7), (40, 250007, 1), (1, 3000017, 0)])
+def test_rows_larger_than_shared_memory(n, v, pad, dtype):
+    on_the_gpu(n, v, dtype, pad)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("v", [90, 5003, 50257])
 def test_masks_and_rows_far_from_zero(v, dtype):
