@@ -701,55 +701,48 @@ __device__ __forceinline__ float sum_rows(const float *p, int width, int first, 
     return s;
 }
 
+// A block to 32 columns of dw2 (blockIdx.y 0), or of dw1 and dgate: a warp adds up every 32nd block's sums, then
+// they are added up.
 template <class T>
-__global__ void __launch_bounds__(512) weights_kernel(BlockArgs a, Shares shares)
+__global__ void __launch_bounds__(1024) weights_kernel(BlockArgs a, Shares shares)
 {
-    __shared__ float sh[16][33];
+    __shared__ float sh[32][33];
     pdl_wait();
     const int lane = threadIdx.x % 32, row = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
     const bool there = c < a.width;
     const int blocks = int(shares.blocks);
-    auto total = [&](float v) {
+    auto total = [&](float v) {  // in the first warp
         sh[row][lane] = v;
         __syncthreads();
         float s = 0.0f;
-        for (int i = 0; i < 16; ++i) s += sh[i][lane];
-        __syncthreads();
+        if (row == 0)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s += sh[i][lane];
         return s;
     };
-    if (a.w_pre) {
-        float s = 0.0f;
-        if (there)
-            s = sum_rows(a.work + c, a.width, row, blocks, 16);
-        s = total(s);
+    if (blockIdx.y == 0) {
+        if (!a.w_pre) return;
+        const float s = total(there ? sum_rows(a.work + c, a.width, row, blocks, 32) : 0.0f);
         if (there && row == 0) store1(static_cast<T *>(a.dw_pre) + c, s);
+        return;
     }
+    if (!a.w_post && !(a.gate && shares.segments)) return;
     const float *const sums = a.work + shares.blocks * a.width;
-    if (!shares.segments || !a.gate) {
-        if (!a.w_post) return;
-        float s = 0.0f;
-        if (there)
-            s = sum_rows(sums + c, a.width, row, blocks, 16);
-        s = total(s);
-        if (there && row == 0) store1(static_cast<T *>(a.dw_post) + c, s);
+    if (!shares.segments || !a.gate || a.groups == 1) {
+        const float s = total(there ? sum_rows(sums + c, a.width, row, blocks, 32) : 0.0f);
+        if (!there || row) return;
+        if (!shares.segments || !a.gate) {  // sums of dw1 itself
+            store1(static_cast<T *>(a.dw_post) + c, s);
+            return;
+        }
+        store1(static_cast<T *>(a.dgate) + c, a.w_post ? s * load1(static_cast<const T *>(a.w_post) + c) : s);
+        if (a.w_post) store1(static_cast<T *>(a.dw_post) + c, s * load1(static_cast<const T *>(a.gate) + c));
         return;
     }
     const float w = there && a.w_post ? load1(static_cast<const T *>(a.w_post) + c) : 1.0f;
     float dw1 = 0.0f;
-    if (a.groups == 1) {
-        float s = 0.0f;
-        if (there)
-            s = sum_rows(sums + c, a.width, row, blocks, 16);
-        s = total(s);
-        if (there && row == 0) {
-            store1(static_cast<T *>(a.dgate) + c, w * s);
-            if (a.w_post) store1(static_cast<T *>(a.dw_post) + c, s * load1(static_cast<const T *>(a.gate) + c));
-        }
-        return;
-    }
-    for (int64_t g = row; there && g < a.groups; g += 16) {
-        float s = 0.0f;
-        s = sum_rows(sums + (g * shares.segments) * a.width + c, a.width, 0, shares.segments, 1);
+    for (int64_t g = row; there && g < a.groups; g += 32) {
+        const float s = sum_rows(sums + g * shares.segments * a.width + c, a.width, 0, shares.segments, 1);
         store1(static_cast<T *>(a.dgate) + g * a.width + c, w * s);
         dw1 = fmaf(s, load1(static_cast<const T *>(a.gate) + g * a.width + c), dw1);
     }
@@ -757,7 +750,7 @@ __global__ void __launch_bounds__(512) weights_kernel(BlockArgs a, Shares shares
     if (a.w_post && there && row == 0) store1(static_cast<T *>(a.dw_post) + c, dw1);
 }
 
-bool whole(const RowsView &v, int size)
+inline bool whole(const RowsView &v, int size)
 {
     return (reinterpret_cast<uintptr_t>(v.ptr) | uintptr_t(v.stride * size)) % 16 == 0;
 }
@@ -844,7 +837,16 @@ cudaError_t backward(const BlockArgs &a, cudaStream_t st)
     kernel<<<unsigned(shares.blocks), s.team * s.teams, s.bytes, st>>>(a, s.team, s.ring, shares);
     if (cudaError_t e = cudaGetLastError()) return e;
     if (!a.w_pre && !a.w_post && !(a.gate && shares.segments)) return cudaSuccess;
-    return launch_dependent(&weights_kernel<T>, (a.width + 31) / 32, 512, 0, st, a, shares);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned((a.width + 31) / 32), 2);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = ZG_PDL;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, &weights_kernel<T>, a, shares);
 }
 
 template <class T, bool BACK>
