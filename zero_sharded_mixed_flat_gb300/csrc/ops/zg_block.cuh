@@ -440,23 +440,22 @@ __host__ __device__ inline Shares shares_of(int64_t rows, int64_t groups)
 template <int VEC, int E, int K, int TEAM>
 __device__ __forceinline__ void hand_in(const Team &team, const float2 (&v)[K][E / 2], float *sh, float *out, int width)
 {
-    for (int t = 0; t < team.count; ++t) {
-        if (team.id == t) {
+    float *const mine = team.count == 1 ? out : sh + team.id * width;
 #pragma unroll
-            for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const int c = column<VEC, E, TEAM>(team, k, i);
-                    if (c >= width) continue;
-                    const float mine = i & 1 ? v[k][i / 2].y : v[k][i / 2].x, sum = t ? sh[c] + mine : mine;
-                    if (t == team.count - 1)
-                        out[c] = sum;
-                    else
-                        sh[c] = sum;
-                }
+        for (int i = 0; i < E; ++i) {
+            const int c = column<VEC, E, TEAM>(team, k, i);
+            if (c < width) mine[c] = i & 1 ? v[k][i / 2].y : v[k][i / 2].x;
         }
-        __syncthreads();
+    if (team.count == 1) return;
+    __syncthreads();
+    for (int c = threadIdx.x; c < width; c += blockDim.x) {
+        float s = sh[c];
+        for (int t = 1; t < team.count; ++t) s += sh[t * width + c];
+        out[c] = s;
     }
+    __syncthreads();
 }
 
 // MANY: whole gates to a team (segments is 0), whose sums it finishes itself. ALL: every tensor of
@@ -784,7 +783,7 @@ Shape shape_of(const BlockArgs &a, int vec, int columns, int team, int tensors, 
     s.ring.stages = int((size_t(kMemory) - beside) / row);
     if (s.ring.stages > kStages) s.ring.stages = kStages;
     s.bytes = row * s.ring.stages + beside;
-    const size_t joint = s.teams > 1 ? size_t(a.width) * 4 : 0;  // of the weights' sums
+    const size_t joint = s.teams > 1 ? size_t(s.teams) * a.width * 4 : 0;  // of the weights' sums
     if (s.bytes < joint) s.bytes = joint;
     return s;
 }
