@@ -221,7 +221,7 @@ struct TeamShared {
 
 // Each team (or, with several blocks, each cluster) takes rows in turn.
 template <class T, int TEAM, int THREADS, bool GRAD, bool STAGED>
-__global__ void __launch_bounds__(THREADS, (TEAM == THREADS ? 1024 / THREADS : 1)) row_kernel(PolicyArgs a, RowShape shape)
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_kernel(PolicyArgs a, RowShape shape)
 {
     constexpr int kTeams = THREADS / TEAM, N = Unit<T>::kN;
     __shared__ TeamShared<TEAM> shared[kTeams];
@@ -549,7 +549,7 @@ constexpr int memory_of(int to_sm) { return 224 * 1024 / to_sm - (to_sm - 1) * 5
 template <class T, int TEAM, int THREADS, bool GRAD, bool STAGED>
 cudaError_t rows_of(const PolicyArgs &a, const RowShape &shape, cudaStream_t st)
 {
-    constexpr int kTeams = THREADS / TEAM, kToSm = TEAM == THREADS ? 1024 / THREADS : 1;
+    constexpr int kTeams = THREADS / TEAM, kToSm = 1024 / THREADS;
     auto *kernel = &row_kernel<T, TEAM, THREADS, GRAD, STAGED>;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
@@ -584,10 +584,8 @@ cudaError_t by_size(const PolicyArgs &a, cudaStream_t st)
         const int64_t fit = memory_of(to_sm) / (int64_t(s.slot) * teams);
         s.stages = int(fit < 2 ? fit : 2);
     };
-    hold(1, 512 / 32, 1);
-    if (units <= 192) return rows_of<T, 32, 512, GRAD, true>(a, s, st);
-    hold(1, 512 / 128, 1);
-    if (units <= 1536) return rows_of<T, 128, 512, GRAD, true>(a, s, st);
+    hold(1, 128 / 32, 8);
+    if (units <= 192) return rows_of<T, 32, 128, GRAD, true>(a, s, st);
     if constexpr (!GRAD) {
         // once over the row, straight from memory: small blocks keep most rows in flight; few rows take more
         // threads, then more blocks
@@ -597,6 +595,8 @@ cudaError_t by_size(const PolicyArgs &a, cudaStream_t st)
         s.stages = 0;
         return a.rows >= 608 ? rows_of<T, 128, 128, GRAD, false>(a, s, st) : rows_of<T, 512, 512, GRAD, false>(a, s, st);
     } else {
+        hold(1, 1, 8);
+        if (units <= 1536) return rows_of<T, 128, 128, GRAD, true>(a, s, st);
         // The smallest blocks that have room for a part, without a cluster where that can be. (4096 x 50257 in bf16:
         // two blocks of 512 threads to an SM 145 us, one of 1024 with two rows in its memory 214, clusters of four
         // blocks of 256 201, of two 158: what a row costs every warp of its own, and the waits for its sum.) Few rows
