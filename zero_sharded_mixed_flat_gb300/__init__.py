@@ -10,7 +10,11 @@ Beside the step the library has training operators that give it its gradients:
 the gated linear recurrence over time (``binding.GatedScan``), the selection of
 a teacher's top logits (``binding.topk_logits``) and the distillation loss on
 them with its gradient (``binding.distill_loss``, ``distill_grad``,
-``distill_loss_grad``); their sources are in ``csrc/ops/``.
+``distill_loss_grad``); the token embedding (``embed``, ``embed_grad``), the norms
+around a block with its gate and residual scale (``block_norm``,
+``block_norm_grad``), the clipped policy loss with its gradient (``token_logp``,
+``policy_loss``, ``policy_grad``, ``policy_loss_grad``) and the clipping of many
+gradients into the flat one (``GradClip``). Their sources are in ``csrc/ops/``.
 
 Importing this package loads nothing; the library is loaded on first use of
 ``binding`` and the import fails loudly if it has not been built.

@@ -16,6 +16,12 @@
 // rows into shared memory while it computes (cp.async: an aligned row's units are
 // copied and read by the same thread, so they need no barrier), and goes over the
 // row in shared memory again where a sum has to be known first.
+//
+// Measured at 16384 x 4096 in bf16: forward 95 us (5.7 TB/s), backward 149 (5.4 TB/s) with 6 for the sums of the weights'
+// gradients; in binary32 172 and 262 us (6.2 and 6.1 TB/s). Issue is active in 45 % of the cycles at 16 warps to an SM: what
+// is left are the two dependent sums of a row. 9001 x 771 in binary32, rows at any alignment: 27 and 50 us (4.2 and 3.3
+// TB/s). Of 16384 columns in bf16 the backward pass has no room in shared memory for its rows and weights
+// and reads rows twice (4096 rows 551 us, forward 137).
 #pragma once
 
 #include <atomic>

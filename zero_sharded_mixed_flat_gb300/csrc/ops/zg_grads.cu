@@ -7,6 +7,9 @@
 // Bound by memory: every gradient is read for the norm, and again and written once the
 // norm is known, the second time in the opposite order, since what was read last is still in
 // L2. A thread has kAhead units of 16 bytes in flight.
+//
+// Measured: 124 M gradients of 148 tensors, matrices in bf16 and vectors in binary32, into a flat bf16 one, 112 us (249 MB read
+// twice and written once: 6.7 TB/s; the squares 38 us, 6.5 TB/s); 0.6 M in binary32 6 us.
 #include "zg_launch.h"
 #include "zg_ops.h"
 #include "zg_rows.cuh"

@@ -4,15 +4,21 @@
 // With z a row of logits, T the temperature and t its token, logp = (z_t - m) / T
 // - log S with m the row's maximum and S = sum exp((z - m) / T); the loss and its
 // slope by logp are the row's own few values; dz = g ([v = t] - exp((z - m) / T) / S)
-// with g = scale dloss slope / T. Differences to the maximum come first throughout, so
-// masks of any size and rows far from zero have their values.
+// with g = scale dloss slope / T.
 //
-// Bound by memory: each logit is read once and its gradient written once. The gradient needs the whole
-// row's sum, so a team of warps copies its next row into shared memory (cp.async) while it goes over
-// the present one, there, twice: a row of 50257 bf16 logits takes an SM's memory with the next one. A
-// thread reads the units that it copied, which needs no barrier. Rows larger than that, and few rows, are
-// shared out over a cluster of blocks, which exchange their maxima and sums through distributed shared
-// memory. The gradient alone, from a kept maximum and sum, is a stream.
+// Bound by memory: each logit is read once and its gradient written once. The loss alone is one pass of small
+// blocks with a running maximum and sum. The gradient needs the whole row's sum first, so a block copies
+// its row into shared memory (cp.async) and goes over it there twice; a thread reads the units that it
+// copied, which needs no barrier, and an SM has several rows, of which some are copied while others
+// wait for their sums. Rows larger than that, and few rows, are shared out over a cluster of blocks, which
+// exchange their maxima and sums through distributed shared memory. The gradient alone, from a kept
+// maximum and sum, is a stream.
+//
+// Measured at 4096 x 50257 in bf16: the loss alone 72 us (5.7 TB/s), loss and gradient 145 (5.7 TB/s of the once-read,
+// once-written bytes), the gradient alone 100 with a third of the rows cut off or padding and so not read, 118
+// without; in binary32 131, 318 and 203 us. 777 x 131075 in bf16, the loss alone and the gradient 39 and 60 us. 37 x
+// 50257 in binary32, eight blocks to a row, 7.9 us. Both in one launch issue in half of the cycles, with
+// two rows to an SM; the exponentials are 41 % of the time of their pipe.
 #include <cooperative_groups.h>
 
 #include <map>
