@@ -17,11 +17,12 @@
 // copied and read by the same thread, so they need no barrier), and goes over the
 // row in shared memory again where a sum has to be known first.
 //
-// Measured at 16384 x 4096 in bf16: forward 95 us (5.7 TB/s), backward 149 (5.4 TB/s) with 6 for the sums of the weights'
-// gradients; in binary32 172 and 262 us (6.2 and 6.1 TB/s). Issue is active in 45 % of the cycles at 16 warps to an SM: what
-// is left are the two dependent sums of a row. 9001 x 771 in binary32, rows at any alignment: 27 and 50 us (4.2 and 3.3
-// TB/s). Of 16384 columns in bf16 the backward pass has no room in shared memory for its rows and weights
-// and reads rows twice (4096 rows 551 us, forward 137).
+// Measured at 16384 x 4096 in bf16: forward 94 us (5.7 TB/s), backward 150 (5.4 TB/s) and some 6 to 10 for the sums of
+// the weights' gradients after it; with a gate for each of 64 sequences 182, of 512 229, of every row 734. In binary32 172
+// and 262 us (6.2 and 6.1 TB/s). Issue is active in 45 to 49 % of the cycles at 16 warps to an SM: what is left are
+// the dependent sums of a row. 9001 x 771 in binary32, rows at any alignment: 27 and 51 us (4.2 and 3.3 TB/s). Of 16384
+// columns in bf16 the backward pass has no room in shared memory for its rows and weights and reads rows from memory
+// twice (4096 rows 551 us, forward 137).
 #pragma once
 
 #include <atomic>
@@ -237,13 +238,24 @@ __device__ __forceinline__ T *out_row(const RowsView &v, int64_t r)
 template <class T, int VEC, int E, int K, int TEAM>
 __device__ __forceinline__ void weights(const void *w, int64_t at, const Team &team, int width, float2 (&v)[K][E / 2])
 {
+    const T *const from = static_cast<const T *>(w) + at;
+    const bool whole = VEC != 1 && w && (reinterpret_cast<uintptr_t>(from) & 15u) == 0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+        if constexpr (VEC != 1) {
+            const int c = column<VEC, E, TEAM>(team, k, 0);
+            if (whole && c + VEC <= width) {
+                Unit<T> u;
+                u.w = *reinterpret_cast<const uint4 *>(from + c);
+                u.get(v[k]);
+                continue;
+            }
+        }
         float e[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) {
             const int c = column<VEC, E, TEAM>(team, k, i);
-            e[i] = c >= width ? 0.0f : w ? load1(static_cast<const T *>(w) + at + c) : 1.0f;
+            e[i] = c >= width ? 0.0f : w ? load1(from + c) : 1.0f;
         }
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) v[k][i] = make_float2(e[2 * i], e[2 * i + 1]);
@@ -419,47 +431,61 @@ __global__ void __launch_bounds__(kMost, 1) forward_kernel(BlockArgs a, int team
 }
 
 // How the rows are shared out: `segments` blocks to each gate, a block's teams taking
-// its rows in turn; or, with segments 0, whole gates to a team, in turn.
+// its rows in turn; or, with segments 0, whole gates to a team, in turn. A block that has all of a gate's
+// rows finishes its gradient itself.
 struct Shares {
     int segments;
     int64_t blocks, each;  // rows to a segment
 };
-__host__ __device__ inline Shares shares_of(int64_t rows, int64_t groups)
+inline Shares shares_of(int64_t rows, int64_t groups)
 {
     Shares s;
-    if (groups >= 2 * kBlocks) {
+    const int64_t in_group = rows / groups;
+    if (groups >= 2 * kBlocks && in_group < 16) {  // too few rows to a gate for a block's beginning and end
         s.segments = 0;
         s.blocks = kBlocks;
         s.each = 0;
         return s;
     }
-    const int64_t in_group = rows / groups;
-    int64_t n = (kBlocks + groups - 1) / groups;
-    if (n > in_group) n = in_group;
-    s.each = (in_group + n - 1) / n;
+    // Blocks come in waves of kBlocks: the number of segments for which the rows of all waves are fewest, of up
+    // to four waves' blocks. (16384 x 4096 in bf16, backward, 64 gates: three segments, a wave and a quarter, 237 us.)
+    int64_t best = 0, least = 0;
+    for (int64_t n = 1; n <= in_group && (n == 1 || groups * n <= 4 * kBlocks); ++n) {
+        const int64_t each = (in_group + n - 1) / n, blocks = groups * ((in_group + each - 1) / each);
+        const int64_t cost = (blocks + kBlocks - 1) / kBlocks * (each + 2);  // a block's own beginning and end, in rows
+        if (!best || cost < least) {
+            best = n;
+            least = cost;
+        }
+    }
+    s.each = (in_group + best - 1) / best;
     s.segments = int((in_group + s.each - 1) / s.each);
     s.blocks = groups * s.segments;
     return s;
 }
 
-// A thread's sums over its columns, added up over the block's teams in their order.
-template <int VEC, int E, int K, int TEAM>
-__device__ __forceinline__ void hand_in(const Team &team, const float2 (&v)[K][E / 2], float *sh, float *out, int width)
+// A thread's sums over its columns, added up over the block's teams in their order: finish(column, sum).
+template <int VEC, int E, int K, int TEAM, class F>
+__device__ __forceinline__ void hand_in(const Team &team, const float2 (&v)[K][E / 2], float *sh, int width, F finish)
 {
-    float *const mine = team.count == 1 ? out : sh + team.id * width;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int i = 0; i < E; ++i) {
             const int c = column<VEC, E, TEAM>(team, k, i);
-            if (c < width) mine[c] = i & 1 ? v[k][i / 2].y : v[k][i / 2].x;
+            const float mine = i & 1 ? v[k][i / 2].y : v[k][i / 2].x;
+            if (c >= width) continue;
+            if (team.count == 1)
+                finish(c, mine);
+            else
+                sh[team.id * width + c] = mine;
         }
     if (team.count == 1) return;
     __syncthreads();
     for (int c = threadIdx.x; c < width; c += blockDim.x) {
         float s = sh[c];
         for (int t = 1; t < team.count; ++t) s += sh[t * width + c];
-        out[c] = s;
+        finish(c, s);
     }
     __syncthreads();
 }
@@ -682,16 +708,24 @@ __global__ void __launch_bounds__(kMost, 1) backward_kernel(BlockArgs a, int tea
     wait_copies(0);
     __syncthreads();  // the rows' memory is free
     float *const joint = reinterpret_cast<float *>(rows);
-    float *const out = a.work + int64_t(blockIdx.x) * width;
-    if (a.w_pre) hand_in<VEC, E, K, TEAM>(team, q, joint, out, width);
+    float *const q_out = a.work + int64_t(blockIdx.x) * width, *const p_out = q_out + shares.blocks * width;
+    if (a.w_pre) hand_in<VEC, E, K, TEAM>(team, q, joint, width, [&](int c, float sum) { q_out[c] = sum; });
     if constexpr (MANY) {
-        if (a.w_post) hand_in<VEC, E, K, TEAM>(team, dw1, joint, out + shares.blocks * width, width);
+        if (a.w_post) hand_in<VEC, E, K, TEAM>(team, dw1, joint, width, [&](int c, float sum) { p_out[c] = sum; });
     } else {
-        if (a.w_post || a.gate) hand_in<VEC, E, K, TEAM>(team, p, joint, out + shares.blocks * width, width);
+        if (a.gate && shares.segments == 1) {
+            const int64_t at = (blockIdx.x / shares.segments) * int64_t(width);
+            hand_in<VEC, E, K, TEAM>(team, p, joint, width, [&](int c, float sum) {
+                const float w1 = a.w_post ? load1(static_cast<const T *>(a.w_post) + c) : 1.0f;
+                store1(static_cast<T *>(a.dgate) + at + c, w1 * sum);
+                p_out[c] = load1(static_cast<const T *>(a.gate) + at + c) * sum;
+            });
+        } else if (a.w_post || a.gate) {
+            hand_in<VEC, E, K, TEAM>(team, p, joint, width, [&](int c, float sum) { p_out[c] = sum; });
+        }
     }
 }
 
-// The sums of the weights' gradients over the blocks.
 // Every step-th of `count` rows from `first` on, eight loads at a time.
 __device__ __forceinline__ float sum_rows(const float *p, int width, int first, int count, int step)
 {
@@ -731,12 +765,13 @@ __global__ void __launch_bounds__(1024) weights_kernel(BlockArgs a, Shares share
         if (there && row == 0) store1(static_cast<T *>(a.dw_pre) + c, s);
         return;
     }
-    if (!a.w_post && !(a.gate && shares.segments)) return;
+    const bool done = !a.gate || shares.segments <= 1;  // the sums are dw1's own
+    if (!a.w_post && done) return;
     const float *const sums = a.work + shares.blocks * a.width;
-    if (!shares.segments || !a.gate || a.groups == 1) {
+    if (done || a.groups == 1) {
         const float s = total(there ? sum_rows(sums + c, a.width, row, blocks, 32) : 0.0f);
         if (!there || row) return;
-        if (!shares.segments || !a.gate) {  // sums of dw1 itself
+        if (done) {
             store1(static_cast<T *>(a.dw_post) + c, s);
             return;
         }
@@ -746,11 +781,21 @@ __global__ void __launch_bounds__(1024) weights_kernel(BlockArgs a, Shares share
     }
     const float w = there && a.w_post ? load1(static_cast<const T *>(a.w_post) + c) : 1.0f;
     float dw1 = 0.0f;
-    for (int64_t g = row; there && g < a.groups; g += 32) {
-        const float s = sum_rows(sums + g * shares.segments * a.width + c, a.width, 0, shares.segments, 1);
+    // few gates: several warps to each
+    const int share = a.groups <= 16 ? 32 / int(a.groups) : 1, part = row % share;
+    for (int64_t g = row / share; g < a.groups; g += 32 / share) {
+        float s = there ? sum_rows(sums + g * shares.segments * a.width + c, a.width, part, shares.segments, share) : 0.0f;
+        if (share > 1) {  // once around: the first 32 / share gates are all
+            sh[row][lane] = s;
+            asm volatile("bar.sync 1, %0;" ::"r"(int(a.groups) * share * 32) : "memory");
+            s = 0.0f;
+            for (int i = 0; i < share; ++i) s += sh[row - part + i][lane];
+        }
+        if (!there || part) continue;
         store1(static_cast<T *>(a.dgate) + g * a.width + c, w * s);
         dw1 = fmaf(s, load1(static_cast<const T *>(a.gate) + g * a.width + c), dw1);
     }
+    __syncthreads();
     dw1 = total(dw1);
     if (a.w_post && there && row == 0) store1(static_cast<T *>(a.dw_post) + c, dw1);
 }
@@ -824,6 +869,7 @@ template <class T, int VEC, int E, int K, int TEAM>
 cudaError_t backward(const BlockArgs &a, cudaStream_t st)
 {
     const Shares shares = shares_of(a.rows, a.groups);
+    if (shares.blocks >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
     const bool all = a.o.ptr && a.n.ptr && a.x_new.ptr && shares.segments;
     Shape s = shape_of(a, VEC, E * K, all ? TEAM : 0, 4, shares.segments > 0);
     static std::atomic<uint64_t> allowed[3];
@@ -841,7 +887,7 @@ cudaError_t backward(const BlockArgs &a, cudaStream_t st)
     if (cudaError_t e = allow(kernel, allowed[which])) return e;
     kernel<<<unsigned(shares.blocks), s.team * s.teams, s.bytes, st>>>(a, s.team, s.ring, shares);
     if (cudaError_t e = cudaGetLastError()) return e;
-    if (!a.w_pre && !a.w_post && !(a.gate && shares.segments)) return cudaSuccess;
+    if (!a.w_pre && !a.w_post && !(a.gate && shares.segments > 1)) return cudaSuccess;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned((a.width + 31) / 32), 2);
     cfg.blockDim = dim3(1024);

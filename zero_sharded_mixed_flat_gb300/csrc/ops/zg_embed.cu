@@ -18,11 +18,10 @@
 //   join   adds the partial rows of tokens that reach over several tiles, in their
 //          order.
 //
-// Measured, 50257 x 768 in bf16: the lookup of 8192 tokens 4.5 us, 65536 18 us (200 MB, of which the table's rows
-// come out of L2 in part); the gradient of 8192 tokens 25 us (the sort 14, of which 12 are the rows
-// without a token's; the sum 7 after it, the join 5), of 65536 78 us; 8192 tokens at 4096 columns 82 us for 479 MB
-// (5.8 TB/s). Added to another gradient in place, 20011 tokens at 771 columns in binary32, 51 us. All tokens the
-// same: 41 us for 8192.
+// Measured, a table of 50257 x 768 in bf16: the lookup of 8192 tokens 4.5 us, of 65536 17 us. The gradient of 8192
+// tokens 25 us for 90 MB: the sort 14 us, beside which most rows without a token are written, then sum and join; of
+// 65536 tokens 78 us; of 8192 at 4096 columns 82 us (479 MB, 5.8 TB/s). Added to another gradient in place, 20011
+// tokens at 771 columns in binary32, 51 us, beside it 89. All 8192 tokens the same: 41 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>

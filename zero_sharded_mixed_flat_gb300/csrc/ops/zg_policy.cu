@@ -15,10 +15,10 @@
 // maximum and sum, is a stream.
 //
 // Measured at 4096 x 50257 in bf16: the loss alone 72 us (5.7 TB/s), loss and gradient 145 (5.7 TB/s of the once-read,
-// once-written bytes), the gradient alone 100 with a third of the rows cut off or padding and so not read, 118
-// without; in binary32 131, 318 and 203 us. 777 x 131075 in bf16, the loss alone and the gradient 39 and 60 us. 37 x
-// 50257 in binary32, eight blocks to a row, 7.9 us. Both in one launch issue in half of the cycles, with
-// two rows to an SM; the exponentials are 41 % of the time of their pipe.
+// once-written bytes), the gradient alone 115 (7.2 TB/s); in binary32 131, 316 and 233 us. 777 x 131075 in bf16, the
+// loss alone and the gradient 39 and 60 us. 37 x 50257 in binary32, eight blocks to a row, 7.9 us. With gradient rows
+// that are not aligned as the logits' are, both 162 and the gradient 122 us. Both in one launch issue in 51 % of the
+// cycles with two rows to an SM; what is left is what the phases of a row wait for.
 #include <cooperative_groups.h>
 
 #include <map>
