@@ -910,7 +910,8 @@ def embed_grad(drows, tokens, vocab: int, scale: float = 1.0, add=None, out=None
 def _weight_ptr(w, x: torch.Tensor, shape, what: str) -> int | None:
     if w is None:
         return None
-    _beside(w, x, shape, what)
+    if not (isinstance(w, torch.Tensor) and w.dtype == x.dtype and w.shape == shape and w.get_device() == x.get_device()):
+        _beside(w, x, shape, what)
     if not w.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return w.data_ptr()
@@ -921,7 +922,9 @@ def _block(x, w_pre, o, w_post, gate, res_scale: float, eps: float) -> _Block:
     shape = x.shape
     if not shape:
         raise ValueError("x must have rows")
-    _like(x, x, "x")
+    if not x.is_cuda:
+        raise TypeError("x must be a CUDA tensor")
+    p_x, x_stride = _rows_like(x, x, "x")
     width = shape[-1]
     vector = (width,)
     groups, p_gate, p_o, o_stride = 1, None, None, 0
@@ -934,7 +937,7 @@ def _block(x, w_pre, o, w_post, gate, res_scale: float, eps: float) -> _Block:
     if o is not None:
         p_o, o_stride = _rows_like(o, x, "o")
     rows = shape[0] if len(shape) == 2 else x.numel() // width if width else 0
-    return _Block(rows, width, groups, dtype, x.data_ptr(), p_o, _stride_of_rows(x, "x"), o_stride,
+    return _Block(rows, width, groups, dtype, p_x, p_o, x_stride, o_stride,
                   _weight_ptr(w_post, x, vector, "w_post"), p_gate, _weight_ptr(w_pre, x, vector, "w_pre"), res_scale, eps)
 
 
@@ -942,6 +945,12 @@ def _rows_like(t, x: torch.Tensor, what: str) -> tuple:
     """Address and row stride of an optional tensor like x."""
     if t is None:
         return None, 0
+    shape = x.shape
+    if not (isinstance(t, torch.Tensor) and t.dtype == x.dtype and t.shape == shape and t.get_device() == x.get_device()):
+        _like(t, x, what)  # says what differs
+    strides = t.stride()
+    if len(strides) == 2 and strides[1] == 1 and shape[0] > 1:
+        return t.data_ptr(), strides[0]
     _like(t, x, what)
     return t.data_ptr(), _stride_of_rows(t, what)
 
@@ -990,16 +999,22 @@ def block_norm_grad(x, kept, dn=None, dx_new=None, w_pre=None, o=None, w_post=No
     if kept is None:
         raise ValueError("kept is None: call block_norm with keep=True")
     b = _block(x, w_pre, o, w_post, gate, res_scale, eps)
-    dx, do = out if out is not None else (_new_rows(x), None if o is None else _new_rows(x))
-    dw_pre, dw_post, dgate = (None if w is None else _new_rows(w) for w in (w_pre, w_post, gate))
+    if out is not None:
+        dx, do = out
+        (p_dx, dx_stride), (p_do, do_stride) = _rows_like(dx, x, "dx"), _rows_like(do, x, "do")
+    else:
+        dx, do = _new_rows(x), None if o is None else _new_rows(x)
+        p_dx, dx_stride, p_do, do_stride = dx.data_ptr(), b.width, None if o is None else do.data_ptr(), b.width
+    dw_pre, dw_post, dgate = (None if w is None else torch.empty_like(w) for w in (w_pre, w_post, gate))
     L = lib()
     work_bytes = L.zg_block_norm_workspace(b.rows, b.width, b.groups)
     _check(min(work_bytes, 0), "zg_block_norm_workspace")
     work = _workspace(work_bytes, x)
     _check(L.zg_block_norm_grad(ctypes.byref(b), _side(kept, torch.float32, (2, b.rows), x, "kept"),
-                                *_rows_like(dn, x, "dn"), *_rows_like(dx_new, x, "dx_new"), *_rows_like(dx, x, "dx"),
-                                *_rows_like(do, x, "do"),
-                                *(None if w is None else w.data_ptr() for w in (dw_pre, dw_post, dgate)),
+                                *_rows_like(dn, x, "dn"), *_rows_like(dx_new, x, "dx_new"), p_dx, dx_stride, p_do, do_stride,
+                                None if dw_pre is None else dw_pre.data_ptr(),
+                                None if dw_post is None else dw_post.data_ptr(),
+                                None if dgate is None else dgate.data_ptr(),
                                 None if work is None else work.data_ptr(), work_bytes, _stream_of(x)), "zg_block_norm_grad")
     return dx, do, dw_pre, dw_post, dgate
 

@@ -447,10 +447,13 @@ inline Shares shares_of(int64_t rows, int64_t groups)
         s.each = 0;
         return s;
     }
-    // Blocks come in waves of kBlocks: the number of segments for which the rows of all waves are fewest, of up
-    // to four waves' blocks. (16384 x 4096 in bf16, backward, 64 gates: three segments, a wave and a quarter, 237 us.)
+    // Blocks come in waves of kBlocks: of the numbers of segments that fill one to four waves, that for which the
+    // rows of all waves are fewest. (16384 x 4096 in bf16, backward, 64 gates: three segments, a wave and a quarter,
+    // 237 us, seven 190.)
     int64_t best = 0, least = 0;
-    for (int64_t n = 1; n <= in_group && (n == 1 || groups * n <= 4 * kBlocks); ++n) {
+    for (int waves = 1; waves <= 4; ++waves) {
+        int64_t n = waves * kBlocks / groups;
+        n = n < 1 ? 1 : n > in_group ? in_group : n;
         const int64_t each = (in_group + n - 1) / n, blocks = groups * ((in_group + each - 1) / each);
         const int64_t cost = (blocks + kBlocks - 1) / kBlocks * (each + 2);  // a block's own beginning and end, in rows
         if (!best || cost < least) {
