@@ -145,7 +145,8 @@ struct Source {
             const uint32_t there = to + team.tid * 16;
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (column<VEC, E, TEAM>(team, k, 0) < width) copy16(there + k * team.threads * 16, mine + k * team.threads * VEC);
+                if (column<VEC, E, TEAM>(team, k, 0) < width)
+                    copy16(there + k * team.threads * 16, mine + k * team.threads * VEC);
         }
     }
     // Once its own copies are here, and before the team's barrier: zeros from a row's end on, over what
@@ -568,7 +569,8 @@ __global__ void __launch_bounds__(kMost, 1) backward_kernel(BlockArgs a, int tea
             const float w1 = in && a.w_post ? load1(static_cast<const T *>(a.w_post) + c) : 1.0f;
             const float g = in && a.gate ? load1(static_cast<const T *>(a.gate) + now.group * width + c) : 1.0f;
             wide[u_of.index(c)] = in ? w1 * g : 0.0f;
-            (wide + Wide<VEC, E, K, TEAM>::size(width))[w2_of.index(c)] = in ? (a.w_pre ? load1(static_cast<const T *>(a.w_pre) + c) : 1.0f) : 0.0f;
+            const float w2 = in && a.w_pre ? load1(static_cast<const T *>(a.w_pre) + c) : 1.0f;
+            (wide + Wide<VEC, E, K, TEAM>::size(width))[w2_of.index(c)] = in ? w2 : 0.0f;
         }
         __syncthreads();
     }

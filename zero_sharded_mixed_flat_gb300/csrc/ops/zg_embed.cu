@@ -651,7 +651,10 @@ int tile_rows(int64_t n, int64_t slabs)
     return rows;
 }
 
-bool whole(const void *p, int64_t stride, int size) { return (reinterpret_cast<uintptr_t>(p) | uintptr_t(stride * size)) % 16 == 0; }
+bool whole(const void *p, int64_t stride, int size)
+{
+    return (reinterpret_cast<uintptr_t>(p) | uintptr_t(stride * size)) % 16 == 0;
+}
 
 template <class T, class D, int VEC>
 cudaError_t sum_and_join(const EmbedArgs &a, const SumPlan &p, cudaStream_t st)
