@@ -36,10 +36,13 @@ namespace zg {
 namespace {
 
 constexpr int kMost = 512;     // threads of a block
-constexpr int kBlocks = 152;   // blocks that share the rows, one to an SM
+constexpr int kBlocks = 152;   // SMs
+// Blocks to an SM: two where a thread's few columns fit half of the registers.
+template <int COLUMNS, bool ALL>
+constexpr int kToSm = ALL && COLUMNS <= 8 ? 2 : 1;
 constexpr int kStages = 4;     // rows of a team in shared memory, at most
 constexpr int kTeams = 8;      // of a block, at most
-constexpr int kMemory = 224 * 1024;  // bytes of a block, an SM's one
+constexpr int kMemory = 224 * 1024;  // of an SM's blocks
 
 // The threads that share a row: whole warps of a block.
 struct Team {
@@ -337,7 +340,7 @@ __device__ __forceinline__ void clear(char *p, int bytes)
 
 // ALL: x_new, o and w_pre are there, and rows are staged.
 template <class T, int VEC, int E, int K, int TEAM, bool ALL>
-__global__ void __launch_bounds__(kMost, 1) forward_kernel(BlockArgs a, int team_threads, Ring ring)
+__global__ void __launch_bounds__(kMost, (kToSm<E * K, ALL>)) forward_kernel(BlockArgs a, int team_threads, Ring ring)
 {
     __shared__ __align__(16) float sh[kTeams * 2 * kMost / 32];
     extern __shared__ __align__(16) char rows[];
@@ -438,25 +441,25 @@ struct Shares {
     int segments;
     int64_t blocks, each;  // rows to a segment
 };
-inline Shares shares_of(int64_t rows, int64_t groups)
+inline Shares shares_of(int64_t rows, int64_t groups, int wave)
 {
     Shares s;
     const int64_t in_group = rows / groups;
-    if (groups >= 2 * kBlocks && in_group < 16) {  // too few rows to a gate for a block's beginning and end
+    if (groups >= 2 * wave && in_group < 16) {  // too few rows to a gate for a block's beginning and end
         s.segments = 0;
-        s.blocks = kBlocks;
+        s.blocks = wave;
         s.each = 0;
         return s;
     }
-    // Blocks come in waves of kBlocks: of the numbers of segments that fill one to four waves, that for which the
+    // Blocks come in waves: of the numbers of segments that fill one to four waves, that for which the
     // rows of all waves are fewest. (16384 x 4096 in bf16, backward, 64 gates: three segments, a wave and a quarter,
     // 237 us, seven 190.)
     int64_t best = 0, least = 0;
     for (int waves = 1; waves <= 4; ++waves) {
-        int64_t n = waves * kBlocks / groups;
+        int64_t n = waves * wave / groups;
         n = n < 1 ? 1 : n > in_group ? in_group : n;
         const int64_t each = (in_group + n - 1) / n, blocks = groups * ((in_group + each - 1) / each);
-        const int64_t cost = (blocks + kBlocks - 1) / kBlocks * (each + 2);  // a block's own beginning and end, in rows
+        const int64_t cost = (blocks + wave - 1) / wave * (each + 2);  // a block's own beginning and end, in rows
         if (!best || cost < least) {
             best = n;
             least = cost;
@@ -497,7 +500,7 @@ __device__ __forceinline__ void hand_in(const Team &team, const float2 (&v)[K][E
 // MANY: whole gates to a team (segments is 0), whose sums it finishes itself. ALL: every tensor of
 // rows is there and staged, which leaves a third of the instructions out.
 template <class T, int VEC, int E, int K, int TEAM, bool MANY, bool ALL>
-__global__ void __launch_bounds__(kMost, 1) backward_kernel(BlockArgs a, int team_threads, Ring ring, Shares shares)
+__global__ void __launch_bounds__(kMost, (kToSm<E * K, ALL && VEC == 1>)) backward_kernel(BlockArgs a, int team_threads, Ring ring, Shares shares)
 {
     __shared__ __align__(16) float sh[kTeams * 6 * kMost / 32];
     extern __shared__ __align__(16) char rows[];
@@ -824,19 +827,20 @@ struct Shape {
     Ring ring;
     size_t bytes;
 };
-Shape shape_of(const BlockArgs &a, int vec, int columns, int team, int tensors, bool wide)
+Shape shape_of(const BlockArgs &a, int vec, int columns, int team, int tensors, bool wide, int to_sm)
 {
     const int size = a.dtype == ZG_DTYPE_BF16 ? 2 : 4;
     Shape s;
     s.team = team ? team : ((a.width + columns - 1) / columns + 31) / 32 * 32;
     s.teams = kMost / s.team;
     if (s.teams > kTeams) s.teams = kTeams;
-    if (a.rows < int64_t(s.teams) * kBlocks) s.teams = int((a.rows + kBlocks - 1) / kBlocks);  // few rows: all SMs
+    const int64_t blocks = kBlocks * to_sm;
+    if (a.rows < s.teams * blocks) s.teams = int((a.rows + blocks - 1) / blocks);  // few rows: all SMs
     const int held = team ? team * columns : a.width;  // columns of a stage
     s.ring.slot = (held * size + (vec == 1 ? 48 : 0) + 15) / 16 * 16;  // a head, and two units that are cleared
     const size_t row = size_t(s.teams) * tensors * s.ring.slot;
     const size_t beside = wide ? size_t(held + 7) / 8 * 64 : 0;  // two weights in binary32
-    s.ring.stages = int((size_t(kMemory) - beside) / row);
+    s.ring.stages = beside < size_t(kMemory / to_sm) ? int((size_t(kMemory / to_sm) - (to_sm - 1) * 4096 - beside) / row) : 0;
     if (s.ring.stages > kStages) s.ring.stages = kStages;
     s.bytes = row * s.ring.stages + beside;
     const size_t joint = s.teams > 1 ? size_t(s.teams) * a.width * 4 : 0;  // of the weights' sums
@@ -860,35 +864,40 @@ cudaError_t allow(F *kernel, std::atomic<uint64_t> &devices)
 template <class T, int VEC, int E, int K, int TEAM>
 cudaError_t forward(const BlockArgs &a, cudaStream_t st)
 {
-    const Shape s = shape_of(a, VEC, E * K, TEAM, 2, false);
-    const bool all = s.ring.stages > 0 && a.o.ptr && a.x_new.ptr && a.w_pre;
+    const bool every = a.o.ptr && a.x_new.ptr && a.w_pre;
+    int to_sm = kToSm<E * K, true>;
+    Shape s = shape_of(a, VEC, E * K, TEAM, 2, false, to_sm);
+    const bool all = every && s.ring.stages > 0;
+    if (!all) s = shape_of(a, VEC, E * K, TEAM, 2, false, to_sm = 1);
     auto *kernel = all ? &forward_kernel<T, VEC, E, K, TEAM, true> : &forward_kernel<T, VEC, E, K, TEAM, false>;
     static std::atomic<uint64_t> allowed[2];
     if (cudaError_t e = allow(kernel, allowed[all])) return e;
     const int64_t want = (a.rows + s.teams - 1) / s.teams;
-    kernel<<<unsigned(want < kBlocks ? want : kBlocks), s.team * s.teams, s.bytes, st>>>(a, s.team, s.ring);
+    kernel<<<unsigned(want < kBlocks * to_sm ? want : kBlocks * to_sm), s.team * s.teams, s.bytes, st>>>(a, s.team, s.ring);
     return cudaGetLastError();
 }
 
 template <class T, int VEC, int E, int K, int TEAM>
 cudaError_t backward(const BlockArgs &a, cudaStream_t st)
 {
-    const Shares shares = shares_of(a.rows, a.groups);
-    if (shares.blocks >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
-    const bool all = a.o.ptr && a.n.ptr && a.x_new.ptr && shares.segments;
-    Shape s = shape_of(a, VEC, E * K, all ? TEAM : 0, 4, shares.segments > 0);
+    constexpr int kMany = kToSm<E * K, VEC == 1>;
     static std::atomic<uint64_t> allowed[3];
     auto *kernel = &backward_kernel<T, VEC, E, K, 0, false, false>;
     int which = 0;
-    if (!shares.segments) {
-        kernel = &backward_kernel<T, VEC, E, K, 0, true, false>;
-        which = 1;
-    } else if (all && s.ring.stages > 0) {
+    Shares shares = shares_of(a.rows, a.groups, kBlocks * kMany);
+    Shape s = shape_of(a, VEC, E * K, TEAM, 4, true, kMany);
+    if (a.o.ptr && a.n.ptr && a.x_new.ptr && shares.segments && s.ring.stages > 0) {
         kernel = &backward_kernel<T, VEC, E, K, TEAM, false, true>;
         which = 2;
-    } else if (all && TEAM) {
-        s = shape_of(a, VEC, E * K, 0, 4, true);
+    } else {
+        shares = shares_of(a.rows, a.groups, kBlocks);
+        s = shape_of(a, VEC, E * K, 0, 4, shares.segments > 0, 1);
+        if (!shares.segments) {
+            kernel = &backward_kernel<T, VEC, E, K, 0, true, false>;
+            which = 1;
+        }
     }
+    if (shares.blocks >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
     if (cudaError_t e = allow(kernel, allowed[which])) return e;
     kernel<<<unsigned(shares.blocks), s.team * s.teams, s.bytes, st>>>(a, s.team, s.ring, shares);
     if (cudaError_t e = cudaGetLastError()) return e;
@@ -908,12 +917,13 @@ cudaError_t backward(const BlockArgs &a, cudaStream_t st)
 template <class T, bool BACK>
 cudaError_t of_type(const BlockArgs &a, cudaStream_t st)
 {
-    // chunks of E columns, K of them to a thread, and at most MOST threads to a row
+    // chunks of E columns, K of them to a thread, and at most MOST threads to a row (backward, aligned rows in bf16, 8
+    // columns to a thread against 16: 8192 x 768 25 and 27 us, 32768 x 1024 90 and 76, 32768 x 2048 178 and 144)
 #define ZG_CASE(MOST, VEC, E, K, TEAM) \
     if (a.width <= (E) * (K) * (MOST)) return BACK ? backward<T, VEC, E, K, TEAM>(a, st) : forward<T, VEC, E, K, TEAM>(a, st);
     constexpr int N = Unit<T>::kN;
     if (in_units(a, BACK)) {
-        ZG_CASE(256, N, N, 8 / N, 0) ZG_CASE(kMost, N, N, 16 / N, 0) ZG_CASE(kMost, N, N, 32 / N, 0)
+        ZG_CASE(BACK ? 96 : 256, N, N, 8 / N, 0) ZG_CASE(kMost, N, N, 16 / N, 0) ZG_CASE(kMost, N, N, 32 / N, 0)
     } else {
         ZG_CASE(64, 1, 8, 1, 64) ZG_CASE(128, 1, 8, 1, 128) ZG_CASE(256, 1, 8, 1, 256) ZG_CASE(512, 1, 8, 1, 512)
         ZG_CASE(kMost, 1, 8, 2, 0) ZG_CASE(kMost, 1, 8, 4, 0)
