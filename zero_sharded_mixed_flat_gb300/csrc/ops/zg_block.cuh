@@ -926,7 +926,7 @@ cudaError_t of_type(const BlockArgs &a, cudaStream_t st)
         ZG_CASE(BACK ? 96 : 256, N, N, 8 / N, 0) ZG_CASE(kMost, N, N, 16 / N, 0) ZG_CASE(kMost, N, N, 32 / N, 0)
     } else {
         ZG_CASE(64, 1, 8, 1, 64) ZG_CASE(128, 1, 8, 1, 128) ZG_CASE(256, 1, 8, 1, 256) ZG_CASE(512, 1, 8, 1, 512)
-        ZG_CASE(kMost, 1, 8, 2, 0) ZG_CASE(kMost, 1, 8, 4, 0)
+        ZG_CASE(kMost, 1, 8, 2, 512) ZG_CASE(kMost, 1, 8, 4, 0)
     }
 #undef ZG_CASE
     return cudaErrorInvalidValue;
