@@ -18,11 +18,11 @@
 // row in shared memory again where a sum has to be known first.
 //
 // Measured at 16384 x 4096 in bf16: forward 94 us (5.7 TB/s), backward 150 (5.4 TB/s) and some 6 to 10 for the sums of
-// the weights' gradients after it; with a gate for each of 64 sequences 182, of 512 229, of every row 734. In binary32 172
+// the weights' gradients after it; with a gate for each of 64 sequences 183, of 512 231, of every row 737. In binary32 172
 // and 262 us (6.2 and 6.1 TB/s). Issue is active in 45 to 49 % of the cycles at 16 warps to an SM: what is left are
-// the dependent sums of a row. 9001 x 771 in binary32, rows at any alignment: 27 and 51 us (4.2 and 3.3 TB/s). Of 16384
-// columns in bf16 the backward pass has no room in shared memory for its rows and weights and reads rows from memory
-// twice (4096 rows 551 us, forward 137).
+// the dependent sums of a row. 32768 x 2048 in bf16 91 and 145 us (5.9 and 5.6 TB/s). 9001 x 771 in binary32, rows at any
+// alignment: 23 and 44 us (4.8 and 3.8 TB/s); 2000 x 4099 35 and 80. Of 16384 columns in bf16 the backward pass has
+// no room in shared memory for its rows and weights and reads rows from memory twice (4096 rows 551 us, forward 137).
 #pragma once
 
 #include <atomic>
