@@ -208,6 +208,51 @@ def test_zero_rows_huge_rows_and_non_finite_ones(dtype):
     assert bool(torch.isnan(bad_n[5]).all()) and bool(torch.isnan(bad_n[7]).any())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,groups,d", [(3001, 1, 64), (3001, 1, 520), (3001, 1, 640), (3000, 1000, 520), (3000, 1000, 1600),
+                                        (3001, 1, 1280), (3001, 1, 1600), (2500, 5, 2880), (1200, 1, 5000), (700, 1, 10000)])
+def test_non_finite_rows_stay_alone_where_lanes_have_no_column(n, groups, d, dtype):
+    """Aligned widths that leave lanes of a team without a column, rows that follow one another in the same shared
+    memory: the finite rows have the same bits whatever the others, or an earlier call, held."""
+    dt, gen = DT[dtype], torch.Generator("cuda").manual_seed(95)
+
+    def rand_here(*shape, scale=1.0, shift=0.0):
+        return torch.randn(*shape, generator=gen, device="cuda").mul_(scale).add_(shift).to(dt)
+
+    x, o = rand_here(n, d, scale=3.0), rand_here(n, d, scale=0.7)
+    dn, dy = rand_here(n, d, scale=1e-3), rand_here(n, d, scale=1e-3)
+    block = {"w_post": rand_here(d, scale=0.1, shift=1.0), "w_pre": rand_here(d, scale=0.1, shift=1.0),
+             "gate": rand_here(groups, d, scale=0.3, shift=0.5), "res_scale": R, "eps": EPS}
+
+    def both(x, o, dn, dy):
+        x_new, nn, kept = zb.block_norm(x, o=o, keep=True, **block)
+        return [x_new, nn, *zb.block_norm_grad(x, kept, dn, dy, o=o, **block)]
+
+    clean = both(x, o, dn, dy)
+    # the first and the last rows of the first and the last gate by the formulas, which take each row by itself
+    each = n // groups
+    for cut in (slice(0, min(each, 20)), slice(n - min(each, 20), n)):
+        g = block["gate"][cut.start // each][None].cpu()
+        w1, w2 = block["w_post"].cpu(), block["w_pre"].cpu()
+        f = ref.block(x[cut].cpu(), o[cut].cpu(), w1, g, w2, R, EPS)
+        want, err = ref.block_grad(x[cut].cpu(), dn[cut].cpu(), dy[cut].cpu(), o[cut].cpu(), w1, g, w2, R, EPS)
+        for got, v, e in ((clean[0], f["x"], f["err"]["x"]), (clean[1], f["n"], f["err"]["n"]), (clean[2], want[0], err[0]),
+                          (clean[3], want[1], err[1])):
+            ref.check(got[cut], v, ref.stored(v, e, dt))
+    nan = torch.full_like(x, math.nan)
+    for _ in range(3):
+        both(nan, nan, nan, nan)
+        again = both(x, o, dn, dy)
+        assert all(torch.equal(p, q) for p, q in zip(again, clean))
+    good = torch.arange(n, device="cuda") % 3 != 1
+    spoilt = [t.clone() for t in (x, o, dn, dy)]
+    for t, bad in zip(spoilt, (math.nan, math.inf, -math.inf, math.nan)):
+        t[1::3, :8] = bad
+    for which in ((0,), (1,), (2,), (3,), (0, 1, 2, 3)):
+        got = both(*(spoilt[i] if i in which else t for i, t in enumerate((x, o, dn, dy))))
+        assert all(torch.equal(p[good], q[good]) for p, q in zip(got[:4], clean)), which
+
+
 def test_gradient_against_differences():
     c, up = make(5, 24, "f32", 5, seed=100)
     k, u = cuda(c), cuda(up)

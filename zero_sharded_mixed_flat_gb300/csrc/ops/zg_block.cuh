@@ -14,8 +14,8 @@
 // Bound by memory: forward reads two rows and writes two, backward reads four and
 // writes two, of which each is moved once. A team of warps works on a row; it copies its next
 // rows into shared memory while it computes (cp.async: an aligned row's units are
-// copied and read by the same thread, so they need no barrier), and goes over the
-// row in shared memory again where a sum has to be known first.
+// copied and read by the same thread, and by no other, so they need no barrier), and goes
+// over the row in shared memory again where a sum has to be known first.
 //
 // Measured at 16384 x 4096 in bf16: forward 94 us (5.7 TB/s), backward 150 (5.4 TB/s) and some 6 to 10 for the sums of
 // the weights' gradients after it; with a gate for each of 64 sequences 183, of 512 231, of every row 737. In binary32 172
@@ -169,8 +169,11 @@ struct Source {
             }
         }
     }
-    // Chunk k of row r. Without TEAM, columns past the width are column 0 again, or (behind a row's end in its
-    // last unit) zero.
+    // Chunk k of row r. Of aligned rows, places past the width are zero without a look: at any other column another
+    // thread's copy may still be on its way, and a NaN found there would stay one times a weight of zero. Of
+    // others, where the team's barrier has made every copy visible, they are (without TEAM) column 0 again.
+    // (The load's condition costs 2 to 4 %: 16384 x 4096 in bf16 96 -> 99 us forward, 156 -> 158 backward, 4096 x
+    // 16384 136 -> 141 and 550 -> 573; a branch in its place 102 for 96 at 32768 x 2048 forward.)
     __device__ __forceinline__ void get(const Team &team, int64_t r, int stage, bool staged, int k, int width,
                                         float2 (&v)[E / 2]) const
     {
@@ -193,20 +196,26 @@ struct Source {
 #pragma unroll
             for (int i = 0; i < E / 2; ++i) v[i] = make_float2(e[2 * i], e[2 * i + 1]);
         } else {
-            const int c = column<VEC, E, TEAM>(team, k, 0), at_c = c < width ? c : 0;
+            const int c = column<VEC, E, TEAM>(team, k, 0);
             Unit<T> u;
-            if (!staged)
-                u.w = *reinterpret_cast<const uint4 *>(ptr + r * stride + at_c);
-            else
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(u.w.x), "=r"(u.w.y), "=r"(u.w.z), "=r"(u.w.w)
-                             : "r"(at + stage * step + at_c * int(sizeof(T))));
+            u.w = make_uint4(0u, 0u, 0u, 0u);
+            if (!staged) {
+                if (c < width) u.w = *reinterpret_cast<const uint4 *>(ptr + r * stride + c);
+            } else {
+                asm volatile("{\n"
+                             "  .reg .pred in;\n"
+                             "  setp.lt.s32 in, %4, %5;\n"
+                             "  @in ld.shared.v4.u32 {%0, %1, %2, %3}, [%6];\n"
+                             "}"
+                             : "+r"(u.w.x), "+r"(u.w.y), "+r"(u.w.z), "+r"(u.w.w)
+                             : "r"(c), "r"(width), "r"(at + stage * step + c * int(sizeof(T))));
+            }
             u.get(v);
-            if (at_c + VEC > width) {
+            if (c + VEC > width) {
 #pragma unroll
                 for (int i = 0; i < E / 2; ++i) {
-                    if (at_c + 2 * i >= width) v[i].x = 0.0f;
-                    if (at_c + 2 * i + 1 >= width) v[i].y = 0.0f;
+                    if (c + 2 * i >= width) v[i].x = 0.0f;
+                    if (c + 2 * i + 1 >= width) v[i].y = 0.0f;
                 }
             }
         }
