@@ -633,14 +633,17 @@ int zg_grads_init(const zg_grad *list, int64_t count, zg_grads **out); /* waits 
 void zg_grads_destroy(zg_grads *grads); /* after the calls on it are done */
 int64_t zg_grads_workspace(const zg_grads *grads); /* bytes, for either call */
 
-/* norm = sqrt(sum over all elements of (scale * g)^2), squares in binary32 and their
- * sums in a fixed order; stats[0] = norm, stats[1] = the coefficient
- * min(1, max_norm / (norm + eps)), or 1 where the norm is not finite. zg_grads_norm
- * has 1 there always. zg_grads_clip writes out = (scale * coefficient) * g, rounded
- * once. A norm that is not finite clips nothing, so that an infinite or NaN element
- * reaches the step that takes the gradients, which then skips. work: 16-byte aligned, the
- * call's alone until it is done. max_norm > 0 and scale > 0 finite (max_norm may
- * be infinite), eps >= 0 finite. */
+/* norm = sqrt(sum over all elements of (scale * g)^2), squares in binary32 (in binary64
+ * where those leave its range) and their sums in a fixed order; stats[0] = norm,
+ * stats[1] = the coefficient min(1, max_norm / (norm + eps)), or 1 where an element is
+ * not finite. zg_grads_clip writes out = (scale * coefficient) * g, rounded once. Finite
+ * elements are clipped whatever their size: where the norm itself is beyond binary32
+ * stats[0] is infinite and the coefficient that of the norm in binary64 (below
+ * 1.2e-38 it has what bits binary32 has there). An infinite or NaN element clips nothing, so
+ * that it reaches the step that takes the gradients, which then skips. zg_grads_norm
+ * has 1 in stats[1] always, and an infinite norm already where squares overflow binary32
+ * (elements of some 1e19 / scale). work: 16-byte aligned, the call's alone until it is done. max_norm > 0
+ * and scale > 0 finite (max_norm may be infinite), eps >= 0 finite. */
 int zg_grads_norm(const zg_grads *grads, float scale, float *stats, void *work, int64_t work_bytes, zg_stream stream);
 int zg_grads_clip(const zg_grads *grads, float max_norm, float eps, float scale, float *stats, void *work,
                   int64_t work_bytes, zg_stream stream);

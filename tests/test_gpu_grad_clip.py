@@ -101,6 +101,47 @@ def test_non_finite_gradients_pass_unclipped(dtype):
     assert float(zb.GradClip(grads).norm()[0]) == math.inf
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "mixed"])
+@pytest.mark.parametrize("size", [1e20, 1e30, 1e35, 1e-19, 1e-20, 1e-25, 1e-30])
+def test_finite_gradients_of_any_size_are_clipped(size, dtype):
+    """Squares that overflow binary32, or vanish in it, of all elements and of one."""
+    sizes = [3000, 20, 70000]
+    every = grads_of(sizes, dtype, 8, size, offset=1)
+    one = grads_of(sizes, dtype, 9, 1e-3 if size > 1 else 0.0, offset=1)
+    one[2][40001] = -size
+    for grads in (every, one):
+        host = [g.cpu() for g in grads]
+        for scale in (0.25, 1.0):
+            norm = float(ref.clip(host, scale, 1.0, 0.0)[0])
+            for max_norm in (norm / 2, 2 * norm):
+                flat = torch.empty(sum(sizes), dtype=torch.float32, device="cuda")
+                stats = zb.GradClip(grads, out=flat).clip(max_norm, 0.0, scale)
+                check(grads, flat.split(sizes), stats, host, scale, max_norm, 0.0)
+            if size < 1:
+                assert abs(float(zb.GradClip(grads).norm(scale)[0]) - norm) <= (ref.DEEP + ref.ULP) * norm
+
+
+def test_one_exploded_element_of_a_long_list():
+    """As many parts as take the sums' own launch."""
+    g = grads_of([34_000_000, 7], "bf16", 10, 1e-3)
+    g[0][33_999_999] = 1e30
+    host, flat = [t.cpu() for t in g], torch.empty(34_000_007, dtype=torch.bfloat16, device="cuda")
+    check(g, flat.split([34_000_000, 7]), zb.GradClip(g, out=flat).clip(1.0), host, 1.0, 1.0)
+    assert float(flat.float().abs().max()) == 1.0
+
+
+def test_a_norm_beyond_binary32():
+    g = torch.full((100,), 3e38, device="cuda")
+    h = g.double()
+    stats = zb.GradClip([g]).clip(1e3)  # norm 3e39
+    assert float(stats[0]) == math.inf
+    coef = 1e3 / float(h.norm())
+    assert abs(float(stats[1]) - coef) <= 4 * ref.ULP * coef
+    assert float(((g - h * coef).abs() / (h * coef)).max()) <= 8 * ref.ULP
+    g[0], g[1] = 0.0, math.inf  # an element that is not finite
+    assert float(zb.GradClip([g]).clip(1e3)[1]) == 1.0
+
+
 def test_zero_gradients_and_no_limit():
     grads = [torch.zeros(100, device="cuda"), torch.zeros(0, device="cuda")]
     stats = zb.GradClip(grads).clip(1.0)

@@ -1148,7 +1148,8 @@ class GradClip:
             self.handle = None
 
     def norm(self, scale: float = 1.0, stream=None) -> torch.Tensor:
-        """A float32 CUDA tensor of two: the norm of ``scale`` times all gradients, and 1."""
+        """A float32 CUDA tensor of two: the norm of ``scale`` times all gradients (infinite where their squares
+        overflow binary32, which ``clip`` bears), and 1."""
         ref = self.tensors[0]
         if stream is not None:
             return _on(stream, ref, self.norm, scale)
@@ -1159,7 +1160,7 @@ class GradClip:
         return stats
 
     def clip(self, max_norm: float, eps: float = 1e-6, scale: float = 1.0, stream=None) -> torch.Tensor:
-        """Write scale * min(1, max_norm / (norm + eps)) times the gradients (scale times them where the norm is
+        """Write scale * min(1, max_norm / (norm + eps)) times the gradients (scale times them where an element is
         not finite): a float32 CUDA tensor of the norm, of ``scale`` times them, and the coefficient."""
         ref = self.tensors[0]
         if stream is not None:

@@ -2,7 +2,8 @@
 //
 // A list is cut into parts of some thousand elements of one tensor, a block to
 // each: the first pass leaves the sum of a part's squares, one block adds the
-// sums up in a fixed order, and the second pass writes (scale * coefficient) * g.
+// sums up in a fixed order, and the second pass writes (scale * coefficient) * g. Squares are
+// binary32's, and binary64's in a part where those overflow or vanish.
 //
 // Bound by memory: every gradient is read for the norm, and again and written once the
 // norm is known, the second time in the opposite order, since what was read last is still in
@@ -61,7 +62,7 @@ __device__ __forceinline__ float2 stats_of(double sum, float max_norm, float eps
 // The squares of a part, in units from the 16-byte boundary at or before it; what a unit has
 // outside the part counts as zero.
 template <class T>
-__device__ __forceinline__ float squares(const GradPart &p, float scale)
+__device__ __forceinline__ float squares(const GradPart &p, float scale, uint32_t &bits)
 {
     constexpr int N = Unit<T>::kN;
     const T *const g = static_cast<const T *>(p.grad);
@@ -72,6 +73,7 @@ __device__ __forceinline__ float squares(const GradPart &p, float scale)
     auto add = [&](uint4 w, int u) {
         Unit<T> x;
         x.w = w;
+        bits |= w.x | w.y | w.z | w.w;
         float2 v[N / 2];
         x.get(v);
         if (u * N < head || (u + 1) * N > end) {
@@ -96,22 +98,57 @@ __device__ __forceinline__ float squares(const GradPart &p, float scale)
         for (int i = 0; i < kAhead; ++i)
             if (u + i * kThreads < units) add(w[i], u + i * kThreads);
     }
+    bits &= sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu;  // zeros of either sign
     return sum.x + sum.y;
 }
+// A thread's squares of the same part in binary64, which holds every finite one of theirs.
+template <class T>
+__device__ double wide_squares(const GradPart &p, float scale)
+{
+    const T *const g = static_cast<const T *>(p.grad);
+    double s = 0.0;
+    for (int i = threadIdx.x; i < p.n; i += kThreads) {
+        const double v = double(load1(g + i)) * double(scale);
+        s = fma(v, v, s);
+    }
+    return s;
+}
 
-__global__ void __launch_bounds__(kThreads) squares_kernel(const GradPart *parts, double *sums, float scale)
+// Sums of squares below this may have lost some of them: of a part's 2^15 squares each is off by at most
+// 2^-150 where it is not normal, 2^-25 of such a sum in all.
+constexpr float kLeastSum = 7.7e-34f;  // 2^-110
+
+// A part whose sum has left binary32's range is added up again in binary64: one exploded
+// element must not keep a list of finite ones from being clipped. `large` is for the sums that overflow; those
+// that vanish though an element is not zero are always made good. The rest pay for the question alone (an or of
+// every unit's bits: the norm of 124 M gradients 43 us with it and without).
+__global__ void __launch_bounds__(kThreads) squares_kernel(const GradPart *parts, double *sums, float scale, bool large)
 {
     pdl_trigger();
-    const GradPart p = parts[blockIdx.x];
     __shared__ float part[kThreads / 32];
-    const float mine = sum_of_warp(p.dtype == ZG_DTYPE_BF16 ? squares<uint16_t>(p, scale) : squares<float>(p, scale));
+    __shared__ double wide[kThreads / 32];
+    uint32_t bits = 0;
+    const GradPart p = parts[blockIdx.x];
+    const float mine =
+        sum_of_warp(p.dtype == ZG_DTYPE_BF16 ? squares<uint16_t>(p, scale, bits) : squares<float>(p, scale, bits));
     if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = mine;
-    __syncthreads();
-    if (threadIdx.x) return;
+    const bool any = __syncthreads_or(bits != 0);
     double total = 0.0;
+    float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) total += part[i];
-    sums[blockIdx.x] = total;
+    for (int i = 0; i < kThreads / 32; ++i) sum += part[i];
+    if ((any && sum < kLeastSum) || (large && !isfinite(sum))) {
+        const GradPart q = parts[blockIdx.x];  // read again: kept, it would cost the first look registers
+        const double again =
+            sum_of_warp(q.dtype == ZG_DTYPE_BF16 ? wide_squares<uint16_t>(q, scale) : wide_squares<float>(q, scale));
+        if (threadIdx.x % 32 == 0) wide[threadIdx.x / 32] = again;
+        __syncthreads();
+        for (int i = 0; i < kThreads / 32; ++i) total += wide[i];
+    } else if (threadIdx.x == 0) {
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) total += part[i];
+    }
+    if (threadIdx.x == 0) sums[blockIdx.x] = total;
 }
 
 __global__ void __launch_bounds__(kThreads) finish_kernel(const double *sums, int64_t count, float max_norm, float eps,
@@ -233,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const GradPart *parts, 
 cudaError_t launch_grads_norm(const GradPart *parts, int64_t count, double *sums, float scale, float max_norm, float eps,
                               float *stats, bool write, cudaStream_t st)
 {
-    if (count) squares_kernel<<<unsigned(count), kThreads, 0, st>>>(parts, sums, scale);
+    if (count) squares_kernel<<<unsigned(count), kThreads, 0, st>>>(parts, sums, scale, write);
     if (cudaError_t e = cudaGetLastError()) return e;
     // up to 1,024 parts are added up by each block that writes: a launch less
     const bool alone = write && count > 0 && count <= 1024;
