@@ -589,7 +589,9 @@ int zg_token_logp(const void *logits, int dtype, int64_t rows, int64_t vocab, in
  *   dlogits_v = scale * dloss * slope / temperature * ([v = token] - softmax_v).
  * ref_logp NULL: no KL term. A row whose token is outside [0, vocab) is a padding
  * row: its loss, logp and gradient are zero, whatever else it holds. Logits may be
- * masked by -inf or any large negative number; a row of nothing but -inf gives NaN. */
+ * masked by -inf or any large negative number; a row of nothing but -inf gives NaN. A ratio or
+ * exp(d) may be beyond binary32 where its product with A or kl is not (A = 0, say); where
+ * scale * dloss * slope / temperature is, the row's gradient is not finite. */
 typedef struct {
     const void *logits; /* row r starts at logits + r * row_stride elements; aligned to its element */
     int64_t rows, vocab, row_stride; /* vocab <= 2^30, row_stride >= vocab */

@@ -275,6 +275,30 @@ def test_bounds_of_the_ratio_and_the_zero_advantage():
     check_policy(z, tokens, old, torch.zeros(12), None, 1.0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("v", [90, 50257])
+def test_ratios_and_references_beyond_binary32(v, dtype):
+    """e^x alone is infinite in binary32; what it is multiplied by makes it zero, or finite again."""
+    n = 8
+    z = logits_of(n, v, DT[dtype], 23)
+    tokens = torch.arange(n) * 11
+    logp = torch.log_softmax(z.double().cpu(), 1).gather(1, tokens[:, None])[:, 0]
+    old = (logp - torch.tensor([100.0, 100.0, 95.0, 81.0, 300.0, 0.05, 79.9, 100.0])).float()
+    adv = torch.tensor([0.0, 1.0, -1e-9, -1e-3, 0.0, 1.0, -1e-3, 1e-12])
+    check_policy(z, tokens, old, adv, None, 1.0)
+    old = (logp - 0.05).float()
+    refl = (logp + torch.tensor([100.0, 95.0, 81.0, 300.0, 0.3, 79.9, -100.0, 88.9])).float()
+    check_policy(z, tokens, old, adv, refl, 1.0, kl=0.0)
+    refl[3] = (logp[3] + 90).float()
+    # the first row's slope is 1e-6 e^100 = 2.69e37: times 64 it is 1.7e39, beyond the largest binary32 (3.4e38), and
+    # a row's gradient is then not finite; the loss is, and the other rows are
+    loss, _, grad = zb.policy_loss_grad(z, tokens.cuda(), old.cuda(), adv.cuda(), refl.cuda(), CLIP, 1e-6, 1.0, 64.0)
+    want = 1e-6 * math.exp(float(refl[0].double() - logp[0]))
+    assert abs(float(loss[0]) - want) <= 400 * ref.EPS * want  # the argument, some 100, carries its logp's error
+    assert not math.isfinite(float(grad[0, 0])) and bool(torch.isfinite(grad[1:]).all())
+    check_policy(z[1:], tokens[1:], old[1:], adv[1:], refl[1:], 1.0, kl=1e-6)
+
+
 def test_gradient_against_differences():
     v, n = 301, 5
     z = logits_of(n, v, torch.float32, 14)

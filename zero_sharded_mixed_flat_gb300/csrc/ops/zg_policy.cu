@@ -81,6 +81,16 @@ __device__ __forceinline__ int token_of(const PolicyArgs &a, int64_t r)
     return t >= 0 && t < a.vocab ? int(t) : -1;
 }
 
+// a e^x, where e^x may be beyond binary32 though the product is not: an advantage or a KL factor of
+// zero, say, beside a ratio that a rare token makes as large as it likes.
+constexpr float kLarge = 80.0f;
+__device__ __forceinline__ float times_exp(float x, float a)
+{
+    if (x <= kLarge) return a * expf(x);
+    if (a == 0.0f && x < INFINITY) return a;
+    return a * expf(0.5f * x) * expf(0.5f * x);
+}
+
 // What a row's loss and slope are made of, beside logp.
 struct Values {
     float adv, old, ref, weight;
@@ -94,13 +104,20 @@ struct Values {
     // The loss and its slope by logp.
     __device__ __forceinline__ float2 loss(const PolicyArgs &a, float logp) const
     {
-        const float ratio = expf(logp - old), high = 1.0f + a.clip_high, low = 1.0f - a.clip_low;
+        const float x = logp - old, ratio = expf(x), high = 1.0f + a.clip_high, low = 1.0f - a.clip_low;
         const bool cut = (adv > 0.0f && ratio > high) || (adv < 0.0f && ratio < low);
-        float l = -(cut ? (adv > 0.0f ? high : low) : ratio) * adv, slope = cut ? 0.0f : -ratio * adv;
+        float slope = cut ? 0.0f : -times_exp(x, adv), l = cut ? -(adv > 0.0f ? high : low) * adv : slope;
         if (a.ref_logp) {
-            const float d = ref - logp, e = expm1f(d);
-            l = fmaf(a.kl, e - d, l);
-            slope = fmaf(-a.kl, e, slope);
+            const float d = ref - logp;
+            if (d > kLarge) {  // 1 + d is far below the exponential's last place
+                const float t = times_exp(d, a.kl);
+                l += t;
+                slope -= t;
+            } else {
+                const float e = expm1f(d);
+                l = fmaf(a.kl, e - d, l);
+                slope = fmaf(-a.kl, e, slope);
+            }
         }
         return make_float2(l, slope);
     }
