@@ -513,7 +513,8 @@ def _dtype(t: torch.Tensor, what: str) -> int:
 
 
 def _like(t: torch.Tensor, ref: torch.Tensor, what: str) -> torch.Tensor:
-    """A CUDA tensor of ref's device, dtype and shape whose last dimension is contiguous."""
+    """A CUDA tensor of ref's device, dtype and shape whose last dimension is contiguous (an empty one's
+    strides lead nowhere, and may be any)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a tensor")
     if not t.is_cuda:

@@ -118,8 +118,10 @@ __device__ __forceinline__ int column(const Team &team, int k, int i)
 __device__ __forceinline__ float2 pair(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float total(float2 v) { return v.x + v.y; }
 
-// The rows of one tensor as a team reads them.
-template <class T, int VEC, int E, int K, int TEAM>
+// The rows of one tensor as a team reads them. Whole warps have places past an aligned row's end, whose units no
+// thread copies. ZEROS: they count as zero in a row's sums. A unit that another thread copies would not do there: its
+// copy may still be on its way, and a NaN found in its place stays one times a weight of zero.
+template <class T, int VEC, int E, int K, int TEAM, bool ZEROS>
 struct Source {
     const T *ptr;
     int64_t stride;
@@ -169,11 +171,24 @@ struct Source {
             }
         }
     }
-    // Chunk k of row r. Of aligned rows, places past the width are zero without a look: at any other column another
-    // thread's copy may still be on its way, and a NaN found there would stay one times a weight of zero. Of
-    // others, where the team's barrier has made every copy visible, they are (without TEAM) column 0 again.
-    // (The load's condition costs 2 to 4 %: 16384 x 4096 in bf16 96 -> 99 us forward, 156 -> 158 backward, 4096 x
-    // 16384 136 -> 141 and 550 -> 573; a branch in its place 102 for 96 at 32768 x 2048 forward.)
+    // Before the first row: zeros in the thread's own places past the row's end, which no copy reaches. (16384 x 2048 in
+    // binary32, backward: 132 us; with loads under a condition 138, with zeros by a condition after them 144, and 4096 x
+    // 8192 183 for 153. The places take room: at 9217 to 9556 columns in binary32 none is left for a row, 495 us for 339.)
+    __device__ __forceinline__ void open(const Team &team, int stages, int width) const
+    {
+        if constexpr (VEC != 1 && ZEROS) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int c = column<VEC, E, TEAM>(team, k, 0);
+                if (c < width) continue;
+                for (int i = 0; i < stages; ++i)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + i * step + c * int(sizeof(T))), "r"(0u)
+                                 : "memory");
+            }
+        }
+    }
+    // Chunk k of row r. Of aligned rows, places past the width are zero, or without ZEROS the thread's own first place
+    // again; of others, where the team's barrier has made every copy visible, they are (without TEAM) column 0 again.
     __device__ __forceinline__ void get(const Team &team, int64_t r, int stage, bool staged, int k, int width,
                                         float2 (&v)[E / 2]) const
     {
@@ -196,20 +211,15 @@ struct Source {
 #pragma unroll
             for (int i = 0; i < E / 2; ++i) v[i] = make_float2(e[2 * i], e[2 * i + 1]);
         } else {
-            const int c = column<VEC, E, TEAM>(team, k, 0);
+            const int place = column<VEC, E, TEAM>(team, k, 0), own = place < width ? place : column<VEC, E, TEAM>(team, 0, 0);
+            const int c = ZEROS ? place : own;
             Unit<T> u;
-            u.w = make_uint4(0u, 0u, 0u, 0u);
-            if (!staged) {
-                if (c < width) u.w = *reinterpret_cast<const uint4 *>(ptr + r * stride + c);
-            } else {
-                asm volatile("{\n"
-                             "  .reg .pred in;\n"
-                             "  setp.lt.s32 in, %4, %5;\n"
-                             "  @in ld.shared.v4.u32 {%0, %1, %2, %3}, [%6];\n"
-                             "}"
-                             : "+r"(u.w.x), "+r"(u.w.y), "+r"(u.w.z), "+r"(u.w.w)
-                             : "r"(c), "r"(width), "r"(at + stage * step + c * int(sizeof(T))));
-            }
+            if (!staged)
+                u.w = *reinterpret_cast<const uint4 *>(ptr + r * stride + min(own, (width - 1) / VEC * VEC));
+            else
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(u.w.x), "=r"(u.w.y), "=r"(u.w.z), "=r"(u.w.w)
+                             : "r"(at + stage * step + c * int(sizeof(T))));
             u.get(v);
             if (c + VEC > width) {
 #pragma unroll
@@ -359,7 +369,7 @@ __global__ void __launch_bounds__(kMost, (kToSm<E * K, ALL>)) forward_kernel(Blo
     const int width = a.width, stages = ring.stages > 0 ? ring.stages : 1;
     const bool staged = TEAM || ALL || ring.stages > 0, block = ALL || a.o.ptr, has_n = ALL || a.w_pre, has_x = ALL || a.x_new.ptr;
     const uint32_t mine = uint32_t(__cvta_generic_to_shared(rows)) + team.id * (2 * ring.slot * ring.stages);
-    const Source<T, VEC, E, K, TEAM> x_in(a.x, mine, 0, ring, 2), o_in(a.o, mine, 1, ring, 2);
+    const Source<T, VEC, E, K, TEAM, false> x_in(a.x, mine, 0, ring, 2), o_in(a.o, mine, 1, ring, 2);
     const int64_t teams = int64_t(gridDim.x) * team.count, each = (a.rows + teams - 1) / teams;
     const int64_t lo = min((int64_t(blockIdx.x) * team.count + team.id) * each, a.rows), hi = min(lo + each, a.rows);
     const int64_t in_group = a.rows / a.groups;
@@ -524,8 +534,8 @@ __global__ void __launch_bounds__(kMost, (kToSm<E * K, ALL && VEC == 1>)) backwa
     const uint32_t mine = uint32_t(__cvta_generic_to_shared(rows)) + team.id * (4 * ring.slot * ring.stages);
     float *const wide = reinterpret_cast<float *>(rows + team.count * (4 * ring.slot * ring.stages));
     const Wide<VEC, E, K, TEAM> u_of(wide, width), w2_of(wide + Wide<VEC, E, K, TEAM>::size(width), width);
-    const Source<T, VEC, E, K, TEAM> x_in(a.x, mine, 0, ring, 4), o_in(a.o, mine, 1, ring, 4), dn_in(a.n, mine, 2, ring, 4),
-        y_in(a.x_new, mine, 3, ring, 4);
+    using In = Source<T, VEC, E, K, TEAM, true>;
+    const In x_in(a.x, mine, 0, ring, 4), o_in(a.o, mine, 1, ring, 4), dn_in(a.n, mine, 2, ring, 4), y_in(a.x_new, mine, 3, ring, 4);
     const int64_t in_group = a.rows / a.groups, group_step = int64_t(gridDim.x) * team.count;
     // The team's rows, one after another: of one gate's segment every count-th, or all of
     // every gate that is the team's.
@@ -561,6 +571,10 @@ __global__ void __launch_bounds__(kMost, (kToSm<E * K, ALL && VEC == 1>)) backwa
         }
         commit_copies();
     };
+    x_in.open(team, ring.stages, width);
+    o_in.open(team, ring.stages, width);
+    dn_in.open(team, ring.stages, width);
+    y_in.open(team, ring.stages, width);
     for (int i = 0; i < stages; ++i) ask(i);
     constexpr int R = MANY ? K : 1;  // what a gate's change or end concerns is a team's own, in registers
     float2 q[K][E / 2], p[K][E / 2], dw1[R][E / 2], u_here[R][E / 2], w2_here[R][E / 2];
@@ -836,7 +850,8 @@ struct Shape {
     Ring ring;
     size_t bytes;
 };
-Shape shape_of(const BlockArgs &a, int vec, int columns, int team, int tensors, bool wide, int to_sm)
+// `places`: what a thread has of an aligned row in shared memory, at least.
+Shape shape_of(const BlockArgs &a, int vec, int columns, int team, int tensors, bool wide, int places, int to_sm)
 {
     const int size = a.dtype == ZG_DTYPE_BF16 ? 2 : 4;
     Shape s;
@@ -845,10 +860,11 @@ Shape shape_of(const BlockArgs &a, int vec, int columns, int team, int tensors, 
     if (s.teams > kTeams) s.teams = kTeams;
     const int64_t blocks = kBlocks * to_sm;
     if (a.rows < s.teams * blocks) s.teams = int((a.rows + blocks - 1) / blocks);  // few rows: all SMs
-    const int held = team ? team * columns : a.width;  // columns of a stage
+    // columns of a stage
+    const int held = team ? team * columns : vec != 1 && a.width < s.team * places ? s.team * places : a.width;
     s.ring.slot = (held * size + (vec == 1 ? 48 : 0) + 15) / 16 * 16;  // a head, and two units that are cleared
     const size_t row = size_t(s.teams) * tensors * s.ring.slot;
-    const size_t beside = wide ? size_t(held + 7) / 8 * 64 : 0;  // two weights in binary32
+    const size_t beside = wide ? size_t((team ? held : a.width) + 7) / 8 * 64 : 0;  // two weights in binary32
     s.ring.stages = beside < size_t(kMemory / to_sm) ? int((size_t(kMemory / to_sm) - (to_sm - 1) * 4096 - beside) / row) : 0;
     if (s.ring.stages > kStages) s.ring.stages = kStages;
     s.bytes = row * s.ring.stages + beside;
@@ -875,9 +891,9 @@ cudaError_t forward(const BlockArgs &a, cudaStream_t st)
 {
     const bool every = a.o.ptr && a.x_new.ptr && a.w_pre;
     int to_sm = kToSm<E * K, true>;
-    Shape s = shape_of(a, VEC, E * K, TEAM, 2, false, to_sm);
+    Shape s = shape_of(a, VEC, E * K, TEAM, 2, false, E, to_sm);
     const bool all = every && s.ring.stages > 0;
-    if (!all) s = shape_of(a, VEC, E * K, TEAM, 2, false, to_sm = 1);
+    if (!all) s = shape_of(a, VEC, E * K, TEAM, 2, false, E, to_sm = 1);
     auto *kernel = all ? &forward_kernel<T, VEC, E, K, TEAM, true> : &forward_kernel<T, VEC, E, K, TEAM, false>;
     static std::atomic<uint64_t> allowed[2];
     if (cudaError_t e = allow(kernel, allowed[all])) return e;
@@ -894,13 +910,13 @@ cudaError_t backward(const BlockArgs &a, cudaStream_t st)
     auto *kernel = &backward_kernel<T, VEC, E, K, 0, false, false>;
     int which = 0;
     Shares shares = shares_of(a.rows, a.groups, kBlocks * kMany);
-    Shape s = shape_of(a, VEC, E * K, TEAM, 4, true, kMany);
+    Shape s = shape_of(a, VEC, E * K, TEAM, 4, true, E * K, kMany);
     if (a.o.ptr && a.n.ptr && a.x_new.ptr && shares.segments && s.ring.stages > 0) {
         kernel = &backward_kernel<T, VEC, E, K, TEAM, false, true>;
         which = 2;
     } else {
         shares = shares_of(a.rows, a.groups, kBlocks);
-        s = shape_of(a, VEC, E * K, 0, 4, shares.segments > 0, 1);
+        s = shape_of(a, VEC, E * K, 0, 4, shares.segments > 0, E * K, 1);
         if (!shares.segments) {
             kernel = &backward_kernel<T, VEC, E, K, 0, true, false>;
             which = 1;
