@@ -7,7 +7,9 @@ at a time (the recurrence's and the norms' single-token forms), is paid for ever
 token that is the last one's successor, and takes the clipped policy loss, with a KL
 term to where it began, of what it sampled. The gradients of all tensors are clipped
 by their common norm into the rank's flat bf16 gradient, and one step reduces and
-applies the P ranks' gradients.
+applies the P ranks' gradients. That clips each rank by itself, so that no rank's
+samples outweigh the others'; the clipping by the norm of the reduced gradient is the
+step's own, which follows (`Hparams.max_grad_norm`).
 
     python examples/policy_recurrent_blocks.py [--steps 30]
 """

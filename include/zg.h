@@ -536,7 +536,9 @@ int zg_embed_grad(const void *drows, int dtype, int64_t drow_stride, const void 
  *   b     = w_post * o * s_o,  s_o = 1 / sqrt(mean(o^2) + eps)   (w_post NULL: b = o)
  *   x_new = res_scale * x + gate * b                             (gate NULL: ones)
  *   n     = w_pre * x_new * s_x,  s_x = 1 / sqrt(mean(x_new^2) + eps)
- * n is of x_new before its rounding. All tensors have one dtype (ZG_DTYPE_*).
+ * n is of x_new before its rounding. Squares are summed in binary32: s is 0 where a row's sum
+ * overflows it (elements of some 1e18); with eps 0 it loses bits where elements are below some
+ * 1e-19, and is infinite where their squares vanish. All tensors have one dtype (ZG_DTYPE_*).
  * gate is `groups` contiguous rows: row r takes the gate of group r / (rows /
  * groups), so 1 is a gate of the channels, the number of sequences one for each of
  * them, and `rows` one for each token. o NULL: there is no block yet (x_new =
@@ -640,8 +642,8 @@ int64_t zg_grads_workspace(const zg_grads *grads); /* bytes, for either call */
  * stats[1] = the coefficient min(1, max_norm / (norm + eps)), or 1 where an element is
  * not finite. zg_grads_clip writes out = (scale * coefficient) * g, rounded once. Finite
  * elements are clipped whatever their size: where the norm itself is beyond binary32
- * stats[0] is infinite and the coefficient that of the norm in binary64 (below
- * 1.2e-38 it has what bits binary32 has there). An infinite or NaN element clips nothing, so
+ * stats[0] is infinite and the coefficient that of the norm in binary64 (it and scale times
+ * it have what bits binary32 has, fewer below 1.2e-38). An infinite or NaN element clips nothing, so
  * that it reaches the step that takes the gradients, which then skips. zg_grads_norm
  * has 1 in stats[1] always, and an infinite norm already where squares overflow binary32
  * (elements of some 1e19 / scale). work: 16-byte aligned, the call's alone until it is done. max_norm > 0

@@ -1101,7 +1101,9 @@ class GradClip:
     memory this object keeps (make another when they get new memory). ``out``: None to clip them
     where they are; a flat tensor, bf16 or float32, that receives them end to end in their order (the flat
     gradient of ``ShardedAdamW.step``, say; elements past them are left as they were); or a list of tensors of
-    their sizes. Calls may run on any stream; two that write at once must be ordered by the caller."""
+    their sizes. Calls may run on any stream; two that write at once must be ordered by the caller. A graph that
+    captured a call needs this object as long as it is replayed. The norm is of this list: over several ranks
+    the clipping by the reduced gradient's norm is ``ShardedAdamW.step``'s own (``max_grad_norm``)."""
 
     def __init__(self, tensors, out=None):
         self.handle = None

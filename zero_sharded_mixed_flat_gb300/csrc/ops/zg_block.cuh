@@ -17,12 +17,12 @@
 // copied and read by the same thread, and by no other, so they need no barrier), and goes
 // over the row in shared memory again where a sum has to be known first.
 //
-// Measured at 16384 x 4096 in bf16: forward 94 us (5.7 TB/s), backward 150 (5.4 TB/s) and some 6 to 10 for the sums of
-// the weights' gradients after it; with a gate for each of 64 sequences 183, of 512 231, of every row 737. In binary32 172
-// and 262 us (6.2 and 6.1 TB/s). Issue is active in 45 to 49 % of the cycles at 16 warps to an SM: what is left are
-// the dependent sums of a row. 32768 x 2048 in bf16 91 and 145 us (5.9 and 5.6 TB/s). 9001 x 771 in binary32, rows at any
+// Measured at 16384 x 4096 in bf16: forward 94 us (5.7 TB/s), backward 151 (5.3 TB/s) and some 6 to 10 for the sums of
+// the weights' gradients after it; with a gate for each of 64 sequences 184, of 512 231, of every row 720. In binary32 172
+// and 252 us (6.2 and 6.4 TB/s). Issue is active in 45 to 49 % of the cycles at 16 warps to an SM: what is left are
+// the dependent sums of a row. 32768 x 2048 in bf16 91 and 147 us (5.9 and 5.5 TB/s). 9001 x 771 in binary32, rows at any
 // alignment: 23 and 44 us (4.8 and 3.8 TB/s); 2000 x 4099 35 and 80. Of 16384 columns in bf16 the backward pass has
-// no room in shared memory for its rows and weights and reads rows from memory twice (4096 rows 551 us, forward 137).
+// no room in shared memory for its rows and weights and reads rows from memory twice (4096 rows 562 us, forward 137).
 #pragma once
 
 #include <atomic>
@@ -37,7 +37,9 @@ namespace {
 
 constexpr int kMost = 512;     // threads of a block
 constexpr int kBlocks = 152;   // SMs
-// Blocks to an SM: two where a thread's few columns fit half of the registers.
+// Blocks to an SM: two where a thread's few columns fit half of the registers. (Not so in the backward pass of aligned
+// rows, whose threads hold whole units of four tensors: 32768 x 768 there in bf16 106 us with two and 79 with one, in
+// binary32 128 and 100.)
 template <int COLUMNS, bool ALL>
 constexpr int kToSm = ALL && COLUMNS <= 8 ? 2 : 1;
 constexpr int kStages = 4;     // rows of a team in shared memory, at most
@@ -942,8 +944,10 @@ cudaError_t backward(const BlockArgs &a, cudaStream_t st)
 template <class T, bool BACK>
 cudaError_t of_type(const BlockArgs &a, cudaStream_t st)
 {
-    // chunks of E columns, K of them to a thread, and at most MOST threads to a row (backward, aligned rows in bf16, 8
-    // columns to a thread against 16: 8192 x 768 25 and 27 us, 32768 x 1024 90 and 76, 32768 x 2048 178 and 144)
+    // chunks of E columns, K of them to a thread, and at most MOST threads to a row (backward, aligned rows, 8 columns to
+    // a thread against 16, in us with a graph's replay: in bf16 8192 x 768 32 and 36, 32768 x 768 79 and 93, 32768 x 1024
+    // 95 and 85, 32768 x 2048 181 and 155; in binary32 8192 x 768 34 and 42, 32768 x 768 100 and 114, 32768 x 1024 132 and
+    // 130, 16384 x 2048 132 both)
 #define ZG_CASE(MOST, VEC, E, K, TEAM) \
     if (a.width <= (E) * (K) * (MOST)) return BACK ? backward<T, VEC, E, K, TEAM>(a, st) : forward<T, VEC, E, K, TEAM>(a, st);
     constexpr int N = Unit<T>::kN;

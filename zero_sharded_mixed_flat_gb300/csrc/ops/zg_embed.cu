@@ -21,7 +21,9 @@
 // Measured, a table of 50257 x 768 in bf16: the lookup of 8192 tokens 4.5 us, of 65536 17 us. The gradient of 8192
 // tokens 25 us for 90 MB: the sort 14 us, beside which most rows without a token are written, then sum and join; of
 // 65536 tokens 78 us; of 8192 at 4096 columns 82 us (479 MB, 5.8 TB/s). Added to another gradient in place, 20011
-// tokens at 771 columns in binary32, 51 us, beside it 89. All 8192 tokens the same: 41 us.
+// tokens at 771 columns in binary32, 51 us, beside it 89 (at 768 columns 78). All 8192 tokens the same: 41 us. The sort
+// is a cluster's, however many tokens there are: from some 65536 on it takes the longer, the more of them. 262144
+// tokens take 256 us, of which the sort 133, 1048576 885, of which 498.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -678,7 +680,10 @@ cudaError_t sum_and_join(const EmbedArgs &a, const SumPlan &p, cudaStream_t st)
     return cudaLaunchKernelEx(&cfg, &join_kernel<T, VEC, K>, a, p);
 }
 
-constexpr int64_t kLooks = 65536;  // tokens up to which the blocks that fill look them all through
+// Tokens up to which the blocks that fill look them all through, beside the sort. (50257 x 768 in bf16, looking and from the
+// sorted list: 8192 tokens 32 and 44 us with a graph's replay, 20011 46 and 59, 65536 85 and 91, 262144 251 and 263,
+// 1048576 912 and 892. A larger bound would gain a little up to some 262144: 262144 x 768 there 296 and 351.)
+constexpr int64_t kLooks = 65536;
 
 template <class T, class D>
 cudaError_t gradient_of(const EmbedArgs &a, cudaStream_t st)

@@ -1,6 +1,6 @@
 // The gradients of many tensors, clipped by their common norm.
 //
-// A list is cut into parts of some thousand elements of one tensor, a block to
+// A list is cut into parts of some thousand elements of one tensor (up to 32,768), a block to
 // each: the first pass leaves the sum of a part's squares, one block adds the
 // sums up in a fixed order, and the second pass writes (scale * coefficient) * g. Squares are
 // binary32's, and binary64's in a part where those overflow or vanish.
@@ -10,7 +10,9 @@
 // L2. A thread has kAhead units of 16 bytes in flight.
 //
 // Measured: 124 M gradients of 148 tensors, matrices in bf16 and vectors in binary32, into a flat bf16 one, 112 us (249 MB read
-// twice and written once: 6.7 TB/s; the squares 38 us, 6.5 TB/s); 0.6 M in binary32 6 us.
+// twice and written once: 6.7 TB/s; the squares 38 us, 6.5 TB/s); 0.6 M in binary32 6 us. Where a part and its output lie
+// differently (a tensor of odd size before it in a flat output), elements are read and written one by one the second
+// time: the same list behind a vector of 50257 bf16 elements 141 us, of binary32 into binary32 246 for 240.
 #include "zg_launch.h"
 #include "zg_ops.h"
 #include "zg_rows.cuh"

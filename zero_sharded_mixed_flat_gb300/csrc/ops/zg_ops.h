@@ -141,9 +141,9 @@ struct GradPart {
     int n;
     uint8_t dtype, out_dtype;
 };
-// Elements of a part: some 1,024 parts to a list, so that small lists have work for all SMs, of what a
-// block reads well (124 M gradients: parts of 8192 elements 163 us, 16384 126, 32768 123, 65536 124; 0.6 M: of 8192
-// 14.5 us, 16384 16.5, 32768 19.9).
+// Elements of a part: at most some 1,024 parts to a list of up to 33 M elements, so that small lists have work for all SMs;
+// of larger lists the most that a block reads well, in as many parts as that makes (124 M gradients: parts of 8192
+// elements 163 us, 16384 126, 32768, some 3,900 parts, 123, 65536 124; 0.6 M: of 8192 14.5 us, 16384 16.5, 32768 19.9).
 constexpr int64_t kGradPartLeast = 4096, kGradPartMost = 32768;
 
 cudaError_t launch_grads_norm(const GradPart *parts, int64_t count, double *sums, float scale, float max_norm, float eps,
